@@ -489,6 +489,128 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
                    void* out, int64_t ldc, uint32_t* error_word, void* stream);
 
 /*
+ * The 8-bit path: a latent cache held in e4m3 with one scale per block of
+ * tokens, and an e4m3 GEMM with scales per block of 128.  The source pages
+ * name an 8-bit MLA cache as the baseline their NVFP4 cache is compared with
+ * ("#33", PR description) and define none of the calls below.
+ *
+ * The cache: e4m3 codes [num_slots, 576] (row = 512 latent features, then the
+ * 64 rotated RoPE features) and fp32 scales [num_slots / 64]: the key of slot
+ * r is codes[r] * scales[r / 64].  num_slots and page_size are multiples of
+ * MLA_FP8_BLOCK, so a block of 64 tokens lies in one page.  576 + 1/16 bytes
+ * a token.  Scales lie in [2^-60, 2^60] (MLA_DEVERR_SCALE otherwise).
+ */
+#define MLA_FP8_BLOCK 64   /* tokens that share one scale            */
+#define MLA_FP8_GROUP 128  /* features that share one GEMM scale     */
+
+/*
+ * mla_nvfp4_fp8_cache_append: the new tokens of every sequence written into
+ * the cache, their RoPE key rotated by their position on the way, and the
+ * new queries' RoPE part rotated by the same angles.
+ *   kv_c         : bf16 [num_tokens, 512], row stride kv_c_stride elements.
+ *   k_pe         : bf16 [num_tokens, 64], unrotated, row stride k_pe_stride.
+ *   cos_sin      : fp32 [max_position, 64]: cos of the 32 angles of a position,
+ *                  then their sin.
+ *   interleaved  : 1: angle i turns features (2i, 2i+1); 0: features (i, i+32).
+ *   cu_seqlens   : int32 [num_seqs + 1]: rows [cu[b], cu[b+1]) of kv_c, k_pe and
+ *                  q_pe are sequence b's new tokens.  Rows outside every
+ *                  sequence (behind the last of a padded batch) are neither
+ *                  read nor written.
+ *   context_lens : int32 [num_seqs]: tokens sequence b holds already; its new
+ *                  token i has position context_lens[b] + i.
+ *   max_new_tokens (host) >= every sequence's number of new tokens.
+ *   page_table   : int32 [num_seqs, max_pages], row stride page_table_stride:
+ *                  position p of sequence b is slot
+ *                  page_table[b][p / page_size] * page_size + p % page_size.
+ *   cache, scales: as above, updated in place.  A block belongs to one
+ *                  sequence of the call (blocks of a shared prefix are full
+ *                  and so never written).
+ *   q_pe, q_out  : bf16 [num_tokens, num_heads, 64], element strides per token
+ *                  and head; q_out may be q_pe with the same strides, or both
+ *                  NULL with num_heads 0.  Rounded once, to bf16.
+ * A block's scale is the smallest power of two s = 2^e, -60 <= e <= 60, with
+ * |key| <= 448 s over the block.  It only grows until the block's first
+ * token is written again, which starts it anew; where it grows, the codes of
+ * the block's earlier tokens are multiplied by s_old / s_new and rounded
+ * again (exact but for results below 2^-6, where e4m3 is subnormal).  Codes
+ * round to nearest even and saturate at +-448; a NaN feature gives the NaN
+ * code and no amax.
+ *   Errors       : MLA_DEVERR_BOUNDS for cu_seqlens out of range, a negative
+ *                  context length (the sequence is skipped), more than
+ *                  max_new_tokens new tokens, a position past the angle or
+ *                  page table, a page outside the cache (those tokens are
+ *                  skipped); MLA_DEVERR_SCALE for an earlier scale out of
+ *                  range (the block's scale then starts anew).
+ * Both row strides, the q strides (in bytes) and all tensors but scales and
+ * the int32 ones are 16-byte aligned.
+ */
+int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                               int64_t num_tokens, const float* cos_sin, int64_t max_position, int interleaved,
+                               const int32_t* cu_seqlens, const int32_t* context_lens, int num_seqs,
+                               int max_new_tokens, const int32_t* page_table, int64_t page_table_stride,
+                               int64_t max_pages, int page_size, uint8_t* cache, int64_t num_slots, float* scales,
+                               const void* q_pe, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
+                               int64_t q_out_stride_t, int64_t q_out_stride_h, int num_heads,
+                               uint32_t* error_word, void* stream);
+
+/*
+ * mla_nvfp4_fp8_decode: absorbed MLA decode over that cache.
+ *   q            : bf16 [batch, num_heads, 576] contiguous = [q_nope.W_UK (512),
+ *                  rotated q_pe (64)] per head.
+ *   page_table   : int32 [batch, max_pages], row stride page_table_stride;
+ *   seq_lens     : int32 [batch], keys of sequence b (its newest token's too).
+ *   out, lse     : bf16 [batch, num_heads, 512]; fp32 [batch, num_heads] natural
+ *                  log, or NULL.  A sequence with no keys gives out = 0 and
+ *                  lse = -inf.
+ *   workspace    : mla_nvfp4_fp8_decode_workspace_size(batch, num_heads) bytes,
+ *                  256-byte aligned, contents ignored: the keys of a sequence
+ *                  are then cut so that all SMs get the same work, and the
+ *                  parts merged by LSE in a fixed order.  NULL: one SM (per
+ *                  32 heads) works through all keys of a sequence.  Calls
+ *                  that may run at once need a workspace each.
+ * scores = softmax_scale * q . key, out = softmax . key[:512].
+ * Rows of the cache that hold no key of the sequence are never used,
+ * whatever their bytes.  Errors: MLA_DEVERR_BOUNDS for a length past the page
+ * table or a page outside the cache, MLA_DEVERR_SCALE for a block scale out
+ * of range: those keys are skipped.
+ */
+int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                         const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                         int64_t max_pages, int page_size, const int32_t* seq_lens, float softmax_scale, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream);
+
+/* Bytes of workspace for mla_nvfp4_fp8_decode; 0 for invalid sizes. */
+size_t mla_nvfp4_fp8_decode_workspace_size(int batch, int num_heads);
+
+/*
+ * mla_nvfp4_fp8_quantize: activations to e4m3 with one scale per 128 features
+ * of a row, the operand A of mla_nvfp4_fp8_gemm.
+ *   x      : bf16 [M, K], row stride x_stride elements; K a multiple of 8.
+ *   codes  : e4m3 [M, K] contiguous;  scales : fp32 [M, ceil(K / 128)].
+ * scale = max(amax / 448, 2^-126) over the group (the last one of a row may
+ * be shorter), code = e4m3 RNE-satfinite(x / scale), both quotients rounded to
+ * nearest.  An infinity in a group gives scale = inf, code NaN for itself and
+ * 0 for finite values; a NaN gives the NaN code and no amax.
+ */
+int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                           void* stream);
+
+/*
+ * mla_nvfp4_fp8_gemm: out[m, n] = sum over blocks j of 128 features of
+ *     a_scales[m, j] * w_scales[n / 128, j] * sum_{k in j} a[m, k] * w[n, k],
+ * summed in fp32 and rounded once to bf16.
+ *   a : e4m3 [M, K], row stride lda bytes;  a_scales : fp32 [M, ceil(K / 128)].
+ *   w : e4m3 [N, K], row stride ldw bytes;  w_scales : fp32
+ *       [ceil(N / 128), ceil(K / 128)].
+ *   out : bf16 [M, N], row stride ldc elements.
+ * K a multiple of 16 (the last block may be shorter), any M and N; a, w, lda
+ * and ldw 16-byte aligned.  M == 0 or N == 0 is a no-op, K == 0 an error.
+ */
+int mla_nvfp4_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int64_t M, const uint8_t* w,
+                       int64_t ldw, const float* w_scales, int64_t N, int64_t K, void* out, int64_t ldc,
+                       uint32_t* error_word, void* stream);
+
+/*
  * Self-test of the bounded waits (test hook; no counterpart on the pages).
  * Every wait of the library's pipelined kernels (decode, prefill) gives up
  * after a time limit, ORs MLA_DEVERR_TIMEOUT into the error word and raises

@@ -24,12 +24,14 @@ __all__ = [
     "mla_nvfp4_decode", "mla_nvfp4_decode_q4", "mla_nvfp4_prefill_fused_out",
     "mla_nvfp4_quantize_rows", "mla_nvfp4_gemm", "mla_nvfp4_gather_latent", "mla_nvfp4_prefill_partial",
     "mla_nvfp4_merge_fused_out", "mla_nvfp4_prefill_qdq", "mla_nvfp4_prefill_fakequant",
-    "mla_nvfp4_prefill_quantized", "abi_symbols", "RECORD_BF16_ROPE", "RECORD_FP8_ROPE",
+    "mla_nvfp4_prefill_quantized", "mla_nvfp4_fp8_cache_append", "mla_nvfp4_fp8_decode",
+    "mla_nvfp4_fp8_decode_workspace_size", "mla_nvfp4_fp8_quantize", "mla_nvfp4_fp8_gemm", "abi_symbols", "RECORD_BF16_ROPE", "RECORD_FP8_ROPE",
     "LAUNCHES_PER_CALL",
 ]
 
 RECORD_BF16_ROPE = 432
 RECORD_FP8_ROPE = 368
+FP8_BLOCK, FP8_GROUP = 64, 128  # tokens per scale of the e4m3 cache; features per scale of the e4m3 GEMM
 DEVERR_BOUNDS, DEVERR_TIMEOUT, DEVERR_SCALE, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8
 
 # Kernels each entry point launches (for launch accounting in the benchmark);
@@ -98,6 +100,15 @@ _SIGS = {
                                              _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "mla_nvfp4_gemm": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_i64,
                                 _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_cache_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_vp,
+                                            _c_int, _c_int, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_vp,
+                                            _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_decode_workspace_size": (ctypes.c_size_t, [_c_int, _c_int]),
+    "mla_nvfp4_fp8_decode": (_c_int, [_c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
+                                      _c_vp, _c_f, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_quantize": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_gemm": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64,
+                                    _c_vp, _c_vp]),
     "mla_nvfp4_selftest_wait": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp]),
 }
 
@@ -634,3 +645,190 @@ def mla_nvfp4_prefill_quantized(q, k, v, cu_seqlens, max_seqlen, softmax_scale, 
     q_cs, k_cs, v_cs = mla_nvfp4_prefill_qdq(q, k, v, cu_seqlens, max_seqlen, *gs, error_word=error_word)
     return mla_nvfp4_prefill_fakequant(q_cs, k_cs, v_cs, cu_seqlens, max_seqlen, softmax_scale, *gs, global_scale,
                                        sparse24=sparse24, return_lse=return_lse, error_word=error_word)
+
+
+def _rows_contiguous(t):
+    """Last dimension contiguous (a tensor without elements, or a last dimension of one, may have any stride)."""
+    return t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1
+
+
+def _fp8_cache(cache, scales, dev):
+    """The e4m3 cache's two tensors: codes [num_slots, 576], scales fp32 [num_slots / 64]."""
+    _need(cache, "cache", torch.float8_e4m3fn, dev)
+    _need(scales, "scales", torch.float32, dev)
+    if cache.dim() != 2 or cache.shape[1] != 576 or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous [num_slots, 576]")
+    if cache.shape[0] % FP8_BLOCK != 0:
+        raise ValueError(f"num_slots must be a multiple of {FP8_BLOCK}")
+    if scales.shape != (cache.shape[0] // FP8_BLOCK,) or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous [num_slots / {FP8_BLOCK}]")
+
+
+def _fp8_pages(page_table, batch, page_size, dev):
+    _need(page_table, "page_table", torch.int32, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.shape[1] < 1:
+        raise ValueError("page_table must be [batch, max_pages]")
+    if not _rows_contiguous(page_table):
+        raise ValueError("page_table rows must be contiguous")
+    if page_size < FP8_BLOCK or page_size % FP8_BLOCK != 0:
+        raise ValueError(f"page_size must be a multiple of {FP8_BLOCK}")
+    # a table of one row may have any stride
+    return max(page_table.stride(0), page_table.shape[1])
+
+
+def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, *,
+                               page_size=64, interleaved=True, q_pe=None, q_out=None, max_new_tokens=None,
+                               error_word=None):
+    """Append every sequence's new tokens to the e4m3 latent cache, the RoPE
+    key rotated by its position: kv_c [T,512], k_pe [T,64] (bf16, unrotated),
+    cos_sin fp32 [max_position, 64] (32 cosines, 32 sines), rows
+    [cu_seqlens[b], cu_seqlens[b+1]) at positions context_lens[b] onwards,
+    into cache (float8_e4m3fn [num_slots, 576]) and its block scales (fp32
+    [num_slots / 64]), in place.  With q_pe [T,H,64] the queries' RoPE part is
+    rotated too, into q_out (default: a new tensor; q_pe itself rotates in
+    place), which is returned.  max_new_tokens bounds the tokens of one
+    sequence (default T; a tighter bound starts fewer CTAs)."""
+    dev = cache.device
+    _fp8_cache(cache, scales, dev)
+    for t, n, d in ((kv_c, "kv_c", 512), (k_pe, "k_pe", 64)):
+        _need(t, n, torch.bfloat16, dev)
+        if t.dim() != 2 or t.shape[1] != d or not _rows_contiguous(t):
+            raise ValueError(f"{n} must be [T, {d}] with a contiguous last dimension")
+    T = kv_c.shape[0]
+    _need(cos_sin, "cos_sin", torch.float32, dev)
+    if k_pe.shape[0] != T:
+        raise ValueError("shape mismatch")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous [max_position, 64]")
+    for t, n in ((cu_seqlens, "cu_seqlens"), (context_lens, "context_lens")):
+        _need(t, n, torch.int32, dev)
+        if t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous and one-dimensional")
+    B = context_lens.shape[0]
+    if cu_seqlens.shape[0] != B + 1:
+        raise ValueError("cu_seqlens must have one entry more than context_lens")
+    _need(error_word, "error_word", torch.int32, dev)
+    pt_stride = _fp8_pages(page_table, B, page_size, dev)
+    H, q_st, q_sh, o_st, o_sh = 0, 0, 0, 0, 0
+    if q_pe is None and q_out is not None:
+        raise ValueError("q_out goes with q_pe")
+    if q_pe is not None:
+        _need(q_pe, "q_pe", torch.bfloat16, dev)
+        if q_out is None:
+            q_out = torch.empty(q_pe.shape, dtype=torch.bfloat16, device=dev)
+        _need(q_out, "q_out", torch.bfloat16, dev)
+        for t, n in ((q_pe, "q_pe"), (q_out, "q_out")):
+            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != 64 or t.shape[1] < 1 or not _rows_contiguous(t):
+                raise ValueError(f"{n} must be [T, H, 64] with a contiguous last dimension")
+        if q_out.shape != q_pe.shape:
+            raise ValueError("q_out must have q_pe's shape")
+        H = q_pe.shape[1]
+        # a dimension of one element may have any stride
+        (q_st, q_sh), (o_st, o_sh) = [
+            (t.stride(0) if T > 1 else max(t.stride(0), 64 * H), t.stride(1) if H > 1 else 64) for t in (q_pe, q_out)]
+    max_new = T if max_new_tokens is None else int(max_new_tokens)
+    kv_st, pe_st = [t.stride(0) if T > 1 else t.shape[1] for t in (kv_c, k_pe)]  # one row: any stride
+    with torch.cuda.device(dev):
+        _check("mla_nvfp4_fp8_cache_append", load_library().mla_nvfp4_fp8_cache_append(
+            _ptr(kv_c), kv_st, _ptr(k_pe), pe_st, T, _ptr(cos_sin), cos_sin.shape[0], 1 if interleaved else 0,
+            _ptr(cu_seqlens), _ptr(context_lens), B, max_new, _ptr(page_table), pt_stride, page_table.shape[1],
+            page_size, _ptr(cache), cache.shape[0], _ptr(scales), _ptr(q_pe), q_st, q_sh, _ptr(q_out), o_st, o_sh, H,
+            _ptr(error_word), _stream(cache)))
+    return q_out
+
+
+def mla_nvfp4_fp8_decode_workspace_size(batch: int, num_heads: int) -> int:
+    return int(load_library().mla_nvfp4_fp8_decode_workspace_size(batch, num_heads))
+
+
+def mla_nvfp4_fp8_decode(q, cache, scales, softmax_scale, *, page_table, seq_lens, page_size=64, out=None, lse=None,
+                         workspace=None, split=True, error_word=None, return_lse=False):
+    """Absorbed MLA decode over the e4m3 cache (codes [num_slots, 576],
+    scales [num_slots / 64]): q [B,H,576] bf16 -> out [B,H,512] bf16 (and lse
+    [B,H] fp32).  split=False works through each sequence without cutting it
+    and needs no workspace; otherwise one is allocated unless given."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16)
+    _fp8_cache(cache, scales, dev)
+    if q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
+        raise ValueError("q must be contiguous [B, H, 576]")
+    B, H, _ = q.shape
+    pt_stride = _fp8_pages(page_table, B, page_size, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous [B]")
+    _need(error_word, "error_word", torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=dev)
+    if return_lse and lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+    for t, n, shape, dt in ((out, "out", (B, H, 512), torch.bfloat16), (lse, "lse", (B, H), torch.float32)):
+        _need(t, n, dt, dev)
+        if t is not None and (t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous {list(shape)}")
+    if workspace is not None and not split:
+        raise ValueError("split=False takes no workspace")
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if split and workspace is None:
+            need = int(lib.mla_nvfp4_fp8_decode_workspace_size(B, H))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _need(workspace, "workspace", torch.uint8, dev)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check("mla_nvfp4_fp8_decode", lib.mla_nvfp4_fp8_decode(
+            _ptr(q), B, H, _ptr(cache), cache.shape[0], _ptr(scales), _ptr(page_table), pt_stride,
+            page_table.shape[1], page_size, _ptr(seq_lens), float(softmax_scale), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel() if workspace is not None else 0, _ptr(error_word), _stream(q)))
+    return (out, lse) if return_lse else out
+
+
+def mla_nvfp4_fp8_quantize(x, *, codes=None, scales=None):
+    """bf16 [M, K] -> (float8_e4m3fn [M, K], fp32 scales [M, ceil(K / 128)]),
+    one scale per 128 features of a row."""
+    dev = x.device
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 2 or not _rows_contiguous(x):
+        raise ValueError("x must be [M, K] with a contiguous last dimension")
+    M, K = x.shape
+    groups = (K + FP8_GROUP - 1) // FP8_GROUP
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty((M, groups), dtype=torch.float32, device=dev)
+    for t, n, shape, dt in ((codes, "codes", (M, K), torch.float8_e4m3fn), (scales, "scales", (M, groups), torch.float32)):
+        _need(t, n, dt, dev)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous {list(shape)}")
+    with torch.cuda.device(dev):
+        _check("mla_nvfp4_fp8_quantize", load_library().mla_nvfp4_fp8_quantize(
+            _ptr(x), x.stride(0) if M > 1 else K, M, K, _ptr(codes), _ptr(scales), _stream(x)))
+    return codes, scales
+
+
+def mla_nvfp4_fp8_gemm(a, a_scales, w, w_scales, *, out=None, error_word=None):
+    """e4m3 x e4m3 -> bf16 [M, N]: a float8_e4m3fn [M, K] with a_scales fp32
+    [M, ceil(K / 128)], w float8_e4m3fn [N, K] with w_scales fp32
+    [ceil(N / 128), ceil(K / 128)]."""
+    dev = a.device
+    _need(a, "a", torch.float8_e4m3fn)
+    _need(w, "w", torch.float8_e4m3fn, dev)
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1] or not _rows_contiguous(a) or not _rows_contiguous(w):
+        raise ValueError("a [M, K] and w [N, K] must share K, with a contiguous last dimension")
+    (M, K), N = a.shape, w.shape[0]
+    kb, nb = (K + FP8_GROUP - 1) // FP8_GROUP, (N + FP8_GROUP - 1) // FP8_GROUP
+    for t, n, shape in ((a_scales, "a_scales", (M, kb)), (w_scales, "w_scales", (nb, kb))):
+        _need(t, n, torch.float32, dev)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous {list(shape)}")
+    _need(error_word, "error_word", torch.int32, dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev)
+    if out.dim() != 2 or out.shape != (M, N) or not _rows_contiguous(out):
+        raise ValueError("out must be [M, N] with a contiguous last dimension")
+    with torch.cuda.device(dev):
+        _check("mla_nvfp4_fp8_gemm", load_library().mla_nvfp4_fp8_gemm(
+            _ptr(a), a.stride(0) if M > 1 else K, _ptr(a_scales), M, _ptr(w), w.stride(0) if N > 1 else K,
+            _ptr(w_scales), N, K, _ptr(out), out.stride(0) if M > 1 else N, _ptr(error_word), _stream(a)))
+    return out

@@ -485,6 +485,109 @@ int mla_nvfp4_quantize_rows(const float* x, int64_t M, int64_t N, const float* g
                                    static_cast<cudaStream_t>(stream));
 }
 
+int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                               int64_t num_tokens, const float* cos_sin, int64_t max_position, int interleaved,
+                               const int32_t* cu_seqlens, const int32_t* context_lens, int num_seqs,
+                               int max_new_tokens, const int32_t* page_table, int64_t page_table_stride,
+                               int64_t max_pages, int page_size, uint8_t* cache, int64_t num_slots, float* scales,
+                               const void* q_pe, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
+                               int64_t q_out_stride_t, int64_t q_out_stride_h, int num_heads,
+                               uint32_t* error_word, void* stream) {
+  if (num_tokens < 0 || num_seqs < 0 || max_new_tokens < 0 || max_position < 0 || num_slots < 0 || num_heads < 0 ||
+      (interleaved != 0 && interleaved != 1))
+    return MLA_ERR_INVALID_ARG;
+  if (page_size < MLA_FP8_BLOCK || page_size % MLA_FP8_BLOCK != 0 || num_slots % MLA_FP8_BLOCK != 0)
+    return MLA_ERR_INVALID_ARG;
+  if ((q_pe == nullptr) != (q_out == nullptr) || (q_pe == nullptr) != (num_heads == 0)) return MLA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || num_seqs == 0 || max_new_tokens == 0) return MLA_OK;
+  if (kv_c == nullptr || k_pe == nullptr || cos_sin == nullptr || cu_seqlens == nullptr || context_lens == nullptr ||
+      page_table == nullptr || cache == nullptr || scales == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (num_tokens > (int64_t(1) << 31) - 1 || kv_c_stride < MLA_D_LATENT || k_pe_stride < MLA_D_ROPE ||
+      max_pages < 1 || page_table_stride < max_pages)
+    return MLA_ERR_INVALID_ARG;
+  if (num_heads > 0 && (q_stride_h < MLA_D_ROPE || q_out_stride_h < MLA_D_ROPE ||
+                        q_stride_t < q_stride_h * (num_heads - 1) + MLA_D_ROPE ||
+                        q_out_stride_t < q_out_stride_h * (num_heads - 1) + MLA_D_ROPE))
+    return MLA_ERR_INVALID_ARG;
+  if (num_heads > 0 && q_pe == q_out && (q_stride_t != q_out_stride_t || q_stride_h != q_out_stride_h))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(cos_sin) || !aligned16(cache) || !aligned16(q_pe) ||
+      !aligned16(q_out) || (kv_c_stride * 2) % 16 || (k_pe_stride * 2) % 16)
+    return MLA_ERR_ALIGNMENT;
+  if (num_heads > 0 &&
+      ((q_stride_t * 2) % 16 || (q_stride_h * 2) % 16 || (q_out_stride_t * 2) % 16 || (q_out_stride_h * 2) % 16))
+    return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  const mla::Fp8AppendArgs a{kv_c, kv_c_stride, k_pe, k_pe_stride, num_tokens, cos_sin, max_position, interleaved,
+                             cu_seqlens, context_lens, num_seqs, max_new_tokens, page_table, page_table_stride,
+                             max_pages, page_size, cache, num_slots, scales, q_pe, q_stride_t, q_stride_h, q_out,
+                             q_out_stride_t, q_out_stride_h, num_heads, error_word};
+  return mla::launch_fp8_append(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t mla_nvfp4_fp8_decode_workspace_size(int batch, int num_heads) {
+  if (batch < 1 || num_heads < 1) return 0;
+  const int sms = device_sms();
+  return mla::fp8_decode_workspace_bytes(batch, num_heads, sms > 0 ? sms : 152);
+}
+
+int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                         const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                         int64_t max_pages, int page_size, const int32_t* seq_lens, float softmax_scale, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream) {
+  if (batch < 0 || num_heads < 1 || num_slots < 0 || page_size < MLA_FP8_BLOCK || page_size % MLA_FP8_BLOCK != 0 ||
+      num_slots % MLA_FP8_BLOCK != 0 || num_slots > (int64_t(1) << 31) - MLA_FP8_BLOCK || max_pages < 1 ||
+      page_table_stride < max_pages)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (q == nullptr || cache == nullptr || scales == nullptr || page_table == nullptr || seq_lens == nullptr ||
+      out == nullptr || num_slots == 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  if (workspace != nullptr && ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                               workspace_bytes < mla::fp8_decode_workspace_bytes(batch, num_heads, sms)))
+    return MLA_ERR_WORKSPACE;
+  const mla::Fp8DecodeArgs a{q, batch, num_heads, cache, num_slots, scales, page_table, page_table_stride, max_pages,
+                             page_size, seq_lens, softmax_scale, out, lse, workspace, error_word};
+  return mla::launch_fp8_decode(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                           void* stream) {
+  if (M < 0 || K < 0 || K % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (M == 0 || K == 0) return MLA_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr || x_stride < K ||
+      M > ((int64_t(1) << 31) - 1) / ((K + MLA_FP8_GROUP - 1) / MLA_FP8_GROUP))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || (x_stride * 2) % 16 || (reinterpret_cast<uintptr_t>(codes) & 7u) != 0)
+    return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  return mla::launch_fp8_quantize(x, x_stride, M, K, codes, scales, static_cast<cudaStream_t>(stream), sms);
+}
+
+int mla_nvfp4_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int64_t M, const uint8_t* w,
+                       int64_t ldw, const float* w_scales, int64_t N, int64_t K, void* out, int64_t ldc,
+                       uint32_t* error_word, void* stream) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 512;  // coordinates of the last tile stay in 32 bits
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0) return MLA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return MLA_OK;
+  if (K == 0 || a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr ||
+      lda < K || ldw < K || ldc < N || M > kMax || N > kMax || K > kMax)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(w) || lda % 16 || ldw % 16 || (reinterpret_cast<uintptr_t>(out) & 1u) != 0)
+    return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  const mla::Fp8GemmArgs args{a, lda, a_scales, M, w, ldw, w_scales, N, K, out, ldc, error_word};
+  return mla::launch_fp8_gemm(args, static_cast<cudaStream_t>(stream), sms);
+}
+
 int mla_nvfp4_selftest_wait(uint32_t* error_word, int64_t limit_ns, unsigned long long* elapsed_ns,
                             void* stream) {
   if (error_word == nullptr || limit_ns < 1000 || limit_ns > 1000000000) return MLA_ERR_INVALID_ARG;

@@ -172,4 +172,73 @@ struct GemmArgs {
 
 int launch_gemm(const GemmArgs& a, cudaStream_t stream, int num_sms);
 
+// The 8-bit path (e4m3 cache and GEMM).
+struct Fp8AppendArgs {
+  const void* kv_c;
+  int64_t kv_stride;
+  const void* k_pe;
+  int64_t pe_stride;
+  int64_t num_tokens;
+  const float* cos_sin;
+  int64_t max_position;
+  int interleaved;
+  const int32_t* cu_seqlens;
+  const int32_t* context_lens;
+  int num_seqs;
+  int max_new;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  int64_t max_pages;
+  int page_size;
+  uint8_t* cache;
+  int64_t num_slots;
+  float* scales;
+  const void* q_pe;
+  int64_t q_st, q_sh;
+  void* q_out;
+  int64_t qo_st, qo_sh;
+  int num_heads;
+  uint32_t* error_word;
+};
+int launch_fp8_append(const Fp8AppendArgs& a, cudaStream_t stream);
+
+struct Fp8DecodeArgs {
+  const void* q;
+  int batch;
+  int num_heads;
+  const uint8_t* cache;
+  int64_t num_slots;
+  const float* scales;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  int64_t max_pages;
+  int page_size;
+  const int32_t* seq_lens;
+  float softmax_scale;
+  void* out;
+  float* lse;
+  void* workspace;  // nullptr: sequences are not cut
+  uint32_t* error_word;
+};
+size_t fp8_decode_workspace_bytes(int batch, int num_heads, int num_sms);
+int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms);
+
+int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                        cudaStream_t stream, int num_sms);
+
+struct Fp8GemmArgs {
+  const uint8_t* a;
+  int64_t lda;
+  const float* a_scales;
+  int64_t M;
+  const uint8_t* w;
+  int64_t ldw;
+  const float* w_scales;
+  int64_t N, K;
+  void* out;
+  int64_t ldc;
+  uint32_t* error_word;
+};
+int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms);
+
 }  // namespace mla
