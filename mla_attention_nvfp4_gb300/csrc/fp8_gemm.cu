@@ -1,6 +1,10 @@
 // e4m3 GEMM with scales per block of 128, and the activations' quantiser.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
+#include "fp8.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -74,40 +78,480 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 }
 
 // ---------------------------------------------------------------------------
-// GEMM: 64 x 64 outputs per CTA, 4 x 4 per thread, fp32 on CUDA cores.
+// GEMM.  The scales vary along K, so the tensor cores' accumulator holds one
+// block of 128 features at a time and the epilogue warps add it, scaled, to
+// fp32 sums in registers, while the next block's products fill the other
+// accumulator.
+//
+// Large: 128 x 256 outputs per tile, persistent CTAs.
+//   warp 0        TMA producer: A and W tiles of one K block, 128-byte swizzle,
+//                 kStages in flight;
+//   warp 1        MMA issuer: four products of K = 32 per block;
+//   warps 4..11   sums: warps 4..7 columns 0..127, warps 8..11 columns 128..255
+//                 (each half has one weight scale per block), thread = row;
+//                 they take the registers the first warpgroup gives up
+//                 (128 sums and two TMEM loads of 32 columns in flight each).
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) fp8_gemm_kernel(const Fp8GemmArgs p) {
-  __shared__ float sa[64][33], sw[64][33];
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 64, n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t kb_n = (p.K + kGroup - 1) / kGroup;
-  float acc[4][4] = {};
-  for (int64_t kb = 0; kb < kb_n; ++kb) {
-    float part[4][4] = {};
-    for (int64_t k0 = kb * kGroup; k0 < p.K && k0 < (kb + 1) * kGroup; k0 += 32) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        const int r = i >> 5, k = i & 31;
-        sa[r][k] = (m0 + r < p.M && k0 + k < p.K) ? e4m3_to_f32(p.a[(m0 + r) * p.lda + k0 + k]) : 0.f;
-        sw[r][k] = (n0 + r < p.N && k0 + k < p.K) ? e4m3_to_f32(p.w[(n0 + r) * p.ldw + k0 + k]) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[ty * 4 + i][k], sw[tx * 4 + j][k], part[i][j]);
+constexpr int kBM = 128, kBN = 256;
+constexpr int kStages = 4;
+constexpr int kThreads = 384;
+constexpr int kRegsIssue = 40, kRegsSum = 232;  // of 168 x 3 warpgroups at launch
+constexpr uint32_t kABytes = kBM * kGroup, kWBytes = kBN * kGroup;
+constexpr uint32_t kStageBytes = kABytes + kWBytes;
+constexpr uint32_t kSmAlloc = kStages * kStageBytes + 1024;
+constexpr int kRaster = 8;  // row tiles that share the weights passing through L2
+static_assert(kSmAlloc + 512 <= 232448, "shared memory budget");
+
+struct Params {
+  const float* a_scales;
+  const float* w_scales;
+  int64_t M, N, ldc;
+  int kb;  // blocks of 128 features
+  __nv_bfloat16* c;
+  int tiles_m, tiles_n;
+  uint32_t* error_word;
+};
+
+__device__ __forceinline__ uint32_t bf16x2_pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Tile t: groups of kRaster row tiles, inside a group column by column.
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& mt, int& nt) {
+  const int group = t / (kRaster * tiles_n);
+  const int rows = min(kRaster, tiles_m - group * kRaster);
+  const int in = t - group * kRaster * tiles_n;
+  mt = group * kRaster + in % rows;
+  nt = in / rows;
+}
+
+struct alignas(8) Barriers {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Barriers bars;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int n_tiles = p.tiles_m * p.tiles_n;
+  uint32_t* err = p.error_word;
+
+  if (threadIdx.x == 0) {
+    abort_s = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-        if (m < p.M && n < p.N)
-          acc[i][j] = fmaf(p.a_scales[m * kb_n + kb] * p.w_scales[n / kGroup * kb_n + kb], part[i][j], acc[i][j]);
-      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], 8);
+    }
+    fence_mbar_init();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m < p.M && n < p.N) static_cast<__nv_bfloat16*>(p.out)[m * p.ldc + n] = __float2bfloat16_rn(acc[i][j]);
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      prefetch_tmap(&tm_a);
+      prefetch_tmap(&tm_w);
+      int it = 0;
+      for (int t = blockIdx.x; t < n_tiles && !abort_s; t += gridDim.x) {
+        int mt, nt;
+        tile_of(t, p.tiles_m, p.tiles_n, mt, nt);
+        for (int kb = 0; kb < p.kb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(&bars.empty[s], ((it / kStages) & 1) ^ 1, err, &abort_s)) break;
+          mbar_expect_tx(&bars.full[s], kStageBytes);
+          tma_load_bytes(s0 + s * kStageBytes, &tm_a, kb * kGroup, mt * kBM, &bars.full[s]);
+          tma_load_bytes(s0 + s * kStageBytes + kABytes, &tm_w, kb * kGroup, nt * kBN, &bars.full[s]);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(kBM, kBN, false, false);
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+        for (int kb = 0; kb < p.kb; ++kb, ++it) {
+          const int s = it % kStages, buf = it & 1;
+          if (!mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s) ||
+              !mbar_wait(&bars.full[s], (it / kStages) & 1, err, &abort_s)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = smem_desc_sw128(s0 + s * kStageBytes, 0, 1024);
+          const uint64_t db = smem_desc_sw128(s0 + s * kStageBytes + kABytes, 0, 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // 32 bytes a step along the swizzled row
+            mma_e4m3(tmem + buf * kBN, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
+          mma_commit(&bars.empty[s]);
+          mma_commit(&bars.acc_full[buf]);
+        }
+      }
     }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
+    const int quad = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter; column half
+    const int r = quad * 32 + lane;
+    const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+      int mt, nt;
+      tile_of(t, p.tiles_m, p.tiles_n, mt, nt);
+      const int64_t row = static_cast<int64_t>(mt) * kBM + r, col0 = static_cast<int64_t>(nt) * kBN + half * 128;
+      const bool live = row < p.M && col0 < p.N;
+      const float* as = p.a_scales + (live ? row : 0) * p.kb;
+      const float* ws = p.w_scales + (live ? col0 / kGroup : 0) * p.kb;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      // scales two blocks ahead of their use (multiplied only there)
+      const int last = p.kb - 1;
+      float a0 = as[0], w0 = ws[0], a1 = as[min(1, last)], w1 = ws[min(1, last)];
+      for (int kb = 0; kb < p.kb; ++kb, ++it) {
+        const int buf = it & 1;
+        const float a2 = as[min(kb + 2, last)], w2 = ws[min(kb + 2, last)];
+        if (!mbar_wait(&bars.acc_full[buf], (it >> 1) & 1, err, &abort_s)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float sc = a0 * w0;
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t v[32], u[32];
+          tmem_ld32(src + buf * kBN + 32 * c, v);
+          tmem_ld32(src + buf * kBN + 32 * c + 32, u);
+          tmem_ld_wait();
+          if (c == 2) {  // the accumulator may be filled again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), sc, acc[32 * c + i]);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[32 * c + 32 + i] = fmaf(__uint_as_float(u[i]), sc, acc[32 * c + 32 + i]);
+        }
+        a0 = a1;
+        w0 = w1;
+        a1 = a2;
+        w1 = w2;
+      }
+      if (!ok || !live) continue;
+      __nv_bfloat16* dst = p.c + row * p.ldc + col0;
+      const int n = p.N - col0 < 128 ? static_cast<int>(p.N - col0) : 128;
+      // 16-byte stores where the row allows them (address and whole group)
+      const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float* f = acc + 8 * i;
+        if (vec && 8 * i + 8 <= n) {
+          *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(bf16x2_pack(f[0], f[1]), bf16x2_pack(f[2], f[3]),
+                                                              bf16x2_pack(f[4], f[5]), bf16x2_pack(f[6], f[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (8 * i + j < n) dst[8 * i + j] = __float2bfloat16_rn(f[j]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the weights are the tensor cores' 128-row operand and kT tokens
+// the other one (N = kT), so that few tokens cost few products and the
+// weights stream through; the K blocks of a tile are split over a cluster's
+// CTAs, whose fp32 sums are added through distributed shared memory in rank
+// order.
+//   warp 0 producer, warp 1 MMA issuer, then four warps of sums per 64 tokens:
+//   thread = weight row.
+// ---------------------------------------------------------------------------
+constexpr int kMaxSplits = 8;   // portable cluster size
+constexpr int kScaleBlocks = 16;  // K blocks whose scales are staged at a time
+
+template <int kT>
+struct Small {
+  static constexpr int halves = kT == 128 ? 2 : 1, tokens = kT / halves;  // groups of sum warps, tokens of each
+  static constexpr int threads = 64 + 128 * halves;
+  static constexpr int resident = kT <= 32 ? 3 : kT == 64 ? 2 : 1;  // CTAs an SM holds
+  static constexpr int stages = kT == 16 ? 4 : kT == 32 ? 3 : kT == 64 ? 4 : 6;
+  static constexpr uint32_t w_bytes = 128 * kGroup, t_bytes = kT * kGroup, stage_bytes = w_bytes + t_bytes;
+  static constexpr uint32_t sum_bytes = kT * 128 * 4;
+  static constexpr uint32_t pipe = stages * stage_bytes;
+  static constexpr uint32_t alloc = (pipe > sum_bytes ? pipe : sum_bytes) + 1024;
+  static constexpr uint32_t cols = 2 * kT;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote)
+               : "memory");
+  return v;
+}
+
+// grid (splits, weight tiles, token tiles), cluster (splits, 1, 1)
+template <int kT>
+__global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
+    fp8_gemm_small_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                          const Params p) {
+  using S = Small<kT>;
+  constexpr int kTok = S::tokens;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ struct alignas(8) {
+    uint64_t full[S::stages], empty[S::stages], acc_full[2], acc_empty[2];
+  } bars;
+  __shared__ alignas(16) float scale_s[kScaleBlocks][kT];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int splits = gridDim.x, rank = blockIdx.x;
+  const int n0 = blockIdx.y * 128, m0 = blockIdx.z * kT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / splits);
+  uint32_t* err = p.error_word;
+
+  if (threadIdx.x == 0) {
+    abort_s = 0;
+    for (int s = 0; s < S::stages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], 4 * S::halves);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_s, S::cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+
+  const int half = (warp - 2) >> 2;  // of the sum warps
+  uint64_t acc[kTok / 2];
+#pragma unroll
+  for (int i = 0; i < kTok / 2; ++i) acc[i] = 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tm_a);
+      prefetch_tmap(&tm_w);
+      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+        const int s = it % S::stages;
+        if (!mbar_wait(&bars.empty[s], ((it / S::stages) & 1) ^ 1, err, &abort_s)) break;
+        mbar_expect_tx(&bars.full[s], S::stage_bytes);
+        tma_load_bytes(s0 + s * S::stage_bytes, &tm_w, kb * kGroup, n0, &bars.full[s]);
+        tma_load_bytes(s0 + s * S::stage_bytes + S::w_bytes, &tm_a, kb * kGroup, m0, &bars.full[s]);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(128, kT, false, false);
+      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+        const int s = it % S::stages, buf = it & 1;
+        if (!mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s) ||
+            !mbar_wait(&bars.full[s], (it / S::stages) & 1, err, &abort_s))
+          break;
+        tc_fence_after();
+        const uint64_t da = smem_desc_sw128(s0 + s * S::stage_bytes, 0, 1024);
+        const uint64_t db = smem_desc_sw128(s0 + s * S::stage_bytes + S::w_bytes, 0, 1024);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_e4m3(tmem + buf * kT, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
+        mma_commit(&bars.empty[s]);
+        mma_commit(&bars.acc_full[buf]);
+      }
+    }
+  } else {
+    constexpr int kSumThreads = S::threads - 64;
+    const int quad = warp & 3, tid = threadIdx.x - 64;
+    const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kTok;
+    const float* ws = p.w_scales + static_cast<int64_t>(blockIdx.y) * p.kb;
+    // scales of the next kScaleBlocks blocks: token by token along K
+    constexpr int kPer = kScaleBlocks * kT / kSumThreads;
+    float next[kPer];
+    auto fetch = [&](int kb_at) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int idx = i * kSumThreads + tid, kb = kb_at + idx % kScaleBlocks;
+        const int64_t m = m0 + idx / kScaleBlocks;
+        next[i] = (kb < kb1 && m < p.M) ? p.a_scales[m * p.kb + kb] * ws[kb] : 0.f;
+      }
+    };
+    fetch(kb0);
+    for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+      const int j = it % kScaleBlocks, buf = it & 1;
+      if (j == 0) {
+        asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");  // the previous blocks' scales have been read
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int idx = i * kSumThreads + tid;
+          scale_s[idx % kScaleBlocks][idx / kScaleBlocks] = next[i];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
+        if (kb + kScaleBlocks < kb1) fetch(kb + kScaleBlocks);
+      }
+      // a wait that gives up still takes part in the barriers above
+      mbar_wait(&bars.acc_full[buf], (it >> 1) & 1, err, &abort_s);
+      tc_fence_after();
+      constexpr int kW = kTok < 32 ? kTok : 32;
+#pragma unroll
+      for (int c = 0; c < kTok / kW; ++c) {
+        uint32_t v[kW];
+        if constexpr (kW == 32)
+          tmem_ld32(src + buf * kT + kW * c, v);
+        else
+          tmem_ld16(src + buf * kT + kW * c, v);
+        tmem_ld_wait();
+        if (c == kTok / kW - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+        }
+#pragma unroll
+        for (int i = 0; i < kW / 4; ++i) {
+          const float4 sc = *reinterpret_cast<const float4*>(&scale_s[j][half * kTok + kW * c + 4 * i]);
+          fma2(acc[kW / 2 * c + 2 * i], pack2(v[4 * i], v[4 * i + 1]), pack2(sc.x, sc.y));
+          fma2(acc[kW / 2 * c + 2 * i + 1], pack2(v[4 * i + 2], v[4 * i + 3]), pack2(sc.z, sc.w));
+        }
+      }
+    }
+  }
+
+  // Results: thread = weight row (output column), tokens one after another:
+  // a warp writes 32 neighbouring columns of one output row.
+  const int r = (warp & 3) * 32 + lane;
+  const int64_t n = static_cast<int64_t>(n0) + r;
+  if (splits == 1) {
+    if (warp >= 2 && n < p.N) {
+#pragma unroll
+      for (int i = 0; i < kTok / 2; ++i) {
+        float lo, hi;
+        unpack2(acc[i], lo, hi);
+        const int64_t m = m0 + half * kTok + 2 * i;
+        if (m < p.M) p.c[m * p.ldc + n] = __float2bfloat16_rn(lo);
+        if (m + 1 < p.M) p.c[(m + 1) * p.ldc + n] = __float2bfloat16_rn(hi);
+      }
+    }
+  } else {
+    // every product has read its operands (each sum waited for them), so the
+    // stages' memory holds the sums [token][row]
+    __syncthreads();
+    if (warp >= 2) {
+      const uint32_t at = s0 + (half * kTok * 128 + r) * 4;
+#pragma unroll
+      for (int i = 0; i < kTok / 2; ++i) {
+        float lo, hi;
+        unpack2(acc[i], lo, hi);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 1024 * i), "f"(lo) : "memory");
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 1024 * i + 512), "f"(hi) : "memory");
+      }
+    }
+    cluster_sync();
+    const int live = static_cast<int>(p.M - m0 < kT ? p.M - m0 : kT);
+    // four neighbouring columns of a row at a time
+    for (int e = rank * S::threads + threadIdx.x; e < live * 32; e += splits * S::threads) {
+      float4 v[kMaxSplits];
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c)
+        if (c < splits) v[c] = ld_cluster(s0 + e * 16, c);
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c)
+        if (c < splits) {
+          f[0] += v[c].x;
+          f[1] += v[c].y;
+          f[2] += v[c].z;
+          f[3] += v[c].w;
+        }
+      const int64_t col = static_cast<int64_t>(n0) + 4 * (e & 31);
+      __nv_bfloat16* dst = p.c + (static_cast<int64_t>(m0) + (e >> 5)) * p.ldc + col;
+      if (col + 4 <= p.N && (reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_pack(f[0], f[1]), bf16x2_pack(f[2], f[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + i < p.N) dst[i] = __float2bfloat16_rn(f[i]);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, S::cols);
+}
+
+template <int kT>
+int launch_small(const CUtensorMap& tm_a, const CUtensorMap& tm_w, const Params& p, int splits, int slot,
+                 cudaStream_t stream) {
+  const void* kern = reinterpret_cast<const void*>(fp8_gemm_small_kernel<kT>);
+  if (const int st = smem_limit_once(kern, static_cast<int>(Small<kT>::alloc), slot)) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits, p.tiles_n, p.tiles_m);
+  cfg.blockDim = dim3(Small<kT>::threads);
+  cfg.dynamicSmemBytes = Small<kT>::alloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = splits;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, fp8_gemm_small_kernel<kT>, tm_a, tm_w, p));
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled from the driver at run time (the library links only
+// the CUDA runtime).
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      f = reinterpret_cast<EncodeTiledFn>(ptr);
+      fn.store(f, std::memory_order_release);
+    }
+  }
+  return f;
 }
 
 }  // namespace
@@ -127,11 +571,64 @@ int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, u
   return launch_status();
 }
 
+bool encode_byte_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t stride, uint32_t box_x,
+                     uint32_t box_rows, bool swizzle64) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t box[2] = {box_x, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
-  (void)num_sms;
-  const dim3 grid(static_cast<unsigned>((a.N + 63) / 64), static_cast<unsigned>((a.M + 63) / 64));
-  fp8_gemm_kernel<<<grid, 256, 0, stream>>>(a);
-  return launch_status();
+  const int kb = static_cast<int>((a.K + kGroup - 1) / kGroup);
+  const int64_t tm = (a.M + kBM - 1) / kBM, tn = (a.N + kBN - 1) / kBN;
+  // Large tiles where they fill the SMs, the streaming form otherwise.
+  const bool large = a.M > 128 && tm * tn >= num_sms;
+  const int kt = large ? kBM : a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  CUtensorMap tm_a, tm_w;
+  if (!encode_byte_map(&tm_a, a.a, a.K, a.M, a.lda, kGroup, static_cast<uint32_t>(kt), false) ||
+      !encode_byte_map(&tm_w, a.w, a.K, a.N, a.ldw, kGroup, large ? kBN : 128, false)) {
+    set_last_error("cuTensorMapEncodeTiled failed for the GEMM operands");
+    return MLA_ERR_LAUNCH;
+  }
+  Params p{a.a_scales, a.w_scales, a.M, a.N, a.ldc, kb, static_cast<__nv_bfloat16*>(a.out), 0, 0, a.error_word};
+  if (large) {
+    if (tm * tn > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
+    p.tiles_m = static_cast<int>(tm);
+    p.tiles_n = static_cast<int>(tn);
+    const int grid = static_cast<int>(tm * tn < num_sms ? tm * tn : num_sms);
+    if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_gemm_kernel), static_cast<int>(kSmAlloc), 14))
+      return st;
+    fp8_gemm_kernel<<<grid, kThreads, kSmAlloc, stream>>>(tm_a, tm_w, p);
+    return launch_status();
+  }
+  const int64_t sn = (a.N + 127) / 128, sm = (a.M + kt - 1) / kt;
+  if (sn > 65535 || sm > 65535) return MLA_ERR_INVALID_ARG;
+  p.tiles_m = static_cast<int>(sm);
+  p.tiles_n = static_cast<int>(sn);
+  // Split K so that the busiest SM has the fewest K blocks to stream; a
+  // CTA's start and end cost about as much as kOverhead of them.
+  constexpr int kOverhead = 3;
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
+    const int64_t cost = (sn * sm * s + num_sms - 1) / num_sms * ((kb + s - 1) / s + kOverhead);
+    if (cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  switch (kt) {
+    case 16: return launch_small<16>(tm_a, tm_w, p, splits, 15, stream);
+    case 32: return launch_small<32>(tm_a, tm_w, p, splits, 16, stream);
+    case 64: return launch_small<64>(tm_a, tm_w, p, splits, 17, stream);
+    default: return launch_small<128>(tm_a, tm_w, p, splits, 18, stream);
+  }
 }
 
 }  // namespace mla

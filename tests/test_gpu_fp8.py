@@ -516,7 +516,8 @@ def test_gemm(M, N, K):
     check_gemm(run_gemm(*p), *p, what=f"{M}x{N}x{K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 576, 7168), (8, 7168, 1536), (513, 1100, 4096), (1030, 640, 7168), (77, 129, 16384)])
+@pytest.mark.parametrize("M,N,K", [(1, 576, 7168), (8, 7168, 1536), (513, 1100, 4096), (1030, 640, 7168), (77, 129, 16384),
+                                   (1300, 3601, 272), (2300, 2111, 400), (130, 40000, 144)])
 def test_gemm_larger(M, N, K):
     rng = np.random.default_rng(M + N + K)
     p = make_gemm(rng, M, N, K)
