@@ -1,7 +1,42 @@
 // Absorbed MLA decode over the e4m3 latent cache (one scale per block of 64
-// tokens).
+// tokens) on tcgen05.
+//
+// The cached bytes are the tensor cores' operands as they lie: tiles of 128
+// keys x 576 features arrive by TMA and serve both products, the keys as
+// 128-row operand of S^T = K Q^T (K-major) and the values as 128-row operand
+// of O^T = V^T P^T (read feature-major, one 128-feature chunk at a time).
+// Queries and probabilities are the other operand: both products therefore
+// cost what the number of heads (N) asks for, and a key is a TMEM lane, so
+// masking a key masks a thread.
+//
+// Two e4m3 terms carry 8 significant bits:
+//   q = 2^e (q1 + q2) with q1 = e4m3(q 2^-e), q2 = e4m3(q 2^-e - q1): a bf16
+//       query exactly (its 8 bits split 4 + 4), down to 2^-17 of the head's
+//       largest feature, below which it is held to an absolute 2^-19 of it;
+//   p = p1 + p2 / gain likewise, at most 2^-8 off relative (what bf16 would
+//       be).  The largest p lies between 2^kReset and 2^kTop, so that the
+//       absolute floor, one step 2^-9 of the second term, lies 2^15 gain or
+//       more below it (gain 16 where the two terms have accumulators of
+//       their own, 1 where they share one).  There the second term is rounded
+//       with an offset that runs evenly through a step over 32 neighbouring
+//       keys: a long tail of equal, tiny weights, which rounding to nearest
+//       would push to one side, keeps its sum.
+//
+// Scales: with s the block's scale, x = log2(e) softmax_scale s q.k8,
+// l = sum 2^(x - m) and O = sum (s 2^(x - m)) k8; m is a per-head reference
+// that follows the maximum of x + log2 s lazily: it is raised, and O and l
+// rescaled, only when a weight would exceed 2^kTop.
+//
+// One CTA per SM, persistent over a contiguous range of the batch's tiles
+// (every range the same size, cut anywhere in a sequence); cut sequences are
+// merged by LSE in a second kernel, in range order.
+//   warp 0     TMA producer: 128-feature chunks of latent in a ring, RoPE apart;
+//   warp 1     MMA issuer: scores of tile n + 1, then values of tile n;
+//   warps 2..5 queries to two terms, softmax (thread = key), output.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "fp8.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -9,84 +44,728 @@
 namespace mla {
 namespace {
 
+using namespace sm100;
+
 constexpr int kKey = MLA_D_LATENT + MLA_D_ROPE;
 constexpr int kBlock = MLA_FP8_BLOCK;
+constexpr int kTile = 128;  // keys
+constexpr int kThreads = 192;
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
+constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
+constexpr float kReset = 6.0f;  // a raised reference puts the tile's largest weight at 2^6
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
-// One CTA per (head, sequence): blocks of 64 keys, online softmax, fp32.
-__global__ void __launch_bounds__(256) fp8_decode_kernel(const Fp8DecodeArgs p) {
-  __shared__ float qs[kKey], ps[kBlock];
-  __shared__ int64_t slot_s;
-  __shared__ float scale_s;
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(b) * p.num_heads + h) * kKey;
-  for (int i = threadIdx.x; i < kKey; i += 256) qs[i] = __bfloat162float(q[i]);
-  int64_t len = p.seq_lens[b];
-  const int64_t room = p.max_pages * p.page_size;
-  if (len > room) {
-    if (threadIdx.x == 0) flag_error(p.error_word, MLA_DEVERR_BOUNDS);
-    len = room;
-  }
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int64_t t0 = 0; t0 < len; t0 += kBlock) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int64_t page = p.page_table[b * p.pt_stride + t0 / p.page_size];
-      const int64_t s = page * p.page_size + t0 % p.page_size;
-      slot_s = (page < 0 || s + kBlock > p.num_slots) ? -1 : s;
-      if (slot_s < 0) flag_error(p.error_word, MLA_DEVERR_BOUNDS);
-      scale_s = slot_s >= 0 ? p.scales[s / kBlock] : 0.f;
-      if (slot_s >= 0 && !(scale_s >= kScaleMin && scale_s <= kScaleMax)) {
-        flag_error(p.error_word, MLA_DEVERR_SCALE);
-        slot_s = -1;
+constexpr uint32_t kChunkBytes = kTile * 128;  // 128 keys x 128 features
+constexpr uint32_t kRopeBytes = kTile * 64;
+
+template <int kH>
+struct Cfg {
+  static_assert(kH == 32 || kH == 64, "heads per CTA");
+  static constexpr int slots = kH == 64 ? 8 : 10;  // latent chunks in flight (4 a tile)
+  static constexpr int ropes = kH == 64 ? 1 : 2;
+  static constexpr uint32_t q_chunk = 2 * kH * 128, q_rope = 2 * kH * 64;
+  static constexpr uint32_t p_bytes = kTile * 64 * (kH / 32);  // [key][p1 | p2] or p1 and p2 apart
+  static constexpr uint32_t off_rope = slots * kChunkBytes;
+  static constexpr uint32_t off_q = off_rope + ropes * kRopeBytes;
+  static constexpr uint32_t off_p = off_q + 4 * q_chunk + q_rope;
+  static constexpr uint32_t off_misc = off_p + p_bytes;
+  static constexpr int gain = kH == 64 ? 1 : 16;  // of the second term: 16 leaves it at most 2^8
+  static constexpr int terms = kH / 32;  // products per value chunk: p1 | p2 as columns, or one after the other
+  static constexpr uint32_t col_s = 256;  // TMEM: O^T in columns 0..255 (64 per chunk), then two S^T of 2 kH
+};
+
+template <int kH>
+struct Misc {
+  uint64_t full[Cfg<kH>::slots], empty[Cfg<kH>::slots], rfull[Cfg<kH>::ropes], rempty[Cfg<kH>::ropes];
+  uint64_t s_full[2], p_ready, pv_done, q_ready;
+  alignas(16) float c[kH], m[kH], move[kH], factor[kH], inv[kH];
+  float part[4][kH];
+  int64_t scan[6], t0, t1, off0;
+  int b0;
+  uint32_t tmem;
+  volatile int abort;
+};
+
+template <int kH>
+constexpr uint32_t smem_bytes() {
+  return Cfg<kH>::off_misc + static_cast<uint32_t>(sizeof(Misc<kH>));
+}
+static_assert(smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448, "shared memory budget");
+
+struct Params {
+  Fp8DecodeArgs a;
+  int ranges, groups;  // ranges of tiles; head groups (grid = ranges * groups)
+  bool split;
+  int64_t* offsets;  // [batch + 1] first tile of each sequence, then tiles per range
+  float* part_lse;   // log2 units, [range][group][2][kH]
+  float* part_o;     // the same rows of 512
+};
+
+__device__ __forceinline__ int clipped_len(const Fp8DecodeArgs& a, int b) {
+  const int64_t room = a.max_pages * a.page_size;
+  const int n = a.seq_lens[b];
+  return n <= 0 ? 0 : n <= room ? n : static_cast<int>(room);
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// First slot of block i (64 tokens) of sequence b, or -1 (page out of range).
+__device__ __forceinline__ int64_t block_slot(const Fp8DecodeArgs& a, int b, int i) {
+  const int per = a.page_size / kBlock;
+  const int64_t page = a.page_table[b * a.pt_stride + i / per];
+  const int64_t slot = page * a.page_size + static_cast<int64_t>(i % per) * kBlock;
+  return page < 0 || slot + kBlock > a.num_slots ? -1 : slot;
+}
+
+// Calls f(b, len, first tile, last tile + 1, tiles of b, part) for every
+// piece of this CTA's work; part: 0 for the piece its range begins with.
+template <int kH, class F>
+__device__ __forceinline__ void for_each_piece(const Params& p, const Misc<kH>& ms, int range, F f) {
+  if (p.split) {
+    int64_t t = ms.t0, off = ms.off0;
+    const int64_t t0 = t, t1 = ms.t1;
+    for (int b = ms.b0; t < t1; ++b) {
+      const int len = clipped_len(p.a, b), n = tiles_of(len);
+      if (n > 0) {
+        const int s = static_cast<int>(t - off);
+        const int e = t1 - off < n ? static_cast<int>(t1 - off) : n;
+        f(b, len, s, e, n, t == t0 ? 0 : 1);
+        t = off + e;
       }
+      off += n;
     }
-    __syncthreads();
-    if (slot_s < 0) continue;
-    const int n = len - t0 < kBlock ? static_cast<int>(len - t0) : kBlock;
-    const uint8_t* base = p.cache + slot_s * kKey;
-    for (int k = warp; k < n; k += 8) {
-      float s = 0.f;
-      for (int i = lane; i < kKey; i += 32) s = fmaf(qs[i], e4m3_to_f32(base[static_cast<int64_t>(k) * kKey + i]), s);
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) ps[k] = s * scale_s * p.softmax_scale;
-    }
-    __syncthreads();
-    float mb = m;
-    for (int k = 0; k < n; ++k) mb = fmaxf(mb, ps[k]);
-    const float f = expf(m - mb);
-    o0 *= f;
-    o1 *= f;
-    l *= f;
-    m = mb;
-    for (int k = 0; k < n; ++k) {
-      const float e = expf(ps[k] - m);
-      l += e;
-      const uint32_t h2 =
-          e4m3x2_to_f16x2_pair(*reinterpret_cast<const uint16_t*>(base + static_cast<int64_t>(k) * kKey + 2 * threadIdx.x));
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      o0 = fmaf(e * scale_s, v.x, o0);
-      o1 = fmaf(e * scale_s, v.y, o1);
+  } else {
+    for (int b = range; b < p.a.batch; b += p.ranges) {
+      const int len = clipped_len(p.a, b), n = tiles_of(len);
+      f(b, len, 0, n, n, 0);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (static_cast<int64_t>(b) * p.num_heads + h) * MLA_D_LATENT;
-  reinterpret_cast<__nv_bfloat162*>(out)[threadIdx.x] = __floats2bfloat162_rn(o0 * inv, o1 * inv);
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[static_cast<int64_t>(b) * p.num_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2_h2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, float s, uint32_t b) {
+  const __half2 r =
+      __hfma2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(s), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 2, 128, a;\n\t"
+      "selp.s32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(v))
+      : "memory");
+  return r != 0;
+}
+
+// The plan: this CTA's range of the batch's tiles, and its first sequence.
+template <int kH>
+__device__ __forceinline__ void make_plan(const Params& p, Misc<kH>& ms, int range, bool publish) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
+  const int per_thread = (B + kThreads - 1) / kThreads;
+  const int first = tid * per_thread, last = min(first + per_thread, B);
+  int64_t sum = 0;
+  for (int b = first; b < last; ++b) sum += tiles_of(clipped_len(p.a, b));
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) ms.scan[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += ms.scan[w];
+    total += ms.scan[w];
+  }
+  const int64_t per = (total + p.ranges - 1) / p.ranges;
+  const int64_t t0 = range * per, t1 = t0 + per < total ? t0 + per : total;
+  int64_t off = before + incl - sum;
+  if (tid == 0) {
+    ms.t0 = t0;
+    ms.t1 = t1;
+  }
+  for (int b = first; b < last; ++b) {
+    const int n = tiles_of(clipped_len(p.a, b));
+    if (publish) p.offsets[b] = off;
+    if (t0 >= off && t0 < off + n) {
+      ms.b0 = b;
+      ms.off0 = off;
+    }
+    off += n;
+  }
+  if (publish && tid == 0) {
+    p.offsets[B] = total;
+    p.offsets[B + 1] = per;
+  }
+}
+
+template <int kH>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
+                      const Params p) {
+  using C = Cfg<kH>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
+  const uint32_t s0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int range = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
+  uint32_t* err = p.a.error_word;
+
+  if (threadIdx.x == 0) {
+    ms.abort = 0;
+    for (int i = 0; i < C::slots; ++i) {
+      mbar_init(&ms.full[i], 1);
+      mbar_init(&ms.empty[i], 1);
+    }
+    for (int i = 0; i < C::ropes; ++i) {
+      mbar_init(&ms.rfull[i], 1);
+      mbar_init(&ms.rempty[i], 1);
+    }
+    mbar_init(&ms.s_full[0], 1);
+    mbar_init(&ms.s_full[1], 1);
+    mbar_init(&ms.p_ready, 4);
+    mbar_init(&ms.pv_done, 1);
+    mbar_init(&ms.q_ready, 4);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ms.tmem, 512);
+    tmem_relinquish();
+  }
+  if (p.split) make_plan<kH>(p, ms, range, blockIdx.x == 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  auto slot_addr = [&](int i) { return s0 + i * kChunkBytes; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&tm_lat);
+      prefetch_tmap(&tm_rope);
+    }
+    int n = 0;
+    bool ok = true;
+    for_each_piece<kH>(p, ms, range, [&](int b, int len, int s, int e, int, int) {
+      const int n_blocks = (len + kBlock - 1) / kBlock;
+      int y = 0;  // lane i: row of block (first block of the batch of 32) + i; past the cache where there is none
+      for (int t = s; t < e && ok; ++t, ++n) {
+        const int at = (2 * (t - s)) & 31;
+        if (at == 0) {
+          const int i = 2 * t + lane;
+          const int64_t slot = i < n_blocks && i < 2 * e ? block_slot(p.a, b, i) : -1;
+          y = static_cast<int>(slot < 0 ? p.a.num_slots : slot);
+        }
+        const int y0 = __shfl_sync(0xffffffffu, y, at), y1 = __shfl_sync(0xffffffffu, y, at + 1);
+        if (lane == 0) {
+#pragma unroll
+          for (int d = 0; d < 4 && ok; ++d) {
+            const int k = 4 * n + d, i = k % C::slots;
+            ok = mbar_wait(&ms.empty[i], ((k / C::slots) & 1) ^ 1, err, &ms.abort);
+            if (!ok) break;
+            mbar_expect_tx(&ms.full[i], kChunkBytes);
+            tma_load_bytes(slot_addr(i), &tm_lat, 128 * d, y0, &ms.full[i]);
+            tma_load_bytes(slot_addr(i) + kChunkBytes / 2, &tm_lat, 128 * d, y1, &ms.full[i]);
+          }
+          if (ok) {
+            const int i = n % C::ropes;
+            ok = mbar_wait(&ms.rempty[i], ((n / C::ropes) & 1) ^ 1, err, &ms.abort);
+            if (ok) {
+              const uint32_t dst = s0 + C::off_rope + i * kRopeBytes;
+              mbar_expect_tx(&ms.rfull[i], kRopeBytes);
+              tma_load_bytes(dst, &tm_rope, MLA_D_LATENT, y0, &ms.rfull[i]);
+              tma_load_bytes(dst + kRopeBytes / 2, &tm_rope, MLA_D_LATENT, y1, &ms.rfull[i]);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+      }
+    });
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_e4m3(128, 2 * kH, false, false);
+      constexpr uint32_t idesc_o = idesc_e4m3(128, 64, true, true);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        ok = ok && mbar_wait(bar, parity, err, &ms.abort);
+        return ok;
+      };
+      auto scores = [&](int n) {  // S^T of tile n
+        const uint32_t d = tmem + C::col_s + (n & 1) * 2 * kH;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int k = 4 * n + c, i = k % C::slots;
+          if (!wait(&ms.full[i], (k / C::slots) & 1)) return;
+          tc_fence_after();
+          const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
+          const uint64_t db = smem_desc_sw128(s0 + C::off_q + c * C::q_chunk, 0, 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc_s, (c > 0 || j > 0) ? 1u : 0u);
+        }
+        const int i = n % C::ropes;
+        if (!wait(&ms.rfull[i], (n / C::ropes) & 1)) return;
+        tc_fence_after();
+        const uint64_t da = smem_desc_sw64(s0 + C::off_rope + i * kRopeBytes, 512);
+        const uint64_t db = smem_desc_sw64(s0 + C::off_q + 4 * C::q_chunk, 512);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc_s, 1u);
+        mma_commit(&ms.rempty[i]);
+        mma_commit(&ms.s_full[n & 1]);
+      };
+      int n = 0, item = 0;
+      for_each_piece<kH>(p, ms, range, [&](int, int, int s, int e, int, int) {
+        if (s >= e) return;
+        // the piece's queries (and with them the previous piece's last S^T) are there
+        if (!wait(&ms.q_ready, item & 1)) return;
+        ++item;
+        scores(n);
+        for (int t = s; t < e; ++t, ++n) {
+          if (t + 1 < e) scores(n + 1);
+          if (!wait(&ms.p_ready, n & 1)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = (4 * n + c) % C::slots;
+            // V^T: 128 features of the chunk as rows, 32 keys (4096 bytes) a step
+            const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
+#pragma unroll
+            for (int term = 0; term < C::terms; ++term) {
+              const uint64_t db = smem_desc_sw64(s0 + C::off_p + term * kTile * 64, 512);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_e4m3(tmem + 64 * c, da + 256 * j, db + 128 * j, idesc_o, (t > s || term > 0 || j > 0) ? 1u : 0u);
+            }
+            mma_commit(&ms.empty[i]);
+          }
+          mma_commit(&ms.pv_done);
+        }
+      });
+    }
+  } else {
+    // ------------------------------------------- queries, softmax, output
+    // A wait that gives up leaves these warps running through their loops
+    // (they meet at named barriers); the error word tells.
+    const int quad = warp & 3, tid = threadIdx.x - 64;
+    const int key = quad * 32 + lane;  // of the tile: a TMEM lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
+    // offset of the second term's rounding: (j + 1/2) / 32 - 1/2 of a step
+    // 2^-9, j the lane's bits reversed
+    const float off = ((__brev(lane) >> 27) + 0.5f) * (1.f / 32) - 0.5f;
+    const __half2 dither_h = __float2half2_rn(off * 0.001953125f);
+    const uint32_t dither = *reinterpret_cast<const uint32_t*>(&dither_h);
+    int n = 0;
+    for_each_piece<kH>(p, ms, range, [&](int b, int len, int s, int e, int tiles, int part) {
+      const bool whole = e - s == tiles;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) +
+                           (static_cast<int64_t>(b) * p.a.num_heads + h0) * MLA_D_LATENT;
+      float* lse = p.a.lse != nullptr ? p.a.lse + static_cast<int64_t>(b) * p.a.num_heads + h0 : nullptr;
+      if (s >= e) {  // no keys
+        for (int i = tid; i < heads * (MLA_D_LATENT / 8); i += 128) reinterpret_cast<uint4*>(out)[i] = uint4{};
+        if (lse != nullptr && tid < heads) lse[tid] = -INFINITY;
+        return;
+      }
+      if (s == 0 && tid == 0 && group == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
+
+      // Queries: a warp takes a head at a time; lane l features 8 l.., and
+      // 256 + 8 l.., lanes 0..7 the RoPE's.
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) +
+                               (static_cast<int64_t>(b) * p.a.num_heads + h0) * kKey;
+#pragma unroll 4
+      for (int i = 0; i < kH / 4; ++i) {
+        const int h = quad + 4 * i;
+        uint4 v[3] = {};
+        if (h < heads) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
+          v[0] = src[lane];
+          v[1] = src[lane + 32];
+          if (lane < 8) v[2] = src[lane + 64];
+        }
+        float f[24], am = 0.f;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          bf16x2_to_f32(v[k].x, f[8 * k], f[8 * k + 1]);
+          bf16x2_to_f32(v[k].y, f[8 * k + 2], f[8 * k + 3]);
+          bf16x2_to_f32(v[k].z, f[8 * k + 4], f[8 * k + 5]);
+          bf16x2_to_f32(v[k].w, f[8 * k + 6], f[8 * k + 7]);
+          am = fmaxf(am, amax8(f + 8 * k));
+        }
+        am = warp_max(am);
+        // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8)
+        const uint32_t u = __float_as_uint(am);
+        int ex = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        ex = max(-60, min(60, ex));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        if (lane == 0) {
+          ms.c[h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+          ms.m[h] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t w1[2], w2[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float* g = f + 8 * k + 4 * j;
+            const float x0 = g[0] * inv, x1 = g[1] * inv, x2 = g[2] * inv, x3 = g[3] * inv;
+            const uint32_t a = cvt_e4m3x2(x0, x1), c = cvt_e4m3x2(x2, x3);
+            const uint32_t ha = e4m3x2_to_f16x2_pair(a), hc = e4m3x2_to_f16x2_pair(c);
+            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
+            const float2 fc = __half22float2(*reinterpret_cast<const __half2*>(&hc));
+            w1[j] = a | (c << 16);
+            w2[j] = cvt_e4m3x2(x0 - fa.x, x1 - fa.y) | (cvt_e4m3x2(x2 - fc.x, x3 - fc.y) << 16);
+          }
+          // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
+          uint32_t a1, a2;
+          if (k < 2) {
+            const int feature = 256 * k + 8 * lane;
+            const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
+            const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
+            a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
+            a2 = base + (kH + h) * 128 + ((unit ^ (h & 7)) << 4) + half;
+          } else {
+            const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
+            const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
+            a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
+            a2 = base + (kH + h) * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
+          }
+          if (k < 2 || lane < 8) {
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a1), "r"(w1[0]), "r"(w1[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a2), "r"(w2[0]), "r"(w2[1]) : "memory");
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.q_ready);
+      softmax_bar();  // c and m are there
+
+      float l[kH];
+#pragma unroll
+      for (int h = 0; h < kH; ++h) l[h] = 0.f;
+      bool set = false;  // the references follow some key
+      // block slots two tiles ahead, scales one
+      const int n_blocks = (len + kBlock - 1) / kBlock;
+      auto slot_at = [&](int t) -> int64_t {
+        const int i = 2 * t + (quad >> 1);
+        return t < e && i < n_blocks ? block_slot(p.a, b, i) : -2;  // -2: no block; -1: a page out of range
+      };
+      int64_t slot_1 = slot_at(s), slot_2 = slot_at(s + 1);
+      float scale_1 = slot_1 >= 0 ? p.a.scales[slot_1 / kBlock] : 0.f;
+      for (int t = s; t < e; ++t, ++n) {
+        const int64_t slot = slot_1;
+        const bool sb_ok = slot >= 0 && scale_1 >= kScaleMin && scale_1 <= kScaleMax;
+        const float sb = sb_ok ? scale_1 : 1.f;
+        if (lane == 0 && (quad & 1) == 0 && slot != -2 && !sb_ok)
+          flag_error(err, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
+        slot_1 = slot_2;
+        scale_1 = slot_1 >= 0 ? p.a.scales[slot_1 / kBlock] : 0.f;
+        slot_2 = slot_at(t + 2);
+        const bool valid = sb_ok && t * kTile + key < len;
+        const float lsb = log2f(sb);
+
+        mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
+        tc_fence_after();
+        float x[kH], top = -INFINITY;
+        const uint32_t src = lanes + C::col_s + (n & 1) * 2 * kH;
+#pragma unroll
+        for (int c = 0; c < kH / 16; ++c) {
+          uint32_t v[16], u[16];
+          tmem_ld16(src + 16 * c, v);
+          tmem_ld16(src + kH + 16 * c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const int h = 16 * c + i;
+            const float4 cc = *reinterpret_cast<const float4*>(&ms.c[h]);
+            const float4 mm = *reinterpret_cast<const float4*>(&ms.m[h]);
+            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float sum = __uint_as_float(v[i + j]) + __uint_as_float(u[i + j]);
+              x[h + j] = valid ? fmaf(sum * sb, cv[j], -mv[j]) : -INFINITY;
+              top = fmaxf(top, x[h + j]);
+            }
+          }
+        }
+        if (softmax_any(top + lsb > kTop || (!set && valid))) {
+          // Raise the references of the heads that need it.
+#pragma unroll
+          for (int g = 0; g < kH; g += 32) {
+            float mine = 0.f;
+#pragma unroll
+            for (int h = 0; h < 32; ++h) {
+              const float r = warp_max(x[g + h] + lsb);
+              if (lane == h) mine = r;
+            }
+            ms.part[quad][g + lane] = mine;
+          }
+          softmax_bar();
+          if (tid < kH) {
+            const float mx = fmaxf(fmaxf(ms.part[0][tid], ms.part[1][tid]), fmaxf(ms.part[2][tid], ms.part[3][tid]));
+            const bool raise = isfinite(mx) && (!set || mx > kTop);
+            const float by = raise ? mx - kReset : 0.f;
+            ms.move[tid] = by;
+            ms.factor[tid] = !set ? 0.f : ex2_approx(-by);
+            ms.m[tid] += by;
+          }
+          softmax_bar();
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            x[h] -= ms.move[h];
+            l[h] *= ms.factor[h];
+          }
+          if (t > s) {  // O holds earlier tiles: all its products are done before it is rescaled
+            mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(lanes + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * ms.factor[(c + i) & (kH - 1)]);
+              tmem_st16(lanes + c, v);
+            }
+            tmem_st_wait();
+          }
+          set = true;
+        }
+        // weights and their two terms; words of four heads
+        uint32_t w1[kH / 4], w2[kH / 4];
+#pragma unroll
+        for (int h = 0; h < kH; h += 4) {
+          uint32_t a[2], r[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float e0 = ex2_approx(x[h + 2 * j]), e1 = ex2_approx(x[h + 2 * j + 1]);
+            l[h + 2 * j] += e0;
+            l[h + 2 * j + 1] += e1;
+            const __half2 ph = __floats2half2_rn(e0 * sb, e1 * sb);
+            const uint32_t pu = *reinterpret_cast<const uint32_t*>(&ph);
+            a[j] = cvt_e4m3x2_h2(pu);
+            r[j] = cvt_e4m3x2_h2(h2_fma(h2_sub(pu, e4m3x2_to_f16x2_pair(a[j])), C::gain, dither));
+          }
+          w1[h / 4] = a[0] | (a[1] << 16);
+          w2[h / 4] = r[0] | (r[1] << 16);
+        }
+        // the previous tile's products have read P (and, at a piece's first
+        // tile, the output was read before this)
+        if (n > 0) mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+        {
+          const uint32_t row = s0 + C::off_p + key * 64, sw = (key >> 1) & 3;
+          if constexpr (kH == 64) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              sts128(row + ((c ^ sw) << 4), make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
+              sts128(row + kTile * 64 + ((c ^ sw) << 4),
+                     make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              sts128(row + ((c ^ sw) << 4), make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
+              sts128(row + (((c + 2) ^ sw) << 4),
+                     make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+            }
+          }
+        }
+        // a row that is no key of the sequence may hold any bytes (NaN too):
+        // as values they are zeros
+        if (!valid && slot >= 0) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t row = slot_addr((4 * n + c) % C::slots) + key * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts128(row + 16 * i, make_uint4(0, 0, 0, 0));
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_ready);
+      }
+
+      // Sums over the keys: halves exchanged until lane i holds heads
+      // i * kH / 32 ...; then across the warps.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+        const int half = kH * o / 32;
+#pragma unroll
+        for (int h = 0; h < kH / 2; ++h) {
+          if (h < half) {
+            const float give = up ? l[h] : l[h + half], keep = up ? l[h + half] : l[h];
+            l[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kH / 32; ++i) ms.part[quad][lane * (kH / 32) + i] = l[i];
+      softmax_bar();
+      const int64_t part_row = ((static_cast<int64_t>(range) * p.groups + group) * 2 + part) * kH;
+      if (tid < kH) {
+        const float sum = (ms.part[0][tid] + ms.part[1][tid]) + (ms.part[2][tid] + ms.part[3][tid]);
+        ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+        const float l2 = sum != 0.f ? ms.m[tid] + log2f(sum) : -INFINITY;
+        if (!whole)
+          p.part_lse[part_row + tid] = l2;
+        else if (lse != nullptr && tid < heads)
+          lse[tid] = l2 * kLn2;
+      }
+      softmax_bar();
+      mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int d = 128 * c + key;  // this thread's feature
+#pragma unroll 1
+        for (int g = 0; g < kH; g += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + 64 * c + g, v);
+          if constexpr (kH == 32) {  // p1's and p2's products
+            uint32_t u[16];
+            tmem_ld16(lanes + 64 * c + 32 + g, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), 1.f / C::gain, __uint_as_float(v[i])));
+          } else {
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int h = g + i;
+            if (h < heads) {
+              const float o = __uint_as_float(v[i]) * ms.inv[h];
+              if (whole)
+                out[h * MLA_D_LATENT + d] = __float2bfloat16_rn(o);
+              else
+                p.part_o[(part_row + h) * MLA_D_LATENT + d] = o;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      softmax_bar();  // part, inv and m are free for the next piece
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Merge of the pieces of cut sequences, in range order, by LSE; sequences
+// without keys get their zeros here.  CTA = (sequence, head), thread = four
+// features.
+template <int kH>
+__global__ void __launch_bounds__(128) fp8_decode_merge_kernel(const Params p) {
+  const int b = blockIdx.x / p.a.num_heads, h = blockIdx.x % p.a.num_heads, tid = threadIdx.x;
+  const int64_t off = p.offsets[b], end = p.offsets[b + 1], per = p.offsets[p.a.batch + 1];
+  const int64_t row = static_cast<int64_t>(b) * p.a.num_heads + h;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT) + tid;
+  if (off == end) {
+    *out = make_uint2(0, 0);
+    if (p.a.lse != nullptr && tid == 0) p.a.lse[row] = -INFINITY;
+    return;
+  }
+  const int64_t r0 = off / per, r1 = (end - 1) / per;
+  if (r0 == r1) return;  // one piece: written already
+  const int g = h / kH;
+  auto piece = [&](int64_t r) {  // its row of partial results
+    const int part = r == r0 && r * per < off ? 1 : 0;
+    return ((r * p.groups + g) * 2 + part) * kH + h % kH;
+  };
+  float m = -INFINITY;
+  for (int64_t r = r0; r <= r1; ++r) m = fmaxf(m, p.part_lse[piece(r)]);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f, o[4] = {};
+  for (int64_t r = r0; r <= r1; ++r) {
+    const int64_t i = piece(r);
+    const float w = ex2_approx(p.part_lse[i] - ref);
+    sum += w;
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + i * MLA_D_LATENT)[tid];
+    o[0] = fmaf(w, v.x, o[0]);
+    o[1] = fmaf(w, v.y, o[1]);
+    o[2] = fmaf(w, v.z, o[2]);
+    o[3] = fmaf(w, v.w, o[3]);
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
+  *out = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (p.a.lse != nullptr && tid == 0) p.a.lse[row] = sum != 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+int heads_per_cta(int num_heads) { return num_heads <= 32 ? 32 : 64; }
+
+struct Layout {
+  int ranges, groups;
+  size_t lse, o, total;
+};
+Layout layout(int batch, int num_heads, int num_sms) {
+  const int kh = heads_per_cta(num_heads);
+  Layout l;
+  l.groups = (num_heads + kh - 1) / kh;
+  l.ranges = num_sms / l.groups > 1 ? num_sms / l.groups : 1;
+  const size_t rows = static_cast<size_t>(l.ranges) * l.groups * 2 * kh;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.lse = up((static_cast<size_t>(batch) + 2) * sizeof(int64_t));
+  l.o = up(l.lse + rows * sizeof(float));
+  l.total = l.o + rows * MLA_D_LATENT * sizeof(float);
+  return l;
+}
+
+template <int kH>
+int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int slot, cudaStream_t stream) {
+  constexpr int bytes = static_cast<int>(smem_bytes<kH>());
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_decode_kernel<kH>), bytes, slot)) return st;
+  const int64_t grid = static_cast<int64_t>(p.ranges) * p.groups;
+  fp8_decode_kernel<kH><<<static_cast<unsigned>(grid), kThreads, bytes, stream>>>(lat, rope, p);
+  if (const int st = launch_status()) return st;
+  if (!p.split) return MLA_OK;
+  fp8_decode_merge_kernel<kH><<<static_cast<unsigned>(p.a.num_heads) * p.a.batch, 128, 0, stream>>>(p);
+  return launch_status();
 }
 
 }  // namespace
 
 size_t fp8_decode_workspace_bytes(int batch, int num_heads, int num_sms) {
-  (void)batch; (void)num_heads; (void)num_sms;
-  return 256;
+  return layout(batch, num_heads, num_sms).total;
 }
 
 int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) {
-  (void)num_sms;
-  fp8_decode_kernel<<<dim3(a.num_heads, a.batch), 256, 0, stream>>>(a);
-  return launch_status();
+  const Layout l = layout(a.batch, a.num_heads, num_sms);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Params p{a, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + l.lse),
+           reinterpret_cast<float*>(ws + l.o)};
+  if (static_cast<int64_t>(a.batch) * a.num_heads > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
+  CUtensorMap lat, rope;
+  if (!encode_byte_map(&lat, a.cache, kKey, a.num_slots, kKey, 128, kBlock, false) ||
+      !encode_byte_map(&rope, a.cache, kKey, a.num_slots, kKey, 64, kBlock, true)) {
+    set_last_error("cuTensorMapEncodeTiled failed for the cache");
+    return MLA_ERR_LAUNCH;
+  }
+  return heads_per_cta(a.num_heads) == 64 ? launch<64>(p, lat, rope, 19, stream) : launch<32>(p, lat, rope, 20, stream);
 }
 
 }  // namespace mla

@@ -75,9 +75,9 @@ def append(cache, scales, kv_c, k_pe, cos_sin, cu, ctx, table, page_size, interl
 
 
 def decode(q, cache, scales, softmax_scale, table, lens, page_size):
-    """(out, lse, softmax @ |v|) in float64; q float [B, H, 576]."""
+    """(out, lse, softmax @ |v|, largest p s times the sum of |k8|) in float64; q float [B, H, 576]."""
     B, H, _ = q.shape
-    out, lse, oabs = np.zeros((B, H, 512)), np.full((B, H), -np.inf), np.zeros((B, H, 512))
+    out, lse, oabs, flat = np.zeros((B, H, 512)), np.full((B, H), -np.inf), np.zeros((B, H, 512)), np.zeros((B, H, 512))
     for b in range(B):
         keys = []
         for t in range(int(lens[b])):
@@ -96,7 +96,9 @@ def decode(q, cache, scales, softmax_scale, table, lens, page_size):
         z = p.sum(1, keepdims=True)
         out[b], oabs[b] = p @ k[:, :512] / z, p @ np.abs(k[:, :512]) / z
         lse[b] = (m + np.log(z))[:, 0]
-    return out, lse, oabs
+        s = np.asarray(scales, np.float64)[keys // BLOCK]
+        flat[b] = np.max(p / z * s, 1)[:, None] * np.abs(k[:, :512] / s[:, None]).sum(0)
+    return out, lse, oabs, flat
 
 
 def quantize(x):

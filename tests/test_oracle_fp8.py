@@ -72,7 +72,7 @@ def test_decode_against_brute_force():
     rng = np.random.default_rng(3)
     cache, scales = fp8.encode(rng.standard_normal((128, 576)) * 50), np.array([2.0 ** -6, 2.0 ** -5], np.float32)
     q = rng.standard_normal((1, 2, 576))
-    out, lse, _ = fp8.decode(q, cache, scales, 0.05, np.array([[1, 0]]), [100], 64)
+    out, lse, _, _ = fp8.decode(q, cache, scales, 0.05, np.array([[1, 0]]), [100], 64)
     k = fp8.decode_codes(cache) * np.repeat(scales, 64)[:, None]
     k = np.concatenate([k[64:], k[:36]])
     w = np.exp(q[0] @ k.T * 0.05)
