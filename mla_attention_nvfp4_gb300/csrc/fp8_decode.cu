@@ -32,7 +32,8 @@
 // merged by LSE in a second kernel, in range order.
 //   warp 0     TMA producer: 128-feature chunks of latent in a ring, RoPE apart;
 //   warp 1     MMA issuer: scores of tile n + 1, then values of tile n;
-//   warps 2..5 queries to two terms, softmax (thread = key), output.
+//   warps 2..9 queries to two terms, softmax (thread = key; warps 2..5 the
+//              first half of the heads, 6..9 the second), output.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -49,7 +50,7 @@ using namespace sm100;
 constexpr int kKey = MLA_D_LATENT + MLA_D_ROPE;
 constexpr int kBlock = MLA_FP8_BLOCK;
 constexpr int kTile = 128;  // keys
-constexpr int kThreads = 192;
+constexpr int kSoftmax = 256, kThreads = 64 + kSoftmax;
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
 constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
 constexpr float kReset = 6.0f;  // a raised reference puts the tile's largest weight at 2^6
@@ -80,8 +81,9 @@ struct Misc {
   uint64_t s_full[2], p_ready, pv_done, q_ready;
   alignas(16) float c[kH], m[kH], move[kH], factor[kH], inv[kH];
   float part[4][kH];
-  int64_t scan[6], t0, t1, off0;
+  int64_t scan[kThreads / 32], t0, t1, off0;
   int b0;
+  uint32_t raised[2];  // heads whose reference moves, a bit each
   uint32_t tmem;
   volatile int abort;
 };
@@ -94,6 +96,8 @@ static_assert(smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448, "shared 
 
 struct Params {
   Fp8DecodeArgs a;
+  uint32_t page_magic;  // division by page_size / 64
+  int page_shift;
   int ranges, groups;  // ranges of tiles; head groups (grid = ranges * groups)
   bool split;
   int64_t* offsets;  // [batch + 1] first tile of each sequence, then tiles per range
@@ -108,12 +112,15 @@ __device__ __forceinline__ int clipped_len(const Fp8DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// First slot of block i (64 tokens) of sequence b, or -1 (page out of range).
-__device__ __forceinline__ int64_t block_slot(const Fp8DecodeArgs& a, int b, int i) {
-  const int per = a.page_size / kBlock;
-  const int64_t page = a.page_table[b * a.pt_stride + i / per];
-  const int64_t slot = page * a.page_size + static_cast<int64_t>(i % per) * kBlock;
-  return page < 0 || slot + kBlock > a.num_slots ? -1 : slot;
+// Block i (64 tokens) of sequence b: its page table entry, and its first slot
+// given that entry, or -1 (page out of range).
+__device__ __forceinline__ int block_page(const Params& p, int b, int i) {
+  return p.a.page_table[b * p.a.pt_stride + div_magic(i, p.page_magic, p.page_shift)];
+}
+__device__ __forceinline__ int block_slot(const Params& p, int page, int i) {
+  const int in = i - static_cast<int>(div_magic(i, p.page_magic, p.page_shift)) * (p.a.page_size / kBlock);
+  const int64_t slot = static_cast<int64_t>(page) * p.a.page_size + static_cast<int64_t>(in) * kBlock;
+  return page < 0 || slot + kBlock > p.a.num_slots ? -1 : static_cast<int>(slot);
 }
 
 // Calls f(b, len, first tile, last tile + 1, tiles of b, part) for every
@@ -160,14 +167,14 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
 __device__ __forceinline__ bool softmax_any(bool v) {
   int r;
   asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 2, 128, a;\n\t"
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 2, %2, a;\n\t"
       "selp.s32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(v))
+      : "r"(static_cast<int>(v)), "n"(kSoftmax)
       : "memory");
   return r != 0;
 }
@@ -239,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ms.s_full[0], 1);
     mbar_init(&ms.s_full[1], 1);
-    mbar_init(&ms.p_ready, 4);
+    mbar_init(&ms.p_ready, kSoftmax / 32);
     mbar_init(&ms.pv_done, 1);
-    mbar_init(&ms.q_ready, 4);
+    mbar_init(&ms.q_ready, kSoftmax / 32);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = (2 * (t - s)) & 31;
         if (at == 0) {
           const int i = 2 * t + lane;
-          const int64_t slot = i < n_blocks && i < 2 * e ? block_slot(p.a, b, i) : -1;
+          const int slot = i < n_blocks && i < 2 * e ? block_slot(p, block_page(p, b, i), i) : -1;
           y = static_cast<int>(slot < 0 ? p.a.num_slots : slot);
         }
         const int y0 = __shfl_sync(0xffffffffu, y, at), y1 = __shfl_sync(0xffffffffu, y, at + 1);
@@ -363,7 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------- queries, softmax, output
     // A wait that gives up leaves these warps running through their loops
     // (they meet at named barriers); the error word tells.
-    const int quad = warp & 3, tid = threadIdx.x - 64;
+    constexpr int kMine = kH / 2;  // heads per thread
+    const int quad = warp & 3, tid = threadIdx.x - 64, wg = tid >> 7;
+    const int hb = wg * kMine;         // this thread's first head
     const int key = quad * 32 + lane;  // of the tile: a TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
@@ -379,39 +388,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (static_cast<int64_t>(b) * p.a.num_heads + h0) * MLA_D_LATENT;
       float* lse = p.a.lse != nullptr ? p.a.lse + static_cast<int64_t>(b) * p.a.num_heads + h0 : nullptr;
       if (s >= e) {  // no keys
-        for (int i = tid; i < heads * (MLA_D_LATENT / 8); i += 128) reinterpret_cast<uint4*>(out)[i] = uint4{};
+        for (int i = tid; i < heads * (MLA_D_LATENT / 8); i += kSoftmax) reinterpret_cast<uint4*>(out)[i] = uint4{};
         if (lse != nullptr && tid < heads) lse[tid] = -INFINITY;
         return;
       }
       if (s == 0 && tid == 0 && group == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
 
+      // Page table entries two tiles ahead, block scales one, each loaded an
+      // iteration before it is used.
+      const int n_blocks = (len + kBlock - 1) / kBlock;
+      auto page_at = [&](int t) {
+        const int i = 2 * t + (quad >> 1);
+        return t < e && i < n_blocks ? block_page(p, b, i) : 0;
+      };
+      auto slot_at = [&](int t, int page) {  // -2: no such block; -1: its page is out of range
+        const int i = 2 * t + (quad >> 1);
+        return t < e && i < n_blocks ? block_slot(p, page, i) : -2;
+      };
+      int slot_n = slot_at(s, page_at(s)), page_n = page_at(s + 1);
+      float scale_n = slot_n >= 0 ? p.a.scales[slot_n / kBlock] : 0.f;
+
       // Queries: a warp takes a head at a time; lane l features 8 l.., and
-      // 256 + 8 l.., lanes 0..7 the RoPE's.
+      // 256 + 8 l.., lanes 0..7 the RoPE's.  All loads first.
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) +
                                (static_cast<int64_t>(b) * p.a.num_heads + h0) * kKey;
-#pragma unroll 4
-      for (int i = 0; i < kH / 4; ++i) {
-        const int h = quad + 4 * i;
-        uint4 v[3] = {};
+      constexpr int kQ = kH / 8;  // heads per warp
+      uint4 qv[kQ][3];
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const int h = (warp - 2) + 8 * i;
+        qv[i][0] = qv[i][1] = qv[i][2] = make_uint4(0, 0, 0, 0);
         if (h < heads) {
           const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
-          v[0] = src[lane];
-          v[1] = src[lane + 32];
-          if (lane < 8) v[2] = src[lane + 64];
+          qv[i][0] = src[lane];
+          qv[i][1] = src[lane + 32];
+          if (lane < 8) qv[i][2] = src[lane + 64];
         }
-        float f[24], am = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const int h = (warp - 2) + 8 * i;
+        // amax from the bf16 bits (sign dropped, they order like integers)
+        uint32_t m2 = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          bf16x2_to_f32(v[k].x, f[8 * k], f[8 * k + 1]);
-          bf16x2_to_f32(v[k].y, f[8 * k + 2], f[8 * k + 3]);
-          bf16x2_to_f32(v[k].z, f[8 * k + 4], f[8 * k + 5]);
-          bf16x2_to_f32(v[k].w, f[8 * k + 6], f[8 * k + 7]);
-          am = fmaxf(am, amax8(f + 8 * k));
+          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            m2 = max(m2, w[j] & 0x7FFF0000u);
+            m2 = max(m2, (w[j] << 16) & 0x7FFF0000u);
+          }
         }
-        am = warp_max(am);
+        m2 = __reduce_max_sync(0xffffffffu, m2);
         // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8)
-        const uint32_t u = __float_as_uint(am);
-        int ex = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
         ex = max(-60, min(60, ex));
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
         if (lane == 0) {
@@ -420,11 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
+          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
           uint32_t w1[2], w2[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float* g = f + 8 * k + 4 * j;
-            const float x0 = g[0] * inv, x1 = g[1] * inv, x2 = g[2] * inv, x3 = g[3] * inv;
+            float x0, x1, x2, x3;
+            bf16x2_to_f32(w[2 * j], x0, x1);
+            bf16x2_to_f32(w[2 * j + 1], x2, x3);
+            x0 *= inv, x1 *= inv, x2 *= inv, x3 *= inv;
             const uint32_t a = cvt_e4m3x2(x0, x1), c = cvt_e4m3x2(x2, x3);
             const uint32_t ha = e4m3x2_to_f16x2_pair(a), hc = e4m3x2_to_f16x2_pair(c);
             const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
@@ -457,45 +490,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.q_ready);
       softmax_bar();  // c and m are there
 
-      float l[kH];
+      float l[kMine];
 #pragma unroll
-      for (int h = 0; h < kH; ++h) l[h] = 0.f;
+      for (int h = 0; h < kMine; ++h) l[h] = 0.f;
       bool set = false;  // the references follow some key
-      // block slots two tiles ahead, scales one
-      const int n_blocks = (len + kBlock - 1) / kBlock;
-      auto slot_at = [&](int t) -> int64_t {
-        const int i = 2 * t + (quad >> 1);
-        return t < e && i < n_blocks ? block_slot(p.a, b, i) : -2;  // -2: no block; -1: a page out of range
-      };
-      int64_t slot_1 = slot_at(s), slot_2 = slot_at(s + 1);
-      float scale_1 = slot_1 >= 0 ? p.a.scales[slot_1 / kBlock] : 0.f;
       for (int t = s; t < e; ++t, ++n) {
-        const int64_t slot = slot_1;
-        const bool sb_ok = slot >= 0 && scale_1 >= kScaleMin && scale_1 <= kScaleMax;
-        const float sb = sb_ok ? scale_1 : 1.f;
-        if (lane == 0 && (quad & 1) == 0 && slot != -2 && !sb_ok)
+        const int slot = slot_n;
+        const bool sb_ok = slot >= 0 && scale_n >= kScaleMin && scale_n <= kScaleMax;
+        const float sb = sb_ok ? scale_n : 1.f, lsb = log2f(sb);
+        if (lane == 0 && (quad & 1) == 0 && wg == 0 && slot != -2 && !sb_ok)
           flag_error(err, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
-        slot_1 = slot_2;
-        scale_1 = slot_1 >= 0 ? p.a.scales[slot_1 / kBlock] : 0.f;
-        slot_2 = slot_at(t + 2);
+        slot_n = slot_at(t + 1, page_n);
+        scale_n = slot_n >= 0 ? p.a.scales[slot_n / kBlock] : 0.f;
+        page_n = page_at(t + 2);
         const bool valid = sb_ok && t * kTile + key < len;
-        const float lsb = log2f(sb);
 
         mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
         tc_fence_after();
-        float x[kH], top = -INFINITY;
-        const uint32_t src = lanes + C::col_s + (n & 1) * 2 * kH;
+        float x[kMine], top = -INFINITY;
+        const uint32_t src = lanes + C::col_s + (n & 1) * 2 * kH + hb;
 #pragma unroll
-        for (int c = 0; c < kH / 16; ++c) {
+        for (int c = 0; c < kMine; c += 16) {
           uint32_t v[16], u[16];
-          tmem_ld16(src + 16 * c, v);
-          tmem_ld16(src + kH + 16 * c, u);
+          tmem_ld16(src + c, v);
+          tmem_ld16(src + kH + c, u);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const int h = 16 * c + i;
-            const float4 cc = *reinterpret_cast<const float4*>(&ms.c[h]);
-            const float4 mm = *reinterpret_cast<const float4*>(&ms.m[h]);
+            const int h = c + i;
+            const float4 cc = *reinterpret_cast<const float4*>(&ms.c[hb + h]);
+            const float4 mm = *reinterpret_cast<const float4*>(&ms.m[hb + h]);
             const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -507,16 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (softmax_any(top + lsb > kTop || (!set && valid))) {
           // Raise the references of the heads that need it.
+          float mine = 0.f;
 #pragma unroll
-          for (int g = 0; g < kH; g += 32) {
-            float mine = 0.f;
-#pragma unroll
-            for (int h = 0; h < 32; ++h) {
-              const float r = warp_max(x[g + h] + lsb);
-              if (lane == h) mine = r;
-            }
-            ms.part[quad][g + lane] = mine;
+          for (int h = 0; h < kMine; ++h) {
+            const float r = warp_max(x[h] + lsb);
+            if (lane == h) mine = r;
           }
+          if (lane < kMine) ms.part[quad][hb + lane] = mine;
           softmax_bar();
           if (tid < kH) {
             const float mx = fmaxf(fmaxf(ms.part[0][tid], ms.part[1][tid]), fmaxf(ms.part[2][tid], ms.part[3][tid]));
@@ -525,34 +546,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             ms.move[tid] = by;
             ms.factor[tid] = !set ? 0.f : ex2_approx(-by);
             ms.m[tid] += by;
+            const uint32_t raised = __ballot_sync(0xffffffffu, raise);
+            if (lane == 0) ms.raised[tid >> 5] = raised;
           }
           softmax_bar();
 #pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            x[h] -= ms.move[h];
-            l[h] *= ms.factor[h];
+          for (int h = 0; h < kMine; h += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(&ms.move[hb + h]);
+            const float4 fv = *reinterpret_cast<const float4*>(&ms.factor[hb + h]);
+            x[h] -= mv.x, x[h + 1] -= mv.y, x[h + 2] -= mv.z, x[h + 3] -= mv.w;
+            l[h] *= fv.x, l[h + 1] *= fv.y, l[h + 2] *= fv.z, l[h + 3] *= fv.w;
           }
-          if (t > s) {  // O holds earlier tiles: all its products are done before it is rescaled
+          if (t > s) {
+            // O holds earlier tiles: once their products are done, the
+            // columns of 16 heads at a time, two value chunks per warp
             mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(lanes + c, v);
+            for (int c = 0; c < 64; c += 16) {
+              const int g = c & (kH - 1);
+              if (((ms.raised[g >> 5] >> (g & 31)) & 0xFFFFu) == 0) continue;
+              const uint32_t at = lanes + 128 * wg + c;
+              uint32_t v[16], u[16];
+              tmem_ld16(at, v);
+              tmem_ld16(at + 64, u);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                v[i] = __float_as_uint(__uint_as_float(v[i]) * ms.factor[(c + i) & (kH - 1)]);
-              tmem_st16(lanes + c, v);
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f4 = *reinterpret_cast<const float4*>(&ms.factor[g + i]);
+                const float fv[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  v[i + j] = __float_as_uint(__uint_as_float(v[i + j]) * fv[j]);
+                  u[i + j] = __float_as_uint(__uint_as_float(u[i + j]) * fv[j]);
+                }
+              }
+              tmem_st16(at, v);
+              tmem_st16(at + 64, u);
             }
             tmem_st_wait();
           }
           set = true;
         }
         // weights and their two terms; words of four heads
-        uint32_t w1[kH / 4], w2[kH / 4];
+        uint32_t w1[kMine / 4], w2[kMine / 4];
 #pragma unroll
-        for (int h = 0; h < kH; h += 4) {
+        for (int h = 0; h < kMine; h += 4) {
           uint32_t a[2], r[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -571,28 +610,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile, the output was read before this)
         if (n > 0) mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
         {
+          // row = key, 64 bytes: heads of one term (kH 64), or p1 | p2
           const uint32_t row = s0 + C::off_p + key * 64, sw = (key >> 1) & 3;
           if constexpr (kH == 64) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              sts128(row + ((c ^ sw) << 4), make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
-              sts128(row + kTile * 64 + ((c ^ sw) << 4),
-                     make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t at = row + (((2 * wg + c) ^ sw) << 4);
+              sts128(at, make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
+              sts128(at + kTile * 64, make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
             }
           } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              sts128(row + ((c ^ sw) << 4), make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
-              sts128(row + (((c + 2) ^ sw) << 4),
-                     make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
-            }
+            sts128(row + ((wg ^ sw) << 4), make_uint4(w1[0], w1[1], w1[2], w1[3]));
+            sts128(row + (((wg + 2) ^ sw) << 4), make_uint4(w2[0], w2[1], w2[2], w2[3]));
           }
         }
         // a row that is no key of the sequence may hold any bytes (NaN too):
         // as values they are zeros
         if (!valid && slot >= 0) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
             const uint32_t row = slot_addr((4 * n + c) % C::slots) + key * 128;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sts128(row + 16 * i, make_uint4(0, 0, 0, 0));
@@ -604,22 +640,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ms.p_ready);
       }
 
-      // Sums over the keys: halves exchanged until lane i holds heads
-      // i * kH / 32 ...; then across the warps.
+      // Sums over the keys: halves exchanged until lane i holds head
+      // hb + i * kMine / 32; then across the warps.
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const bool up = (lane & o) != 0;
-        const int half = kH * o / 32;
+        const int half = kMine * o / 32;
+        if (half == 0) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
 #pragma unroll
-        for (int h = 0; h < kH / 2; ++h) {
+        for (int h = 0; h < kMine / 2; ++h) {
           if (h < half) {
             const float give = up ? l[h] : l[h + half], keep = up ? l[h + half] : l[h];
             l[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kH / 32; ++i) ms.part[quad][lane * (kH / 32) + i] = l[i];
+      ms.part[quad][hb + lane * kMine / 32] = l[0];
       softmax_bar();
       const int64_t part_row = ((static_cast<int64_t>(range) * p.groups + group) * 2 + part) * kH;
       if (tid < kH) {
@@ -634,33 +670,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       softmax_bar();
       mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
       tc_fence_after();
+      // Two value chunks per warp, thread = feature; neighbouring threads
+      // swap halves of two heads so that each stores two features of one.
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int d = 128 * c + key;  // this thread's feature
+      for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
+        const int d = 128 * c + key;
 #pragma unroll 1
-        for (int g = 0; g < kH; g += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes + 64 * c + g, v);
+        for (int g = 0; g < kH; g += 32) {
+          uint32_t v[32];
+          tmem_ld32(lanes + 64 * c + g, v);
           if constexpr (kH == 32) {  // p1's and p2's products
-            uint32_t u[16];
-            tmem_ld16(lanes + 64 * c + 32 + g, u);
+            uint32_t u[32];
+            tmem_ld32(lanes + 64 * c + 32, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
               v[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), 1.f / C::gain, __uint_as_float(v[i])));
           } else {
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int h = g + i;
-            if (h < heads) {
-              const float o = __uint_as_float(v[i]) * ms.inv[h];
-              if (whole)
-                out[h * MLA_D_LATENT + d] = __float2bfloat16_rn(o);
-              else
-                p.part_o[(part_row + h) * MLA_D_LATENT + d] = o;
+          for (int i = 0; i < 32; i += 4) {
+            const float4 iv = *reinterpret_cast<const float4*>(&ms.inv[g + i]);
+            v[i] = __float_as_uint(__uint_as_float(v[i]) * iv.x);
+            v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) * iv.y);
+            v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) * iv.z);
+            v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) * iv.w);
+          }
+          if (whole) {
+            const int odd = lane & 1;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(out + (g + odd) * MLA_D_LATENT + (d - odd));
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
+              const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 1);
+              const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, mine) : __floats2bfloat162_rn(mine, got);
+              if (g + i + odd < heads) dst[i * (MLA_D_LATENT / 2)] = *reinterpret_cast<const uint32_t*>(&o);
             }
+          } else {
+            float* dst = p.part_o + (part_row + g) * MLA_D_LATENT + d;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (g + i < heads) dst[i * MLA_D_LATENT] = __uint_as_float(v[i]);
           }
         }
       }
@@ -756,7 +807,10 @@ size_t fp8_decode_workspace_bytes(int batch, int num_heads, int num_sms) {
 int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) {
   const Layout l = layout(a.batch, a.num_heads, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  Params p{a, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + l.lse),
+  uint32_t magic;
+  int shift;
+  magic_divisor(a.page_size / kBlock, &magic, &shift);
+  Params p{a, magic, shift, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + l.lse),
            reinterpret_cast<float*>(ws + l.o)};
   if (static_cast<int64_t>(a.batch) * a.num_heads > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   CUtensorMap lat, rope;
