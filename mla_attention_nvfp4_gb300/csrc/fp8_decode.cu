@@ -127,25 +127,29 @@ __device__ __forceinline__ int block_slot(const Params& p, int page, int i) {
 // piece of this CTA's work; part: 0 for the piece its range begins with.
 template <int kH, class F>
 __device__ __forceinline__ void for_each_piece(const Params& p, const Misc<kH>& ms, int range, F f) {
-  if (p.split) {
-    int64_t t = ms.t0, off = ms.off0;
-    const int64_t t0 = t, t1 = ms.t1;
-    for (int b = ms.b0; t < t1; ++b) {
-      const int len = clipped_len(p.a, b), n = tiles_of(len);
-      if (n > 0) {
-        const int s = static_cast<int>(t - off);
-        const int e = t1 - off < n ? static_cast<int>(t1 - off) : n;
-        f(b, len, s, e, n, t == t0 ? 0 : 1);
-        t = off + e;
-      }
+  // one loop (and one copy of f's code) for both forms: a range of tiles, or
+  // whole sequences range, range + ranges, ...
+  const bool split = p.split;
+  int64_t t = split ? ms.t0 : 0, off = split ? ms.off0 : 0;
+  const int64_t t0 = t, t1 = split ? ms.t1 : 0;
+  for (int b = split ? ms.b0 : range; split ? t < t1 : b < p.a.batch; b += split ? 1 : p.ranges) {
+    const int len = clipped_len(p.a, b), n = tiles_of(len);
+    const int s = split ? static_cast<int>(t - off) : 0;
+    const int e = split && t1 - off < n ? static_cast<int>(t1 - off) : n;
+    if (n > 0 || !split) f(b, len, s, e, n, t == t0 ? 0 : 1);
+    if (split) {
+      if (n > 0) t = off + e;
       off += n;
     }
-  } else {
-    for (int b = range; b < p.a.batch; b += p.ranges) {
-      const int len = clipped_len(p.a, b), n = tiles_of(len);
-      f(b, len, 0, n, n, 0);
-    }
   }
+}
+
+// mbar_wait with the loop kept out of line: one try where it is used.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
+  return mbar_wait(bar, parity, err, abort);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, err, abort);
 }
 
 __device__ __forceinline__ uint32_t cvt_e4m3x2_h2(uint32_t h2) {
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int d = 0; d < 4 && ok; ++d) {
             const int k = 4 * n + d, i = k % C::slots;
-            ok = mbar_wait(&ms.empty[i], ((k / C::slots) & 1) ^ 1, err, &ms.abort);
+            ok = wait(&ms.empty[i], ((k / C::slots) & 1) ^ 1, err, &ms.abort);
             if (!ok) break;
             mbar_expect_tx(&ms.full[i], kChunkBytes);
             tma_load_bytes(slot_addr(i), &tm_lat, 128 * d, y0, &ms.full[i]);
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (ok) {
             const int i = n % C::ropes;
-            ok = mbar_wait(&ms.rempty[i], ((n / C::ropes) & 1) ^ 1, err, &ms.abort);
+            ok = wait(&ms.rempty[i], ((n / C::ropes) & 1) ^ 1, err, &ms.abort);
             if (ok) {
               const uint32_t dst = s0 + C::off_rope + i * kRopeBytes;
               mbar_expect_tx(&ms.rfull[i], kRopeBytes);
@@ -311,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_s = idesc_e4m3(128, 2 * kH, false, false);
       constexpr uint32_t idesc_o = idesc_e4m3(128, 64, true, true);
       bool ok = true;
-      auto wait = [&](uint64_t* bar, int parity) {
-        ok = ok && mbar_wait(bar, parity, err, &ms.abort);
+      auto ready = [&](uint64_t* bar, int parity) {
+        ok = ok && wait(bar, parity, err, &ms.abort);
         return ok;
       };
       auto scores = [&](int n) {  // S^T of tile n
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int k = 4 * n + c, i = k % C::slots;
-          if (!wait(&ms.full[i], (k / C::slots) & 1)) return;
+          if (!ready(&ms.full[i], (k / C::slots) & 1)) return;
           tc_fence_after();
           const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
           const uint64_t db = smem_desc_sw128(s0 + C::off_q + c * C::q_chunk, 0, 1024);
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc_s, (c > 0 || j > 0) ? 1u : 0u);
         }
         const int i = n % C::ropes;
-        if (!wait(&ms.rfull[i], (n / C::ropes) & 1)) return;
+        if (!ready(&ms.rfull[i], (n / C::ropes) & 1)) return;
         tc_fence_after();
         const uint64_t da = smem_desc_sw64(s0 + C::off_rope + i * kRopeBytes, 512);
         const uint64_t db = smem_desc_sw64(s0 + C::off_q + 4 * C::q_chunk, 512);
@@ -341,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for_each_piece<kH>(p, ms, range, [&](int, int, int s, int e, int, int) {
         if (s >= e) return;
         // the piece's queries (and with them the previous piece's last S^T) are there
-        if (!wait(&ms.q_ready, item & 1)) return;
+        if (!ready(&ms.q_ready, item & 1)) return;
         ++item;
         scores(n);
         for (int t = s; t < e; ++t, ++n) {
           if (t + 1 < e) scores(n + 1);
-          if (!wait(&ms.p_ready, n & 1)) return;
+          if (!ready(&ms.p_ready, n & 1)) return;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -408,31 +412,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot_n = slot_at(s, page_at(s)), page_n = page_at(s + 1);
       float scale_n = slot_n >= 0 ? p.a.scales[slot_n / kBlock] : 0.f;
 
-      // Queries: a warp takes a head at a time; lane l features 8 l.., and
-      // 256 + 8 l.., lanes 0..7 the RoPE's.  All loads first.
+      // Queries: a warp takes every eighth head; lane l features 8 l.., and
+      // 256 + 8 l.., lanes 0..7 the RoPE's.  The lines of this sequence's and
+      // the next one's are asked for first.
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) +
                                (static_cast<int64_t>(b) * p.a.num_heads + h0) * kKey;
-      constexpr int kQ = kH / 8;  // heads per warp
-      uint4 qv[kQ][3];
-#pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const int h = (warp - 2) + 8 * i;
-        qv[i][0] = qv[i][1] = qv[i][2] = make_uint4(0, 0, 0, 0);
-        if (h < heads) {
-          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
-          qv[i][0] = src[lane];
-          qv[i][1] = src[lane + 32];
-          if (lane < 8) qv[i][2] = src[lane + 64];
+      {
+        const char* line = reinterpret_cast<const char*>(q) + 128 * tid;
+        const int64_t next = static_cast<int64_t>(p.a.num_heads) * kKey * 2;
+        for (int i = tid; i < heads * (kKey * 2 / 128); i += kSoftmax, line += 128 * kSoftmax) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+          if (b + 1 < p.a.batch) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + next));
         }
       }
+      auto load_head = [&](int h, uint4(&v)[3]) {
+        v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
+        if (h < heads) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
+          v[0] = src[lane];
+          v[1] = src[lane + 32];
+          if (lane < 8) v[2] = src[lane + 64];
+        }
+      };
+      uint4 v_next[3], v_after[3];
+      load_head(warp - 2, v_next);
+      load_head(warp + 6, v_after);
+#pragma unroll 1
+      for (int h = warp - 2; h < kH; h += 8) {
+        uint4 v[3];
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const int h = (warp - 2) + 8 * i;
+        for (int k = 0; k < 3; ++k) {
+          v[k] = v_next[k];
+          v_next[k] = v_after[k];
+        }
+        load_head(h + 16, v_after);
         // amax from the bf16 bits (sign dropped, they order like integers)
         uint32_t m2 = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             m2 = max(m2, w[j] & 0x7FFF0000u);
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {qv[i][k].x, qv[i][k].y, qv[i][k].z, qv[i][k].w};
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           uint32_t w1[2], w2[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -472,12 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
             const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
             a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
-            a2 = base + (kH + h) * 128 + ((unit ^ (h & 7)) << 4) + half;
+            a2 = a1 + kH * 128;
           } else {
             const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
             const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
             a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
-            a2 = base + (kH + h) * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
+            a2 = a1 + kH * 64;
           }
           if (k < 2 || lane < 8) {
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a1), "r"(w1[0]), "r"(w1[1]) : "memory");
@@ -505,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         page_n = page_at(t + 2);
         const bool valid = sb_ok && t * kTile + key < len;
 
-        mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
+        wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
         tc_fence_after();
         float x[kMine], top = -INFINITY;
         const uint32_t src = lanes + C::col_s + (n & 1) * 2 * kH + hb;
@@ -560,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t > s) {
             // O holds earlier tiles: once their products are done, the
             // columns of 16 heads at a time, two value chunks per warp
-            mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+            wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
@@ -608,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the previous tile's products have read P (and, at a piece's first
         // tile, the output was read before this)
-        if (n > 0) mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+        if (n > 0) wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
         {
           // row = key, 64 bytes: heads of one term (kH 64), or p1 | p2
           const uint32_t row = s0 + C::off_p + key * 64, sw = (key >> 1) & 3;
@@ -668,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lse[tid] = l2 * kLn2;
       }
       softmax_bar();
-      mbar_wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+      wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
       tc_fence_after();
       // Two value chunks per warp, thread = feature; neighbouring threads
       // swap halves of two heads so that each stores two features of one.
