@@ -62,6 +62,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
+// One column: lane = this thread's.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(v) : "memory");
+}
+
 // acc (two floats) += v (two floats) * s (two floats), each a fused
 // multiply-add rounded to nearest.
 __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) {

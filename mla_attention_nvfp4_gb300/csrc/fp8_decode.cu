@@ -5,17 +5,22 @@
 // keys x 576 features arrive by TMA and serve both products, the keys as
 // 128-row operand of S^T = K Q^T (K-major) and the values as 128-row operand
 // of O^T = V^T P^T (read feature-major, one 128-feature chunk at a time).
-// Queries and probabilities are the other operand: 32 heads a CTA, so that a
-// call with few heads pays for few, and a key is a TMEM lane, so that masking
-// a key masks a thread.
+// Queries and probabilities are the other operand, kH heads a CTA (32 or 64),
+// so that a call with few heads pays for few, and a key is a TMEM lane, so
+// that masking a key masks a thread.
 //
-// Two e4m3 terms, side by side as columns of that operand, carry 8 bits:
+// Two 8-bit terms carry 8 significant bits:
 //   q = 2^e (q1 + q2) with q1 = e4m3(q 2^-e), q2 = e4m3(q 2^-e - q1): a bf16
 //       query exactly (its 8 bits split 4 + 4), down to 2^-17 of the head's
-//       largest feature, below which it is held to an absolute 2^-19 of it;
-//   p = p1 + p2 / 16 likewise, at most 2^-8 off relative (what bf16 would be).
-//       The largest p lies between 2^kReset and 2^kTop, so that the absolute
-//       floor, one step 2^-9 of the second term, lies 2^17 or more below it.
+//       largest feature, below which it is held to an absolute 2^-19 of it.
+//       The terms are 2 kH columns of one product, added as S^T is read.
+//   p = p1 + p2 with p1 = e4m3(p), at most 2^-8 off relative (what bf16 would
+//       be).  The largest p lies between 2^kReset and 2^kTop, and the terms'
+//       absolute floor, 2^-13, 2^17 or more below it:
+//         32 heads: p2 = e4m3(16 (p - p1)), both terms in one product, with
+//           accumulators of their own;
+//         64 heads: one accumulator (TMEM holds no more), two products, and
+//           p2 = e5m2(p - p1), which reaches as far down by itself.
 //       There the second term is rounded with an offset that runs evenly
 //       through a step over 32 neighbouring keys: a long tail of equal, tiny
 //       weights, which rounding to nearest would push to one side, keeps its
@@ -33,8 +38,11 @@
 //   warp 1       issues the score products, up to two tiles ahead;
 //   warp 14      issues the value products (issuers of their own, so that
 //                neither's waits leave the tensor cores without work);
-//   warps 2..9   softmax (thread = key; warps 2..5 heads 0..15, 6..9 the rest);
-//   warps 10..13 the next piece's queries to two terms, the last one's output.
+//   warps 2..9   queries to two terms, softmax (thread = key; warps 2..5 the
+//                first half of the heads, 6..9 the second);
+//   warps 10..13 a piece's output, while the next one starts.
+// The code of each role is kept short (rolled loops, one copy): unrolled
+// further, the warps waited for instructions more than for anything else.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -51,37 +59,51 @@ using namespace sm100;
 constexpr int kKey = MLA_D_LATENT + MLA_D_ROPE;
 constexpr int kBlock = MLA_FP8_BLOCK;
 constexpr int kTile = 128;  // keys
-constexpr int kH = 32, kMine = 16;  // heads per CTA; per softmax thread
-constexpr int kSoftmax = 256, kHelper = 128, kThreads = 96 + kSoftmax + kHelper;
+constexpr int kSoftmax = 256, kOutput = 128, kThreads = 96 + kSoftmax + kOutput;
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
 constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
 constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest weight at 2^4
-constexpr float kGain = 16.f;   // of the second term: the first's rounding error, at most 16, becomes 256
+constexpr float kGain = 16.f;   // 32 heads: the first term's rounding error, at most 16, becomes 256
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-
-// Shared memory: latent chunks (128 keys x 128 features, four a tile), RoPE
-// tiles, two pieces' queries (rows q1 0..31, q2 32..63; four chunks of 128
-// features and the RoPE), weights (row = key: p1 | p2), the rest.
-constexpr int kSlots = 8, kRopes = 2;
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64;
-constexpr uint32_t kQChunk = 2 * kH * 128, kQBytes = 2 * kH * kKey;
-constexpr uint32_t kOffRope = kSlots * kChunkBytes, kOffQ = kOffRope + kRopes * kRopeBytes;
-constexpr uint32_t kOffP = kOffQ + 2 * kQBytes, kOffMisc = kOffP + kTile * 2 * kH;
-constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0..255 (64 per chunk: p1 | p2), then two S^T of 64 (q1 | q2)
+constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0..255 (64 per value chunk), then two S^T of 2 kH (q1 | q2)
 
+// Shared memory: a ring of latent chunks (128 keys x 128 features, four a
+// tile), RoPE tiles, queries (rows q1, then q2; four chunks of 128 features
+// and the RoPE), weights (rows of 64 bytes, one per key: p1 | p2, or p1 and
+// p2 apart), the rest.
+template <int kH>
+struct Cfg {
+  static_assert(kH == 32 || kH == 64, "heads per CTA");
+  static constexpr int mine = kH / 2;  // heads per softmax thread
+  static constexpr int slots = kH == 64 ? 8 : 10, ropes = kH == 64 ? 1 : 2, info = 4;
+  static constexpr int terms = kH / 32;  // value products per chunk
+  static constexpr uint32_t q_chunk = 2 * kH * 128;
+  static constexpr uint32_t off_rope = slots * kChunkBytes, off_q = off_rope + ropes * kRopeBytes;
+  static constexpr uint32_t off_p = off_q + 2 * kH * kKey, off_misc = off_p + kTile * 64 * terms;
+};
+
+template <int kH>
 struct Misc {
-  uint64_t full[kSlots], empty[kSlots], rfull[kRopes], rempty[kRopes];
-  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready[2], sums_ready, o_free;
-  alignas(16) float c[2][kH], m[kH], move[kH], factor[kH], inv[kH];
-  float part[4][kH];
-  int64_t scan[kThreads / 32], t0, t1, off0;
+  using C = Cfg<kH>;
+  uint64_t full[C::slots], empty[C::slots], rfull[C::ropes], rempty[C::ropes], info_full[C::info];
+  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready, sums_ready, o_free;
+  alignas(16) float c[kH], m[2][kH];  // m by the piece's parity
+  alignas(16) float factor[kH], inv[kH], sums[4][kH];
+  int top[kH];  // a head's maximum, as an integer that orders like it
+  alignas(16) uint32_t over[2][4];
+  float scale[C::info][2];  // of a tile's two blocks; 0: the block is no part of the sequence
+  int64_t t0, t1, off0;
   int b0;
-  uint32_t raised;  // heads whose reference moves, a bit each
   uint32_t tmem;
   volatile int abort;
 };
-constexpr uint32_t kSmemBytes = kOffMisc + static_cast<uint32_t>(sizeof(Misc));
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+template <int kH>
+constexpr uint32_t smem_bytes() {
+  return Cfg<kH>::off_misc + static_cast<uint32_t>(sizeof(Misc<kH>));
+}
+static_assert(smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448, "shared memory budget");
 
 struct Params {
   Fp8DecodeArgs a;
@@ -112,26 +134,47 @@ __device__ __forceinline__ int block_slot(const Params& p, int page, int i) {
   return page < 0 || slot + kBlock > p.a.num_slots ? -1 : static_cast<int>(slot);
 }
 
-// Calls f(b, len, first tile, last tile + 1, tiles of b, part) for every
-// piece of this CTA's work; part: 0 for the piece its range begins with.
-template <class F>
-__device__ __forceinline__ void for_each_piece(const Params& p, const Misc& ms, int range, F f) {
-  // one loop (and one copy of f's code) for both forms: a range of tiles, or
-  // whole sequences range, range + ranges, ...
-  const bool split = p.split;
-  int64_t t = split ? ms.t0 : 0, off = split ? ms.off0 : 0;
-  const int64_t t0 = t, t1 = split ? ms.t1 : 0;
-  for (int b = split ? ms.b0 : range; split ? t < t1 : b < p.a.batch; b += split ? 1 : p.ranges) {
-    const int len = clipped_len(p.a, b), n = tiles_of(len);
-    const int s = split ? static_cast<int>(t - off) : 0;
-    const int e = split && t1 - off < n ? static_cast<int>(t1 - off) : n;
-    if (n > 0 || !split) f(b, len, s, e, n, t == t0 ? 0 : 1);
-    if (split) {
-      if (n > 0) t = off + e;
-      off += n;
-    }
+// The pieces of a CTA's work, one after another: tiles [s, e) of sequence b
+// (len keys, n tiles).  Cut form: the pieces of a range of tiles; part is 0
+// for the one the range begins with, else 1.  Whole form: sequences range,
+// range + ranges, ..., those without keys too.
+struct Pieces {
+  int b = 0, len = 0, s = 0, e = 0, n = 0, part = 0;
+
+  template <class M>
+  __device__ __forceinline__ Pieces(const Params& p, const M& ms, int range)
+      : split_(p.split), step_(p.split ? 1 : p.ranges), next_(p.split ? ms.b0 : range), t_(p.split ? ms.t0 : 0),
+        t0_(t_), t1_(p.split ? ms.t1 : 0), off_(p.split ? ms.off0 : 0) {
+    next_len_ = load(p);
   }
-}
+  __device__ __forceinline__ bool next(const Params& p) {
+    do {
+      if (split_ ? t_ >= t1_ : next_ >= p.a.batch) return false;
+      b = next_;
+      len = next_len_;
+      n = tiles_of(len);
+      next_ += step_;
+      next_len_ = load(p);  // ahead of its use
+      s = split_ ? static_cast<int>(t_ - off_) : 0;
+      e = split_ && t1_ - off_ < n ? static_cast<int>(t1_ - off_) : n;
+      part = t_ == t0_ ? 0 : 1;
+      if (split_) {
+        if (n > 0) t_ = off_ + e;
+        off_ += n;
+      }
+    } while (split_ && n == 0);
+    return true;
+  }
+
+ private:
+  __device__ __forceinline__ int load(const Params& p) const { return next_ < p.a.batch ? clipped_len(p.a, next_) : 0; }
+  const bool split_;
+  const int step_;
+  int next_, next_len_;
+  int64_t t_;
+  const int64_t t0_, t1_;
+  int64_t off_;
+};
 
 // mbar_wait with the loop kept out of line: one try where it is used.
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
@@ -146,6 +189,11 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2_h2(uint32_t h2) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
 }
+__device__ __forceinline__ uint32_t cvt_e5m2x2_h2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
 __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -155,24 +203,36 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, float s, uint32_t b) {
       __hfma2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(s), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
-__device__ __forceinline__ bool softmax_any(bool v) {
+// Floats as integers of the same order, for an integer maximum.
+__device__ __forceinline__ int ordered(float v) {
+  const int i = __float_as_int(v);
+  return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+
+// Barriers of one half of the softmax warps (128 threads): kH / 2 heads,
+// whose references and sums are that half's alone.
+__device__ __forceinline__ void half_bar(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
+__device__ __forceinline__ bool half_any(int wg, bool v) {
   int r;
   asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, 2, %2, a;\n\t"
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, %2, 128, a;\n\t"
       "selp.s32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(v)), "n"(kSoftmax)
+      : "r"(static_cast<int>(v)), "r"(3 + wg)
       : "memory");
   return r != 0;
 }
 
 // The plan: this CTA's range of the batch's tiles, and its first sequence.
-__device__ __forceinline__ void make_plan(const Params& p, Misc& ms, int range, bool publish) {
+// scan: kThreads / 32 words of shared memory.
+template <class M>
+__device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan, int range, bool publish) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
   const int per_thread = (B + kThreads - 1) / kThreads;
   const int first = tid * per_thread, last = min(first + per_thread, B);
   int64_t sum = 0;
+#pragma unroll 1
   for (int b = first; b < last; ++b) sum += tiles_of(clipped_len(p.a, b));
   int64_t incl = sum;
 #pragma unroll
@@ -180,12 +240,13 @@ __device__ __forceinline__ void make_plan(const Params& p, Misc& ms, int range, 
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) ms.scan[warp] = incl;
+  if (lane == 31) scan[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += ms.scan[w];
-    total += ms.scan[w];
+    if (w < warp) before += scan[w];
+    total += scan[w];
   }
   const int64_t per = (total + p.ranges - 1) / p.ranges;
   const int64_t t0 = range * per, t1 = t0 + per < total ? t0 + per : total;
@@ -194,6 +255,7 @@ __device__ __forceinline__ void make_plan(const Params& p, Misc& ms, int range, 
     ms.t0 = t0;
     ms.t1 = t1;
   }
+#pragma unroll 1
   for (int b = first; b < last; ++b) {
     const int n = tiles_of(clipped_len(p.a, b));
     if (publish) p.offsets[b] = off;
@@ -209,43 +271,50 @@ __device__ __forceinline__ void make_plan(const Params& p, Misc& ms, int range, 
   }
 }
 
+template <int kH>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const Params p) {
+  using C = Cfg<kH>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int range = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
+  const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
   uint32_t* err = p.a.error_word;
 
   if (threadIdx.x == 0) {
     ms.abort = 0;
-    for (int i = 0; i < kSlots; ++i) {
+    ms.b0 = 0;  // a range without tiles has no first sequence
+    ms.off0 = 0;
+#pragma unroll 1
+    for (int i = 0; i < C::slots; ++i) {
       mbar_init(&ms.full[i], 1);
       mbar_init(&ms.empty[i], 1);
     }
-    for (int i = 0; i < kRopes; ++i) {
+    for (int i = 0; i < C::ropes; ++i) {
       mbar_init(&ms.rfull[i], 1);
       mbar_init(&ms.rempty[i], 1);
     }
-    mbar_init(&ms.s_full[0], 1);
-    mbar_init(&ms.s_full[1], 1);
-    mbar_init(&ms.s_free[0], kSoftmax / 32);
-    mbar_init(&ms.s_free[1], kSoftmax / 32);
+#pragma unroll 1
+    for (int i = 0; i < C::info; ++i) mbar_init(&ms.info_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.s_free[i], kSoftmax / 32);
+    }
     mbar_init(&ms.p_ready, kSoftmax / 32);
     mbar_init(&ms.pv_done, 1);
-    mbar_init(&ms.q_ready[0], kHelper / 32);
-    mbar_init(&ms.q_ready[1], kHelper / 32);
+    mbar_init(&ms.q_ready, kSoftmax / 32);
     mbar_init(&ms.sums_ready, kSoftmax / 32);
-    mbar_init(&ms.o_free, kHelper / 32);
+    mbar_init(&ms.o_free, kOutput / 32);
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
-  if (p.split) make_plan(p, ms, range, blockIdx.x == 0);
+  if (p.split) make_plan(p, ms, reinterpret_cast<int64_t*>(&ms.sums[0][0]), range, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -260,32 +329,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n = 0;
     bool ok = true;
-    for_each_piece(p, ms, range, [&](int b, int len, int s, int e, int, int) {
-      const int n_blocks = (len + kBlock - 1) / kBlock;
-      int y = 0;  // lane i: row of block (first block of the batch of 32) + i; past the cache where there is none
+    for (Pieces it(p, ms, range); it.next(p);) {
+      const int b = it.b, len = it.len, s = it.s, e = it.e;
+      // 32 blocks (16 tiles) at a time, one a lane: the block's first slot
+      // (past the cache where there is none, so that it reads as zeros) and
+      // its scale.  The next 32 page table entries are loaded ahead.
+      if (s == 0 && group == 0 && lane == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
+      const int n_blocks = min((len + kBlock - 1) / kBlock, 2 * e);
+      auto page_of = [&](int i) { return i < n_blocks ? block_page(p, b, i) : -1; };
+      int page = page_of(2 * s + lane), y = 0;
+      float scale = 0.f;
+#pragma unroll 1
       for (int t = s; t < e && ok; ++t, ++n) {
         const int at = (2 * (t - s)) & 31;
         if (at == 0) {
           const int i = 2 * t + lane;
-          const int slot = i < n_blocks && i < 2 * e ? block_slot(p, block_page(p, b, i), i) : -1;
+          const int slot = i < n_blocks ? block_slot(p, page, i) : -1;
+          page = page_of(i + 32);
           y = static_cast<int>(slot < 0 ? p.a.num_slots : slot);
+          scale = slot < 0 ? 0.f : p.a.scales[slot / kBlock];
+          const bool good = scale >= kScaleMin && scale <= kScaleMax;
+          if (i < n_blocks && !good) flag_error(err, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
+          if (!good) scale = 0.f;
         }
         const int y0 = __shfl_sync(0xffffffffu, y, at), y1 = __shfl_sync(0xffffffffu, y, at + 1);
+        const float sc0 = __shfl_sync(0xffffffffu, scale, at), sc1 = __shfl_sync(0xffffffffu, scale, at + 1);
         if (lane == 0) {
-#pragma unroll
+#pragma unroll 1
           for (int d = 0; d < 4 && ok; ++d) {
-            const int k = 4 * n + d, i = k % kSlots;
-            ok = wait(&ms.empty[i], ((k / kSlots) & 1) ^ 1, err, &ms.abort);
+            const int k = 4 * n + d, i = k % C::slots;
+            ok = wait(&ms.empty[i], ((k / C::slots) & 1) ^ 1, err, &ms.abort);
             if (!ok) break;
             mbar_expect_tx(&ms.full[i], kChunkBytes);
             tma_load_bytes(slot_addr(i), &tm_lat, 128 * d, y0, &ms.full[i]);
             tma_load_bytes(slot_addr(i) + kChunkBytes / 2, &tm_lat, 128 * d, y1, &ms.full[i]);
+            if (d == 0) {
+              // tile n - 4, whose place this is, is done: this chunk took
+              // the place of one of tile n - 3 or a later one
+              ms.scale[n % C::info][0] = sc0;
+              ms.scale[n % C::info][1] = sc1;
+              mbar_arrive(&ms.info_full[n % C::info]);
+            }
           }
           if (ok) {
-            const int i = n % kRopes;
-            ok = wait(&ms.rempty[i], ((n / kRopes) & 1) ^ 1, err, &ms.abort);
+            const int i = n % C::ropes;
+            ok = wait(&ms.rempty[i], ((n / C::ropes) & 1) ^ 1, err, &ms.abort);
             if (ok) {
-              const uint32_t dst = s0 + kOffRope + i * kRopeBytes;
+              const uint32_t dst = s0 + C::off_rope + i * kRopeBytes;
               mbar_expect_tx(&ms.rfull[i], kRopeBytes);
               tma_load_bytes(dst, &tm_rope, MLA_D_LATENT, y0, &ms.rfull[i]);
               tma_load_bytes(dst + kRopeBytes / 2, &tm_rope, MLA_D_LATENT, y1, &ms.rfull[i]);
@@ -294,375 +384,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       }
-    });
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------- score products
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3(128, 2 * kH, false, false);
+      const uint64_t dq = smem_desc_sw128(s0 + C::off_q, 0, 1024);
+      const uint64_t dq_rope = smem_desc_sw64(s0 + C::off_q + 4 * C::q_chunk, 512);
       bool ok = true;
       auto ready = [&](uint64_t* bar, int parity) {
         ok = ok && wait(bar, parity, err, &ms.abort);
         return ok;
       };
       int n = 0, piece = 0;
-      for_each_piece(p, ms, range, [&](int, int, int s, int e, int, int) {
-        if (s >= e || !ready(&ms.q_ready[piece & 1], (piece >> 1) & 1)) return;
-        const uint32_t q = s0 + kOffQ + (piece & 1) * kQBytes;
+      for (Pieces it(p, ms, range); ok && it.next(p);) {
+        const int s = it.s, e = it.e;
+        if (s >= e) continue;
+        if (!ready(&ms.q_ready, piece & 1)) break;
+#pragma unroll 1
         for (int t = s; t < e; ++t, ++n) {
           const uint32_t d = tmem + kColS + (n & 1) * 2 * kH;
-          if (!ready(&ms.s_free[n & 1], ((n >> 1) & 1) ^ 1)) return;
-#pragma unroll
+          if (!ready(&ms.s_free[n & 1], ((n >> 1) & 1) ^ 1)) break;
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const int k = 4 * n + c, i = k % kSlots;
-            if (!ready(&ms.full[i], (k / kSlots) & 1)) return;
+            const int k = 4 * n + c, i = k % C::slots;
+            if (!ready(&ms.full[i], (k / C::slots) & 1)) break;
             tc_fence_after();
-            const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024), db = smem_desc_sw128(q + c * kQChunk, 0, 1024);
+            const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024), db = dq + c * (C::q_chunk >> 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
           }
-          const int i = n % kRopes;
-          if (!ready(&ms.rfull[i], (n / kRopes) & 1)) return;
+          const int i = n % C::ropes;
+          if (!ready(&ms.rfull[i], (n / C::ropes) & 1)) break;
           tc_fence_after();
-          const uint64_t da = smem_desc_sw64(s0 + kOffRope + i * kRopeBytes, 512);
-          const uint64_t db = smem_desc_sw64(q + 4 * kQChunk, 512);
+          const uint64_t da = smem_desc_sw64(s0 + C::off_rope + i * kRopeBytes, 512);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, 1u);
+          for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, dq_rope + 2 * j, idesc, 1u);
           mma_commit(&ms.rempty[i]);
           mma_commit(&ms.s_full[n & 1]);
         }
         ++piece;
-      });
+      }
     }
   } else if (warp == 14) {
     // -------------------------------------------------------- value products
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, 2 * kH, true, true);
+      const uint64_t dp = smem_desc_sw64(s0 + C::off_p, 512);
       bool ok = true;
       int n = 0, piece = 0;
-      for_each_piece(p, ms, range, [&](int, int, int s, int e, int, int) {
-        if (s >= e) return;
+      for (Pieces it(p, ms, range); ok && it.next(p);) {
+        const int s = it.s, e = it.e;
+        if (s >= e) continue;
+#pragma unroll 1
         for (int t = s; t < e; ++t, ++n) {
           ok = ok && wait(&ms.p_ready, n & 1, err, &ms.abort);
           // the previous piece's output has been read
           if (t == s && piece > 0) ok = ok && wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
-          if (!ok) return;
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t db = smem_desc_sw64(s0 + kOffP, 512);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const int i = (4 * n + c) % kSlots;
+            const int i = (4 * n + c) % C::slots;
             // V^T: 128 features of the chunk as rows, 32 keys (4096 bytes) a
             // step.  The scores of this tile are done (P came of them), so
             // the chunk is free after these.
             const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_e4m3(tmem + 64 * c, da + 256 * j, db + 128 * j, idesc, (t > s || j > 0) ? 1u : 0u);
+            for (int term = 0; term < C::terms; ++term) {
+              // e4m3 x e4m3, or e4m3 x e5m2 (format 1) for the second term
+              const uint32_t idesc = idesc_e4m3(128, 64, true, true) | (term == 1 ? 1u << 10 : 0u);
+              const uint64_t db = dp + term * (kTile * 64 >> 4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_e4m3(tmem + 64 * c, da + 256 * j, db + 128 * j, idesc, (t > s || term > 0 || j > 0) ? 1u : 0u);
+            }
             mma_commit(&ms.empty[i]);
           }
           mma_commit(&ms.pv_done);
         }
         ++piece;
-      });
+      }
     }
   } else if (warp < 10) {
-    // ------------------------------------------------------------- softmax
+    // ---------------------------------------------------- queries, softmax
     // A wait that gives up leaves these warps running through their loops
     // (they meet at named barriers); the error word tells.
-    const int quad = warp & 3, tid = threadIdx.x - 64, wg = tid >> 7;
+    constexpr int kMine = C::mine;
+    const int quad = warp & 3, wg = (warp - 2) >> 2, tid = (threadIdx.x - 64) & 127;
     const int hb = wg * kMine;         // this thread's first head
     const int key = quad * 32 + lane;  // of the tile: a TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
-    // offset of the second term's rounding: (j + 1/2) / 32 - 1/2 of a step
-    // 2^-9, j the lane's bits reversed
+    // offset of the second term's rounding: (j + 1/2) / 32 - 1/2, j the
+    // lane's bits reversed, of a step 2^-13 (2^-9 times the gain)
     const float off = ((__brev(lane) >> 27) + 0.5f) * (1.f / 32) - 0.5f;
-    const __half2 dither_h = __float2half2_rn(off * 0.001953125f);
+    const __half2 dither_h = __float2half2_rn(off * (kH == 32 ? kGain : 1.f) * 0.0001220703125f);
     const uint32_t dither = *reinterpret_cast<const uint32_t*>(&dither_h);
     int n = 0, piece = 0;
-    for_each_piece(p, ms, range, [&](int b, int len, int s, int e, int tiles, int part) {
-      float* lse = p.a.lse != nullptr ? p.a.lse + static_cast<int64_t>(b) * p.a.num_heads + h0 : nullptr;
+    for (Pieces it(p, ms, range); it.next(p);) {
+      const int b = it.b, len = it.len, s = it.s, e = it.e;
       if (s >= e) {  // no keys
-        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) +
-                                              (static_cast<int64_t>(b) * p.a.num_heads + h0) * MLA_D_LATENT);
-        for (int i = tid; i < heads * (MLA_D_LATENT / 8); i += kSoftmax) out[i] = make_uint4(0, 0, 0, 0);
-        if (lse != nullptr && tid < heads) lse[tid] = -INFINITY;
-        return;
+        const int64_t row = static_cast<int64_t>(b) * p.a.num_heads + h0;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT);
+        for (int i = threadIdx.x - 64; i < heads * (MLA_D_LATENT / 8); i += kSoftmax) out[i] = make_uint4(0, 0, 0, 0);
+        if (p.a.lse != nullptr)
+          for (int i = threadIdx.x - 64; i < heads; i += kSoftmax) p.a.lse[row + i] = -INFINITY;
+        continue;
       }
-      if (s == 0 && tid == 0 && group == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
-
-      // Page table entries two tiles ahead, block scales one, each loaded an
-      // iteration before it is used.
-      const int n_blocks = (len + kBlock - 1) / kBlock;
-      auto page_at = [&](int t) {
-        const int i = 2 * t + (quad >> 1);
-        return t < e && i < n_blocks ? block_page(p, b, i) : 0;
-      };
-      auto slot_at = [&](int t, int page) {  // -2: no such block; -1: its page is out of range
-        const int i = 2 * t + (quad >> 1);
-        return t < e && i < n_blocks ? block_slot(p, page, i) : -2;
-      };
-      int slot_n = slot_at(s, page_at(s)), page_n = page_at(s + 1);
-      float scale_n = slot_n >= 0 ? p.a.scales[slot_n / kBlock] : 0.f;
-
-      if (tid < kH) ms.m[tid] = 0.f;
-      wait(&ms.q_ready[piece & 1], (piece >> 1) & 1, err, &ms.abort);  // c is there
-      softmax_bar();                                 // and m
-      const float* cs = ms.c[piece & 1] + hb;
-      const float* mr = ms.m + hb;
-      float l[kMine];
-#pragma unroll
-      for (int h = 0; h < kMine; ++h) l[h] = 0.f;
-      bool set = false;  // the references follow some key
-      for (int t = s; t < e; ++t, ++n) {
-        const int slot = slot_n;
-        const bool sb_ok = slot >= 0 && scale_n >= kScaleMin && scale_n <= kScaleMax;
-        const float sb = sb_ok ? scale_n : 1.f, lsb = log2f(sb);
-        if (lane == 0 && (quad & 1) == 0 && wg == 0 && slot != -2 && !sb_ok)
-          flag_error(err, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
-        const bool valid = sb_ok && t * kTile + key < len;
-
-        wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
-        tc_fence_after();
-        float x[kMine], top = -INFINITY;
-        {
-          const uint32_t src = lanes + kColS + (n & 1) * 2 * kH + hb;
-          uint32_t v[16], u[16];
-          tmem_ld16(src, v);
-          tmem_ld16(src + kH, u);
-          tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.s_free[n & 1]);
-#pragma unroll
-          for (int h = 0; h < kMine; h += 4) {
-            const float4 cc = *reinterpret_cast<const float4*>(cs + h), mm = *reinterpret_cast<const float4*>(mr + h);
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float sum = __uint_as_float(v[h + j]) + __uint_as_float(u[h + j]);
-              x[h + j] = valid ? fmaf(sum * sb, cv[j], -mv[j]) : -INFINITY;
-              top = fmaxf(top, x[h + j]);
-            }
-          }
-        }
-        if (softmax_any(top + lsb > kTop || (!set && valid))) {
-          // Raise the references of the heads that need it: each head's
-          // maximum over the warp's keys by exchanging halves (lane i ends
-          // with head hb + i / 2), then over the warps.
-          float v[kMine];
-#pragma unroll
-          for (int h = 0; h < kMine; ++h) v[h] = x[h] + lsb;
-#pragma unroll
-          for (int o = 16; o > 1; o >>= 1) {
-            const bool up = (lane & o) != 0;
-#pragma unroll
-            for (int h = 0; h < kMine / 2; ++h) {
-              if (h < o / 2) {
-                const float give = up ? v[h] : v[h + o / 2], keep = up ? v[h + o / 2] : v[h];
-                v[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
-              }
-            }
-          }
-          v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
-          ms.part[quad][hb + lane / 2] = v[0];
-          softmax_bar();
-          if (tid < kH) {
-            const float mx = fmaxf(fmaxf(ms.part[0][tid], ms.part[1][tid]), fmaxf(ms.part[2][tid], ms.part[3][tid]));
-            const bool raise = isfinite(mx) && (!set || mx > kTop);
-            const float by = raise ? mx - kReset : 0.f;
-            ms.move[tid] = by;
-            ms.factor[tid] = !set ? 0.f : ex2_approx(-by);
-            ms.m[tid] += by;
-            const uint32_t raised = __ballot_sync(0xffffffffu, raise);
-            if (lane == 0) ms.raised = raised;
-          }
-          softmax_bar();
-#pragma unroll
-          for (int h = 0; h < kMine; h += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(&ms.move[hb + h]);
-            const float4 fv = *reinterpret_cast<const float4*>(&ms.factor[hb + h]);
-            x[h] -= mv.x, x[h + 1] -= mv.y, x[h + 2] -= mv.z, x[h + 3] -= mv.w;
-            l[h] *= fv.x, l[h + 1] *= fv.y, l[h + 2] *= fv.z, l[h + 3] *= fv.w;
-          }
-          if (t > s) {
-            // O holds earlier tiles: once their products are done, the
-            // columns of 16 heads at a time, two value chunks per warp
-            wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 64; c += 16) {
-              const int g = c & (kH - 1);
-              if (((ms.raised >> g) & 0xFFFFu) == 0) continue;
-              const uint32_t at = lanes + 128 * wg + c;
-              uint32_t a[16], u[16];
-              tmem_ld16(at, a);
-              tmem_ld16(at + 64, u);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float4 f4 = *reinterpret_cast<const float4*>(&ms.factor[g + i]);
-                const float fv[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  a[i + j] = __float_as_uint(__uint_as_float(a[i + j]) * fv[j]);
-                  u[i + j] = __float_as_uint(__uint_as_float(u[i + j]) * fv[j]);
-                }
-              }
-              tmem_st16(at, a);
-              tmem_st16(at + 64, u);
-            }
-            tmem_st_wait();
-          }
-          set = true;
-        }
-        slot_n = slot_at(t + 1, page_n);
-        scale_n = slot_n >= 0 ? p.a.scales[slot_n / kBlock] : 0.f;
-        page_n = page_at(t + 2);
-        // weights and their two terms; words of four heads
-        uint32_t w1[kMine / 4], w2[kMine / 4];
-#pragma unroll
-        for (int h = 0; h < kMine; h += 4) {
-          uint32_t a[2], r[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float e0 = ex2_approx(x[h + 2 * j]), e1 = ex2_approx(x[h + 2 * j + 1]);
-            l[h + 2 * j] += e0;
-            l[h + 2 * j + 1] += e1;
-            const __half2 ph = __floats2half2_rn(e0 * sb, e1 * sb);
-            const uint32_t pu = *reinterpret_cast<const uint32_t*>(&ph);
-            a[j] = cvt_e4m3x2_h2(pu);
-            r[j] = cvt_e4m3x2_h2(h2_fma(h2_sub(pu, e4m3x2_to_f16x2_pair(a[j])), kGain, dither));
-          }
-          w1[h / 4] = a[0] | (a[1] << 16);
-          w2[h / 4] = r[0] | (r[1] << 16);
-        }
-        // the previous tile's products have read P
-        if (n > 0) wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
-        {
-          // row = key, 64 bytes p1 | p2, 16-byte units swizzled by the row
-          const uint32_t row = s0 + kOffP + key * 64, sw = (key >> 1) & 3;
-          sts128(row + ((wg ^ sw) << 4), make_uint4(w1[0], w1[1], w1[2], w1[3]));
-          sts128(row + (((wg + 2) ^ sw) << 4), make_uint4(w2[0], w2[1], w2[2], w2[3]));
-        }
-        // a row that is no key of the sequence may hold any bytes (NaN too):
-        // as values they are zeros
-        if (!valid && slot >= 0) {
-#pragma unroll 1
-          for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
-            const uint32_t row = slot_addr((4 * n + c) % kSlots) + key * 128;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sts128(row + 16 * i, make_uint4(0, 0, 0, 0));
-          }
-        }
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_ready);
-      }
-
-      // Sums over the keys: halves exchanged as above, then across the warps.
-#pragma unroll
-      for (int o = 16; o > 1; o >>= 1) {
-        const bool up = (lane & o) != 0;
-#pragma unroll
-        for (int h = 0; h < kMine / 2; ++h) {
-          if (h < o / 2) {
-            const float give = up ? l[h] : l[h + o / 2], keep = up ? l[h + o / 2] : l[h];
-            l[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-        }
-      }
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-      ms.part[quad][hb + lane / 2] = l[0];
-      softmax_bar();
-      // the previous piece's output warps have read inv
-      if (piece > 0) wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
-      if (tid < kH) {
-        const float sum = (ms.part[0][tid] + ms.part[1][tid]) + (ms.part[2][tid] + ms.part[3][tid]);
-        ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-        const float l2 = sum != 0.f ? ms.m[tid] + log2f(sum) : -INFINITY;
-        if (e - s < tiles)
-          p.part_lse[((static_cast<int64_t>(range) * p.groups + group) * 2 + part) * kH + tid] = l2;
-        else if (lse != nullptr && tid < heads)
-          lse[tid] = l2 * kLn2;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.sums_ready);
-      softmax_bar();  // part and m are free for the next piece
-      ++piece;
-    });
-  } else {
-    // ----------------------------------------------------- queries, output
-    const int quad = warp & 3;
-    const int row = quad * 32 + lane;  // of a value chunk: a TMEM lane
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
-    int n_last = -1;  // last tile of the pieces so far
-    // A piece's queries are laid out while the piece before it runs, its
-    // output written while the piece after it starts.
-    struct { int b, part, whole, n; } done = {-1, 0, 0, 0};
-    int piece = 0, written = 0;
-    auto output = [&]() {
-      // sums first: then the last tile's products are the next phase of pv_done
-      wait(&ms.sums_ready, written & 1, err, &ms.abort);
-      wait(&ms.pv_done, done.n & 1, err, &ms.abort);
-      tc_fence_after();
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) +
-                           (static_cast<int64_t>(done.b) * p.a.num_heads + h0) * MLA_D_LATENT;
-      float* part_o = p.part_o + ((static_cast<int64_t>(range) * p.groups + group) * 2 + done.part) * kH * MLA_D_LATENT;
-      // thread = feature; neighbouring threads swap halves of two heads so
-      // that each stores two features of one
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int d = 128 * c + row;
-        uint32_t v[32], u[32];
-        tmem_ld32(lanes + 64 * c, v);
-        tmem_ld32(lanes + 64 * c + 32, u);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 iv4 = *reinterpret_cast<const float4*>(&ms.inv[i]);
-          const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[i + j] = __float_as_uint(fmaf(__uint_as_float(u[i + j]), 1.f / kGain, __uint_as_float(v[i + j])) * iv[j]);
-        }
-        if (c == 3) {  // O and inv are free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.o_free);
-        }
-        if (done.whole) {
-          const int odd = lane & 1;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(out + odd * MLA_D_LATENT + (d - odd));
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float mine = __uint_as_float(odd ? v[i + 1] : v[i]);
-            const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 1);
-            const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, mine) : __floats2bfloat162_rn(mine, got);
-            if (i + odd < heads) dst[i * (MLA_D_LATENT / 2)] = *reinterpret_cast<const uint32_t*>(&o);
-          }
-        } else {
-          float* dst = part_o + d;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < heads) dst[i * MLA_D_LATENT] = __uint_as_float(v[i]);
-        }
-      }
-      ++written;
-    };
-    for_each_piece(p, ms, range, [&](int b, int, int s, int e, int tiles, int part) {
-      if (s >= e) return;
-      // Queries: a warp takes every fourth head; lane l features 8 l.., and
-      // 256 + 8 l.., lanes 0..7 the RoPE's; two heads' loads in flight.
-      // Their buffer's last reader, the piece before the last, is written.
+      // Queries (the previous piece's last scores, which this half has read,
+      // were the last to use them): a warp takes every fourth head of its
+      // half; lane l features 8 l.., and 256 + 8 l.., lanes 0..7 the RoPE's.
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) +
                                (static_cast<int64_t>(b) * p.a.num_heads + h0) * kKey;
-      const uint32_t dst = s0 + kOffQ + (piece & 1) * kQBytes;
       auto load_head = [&](int h, uint4(&v)[3]) {
         v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
-        if (h < heads) {
+        if (h < heads && h < hb + kMine) {
           const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
           v[0] = src[lane];
           v[1] = src[lane + 32];
@@ -670,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       uint4 v_next[3], v_after[3];
-      load_head(quad, v_next);
-      load_head(quad + 4, v_after);
+      load_head(hb + quad, v_next);
+      load_head(hb + quad + 4, v_after);
 #pragma unroll 1
-      for (int h = quad; h < kH; h += 4) {
+      for (int h = hb + quad; h < hb + kMine; h += 4) {
         uint4 v[3];
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -698,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ex = max(-60, min(60, ex));
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
         if (lane == 0)
-          ms.c[piece & 1][h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+          ms.c[h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -720,12 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t a1, a2;
           if (k < 2) {
             const int feature = 256 * k + 8 * lane;
-            const uint32_t base = dst + (feature >> 7) * kQChunk;
+            const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
             const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
             a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
             a2 = a1 + kH * 128;
           } else {
-            const uint32_t base = dst + 4 * kQChunk;
+            const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
             const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
             a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
             a2 = a1 + kH * 64;
@@ -738,13 +573,301 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.q_ready[piece & 1]);
+      if (lane == 0) mbar_arrive(&ms.q_ready);
+      const float* cs = ms.c + hb;
+      float* mr = ms.m[piece & 1] + hb;  // the references
+      if (tid < kMine) mr[tid] = 0.f;
+      half_bar(wg);
+
+      float l[kMine];
+#pragma unroll
+      for (int h = 0; h < kMine; ++h) l[h] = 0.f;
+      bool set = false;  // the references follow some key
+#pragma unroll 1
+      for (int t = s; t < e; ++t, ++n) {
+        wait(&ms.info_full[n % C::info], (n / C::info) & 1, err, &ms.abort);
+        const float scale = ms.scale[n % C::info][quad >> 1];
+        const float sb = scale > 0.f ? scale : 1.f, lsb = log2f(sb);
+        const bool valid = scale > 0.f && t * kTile + key < len;
+        const bool full = __all_sync(0xffffffffu, valid);
+
+        wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
+        tc_fence_after();
+        const uint32_t src = lanes + kColS + (n & 1) * 2 * kH + hb;
+        float x[kMine];
+        // A second pass where references were raised.
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < kMine; g += 16) {
+            uint32_t v[16], u[16];
+            tmem_ld16(src + g, v);
+            tmem_ld16(src + kH + g, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const int h = g + i;
+              const float4 cc = *reinterpret_cast<const float4*>(cs + h), mm = *reinterpret_cast<const float4*>(mr + h);
+              const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[h + j] = fmaf((__uint_as_float(v[i + j]) + __uint_as_float(u[i + j])) * sb, cv[j], -mv[j]);
+            }
+          }
+          if (!full) {
+#pragma unroll
+            for (int h = 0; h < kMine; ++h) x[h] = valid ? x[h] : -INFINITY;
+          }
+#pragma unroll
+          for (int h = 0; h < kMine; ++h) top = fmaxf(top, x[h]);
+          if (pass == 1 || !half_any(wg, top + lsb > kTop || (!set && valid))) break;
+
+          // Raise the references of the heads that need it: all at a piece's
+          // first key, then one or two now and then.
+          uint32_t over = 0;
+          if (set) {
+#pragma unroll
+            for (int h = 0; h < kMine; ++h) over |= x[h] + lsb > kTop ? 1u << h : 0u;
+            over = __reduce_or_sync(0xffffffffu, over);
+          } else {
+            over = 0xFFFFFFFFu >> (32 - kMine);
+          }
+          if (lane == 0) ms.over[wg][quad] = over;
+          if (tid < kMine) {
+            ms.factor[hb + tid] = 1.f;
+            ms.top[hb + tid] = ordered(-INFINITY);
+          }
+          half_bar(wg);
+          over = ms.over[wg][0] | ms.over[wg][1] | ms.over[wg][2] | ms.over[wg][3];
+          if (set) {
+            // a head at a time, its scores read again
+#pragma unroll 1
+            for (uint32_t left = over; left != 0; left &= left - 1) {
+              const int h = __ffs(left) - 1;
+              float a, c;
+              tmem_ld1(src + h, a);
+              tmem_ld1(src + kH + h, c);
+              tmem_ld_wait();
+              const int y = valid ? ordered(fmaf((a + c) * sb, cs[h], -mr[h]) + lsb) : ordered(-INFINITY);
+              const int most = __reduce_max_sync(0xffffffffu, y);
+              if (lane == 0) atomicMax(&ms.top[hb + h], most);
+            }
+          } else {
+            // all heads: halves exchanged until lane i holds head i * kMine / 32
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              const bool up = (lane & o) != 0;
+              const int half = kMine * o / 32;
+              if (half == 0) x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
+#pragma unroll
+              for (int h = 0; h < kMine / 2; ++h) {
+                if (h < half) {
+                  const float give = up ? x[h] : x[h + half], keep = up ? x[h + half] : x[h];
+                  x[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                }
+              }
+            }
+            atomicMax(&ms.top[hb + lane * kMine / 32], ordered(x[0] + lsb));
+          }
+          half_bar(wg);
+          if (tid < kMine && ((over >> tid) & 1) != 0) {
+            const float mx = from_ordered(ms.top[hb + tid]);
+            const float by = isfinite(mx) ? mx - kReset : 0.f;
+            mr[tid] += by;
+            ms.factor[hb + tid] = set ? ex2_approx(-by) : 0.f;
+          }
+          // O holds earlier tiles: their products first
+          if (t > s) {
+            wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+            tc_fence_after();
+          }
+          half_bar(wg);
+          if (t > s) {
+#pragma unroll 1
+            for (uint32_t left = over; left != 0; left &= left - 1) {
+              const int h = hb + __ffs(left) - 1;
+              const float f = ms.factor[h];
+              constexpr int kCols = 256 / kH;  // of a head: four chunks, of 32 heads with two terms
+              float o[kCols];
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) tmem_ld1(lanes + kH * i + h, o[i]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) tmem_st1(lanes + kH * i + h, o[i] * f);
+            }
+            tmem_st_wait();
+          }
+#pragma unroll
+          for (int h = 0; h < kMine; h += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(&ms.factor[hb + h]);
+            l[h] *= f4.x, l[h + 1] *= f4.y, l[h + 2] *= f4.z, l[h + 3] *= f4.w;
+          }
+          set = true;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_free[n & 1]);
+        // weights and their two terms; words of four heads
+        uint32_t w1[kMine / 4], w2[kMine / 4];
+#pragma unroll
+        for (int h = 0; h < kMine; h += 4) {
+          uint32_t a[2], r[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float e0 = ex2_approx(x[h + 2 * j]), e1 = ex2_approx(x[h + 2 * j + 1]);
+            l[h + 2 * j] += e0;
+            l[h + 2 * j + 1] += e1;
+            const __half2 ph = __floats2half2_rn(e0 * sb, e1 * sb);
+            const uint32_t pu = *reinterpret_cast<const uint32_t*>(&ph);
+            a[j] = cvt_e4m3x2_h2(pu);
+            const uint32_t rest = h2_sub(pu, e4m3x2_to_f16x2_pair(a[j]));
+            r[j] = kH == 32 ? cvt_e4m3x2_h2(h2_fma(rest, kGain, dither)) : cvt_e5m2x2_h2(h2_fma(rest, 1.f, dither));
+          }
+          w1[h / 4] = a[0] | (a[1] << 16);
+          w2[h / 4] = r[0] | (r[1] << 16);
+        }
+        // the previous tile's products have read P
+        if (n > 0) wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
+        {
+          // row = key, 64 bytes: heads of one term, or p1 | p2; 16-byte units
+          // swizzled by the row
+          const uint32_t row = s0 + C::off_p + key * 64, sw = (key >> 1) & 3;
+          if constexpr (kH == 64) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t at = row + (((2 * wg + c) ^ sw) << 4);
+              sts128(at, make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]));
+              sts128(at + kTile * 64, make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]));
+            }
+          } else {
+            sts128(row + ((wg ^ sw) << 4), make_uint4(w1[0], w1[1], w1[2], w1[3]));
+            sts128(row + (((wg + 2) ^ sw) << 4), make_uint4(w2[0], w2[1], w2[2], w2[3]));
+          }
+        }
+        // a row that is no key of the sequence may hold any bytes (NaN too):
+        // as values they are zeros
+        if (!valid) {
+#pragma unroll 1
+          for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
+            const uint32_t row = slot_addr((4 * n + c) % C::slots) + key * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts128(row + 16 * ((i + lane) & 7), make_uint4(0, 0, 0, 0));  // all banks
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_ready);
+      }
+
+      // The weights' sums over this warp's keys, exchanged as above, for the
+      // output warps (done with the previous piece's).
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+        const int half = kMine * o / 32;
+        if (half == 0) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+#pragma unroll
+        for (int h = 0; h < kMine / 2; ++h) {
+          if (h < half) {
+            const float give = up ? l[h] : l[h + half], keep = up ? l[h + half] : l[h];
+            l[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        }
+      }
+      if (piece > 0) wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
+      ms.sums[quad][hb + lane * kMine / 32] = l[0];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.sums_ready);
+      half_bar(wg);  // c is free for the next piece
       ++piece;
-      if (done.b >= 0) output();
-      n_last += e - s;
-      done = {b, part, e - s == tiles, n_last};
-    });
-    if (done.b >= 0) output();
+    }
+  } else {
+    // --------------------------------------------------------------- output
+    const int quad = warp & 3, tid = (threadIdx.x - 64) & 127;
+    const int row = quad * 32 + lane;  // of a value chunk: a TMEM lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    int piece = 0, n_last = -1;  // the piece's last tile
+    for (Pieces it(p, ms, range); it.next(p);) {
+      if (it.s >= it.e) continue;
+      const int b = it.b;
+      const bool whole = it.e - it.s == it.n;
+      const int64_t out_row = static_cast<int64_t>(b) * p.a.num_heads + h0;
+      const int64_t part_row = ((static_cast<int64_t>(range) * p.groups + group) * 2 + it.part) * kH;
+      n_last += it.e - it.s;
+      // the next sequence's queries, into L2 meanwhile
+      if (b + 1 < p.a.batch) {
+        const char* q = static_cast<const char*>(p.a.q) + (out_row + p.a.num_heads) * (kKey * 2);
+        for (int i = tid; i < heads * (kKey * 2 / 128); i += kOutput)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128 * i));
+      }
+      // sums first: then the last tile's products are the next phase of pv_done
+      wait(&ms.sums_ready, piece & 1, err, &ms.abort);
+      if (tid < kH) {
+        const float sum = (ms.sums[0][tid] + ms.sums[1][tid]) + (ms.sums[2][tid] + ms.sums[3][tid]);
+        ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+        const float l2 = sum != 0.f ? ms.m[piece & 1][tid] + log2f(sum) : -INFINITY;
+        if (!whole)
+          p.part_lse[part_row + tid] = l2;
+        else if (p.a.lse != nullptr && tid < heads)
+          p.a.lse[out_row + tid] = l2 * kLn2;
+      }
+      asm volatile("bar.sync 5, %0;" ::"n"(kOutput) : "memory");
+      wait(&ms.pv_done, n_last & 1, err, &ms.abort);
+      tc_fence_after();
+      // thread = feature; neighbouring threads swap halves of two heads so
+      // that each stores two features of one
+#pragma unroll 1
+      for (int i = 0; i < 4 * C::terms; ++i) {
+        const int c = i / C::terms, g = 32 * (i % C::terms);  // value chunk, first head
+        const int d = 128 * c + row;
+        uint32_t v[32];
+        tmem_ld32(lanes + 64 * c + g, v);
+        if constexpr (kH == 32) {  // p1's and p2's products
+          uint32_t u[32];
+          tmem_ld32(lanes + 64 * c + 32, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            v[h] = __float_as_uint(fmaf(__uint_as_float(u[h]), 1.f / kGain, __uint_as_float(v[h])));
+        } else {
+          tmem_ld_wait();
+        }
+        if (i == 4 * C::terms - 1) {  // O is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.o_free);
+        }
+#pragma unroll
+        for (int h = 0; h < 32; h += 4) {
+          const float4 iv = *reinterpret_cast<const float4*>(&ms.inv[g + h]);
+          v[h] = __float_as_uint(__uint_as_float(v[h]) * iv.x);
+          v[h + 1] = __float_as_uint(__uint_as_float(v[h + 1]) * iv.y);
+          v[h + 2] = __float_as_uint(__uint_as_float(v[h + 2]) * iv.z);
+          v[h + 3] = __float_as_uint(__uint_as_float(v[h + 3]) * iv.w);
+        }
+        if (whole) {
+          const int odd = lane & 1;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) +
+                                                      (out_row + g + odd) * MLA_D_LATENT + (d - odd));
+#pragma unroll
+          for (int h = 0; h < 32; h += 2) {
+            const float mine = __uint_as_float(odd ? v[h + 1] : v[h]);
+            const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[h] : v[h + 1]), 1);
+            const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, mine) : __floats2bfloat162_rn(mine, got);
+            if (g + h + odd < heads) dst[h * (MLA_D_LATENT / 2)] = *reinterpret_cast<const uint32_t*>(&o);
+          }
+        } else {
+          float* dst = p.part_o + (part_row + g) * MLA_D_LATENT + d;
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            if (g + h < heads) dst[h * MLA_D_LATENT] = __uint_as_float(v[h]);
+        }
+      }
+      asm volatile("bar.sync 5, %0;" ::"n"(kOutput) : "memory");  // inv is free for the next piece
+      ++piece;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -755,6 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merge of the pieces of cut sequences, in range order, by LSE; sequences
 // without keys get their zeros here.  CTA = (sequence, head), thread = four
 // features.
+template <int kH>
 __global__ void __launch_bounds__(128) fp8_decode_merge_kernel(const Params p) {
   const int b = blockIdx.x / p.a.num_heads, h = blockIdx.x % p.a.num_heads, tid = threadIdx.x;
   const int64_t off = p.offsets[b], end = p.offsets[b + 1], per = p.offsets[p.a.batch + 1];
@@ -793,20 +917,34 @@ __global__ void __launch_bounds__(128) fp8_decode_merge_kernel(const Params p) {
   if (p.a.lse != nullptr && tid == 0) p.a.lse[row] = sum != 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
+int heads_per_cta(int num_heads) { return num_heads <= 32 ? 32 : 64; }
+
 struct Layout {
   int ranges, groups;
   size_t lse, o, total;
 };
 Layout layout(int batch, int num_heads, int num_sms) {
+  const int kh = heads_per_cta(num_heads);
   Layout l;
-  l.groups = (num_heads + kH - 1) / kH;
+  l.groups = (num_heads + kh - 1) / kh;
   l.ranges = num_sms / l.groups > 1 ? num_sms / l.groups : 1;
-  const size_t rows = static_cast<size_t>(l.ranges) * l.groups * 2 * kH;
+  const size_t rows = static_cast<size_t>(l.ranges) * l.groups * 2 * kh;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   l.lse = up((static_cast<size_t>(batch) + 2) * sizeof(int64_t));
   l.o = up(l.lse + rows * sizeof(float));
   l.total = l.o + rows * MLA_D_LATENT * sizeof(float);
   return l;
+}
+
+template <int kH>
+int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int slot, cudaStream_t stream) {
+  constexpr int bytes = static_cast<int>(smem_bytes<kH>());
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_decode_kernel<kH>), bytes, slot)) return st;
+  fp8_decode_kernel<kH><<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
+  if (const int st = launch_status()) return st;
+  if (!p.split) return MLA_OK;
+  fp8_decode_merge_kernel<kH><<<static_cast<unsigned>(p.a.num_heads) * p.a.batch, 128, 0, stream>>>(p);
+  return launch_status();
 }
 
 }  // namespace
@@ -830,13 +968,7 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
     set_last_error("cuTensorMapEncodeTiled failed for the cache");
     return MLA_ERR_LAUNCH;
   }
-  if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_decode_kernel), static_cast<int>(kSmemBytes), 19))
-    return st;
-  fp8_decode_kernel<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, kSmemBytes, stream>>>(lat, rope, p);
-  if (const int st = launch_status()) return st;
-  if (!p.split) return MLA_OK;
-  fp8_decode_merge_kernel<<<static_cast<unsigned>(a.num_heads) * a.batch, 128, 0, stream>>>(p);
-  return launch_status();
+  return heads_per_cta(a.num_heads) == 64 ? launch<64>(p, lat, rope, 19, stream) : launch<32>(p, lat, rope, 20, stream);
 }
 
 }  // namespace mla
