@@ -40,7 +40,8 @@
 //                neither's waits leave the tensor cores without work);
 //   warps 2..9   queries to two terms, softmax (thread = key; warps 2..5 the
 //                first half of the heads, 6..9 the second);
-//   warps 10..13 a piece's output, while the next one starts.
+//   warps 10..13 rescale O where references were raised, while the softmax
+//                goes on; a piece's output, while the next one starts.
 // The code of each role is kept short (rolled loops, one copy): unrolled
 // further, the warps waited for instructions more than for anything else.
 #include <cuda.h>
@@ -87,11 +88,13 @@ template <int kH>
 struct Misc {
   using C = Cfg<kH>;
   uint64_t full[C::slots], empty[C::slots], rfull[C::ropes], rempty[C::ropes], info_full[C::info];
-  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready, sums_ready, o_free;
-  alignas(16) float c[kH], m[2][kH];  // m by the piece's parity
-  alignas(16) float factor[kH], inv[kH], sums[4][kH];
-  int top[kH];  // a head's maximum, as an integer that orders like it
-  alignas(16) uint32_t over[2][4];
+  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready, sums_ready, o_free, moved[2], rescaled[2];
+  alignas(16) float c[kH], m[kH];
+  alignas(16) float move[2][kH];  // what a tile raises the references by, in turn
+  alignas(16) float inv[kH];      // a piece's references, then 1 / its sums
+  alignas(16) float sums[4][kH];
+  int top[kH];            // a head's maximum, as an integer that orders like it
+  uint32_t raised[2][2];  // heads (of either half) whose part of O is to be rescaled
   float scale[C::info][2];  // of a tile's two blocks; 0: the block is no part of the sequence
   int64_t t0, t1, off0;
   int b0;
@@ -111,7 +114,7 @@ struct Params {
   int page_shift;
   int ranges, groups;  // ranges of tiles; head groups (grid = ranges * groups)
   bool split;
-  int64_t* offsets;  // [batch + 1] first tile of each sequence, then tiles per range
+  int2* cuts;      // [batch]: a sequence's first range, and its pieces | (1 << 30 where the first is part 1)
   float* part_lse;   // log2 units, [range][group][2][kH]
   float* part_o;     // the same rows of 512
 };
@@ -258,16 +261,15 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
     const int n = tiles_of(clipped_len(p.a, b));
-    if (publish) p.offsets[b] = off;
+    if (publish) {
+      const int r0 = n > 0 ? static_cast<int>(off / per) : 0, r1 = n > 0 ? static_cast<int>((off + n - 1) / per) : -1;
+      p.cuts[b] = make_int2(r0, (r1 - r0 + 1) | (r0 * per < off ? 1 << 30 : 0));
+    }
     if (t0 >= off && t0 < off + n) {
       ms.b0 = b;
       ms.off0 = off;
     }
     off += n;
-  }
-  if (publish && tid == 0) {
-    p.offsets[B] = total;
-    p.offsets[B + 1] = per;
   }
 }
 
@@ -308,6 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms.q_ready, kSoftmax / 32);
     mbar_init(&ms.sums_ready, kSoftmax / 32);
     mbar_init(&ms.o_free, kOutput / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.moved[i], kSoftmax / 32);
+      mbar_init(&ms.rescaled[i], kOutput / 32);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -431,15 +437,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint64_t dp = smem_desc_sw64(s0 + C::off_p, 512);
       bool ok = true;
-      int n = 0, piece = 0;
+      int n = 0, piece = 0, k = 0;  // tiles, pieces, tiles that are no piece's first
       for (Pieces it(p, ms, range); ok && it.next(p);) {
         const int s = it.s, e = it.e;
         if (s >= e) continue;
 #pragma unroll 1
         for (int t = s; t < e; ++t, ++n) {
           ok = ok && wait(&ms.p_ready, n & 1, err, &ms.abort);
-          // the previous piece's output has been read
-          if (t == s && piece > 0) ok = ok && wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
+          // O as it is to be added to: the previous piece's read, this one's
+          // rescaled
+          if (t > s) {
+            ok = ok && wait(&ms.rescaled[k & 1], (k >> 1) & 1, err, &ms.abort);
+            ++k;
+          } else if (piece > 0) {
+            ok = ok && wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
+          }
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float off = ((__brev(lane) >> 27) + 0.5f) * (1.f / 32) - 0.5f;
     const __half2 dither_h = __float2half2_rn(off * (kH == 32 ? kGain : 1.f) * 0.0001220703125f);
     const uint32_t dither = *reinterpret_cast<const uint32_t*>(&dither_h);
-    int n = 0, piece = 0;
+    int n = 0, piece = 0, k = 0;
     for (Pieces it(p, ms, range); it.next(p);) {
       const int b = it.b, len = it.len, s = it.s, e = it.e;
       if (s >= e) {  // no keys
@@ -575,8 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.q_ready);
       const float* cs = ms.c + hb;
-      float* mr = ms.m[piece & 1] + hb;  // the references
-      if (tid < kMine) mr[tid] = 0.f;
+      float* mr = ms.m + hb;  // the references
+      if (tid < kMine) {
+        mr[tid] = 0.f;
+        ms.top[hb + tid] = ordered(-INFINITY);
+      }
       half_bar(wg);
 
       float l[kMine];
@@ -594,120 +609,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
         tc_fence_after();
         const uint32_t src = lanes + kColS + (n & 1) * 2 * kH + hb;
-        float x[kMine];
-        // A second pass where references were raised.
-#pragma unroll 1
-        for (int pass = 0;; ++pass) {
-          float top = -INFINITY;
+        float x[kMine], top = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < kMine; g += 16) {
-            uint32_t v[16], u[16];
-            tmem_ld16(src + g, v);
-            tmem_ld16(src + kH + g, u);
-            tmem_ld_wait();
+        for (int g = 0; g < kMine; g += 16) {
+          uint32_t v[16], u[16];
+          tmem_ld16(src + g, v);
+          tmem_ld16(src + kH + g, u);
+          tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const int h = g + i;
-              const float4 cc = *reinterpret_cast<const float4*>(cs + h), mm = *reinterpret_cast<const float4*>(mr + h);
-              const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
+          for (int i = 0; i < 16; i += 4) {
+            const int h = g + i;
+            const float4 cc = *reinterpret_cast<const float4*>(cs + h), mm = *reinterpret_cast<const float4*>(mr + h);
+            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                x[h + j] = fmaf((__uint_as_float(v[i + j]) + __uint_as_float(u[i + j])) * sb, cv[j], -mv[j]);
-            }
+            for (int j = 0; j < 4; ++j)
+              x[h + j] = fmaf((__uint_as_float(v[i + j]) + __uint_as_float(u[i + j])) * sb, cv[j], -mv[j]);
           }
-          if (!full) {
-#pragma unroll
-            for (int h = 0; h < kMine; ++h) x[h] = valid ? x[h] : -INFINITY;
-          }
-#pragma unroll
-          for (int h = 0; h < kMine; ++h) top = fmaxf(top, x[h]);
-          if (pass == 1 || !half_any(wg, top + lsb > kTop || (!set && valid))) break;
-
-          // Raise the references of the heads that need it: all at a piece's
-          // first key, then one or two now and then.
-          uint32_t over = 0;
-          if (set) {
-#pragma unroll
-            for (int h = 0; h < kMine; ++h) over |= x[h] + lsb > kTop ? 1u << h : 0u;
-            over = __reduce_or_sync(0xffffffffu, over);
-          } else {
-            over = 0xFFFFFFFFu >> (32 - kMine);
-          }
-          if (lane == 0) ms.over[wg][quad] = over;
-          if (tid < kMine) {
-            ms.factor[hb + tid] = 1.f;
-            ms.top[hb + tid] = ordered(-INFINITY);
-          }
-          half_bar(wg);
-          over = ms.over[wg][0] | ms.over[wg][1] | ms.over[wg][2] | ms.over[wg][3];
-          if (set) {
-            // a head at a time, its scores read again
-#pragma unroll 1
-            for (uint32_t left = over; left != 0; left &= left - 1) {
-              const int h = __ffs(left) - 1;
-              float a, c;
-              tmem_ld1(src + h, a);
-              tmem_ld1(src + kH + h, c);
-              tmem_ld_wait();
-              const int y = valid ? ordered(fmaf((a + c) * sb, cs[h], -mr[h]) + lsb) : ordered(-INFINITY);
-              const int most = __reduce_max_sync(0xffffffffu, y);
-              if (lane == 0) atomicMax(&ms.top[hb + h], most);
-            }
-          } else {
-            // all heads: halves exchanged until lane i holds head i * kMine / 32
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const bool up = (lane & o) != 0;
-              const int half = kMine * o / 32;
-              if (half == 0) x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
-#pragma unroll
-              for (int h = 0; h < kMine / 2; ++h) {
-                if (h < half) {
-                  const float give = up ? x[h] : x[h + half], keep = up ? x[h + half] : x[h];
-                  x[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
-                }
-              }
-            }
-            atomicMax(&ms.top[hb + lane * kMine / 32], ordered(x[0] + lsb));
-          }
-          half_bar(wg);
-          if (tid < kMine && ((over >> tid) & 1) != 0) {
-            const float mx = from_ordered(ms.top[hb + tid]);
-            const float by = isfinite(mx) ? mx - kReset : 0.f;
-            mr[tid] += by;
-            ms.factor[hb + tid] = set ? ex2_approx(-by) : 0.f;
-          }
-          // O holds earlier tiles: their products first
-          if (t > s) {
-            wait(&ms.pv_done, (n - 1) & 1, err, &ms.abort);
-            tc_fence_after();
-          }
-          half_bar(wg);
-          if (t > s) {
-#pragma unroll 1
-            for (uint32_t left = over; left != 0; left &= left - 1) {
-              const int h = hb + __ffs(left) - 1;
-              const float f = ms.factor[h];
-              constexpr int kCols = 256 / kH;  // of a head: four chunks, of 32 heads with two terms
-              float o[kCols];
-#pragma unroll
-              for (int i = 0; i < kCols; ++i) tmem_ld1(lanes + kH * i + h, o[i]);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < kCols; ++i) tmem_st1(lanes + kH * i + h, o[i] * f);
-            }
-            tmem_st_wait();
-          }
-#pragma unroll
-          for (int h = 0; h < kMine; h += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(&ms.factor[hb + h]);
-            l[h] *= f4.x, l[h + 1] *= f4.y, l[h + 2] *= f4.z, l[h + 3] *= f4.w;
-          }
-          set = true;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.s_free[n & 1]);
+        if (!full) {
+#pragma unroll
+          for (int h = 0; h < kMine; ++h) x[h] = valid ? x[h] : -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < kMine; ++h) top = fmaxf(top, x[h]);
+        if (half_any(wg, top + lsb > kTop || (!set && valid))) {
+          // Raise the references of the heads that need it.  A head's
+          // maximum: halves exchanged until lane i holds head
+          // i * kMine / 32 of the warp's keys, then over the warps.
+          float f[kMine / 2];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const bool up = (lane & o) != 0;
+            const int half = kMine * o / 32;
+            if (half == 0) f[0] = fmaxf(f[0], __shfl_xor_sync(0xffffffffu, f[0], o));
+#pragma unroll
+            for (int h = 0; h < kMine / 2; ++h) {
+              if (h < half) {
+                const float lo = o == 16 ? x[h] : f[h], hi = o == 16 ? x[h + half] : f[(h + half) % (kMine / 2)];
+                f[h] = fmaxf(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, o));
+              }
+            }
+          }
+          atomicMax(&ms.top[hb + lane * kMine / 32], ordered(f[0] + lsb));
+          half_bar(wg);
+          if (tid < 32) {
+            bool raise = false;
+            if (tid < kMine) {
+              const float mx = from_ordered(ms.top[hb + tid]);
+              raise = isfinite(mx) && (!set || mx > kTop);
+              const float by = raise ? mx - kReset : 0.f;
+              ms.move[k & 1][hb + tid] = by;
+              mr[tid] += by;
+              ms.top[hb + tid] = ordered(-INFINITY);
+            }
+            // without earlier keys O is zero (or yet to be written)
+            const uint32_t raised = __ballot_sync(0xffffffffu, raise && set);
+            if (lane == 0) ms.raised[k & 1][wg] = raised;
+          }
+          half_bar(wg);
+#pragma unroll
+          for (int h = 0; h < kMine; h += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(&ms.move[k & 1][hb + h]);
+            const float by[4] = {mv.x, mv.y, mv.z, mv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[h + j] -= by[j];
+              l[h + j] = set ? l[h + j] * ex2_approx(-by[j]) : 0.f;
+            }
+          }
+          set = true;
+        } else if (tid == 0) {
+          ms.raised[k & 1][wg] = 0;
+        }
+        if (t > s) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.moved[k & 1]);
+          ++k;
+        }
         // weights and their two terms; words of four heads
         uint32_t w1[kMine / 4], w2[kMine / 4];
 #pragma unroll
@@ -778,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (piece > 0) wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
       ms.sums[quad][hb + lane * kMine / 32] = l[0];
+      if (tid < kMine) ms.inv[hb + tid] = mr[tid];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.sums_ready);
       half_bar(wg);  // c is free for the next piece
@@ -788,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, tid = (threadIdx.x - 64) & 127;
     const int row = quad * 32 + lane;  // of a value chunk: a TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    int piece = 0, n_last = -1;  // the piece's last tile
+    int piece = 0, n_last = -1, k = 0;  // the piece's last tile; tiles that are no piece's first
     for (Pieces it(p, ms, range); it.next(p);) {
       if (it.s >= it.e) continue;
       const int b = it.b;
@@ -802,12 +784,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = tid; i < heads * (kKey * 2 / 128); i += kOutput)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128 * i));
       }
+      // Rescaling: a head's columns of the value chunks (kH 32: of both terms)
+      // times 2^-move, once the tile before is in.
+#pragma unroll 1
+      for (int n = n_last - (it.e - it.s) + 1; n < n_last; ++n, ++k) {
+        wait(&ms.moved[k & 1], (k >> 1) & 1, err, &ms.abort);
+        uint64_t raised = ms.raised[k & 1][0] | static_cast<uint64_t>(ms.raised[k & 1][1]) << (kH / 2);
+        if (raised != 0) {
+          wait(&ms.pv_done, n & 1, err, &ms.abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (; raised != 0; raised &= raised - 1) {
+            const int h = __ffsll(static_cast<long long>(raised)) - 1;
+            const float f = ex2_approx(-ms.move[k & 1][h]);
+            constexpr int kCols = 256 / kH;
+            float o[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) tmem_ld1(lanes + kH * i + h, o[i]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) tmem_st1(lanes + kH * i + h, o[i] * f);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.rescaled[k & 1]);
+      }
       // sums first: then the last tile's products are the next phase of pv_done
       wait(&ms.sums_ready, piece & 1, err, &ms.abort);
       if (tid < kH) {
+        const float m = ms.inv[tid];
         const float sum = (ms.sums[0][tid] + ms.sums[1][tid]) + (ms.sums[2][tid] + ms.sums[3][tid]);
         ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-        const float l2 = sum != 0.f ? ms.m[piece & 1][tid] + log2f(sum) : -INFINITY;
+        const float l2 = sum != 0.f ? m + log2f(sum) : -INFINITY;
         if (!whole)
           p.part_lse[part_row + tid] = l2;
         else if (p.a.lse != nullptr && tid < heads)
@@ -834,11 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           tmem_ld_wait();
         }
-        if (i == 4 * C::terms - 1) {  // O is free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.o_free);
-        }
 #pragma unroll
         for (int h = 0; h < 32; h += 4) {
           const float4 iv = *reinterpret_cast<const float4*>(&ms.inv[g + h]);
@@ -846,6 +851,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[h + 1] = __float_as_uint(__uint_as_float(v[h + 1]) * iv.y);
           v[h + 2] = __float_as_uint(__uint_as_float(v[h + 2]) * iv.z);
           v[h + 3] = __float_as_uint(__uint_as_float(v[h + 3]) * iv.w);
+        }
+        if (i == 4 * C::terms - 1) {  // O and inv are free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.o_free);
         }
         if (whole) {
           const int odd = lane & 1;
@@ -865,7 +875,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g + h < heads) dst[h * MLA_D_LATENT] = __uint_as_float(v[h]);
         }
       }
-      asm volatile("bar.sync 5, %0;" ::"n"(kOutput) : "memory");  // inv is free for the next piece
       ++piece;
     }
   }
@@ -876,45 +885,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of the pieces of cut sequences, in range order, by LSE; sequences
-// without keys get their zeros here.  CTA = (sequence, head), thread = four
-// features.
+// without keys get their zeros here.  Warp = half the features of one
+// (sequence, head), 8 a lane.
 template <int kH>
-__global__ void __launch_bounds__(128) fp8_decode_merge_kernel(const Params p) {
-  const int b = blockIdx.x / p.a.num_heads, h = blockIdx.x % p.a.num_heads, tid = threadIdx.x;
-  const int64_t off = p.offsets[b], end = p.offsets[b + 1], per = p.offsets[p.a.batch + 1];
-  const int64_t row = static_cast<int64_t>(b) * p.a.num_heads + h;
-  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT) + tid;
-  if (off == end) {
-    *out = make_uint2(0, 0);
-    if (p.a.lse != nullptr && tid == 0) p.a.lse[row] = -INFINITY;
-    return;
-  }
-  const int64_t r0 = off / per, r1 = (end - 1) / per;
-  if (r0 == r1) return;  // one piece: written already
-  const int g = h / kH;
-  auto piece = [&](int64_t r) {  // its row of partial results
-    const int part = r == r0 && r * per < off ? 1 : 0;
-    return ((r * p.groups + g) * 2 + part) * kH + h % kH;
-  };
+__global__ void __launch_bounds__(256) fp8_decode_merge_kernel(const Params p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  const int64_t row = id >> 1;
+  if (row >= static_cast<int64_t>(p.a.batch) * p.a.num_heads) return;
+  const int b = static_cast<int>(row / p.a.num_heads), h = static_cast<int>(row - static_cast<int64_t>(b) * p.a.num_heads);
+  const int half = static_cast<int>(id & 1);
+  const int2 cut = p.cuts[b];
+  const int n = cut.y & ~(1 << 30), first = cut.y >> 30;  // pieces; part of the first
+  if (n == 1) return;                                     // written already
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT + 256 * half + 4 * lane;
+  // lane i: LSE of piece i, i + 32, ...
+  const int64_t stride = static_cast<int64_t>(p.groups) * 2 * kH;  // rows of partial results a range
+  const int64_t row0 = cut.x * stride + (h / kH) * 2 * kH + h % kH;
+  auto lse_of = [&](int i) { return i < n ? p.part_lse[row0 + i * stride + (i == 0 ? first * kH : 0)] : -INFINITY; };
   float m = -INFINITY;
-  for (int64_t r = r0; r <= r1; ++r) m = fmaxf(m, p.part_lse[piece(r)]);
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, lse_of(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f, o[4] = {};
-  for (int64_t r = r0; r <= r1; ++r) {
-    const int64_t i = piece(r);
-    const float w = ex2_approx(p.part_lse[i] - ref);
-    sum += w;
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + i * MLA_D_LATENT)[tid];
-    o[0] = fmaf(w, v.x, o[0]);
-    o[1] = fmaf(w, v.y, o[1]);
-    o[2] = fmaf(w, v.z, o[2]);
-    o[3] = fmaf(w, v.w, o[3]);
+  float sum = 0.f, acc[8] = {};
+  for (int base = 0; base < n; base += 32) {
+    const float w_mine = ex2_approx(lse_of(base + lane) - ref);
+    const int count = min(32, n - base);
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+      const float w = __shfl_sync(0xffffffffu, w_mine, j);
+      const int i = base + j;
+      const float4* o = reinterpret_cast<const float4*>(
+          p.part_o + (row0 + i * stride + (i == 0 ? first * kH : 0)) * MLA_D_LATENT + 256 * half + 4 * lane);
+      const float4 u = o[0], v = o[32];
+      sum += w;
+      acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]);
+      acc[2] = fmaf(w, u.z, acc[2]), acc[3] = fmaf(w, u.w, acc[3]);
+      acc[4] = fmaf(w, v.x, acc[4]), acc[5] = fmaf(w, v.y, acc[5]);
+      acc[6] = fmaf(w, v.z, acc[6]), acc[7] = fmaf(w, v.w, acc[7]);
+    }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-  *out = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (p.a.lse != nullptr && tid == 0) p.a.lse[row] = sum != 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[4 * k] * inv, acc[4 * k + 1] * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv);
+    *reinterpret_cast<uint2*>(out + 128 * k) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+  if (p.a.lse != nullptr && half == 0 && lane == 0) p.a.lse[row] = sum != 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int heads_per_cta(int num_heads) { return num_heads <= 32 ? 32 : 64; }
@@ -930,7 +950,7 @@ Layout layout(int batch, int num_heads, int num_sms) {
   l.ranges = num_sms / l.groups > 1 ? num_sms / l.groups : 1;
   const size_t rows = static_cast<size_t>(l.ranges) * l.groups * 2 * kh;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  l.lse = up((static_cast<size_t>(batch) + 2) * sizeof(int64_t));
+  l.lse = up(static_cast<size_t>(batch) * sizeof(int2));
   l.o = up(l.lse + rows * sizeof(float));
   l.total = l.o + rows * MLA_D_LATENT * sizeof(float);
   return l;
@@ -943,7 +963,8 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   fp8_decode_kernel<kH><<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
   if (const int st = launch_status()) return st;
   if (!p.split) return MLA_OK;
-  fp8_decode_merge_kernel<kH><<<static_cast<unsigned>(p.a.num_heads) * p.a.batch, 128, 0, stream>>>(p);
+  const int64_t warps = 2 * static_cast<int64_t>(p.a.num_heads) * p.a.batch;
+  fp8_decode_merge_kernel<kH><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(p);
   return launch_status();
 }
 
@@ -959,7 +980,7 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
   uint32_t magic;
   int shift;
   magic_divisor(a.page_size / kBlock, &magic, &shift);
-  Params p{a, magic, shift, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + l.lse),
+  Params p{a, magic, shift, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),
            reinterpret_cast<float*>(ws + l.o)};
   if (static_cast<int64_t>(a.batch) * a.num_heads > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   CUtensorMap lat, rope;
