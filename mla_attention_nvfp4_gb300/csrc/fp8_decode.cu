@@ -66,6 +66,7 @@ constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 4
 constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest weight at 2^4
 constexpr float kGain = 16.f;   // 32 heads: the first term's rounding error, at most 16, becomes 256
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0..255 (64 per value chunk), then two S^T of 2 kH (q1 | q2)
 
@@ -228,44 +229,59 @@ __device__ __forceinline__ bool half_any(int wg, bool v) {
 }
 
 // The plan: this CTA's range of the batch's tiles, and its first sequence.
-// scan: kThreads / 32 words of shared memory.
+// scan: two words of shared memory a warp.
 template <class M>
 __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan, int range, bool publish) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
   const int per_thread = (B + kThreads - 1) / kThreads;
   const int first = tid * per_thread, last = min(first + per_thread, B);
   int64_t sum = 0;
+  int most = 0;
 #pragma unroll 1
-  for (int b = first; b < last; ++b) sum += tiles_of(clipped_len(p.a, b));
+  for (int b = first; b < last; ++b) {
+    const int n = tiles_of(clipped_len(p.a, b));
+    sum += n;
+    most = max(most, n);
+  }
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) scan[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    scan[2 * warp] = incl;
+    scan[2 * warp + 1] = most;
+  }
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+    if (w < warp) before += scan[2 * w];
+    total += scan[2 * w];
+    most = max(most, static_cast<int>(scan[2 * w + 1]));
   }
   const int64_t per = (total + p.ranges - 1) / p.ranges;
-  const int64_t t0 = range * per, t1 = t0 + per < total ? t0 + per : total;
+  // A CTA each for whole sequences, where that takes no longer than equal
+  // ranges: those begin two pieces (of one sequence's end and the next one's
+  // start), and the cut ones are merged.
+  const bool uncut = B <= p.ranges && most + kPiece <= per + 2 * kPiece + kMerge;
+  const int64_t t0 = uncut ? 0 : range * per;
   int64_t off = before + incl - sum;
   if (tid == 0) {
     ms.t0 = t0;
-    ms.t1 = t1;
+    ms.t1 = uncut ? (range < B ? tiles_of(clipped_len(p.a, range)) : 0) : t0 + per < total ? t0 + per : total;
+    if (uncut) ms.b0 = range;
   }
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
     const int n = tiles_of(clipped_len(p.a, b));
     if (publish) {
       const int r0 = n > 0 ? static_cast<int>(off / per) : 0, r1 = n > 0 ? static_cast<int>((off + n - 1) / per) : -1;
-      p.cuts[b] = make_int2(r0, (r1 - r0 + 1) | (r0 * per < off ? 1 << 30 : 0));
+      p.cuts[b] = uncut ? make_int2(b, n > 0 ? 1 : 0) : make_int2(r0, (r1 - r0 + 1) | (r0 * per < off ? 1 << 30 : 0));
     }
-    if (t0 >= off && t0 < off + n) {
+    if (!uncut && t0 >= off && t0 < off + n) {
       ms.b0 = b;
       ms.off0 = off;
     }
@@ -549,19 +565,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          uint32_t w1[2], w2[2];
+          // in f16 pairs: 8 significant bits down to 2^-17, then steps of 2^-24
+          uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float x0, x1, x2, x3;
-            bf16x2_to_f32(w[2 * j], x0, x1);
-            bf16x2_to_f32(w[2 * j + 1], x2, x3);
-            x0 *= inv, x1 *= inv, x2 *= inv, x3 *= inv;
-            const uint32_t a = cvt_e4m3x2(x0, x1), c = cvt_e4m3x2(x2, x3);
-            const uint32_t ha = e4m3x2_to_f16x2_pair(a), hc = e4m3x2_to_f16x2_pair(c);
-            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-            const float2 fc = __half22float2(*reinterpret_cast<const __half2*>(&hc));
-            w1[j] = a | (c << 16);
-            w2[j] = cvt_e4m3x2(x0 - fa.x, x1 - fa.y) | (cvt_e4m3x2(x2 - fc.x, x3 - fc.y) << 16);
+          for (int j = 0; j < 4; ++j) {
+            float x0, x1;
+            bf16x2_to_f32(w[j], x0, x1);
+            const __half2 xh = __floats2half2_rn(x0 * inv, x1 * inv);
+            const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
+            const uint32_t a = cvt_e4m3x2_h2(xu);
+            w1[j >> 1] |= a << (16 * (j & 1));
+            w2[j >> 1] |= cvt_e4m3x2_h2(h2_sub(xu, e4m3x2_to_f16x2_pair(a))) << (16 * (j & 1));
           }
           // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
           uint32_t a1, a2;
