@@ -585,7 +585,8 @@ size_t mla_nvfp4_fp8_decode_workspace_size(int batch, int num_heads);
 /*
  * mla_nvfp4_fp8_quantize: activations to e4m3 with one scale per 128 features
  * of a row, the operand A of mla_nvfp4_fp8_gemm.
- *   x      : bf16 [M, K], row stride x_stride elements; K a multiple of 8.
+ *   x      : bf16 [M, K], row stride x_stride elements; K a multiple of 8; x,
+ *            its row stride (in bytes) and codes 16-byte aligned.
  *   codes  : e4m3 [M, K] contiguous;  scales : fp32 [M, ceil(K / 128)].
  * scale = max(amax / 448, 2^-126) over the group (the last one of a row may
  * be shorter), code = e4m3 RNE-satfinite(x / scale), both quotients rounded to

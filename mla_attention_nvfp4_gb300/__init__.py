@@ -647,33 +647,86 @@ def mla_nvfp4_prefill_quantized(q, k, v, cu_seqlens, max_seqlen, softmax_scale, 
                                        sparse24=sparse24, return_lse=return_lse, error_word=error_word)
 
 
+# The calls of the 8-bit path check each tensor once, with few Python calls:
+# on the smallest calls the host's time is the larger part.
+_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
+def _index(t, name, dtype):
+    """Device index of the call: that of its first tensor."""
+    if not t.is_cuda or t.dtype is not dtype:
+        _need(t, name, dtype)
+    return t.get_device()
+
+
+def _same(t, name, dtype, idx):
+    if t.dtype is not dtype or t.get_device() != idx:
+        _need(t, name, dtype, torch.device("cuda", idx))
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{idx}")
+
+
+def _optional(t, name, dtype, idx):
+    """Pointer of an optional contiguous tensor, or None."""
+    if t is None:
+        return None
+    _same(t, name, dtype, idx)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _output(t, name, shape, dtype, dev, idx):
+    """A new output tensor, or the given one checked."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _same(t, name, dtype, idx)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}")
+    return t
+
+
+def _call(name, idx, *args):
+    """A library call on device idx, the arguments followed by its current stream."""
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == idx:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
+    else:
+        with torch.cuda.device(idx):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
+    if st != 0:
+        raise MLAError(name, st)
+
+
 def _rows_contiguous(t):
     """Last dimension contiguous (a tensor without elements, or a last dimension of one, may have any stride)."""
-    return t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1
+    return t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0
 
 
-def _fp8_cache(cache, scales, dev):
-    """The e4m3 cache's two tensors: codes [num_slots, 576], scales fp32 [num_slots / 64]."""
-    _need(cache, "cache", torch.float8_e4m3fn, dev)
-    _need(scales, "scales", torch.float32, dev)
+def _fp8_cache(cache, scales, idx):
+    """The e4m3 cache's two tensors: codes [num_slots, 576], scales fp32 [num_slots / 64]; returns num_slots."""
+    _same(cache, "cache", _F8, idx)
+    _same(scales, "scales", _F32, idx)
     if cache.dim() != 2 or cache.shape[1] != 576 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous [num_slots, 576]")
-    if cache.shape[0] % FP8_BLOCK != 0:
+    slots = cache.shape[0]
+    if slots % FP8_BLOCK != 0:
         raise ValueError(f"num_slots must be a multiple of {FP8_BLOCK}")
-    if scales.shape != (cache.shape[0] // FP8_BLOCK,) or not scales.is_contiguous():
+    if scales.dim() != 1 or scales.shape[0] != slots // FP8_BLOCK or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [num_slots / {FP8_BLOCK}]")
+    return slots
 
 
-def _fp8_pages(page_table, batch, page_size, dev):
-    _need(page_table, "page_table", torch.int32, dev)
+def _fp8_pages(page_table, batch, page_size, idx):
+    """(row stride, pages a row) of the page table."""
+    _same(page_table, "page_table", _I32, idx)
     if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.shape[1] < 1:
         raise ValueError("page_table must be [batch, max_pages]")
     if not _rows_contiguous(page_table):
         raise ValueError("page_table rows must be contiguous")
     if page_size < FP8_BLOCK or page_size % FP8_BLOCK != 0:
         raise ValueError(f"page_size must be a multiple of {FP8_BLOCK}")
-    # a table of one row may have any stride
-    return max(page_table.stride(0), page_table.shape[1])
+    pages = page_table.shape[1]
+    return (page_table.stride(0) if batch > 1 else pages), pages  # one row: any stride
 
 
 def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, *,
@@ -688,56 +741,57 @@ def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, pa
     rotated too, into q_out (default: a new tensor; q_pe itself rotates in
     place), which is returned.  max_new_tokens bounds the tokens of one
     sequence (default T; a tighter bound starts fewer CTAs)."""
-    dev = cache.device
-    _fp8_cache(cache, scales, dev)
-    for t, n, d in ((kv_c, "kv_c", 512), (k_pe, "k_pe", 64)):
-        _need(t, n, torch.bfloat16, dev)
-        if t.dim() != 2 or t.shape[1] != d or not _rows_contiguous(t):
-            raise ValueError(f"{n} must be [T, {d}] with a contiguous last dimension")
+    idx = _index(cache, "cache", _F8)
+    slots = _fp8_cache(cache, scales, idx)
+    _same(kv_c, "kv_c", _BF16, idx)
+    _same(k_pe, "k_pe", _BF16, idx)
+    if kv_c.dim() != 2 or kv_c.shape[1] != 512 or not _rows_contiguous(kv_c):
+        raise ValueError("kv_c must be [T, 512] with a contiguous last dimension")
     T = kv_c.shape[0]
-    _need(cos_sin, "cos_sin", torch.float32, dev)
-    if k_pe.shape[0] != T:
-        raise ValueError("shape mismatch")
+    if k_pe.dim() != 2 or k_pe.shape[0] != T or k_pe.shape[1] != 64 or not _rows_contiguous(k_pe):
+        raise ValueError("k_pe must be [T, 64] with a contiguous last dimension")
+    _same(cos_sin, "cos_sin", _F32, idx)
     if cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous [max_position, 64]")
-    for t, n in ((cu_seqlens, "cu_seqlens"), (context_lens, "context_lens")):
-        _need(t, n, torch.int32, dev)
-        if t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous and one-dimensional")
+    _same(cu_seqlens, "cu_seqlens", _I32, idx)
+    _same(context_lens, "context_lens", _I32, idx)
+    if cu_seqlens.dim() != 1 or context_lens.dim() != 1 or not cu_seqlens.is_contiguous() \
+            or not context_lens.is_contiguous():
+        raise ValueError("cu_seqlens and context_lens must be contiguous and one-dimensional")
     B = context_lens.shape[0]
     if cu_seqlens.shape[0] != B + 1:
         raise ValueError("cu_seqlens must have one entry more than context_lens")
-    _need(error_word, "error_word", torch.int32, dev)
-    pt_stride = _fp8_pages(page_table, B, page_size, dev)
-    H, q_st, q_sh, o_st, o_sh = 0, 0, 0, 0, 0
-    if q_pe is None and q_out is not None:
-        raise ValueError("q_out goes with q_pe")
+    pt_stride, pages = _fp8_pages(page_table, B, page_size, idx)
+    H, q_ptr, q_st, q_sh, o_ptr, o_st, o_sh = 0, None, 0, 0, None, 0, 0
     if q_pe is not None:
-        _need(q_pe, "q_pe", torch.bfloat16, dev)
+        _same(q_pe, "q_pe", _BF16, idx)
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or q_pe.shape[1] < 1 \
+                or not _rows_contiguous(q_pe):
+            raise ValueError("q_pe must be [T, H, 64] with a contiguous last dimension")
         if q_out is None:
-            q_out = torch.empty(q_pe.shape, dtype=torch.bfloat16, device=dev)
-        _need(q_out, "q_out", torch.bfloat16, dev)
-        for t, n in ((q_pe, "q_pe"), (q_out, "q_out")):
-            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != 64 or t.shape[1] < 1 or not _rows_contiguous(t):
-                raise ValueError(f"{n} must be [T, H, 64] with a contiguous last dimension")
-        if q_out.shape != q_pe.shape:
-            raise ValueError("q_out must have q_pe's shape")
+            q_out = torch.empty(q_pe.shape, dtype=_BF16, device=q_pe.device)
+        else:
+            _same(q_out, "q_out", _BF16, idx)
+            if q_out.shape != q_pe.shape or not _rows_contiguous(q_out):
+                raise ValueError("q_out must have q_pe's shape and a contiguous last dimension")
         H = q_pe.shape[1]
         # a dimension of one element may have any stride
-        (q_st, q_sh), (o_st, o_sh) = [
-            (t.stride(0) if T > 1 else max(t.stride(0), 64 * H), t.stride(1) if H > 1 else 64) for t in (q_pe, q_out)]
-    max_new = T if max_new_tokens is None else int(max_new_tokens)
-    kv_st, pe_st = [t.stride(0) if T > 1 else t.shape[1] for t in (kv_c, k_pe)]  # one row: any stride
-    with torch.cuda.device(dev):
-        _check("mla_nvfp4_fp8_cache_append", load_library().mla_nvfp4_fp8_cache_append(
-            _ptr(kv_c), kv_st, _ptr(k_pe), pe_st, T, _ptr(cos_sin), cos_sin.shape[0], 1 if interleaved else 0,
-            _ptr(cu_seqlens), _ptr(context_lens), B, max_new, _ptr(page_table), pt_stride, page_table.shape[1],
-            page_size, _ptr(cache), cache.shape[0], _ptr(scales), _ptr(q_pe), q_st, q_sh, _ptr(q_out), o_st, o_sh, H,
-            _ptr(error_word), _stream(cache)))
+        q_sh, o_sh = (q_pe.stride(1), q_out.stride(1)) if H > 1 else (64, 64)
+        q_st, o_st = (q_pe.stride(0), q_out.stride(0)) if T > 1 else (max(64, q_sh) * H, max(64, o_sh) * H)
+        q_ptr, o_ptr = q_pe.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out goes with q_pe")
+    kv_st, pe_st = (kv_c.stride(0), k_pe.stride(0)) if T > 1 else (512, 64)  # one row: any stride
+    _call("mla_nvfp4_fp8_cache_append", idx, kv_c.data_ptr(), kv_st, k_pe.data_ptr(), pe_st, T, cos_sin.data_ptr(),
+          cos_sin.shape[0], 1 if interleaved else 0, cu_seqlens.data_ptr(), context_lens.data_ptr(), B,
+          T if max_new_tokens is None else int(max_new_tokens), page_table.data_ptr(), pt_stride, pages, page_size,
+          cache.data_ptr(), slots, scales.data_ptr(), q_ptr, q_st, q_sh, o_ptr, o_st, o_sh, H,
+          _optional(error_word, "error_word", _I32, idx))
     return q_out
 
 
 def mla_nvfp4_fp8_decode_workspace_size(batch: int, num_heads: int) -> int:
+    """Bytes of workspace on the current device; the contents need no preparation."""
     return int(load_library().mla_nvfp4_fp8_decode_workspace_size(batch, num_heads))
 
 
@@ -747,62 +801,46 @@ def mla_nvfp4_fp8_decode(q, cache, scales, softmax_scale, *, page_table, seq_len
     scales [num_slots / 64]): q [B,H,576] bf16 -> out [B,H,512] bf16 (and lse
     [B,H] fp32).  split=False works through each sequence without cutting it
     and needs no workspace; otherwise one is allocated unless given."""
-    dev = q.device
-    _need(q, "q", torch.bfloat16)
-    _fp8_cache(cache, scales, dev)
+    idx = _index(q, "q", _BF16)
+    slots = _fp8_cache(cache, scales, idx)
     if q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
         raise ValueError("q must be contiguous [B, H, 576]")
     B, H, _ = q.shape
-    pt_stride = _fp8_pages(page_table, B, page_size, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
-    if seq_lens.shape != (B,) or not seq_lens.is_contiguous():
+    pt_stride, pages = _fp8_pages(page_table, B, page_size, idx)
+    _same(seq_lens, "seq_lens", _I32, idx)
+    if seq_lens.dim() != 1 or seq_lens.shape[0] != B or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be contiguous [B]")
-    _need(error_word, "error_word", torch.int32, dev)
-    if out is None:
-        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=dev)
-    if return_lse and lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
-    for t, n, shape, dt in ((out, "out", (B, H, 512), torch.bfloat16), (lse, "lse", (B, H), torch.float32)):
-        _need(t, n, dt, dev)
-        if t is not None and (t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{n} must be contiguous {list(shape)}")
+    dev = q.device
+    out = _output(out, "out", (B, H, 512), _BF16, dev, idx)
+    if return_lse or lse is not None:
+        lse = _output(lse, "lse", (B, H), _F32, dev, idx)
     if workspace is not None and not split:
         raise ValueError("split=False takes no workspace")
-    lib = load_library()
-    with torch.cuda.device(dev):
-        if split and workspace is None:
-            need = int(lib.mla_nvfp4_fp8_decode_workspace_size(B, H))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _need(workspace, "workspace", torch.uint8, dev)
-        if workspace is not None and not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        _check("mla_nvfp4_fp8_decode", lib.mla_nvfp4_fp8_decode(
-            _ptr(q), B, H, _ptr(cache), cache.shape[0], _ptr(scales), _ptr(page_table), pt_stride,
-            page_table.shape[1], page_size, _ptr(seq_lens), float(softmax_scale), _ptr(out), _ptr(lse),
-            _ptr(workspace), workspace.numel() if workspace is not None else 0, _ptr(error_word), _stream(q)))
+    if split and workspace is None and B > 0 and H > 0:
+        with torch.cuda.device(idx):
+            need = load_library().mla_nvfp4_fp8_decode_workspace_size(B, H)
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+    _call("mla_nvfp4_fp8_decode", idx, q.data_ptr(), B, H, cache.data_ptr(), slots, scales.data_ptr(),
+          page_table.data_ptr(), pt_stride, pages, page_size, seq_lens.data_ptr(), float(softmax_scale),
+          out.data_ptr(), lse.data_ptr() if lse is not None else None, _optional(workspace, "workspace", _U8, idx),
+          workspace.numel() if workspace is not None else 0,
+          _optional(error_word, "error_word", _I32, idx))
     return (out, lse) if return_lse else out
 
 
 def mla_nvfp4_fp8_quantize(x, *, codes=None, scales=None):
     """bf16 [M, K] -> (float8_e4m3fn [M, K], fp32 scales [M, ceil(K / 128)]),
     one scale per 128 features of a row."""
-    dev = x.device
-    _need(x, "x", torch.bfloat16)
+    idx = _index(x, "x", _BF16)
     if x.dim() != 2 or not _rows_contiguous(x):
         raise ValueError("x must be [M, K] with a contiguous last dimension")
     M, K = x.shape
     groups = (K + FP8_GROUP - 1) // FP8_GROUP
-    if codes is None:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
-    if scales is None:
-        scales = torch.empty((M, groups), dtype=torch.float32, device=dev)
-    for t, n, shape, dt in ((codes, "codes", (M, K), torch.float8_e4m3fn), (scales, "scales", (M, groups), torch.float32)):
-        _need(t, n, dt, dev)
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous {list(shape)}")
-    with torch.cuda.device(dev):
-        _check("mla_nvfp4_fp8_quantize", load_library().mla_nvfp4_fp8_quantize(
-            _ptr(x), x.stride(0) if M > 1 else K, M, K, _ptr(codes), _ptr(scales), _stream(x)))
+    dev = x.device
+    codes = _output(codes, "codes", (M, K), _F8, dev, idx)
+    scales = _output(scales, "scales", (M, groups), _F32, dev, idx)
+    _call("mla_nvfp4_fp8_quantize", idx, x.data_ptr(), x.stride(0) if M > 1 else K, M, K, codes.data_ptr(),
+          scales.data_ptr())
     return codes, scales
 
 
@@ -810,25 +848,24 @@ def mla_nvfp4_fp8_gemm(a, a_scales, w, w_scales, *, out=None, error_word=None):
     """e4m3 x e4m3 -> bf16 [M, N]: a float8_e4m3fn [M, K] with a_scales fp32
     [M, ceil(K / 128)], w float8_e4m3fn [N, K] with w_scales fp32
     [ceil(N / 128), ceil(K / 128)]."""
-    dev = a.device
-    _need(a, "a", torch.float8_e4m3fn)
-    _need(w, "w", torch.float8_e4m3fn, dev)
+    idx = _index(a, "a", _F8)
+    _same(w, "w", _F8, idx)
     if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1] or not _rows_contiguous(a) or not _rows_contiguous(w):
         raise ValueError("a [M, K] and w [N, K] must share K, with a contiguous last dimension")
     (M, K), N = a.shape, w.shape[0]
-    kb, nb = (K + FP8_GROUP - 1) // FP8_GROUP, (N + FP8_GROUP - 1) // FP8_GROUP
-    for t, n, shape in ((a_scales, "a_scales", (M, kb)), (w_scales, "w_scales", (nb, kb))):
-        _need(t, n, torch.float32, dev)
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous {list(shape)}")
-    _need(error_word, "error_word", torch.int32, dev)
+    kb = (K + FP8_GROUP - 1) // FP8_GROUP
+    if a_scales.shape != (M, kb):
+        raise ValueError(f"a_scales must be contiguous {[M, kb]}")
+    if w_scales.shape != ((N + FP8_GROUP - 1) // FP8_GROUP, kb):
+        raise ValueError(f"w_scales must be contiguous {[(N + FP8_GROUP - 1) // FP8_GROUP, kb]}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev)
-    if out.dim() != 2 or out.shape != (M, N) or not _rows_contiguous(out):
-        raise ValueError("out must be [M, N] with a contiguous last dimension")
-    with torch.cuda.device(dev):
-        _check("mla_nvfp4_fp8_gemm", load_library().mla_nvfp4_fp8_gemm(
-            _ptr(a), a.stride(0) if M > 1 else K, _ptr(a_scales), M, _ptr(w), w.stride(0) if N > 1 else K,
-            _ptr(w_scales), N, K, _ptr(out), out.stride(0) if M > 1 else N, _ptr(error_word), _stream(a)))
+        out = torch.empty((M, N), dtype=_BF16, device=a.device)
+    else:
+        _same(out, "out", _BF16, idx)
+        if out.shape != (M, N) or not _rows_contiguous(out):
+            raise ValueError("out must be [M, N] with a contiguous last dimension")
+    # one row: any stride
+    _call("mla_nvfp4_fp8_gemm", idx, a.data_ptr(), a.stride(0) if M > 1 else K, _optional(a_scales, "a_scales", _F32, idx),
+          M, w.data_ptr(), w.stride(0) if N > 1 else K, _optional(w_scales, "w_scales", _F32, idx), N, K, out.data_ptr(),
+          out.stride(0) if M > 1 else N, _optional(error_word, "error_word", _I32, idx))
     return out

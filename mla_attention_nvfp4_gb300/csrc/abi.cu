@@ -564,8 +564,7 @@ int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K
   if (x == nullptr || codes == nullptr || scales == nullptr || x_stride < K ||
       M > ((int64_t(1) << 31) - 1) / ((K + MLA_FP8_GROUP - 1) / MLA_FP8_GROUP))
     return MLA_ERR_INVALID_ARG;
-  if (!aligned16(x) || (x_stride * 2) % 16 || (reinterpret_cast<uintptr_t>(codes) & 7u) != 0)
-    return MLA_ERR_ALIGNMENT;
+  if (!aligned16(x) || (x_stride * 2) % 16 || !aligned16(codes)) return MLA_ERR_ALIGNMENT;
   const int sms = device_sms();
   if (sms < 0) return -sms;
   return mla::launch_fp8_quantize(x, x_stride, M, K, codes, scales, static_cast<cudaStream_t>(stream), sms);

@@ -1,21 +1,33 @@
 // Append to the e4m3 latent cache: new tokens' latent and rotated RoPE key,
 // one power-of-two scale per block of 64 tokens, and the rotation of the new
-// queries' RoPE part by the same angles.  No tensor cores: 16-byte loads, one
-// pass over the new rows, which wait in registers while their block's amax
-// is found.
+// queries' RoPE part by the same angles.  No tensor cores; HBM-bound.  A
+// block's new rows wait in shared memory (bulk copies, a row each) while
+// their amax is found, so that few registers and many bytes are in flight.
 #include <cuda_runtime.h>
 
 #include "launch.h"
 #include "nvfp4.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 namespace {
 
+using namespace sm100;
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = MLA_FP8_BLOCK, kRows = kBlock / kWarps;  // rows of a block per warp
 constexpr int kKey = MLA_D_LATENT + MLA_D_ROPE;
-constexpr int kQPairs = 4 * kThreads / 8;  // (token, head) rows of 64 per query CTA
+constexpr int kQPairs = kThreads;  // (token, head) rows of 64 per query CTA
+constexpr int kPeBytes = MLA_D_ROPE * 2, kKvBytes = MLA_D_LATENT * 2;
+constexpr int kSmemBytes = kBlock * (kKvBytes + kPeBytes);  // 72 KB: three CTAs an SM
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
+
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 // The smallest 2^e, -60 <= e <= 60, with amax <= 448 * 2^e (448 = 1.75 * 2^8):
 // from amax's exponent and whether its fraction is above .75.
@@ -76,7 +88,7 @@ __device__ __forceinline__ bool sequence_span(const Fp8AppendArgs& p, int b, Spa
 // and query parts (kQPairs rows of 64 each); a grid of num_seqs * (n_kv + n_q)
 // CTAs covers the longest sequence, and CTAs past a sequence's end return.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendArgs p, int n_kv, int n_q) {
+__global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8AppendArgs p, int n_kv, int n_q) {
   const int per = n_kv + n_q;
   const int b = blockIdx.x / per, part = blockIdx.x % per;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -95,20 +107,33 @@ __global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendArg
     const int c = tid % kPer;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q_pe);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.q_out);
+    // all loads first (q_out may be q_pe: every thread writes what it read)
+    constexpr int kVec = kInterleaved ? 1 : 2;  // 16-byte units a row and thread
+    uint4 v[kIter][kVec];
+    int row_of[kIter];  // token of the sequence, or -1
+    int head_of[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int64_t pair = first + i * (kThreads / kPer) + tid / kPer;
-      if (pair >= total) break;
-      const int64_t t = pair / p.num_heads;
-      const int h = static_cast<int>(pair - t * p.num_heads);
-      const float* cs = p.cos_sin + (sp.ctx + t) * 64;
-      const __nv_bfloat16* src = q + (sp.row + t) * p.q_st + h * p.q_sh + 8 * c;
-      __nv_bfloat16* dst = o + (sp.row + t) * p.qo_st + h * p.qo_sh + 8 * c;
+      row_of[i] = -1;
+      head_of[i] = 0;
+      if (pair < total) {
+        row_of[i] = static_cast<int>(pair / p.num_heads);
+        head_of[i] = static_cast<int>(pair - static_cast<int64_t>(row_of[i]) * p.num_heads);
+        const __nv_bfloat16* src = q + (sp.row + row_of[i]) * p.q_st + head_of[i] * p.q_sh + 8 * c;
+        v[i][0] = *reinterpret_cast<const uint4*>(src);
+        if constexpr (!kInterleaved) v[i][1] = *reinterpret_cast<const uint4*>(src + 32);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      if (row_of[i] < 0) break;
+      const float* cs = p.cos_sin + (sp.ctx + row_of[i]) * 64;
+      __nv_bfloat16* dst = o + (sp.row + row_of[i]) * p.qo_st + head_of[i] * p.qo_sh + 8 * c;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v[i][0]);
       if constexpr (kInterleaved) {
-        uint4 v = *reinterpret_cast<const uint4*>(src);
         const float4 cc = *reinterpret_cast<const float4*>(cs + 4 * c);
         const float4 ss = *reinterpret_cast<const float4*>(cs + 32 + 4 * c);
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
         const float cw[4] = {cc.x, cc.y, cc.z, cc.w}, sw[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -117,24 +142,27 @@ __global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendArg
           turn(x, y, cw[k], sw[k]);
           w[k] = bf16x2_pack(x, y);
         }
-        *reinterpret_cast<uint4*>(dst) = v;
+        *reinterpret_cast<uint4*>(dst) = v[i][0];
       } else {
-        uint4 v = *reinterpret_cast<const uint4*>(src), u = *reinterpret_cast<const uint4*>(src + 32);
-        uint32_t *vw = reinterpret_cast<uint32_t*>(&v), *uw = reinterpret_cast<uint32_t*>(&u);
+        uint32_t* u = reinterpret_cast<uint32_t*>(&v[i][kVec - 1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 cc = *reinterpret_cast<const float2*>(cs + 8 * c + 2 * k);
-          const float2 ss = *reinterpret_cast<const float2*>(cs + 32 + 8 * c + 2 * k);
-          float x0, x1, y0, y1;
-          bf16x2_to_f32(vw[k], x0, x1);
-          bf16x2_to_f32(uw[k], y0, y1);
-          turn(x0, y0, cc.x, ss.x);
-          turn(x1, y1, cc.y, ss.y);
-          vw[k] = bf16x2_pack(x0, x1);
-          uw[k] = bf16x2_pack(y0, y1);
+        for (int k = 0; k < 4; k += 2) {
+          const float4 cc = *reinterpret_cast<const float4*>(cs + 8 * c + 2 * k);
+          const float4 ss = *reinterpret_cast<const float4*>(cs + 32 + 8 * c + 2 * k);
+          const float cw[4] = {cc.x, cc.y, cc.z, cc.w}, sw[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x0, x1, y0, y1;
+            bf16x2_to_f32(w[k + j], x0, x1);
+            bf16x2_to_f32(u[k + j], y0, y1);
+            turn(x0, y0, cw[2 * j], sw[2 * j]);
+            turn(x1, y1, cw[2 * j + 1], sw[2 * j + 1]);
+            w[k + j] = bf16x2_pack(x0, x1);
+            u[k + j] = bf16x2_pack(y0, y1);
+          }
         }
-        *reinterpret_cast<uint4*>(dst) = v;
-        *reinterpret_cast<uint4*>(dst + 32) = u;
+        *reinterpret_cast<uint4*>(dst) = v[i][0];
+        *reinterpret_cast<uint4*>(dst + 32) = v[i][kVec - 1];
       }
     }
     return;
@@ -154,43 +182,65 @@ __global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendArg
   float* scale_ptr = p.scales + slot0 / kBlock;
   const float was = lo > 0 ? *scale_ptr : 0.f;
 
-  // This warp's rows, all loads first: lane l holds latent features
-  // [16 l, 16 l + 16) and pair l of the RoPE key.
-  uint4 va[kRows], vb[kRows];
-  float r0[kRows], r1[kRows];
+  extern __shared__ __align__(128) uint8_t smem[];  // latent rows, then RoPE rows
+  __shared__ uint64_t bar;
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    mbar_expect_tx(&bar, (hi - lo) * (kKvBytes + kPeBytes));
+  }
+  __syncthreads();
+  if (tid >= lo && tid < hi) {
+    const int64_t row = sp.row + (pos0 + tid - sp.ctx);
+    bulk_load(smem_u32(smem) + tid * kKvBytes, static_cast<const __nv_bfloat16*>(p.kv_c) + row * p.kv_stride, kKvBytes,
+              &bar);
+    bulk_load(smem_u32(smem) + kBlock * kKvBytes + tid * kPeBytes,
+              static_cast<const __nv_bfloat16*>(p.k_pe) + row * p.pe_stride, kPeBytes, &bar);
+  }
+  // Rows warp, warp + 8, ..: lane l holds latent features [8 l, 8 l + 8) and
+  // [256 + 8 l, ..), and pair l of the RoPE key, whose angles come meanwhile.
+  float cosine[kRows], sine[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = warp + i * kWarps;
-    va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-    r0[i] = r1[i] = 0.f;
+    cosine[i] = sine[i] = 0.f;
     if (r >= lo && r < hi) {
-      const int64_t row = sp.row + (pos0 + r - sp.ctx);
-      const uint4* src =
-          reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv_c) + row * p.kv_stride + 16 * lane);
-      va[i] = src[0];
-      vb[i] = src[1];
-      const __nv_bfloat16* pe = static_cast<const __nv_bfloat16*>(p.k_pe) + row * p.pe_stride;
-      if constexpr (kInterleaved) {
-        bf16x2_to_f32(*reinterpret_cast<const uint32_t*>(pe + 2 * lane), r0[i], r1[i]);
-      } else {
-        r0[i] = __bfloat162float(pe[lane]);
-        r1[i] = __bfloat162float(pe[lane + 32]);
-      }
       const float* cs = p.cos_sin + (pos0 + r) * 64;
-      turn(r0[i], r1[i], cs[lane], cs[lane + 32]);
+      cosine[i] = cs[lane];
+      sine[i] = cs[lane + 32];
     }
   }
+  if (!mbar_wait(&bar, 0, p.error_word, nullptr)) return;
+  auto latent = [&](int r, int half) { return *reinterpret_cast<const uint4*>(smem + r * kKvBytes + 512 * half + 16 * lane); };
+  auto rope = [&](int r, int i, float& a, float& b) {  // the rotated pair
+    const uint8_t* pe = smem + kBlock * kKvBytes + r * kPeBytes;
+    if constexpr (kInterleaved) {
+      bf16x2_to_f32(reinterpret_cast<const uint32_t*>(pe)[lane], a, b);
+    } else {
+      a = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pe)[lane]);
+      b = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pe)[lane + 32]);
+    }
+    turn(a, b, cosine[i], sine[i]);
+  };
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const uint32_t w[8] = {va[i].x, va[i].y, va[i].z, va[i].w, vb[i].x, vb[i].y, vb[i].z, vb[i].w};
+    const int r = warp + i * kWarps;
+    if (r < lo || r >= hi) continue;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float x, y;
-      bf16x2_to_f32(w[k], x, y);
-      am = fmaxf(am, fmaxf(fabsf(x), fabsf(y)));
+    for (int half = 0; half < 2; ++half) {
+      const uint4 v = latent(r, half);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x, y;
+        bf16x2_to_f32(w[k], x, y);
+        am = fmaxf(am, fmaxf(fabsf(x), fabsf(y)));
+      }
     }
-    am = fmaxf(am, fmaxf(fabsf(r0[i]), fabsf(r1[i])));
+    float x, y;
+    rope(r, i, x, y);
+    am = fmaxf(am, fmaxf(fabsf(x), fabsf(y)));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
@@ -232,23 +282,29 @@ __global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendArg
   for (int i = 0; i < kRows; ++i) {
     const int r = warp + i * kWarps;
     if (r < lo || r >= hi) continue;
-    const uint32_t w[8] = {va[i].x, va[i].y, va[i].z, va[i].w, vb[i].x, vb[i].y, vb[i].z, vb[i].w};
-    uint32_t out[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float a, c, d, e;
-      bf16x2_to_f32(w[2 * k], a, c);
-      bf16x2_to_f32(w[2 * k + 1], d, e);
-      out[k] = cvt_e4m3x2(a * inv, c * inv) | (cvt_e4m3x2(d * inv, e * inv) << 16);
-    }
     uint8_t* rec = rec0 + static_cast<int64_t>(r) * kKey;
-    *reinterpret_cast<uint4*>(rec + 16 * lane) = make_uint4(out[0], out[1], out[2], out[3]);
-    const uint32_t rope = cvt_e4m3x2(r0[i] * inv, r1[i] * inv);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint4 v = latent(r, half);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t out[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float a, b2, c, d;
+        bf16x2_to_f32(w[2 * k], a, b2);
+        bf16x2_to_f32(w[2 * k + 1], c, d);
+        out[k] = cvt_e4m3x2(a * inv, b2 * inv) | (cvt_e4m3x2(c * inv, d * inv) << 16);
+      }
+      *reinterpret_cast<uint2*>(rec + 256 * half + 8 * lane) = make_uint2(out[0], out[1]);
+    }
+    float x, y;
+    rope(r, i, x, y);
+    const uint32_t two = cvt_e4m3x2(x * inv, y * inv);
     if constexpr (kInterleaved) {
-      *reinterpret_cast<uint16_t*>(rec + MLA_D_LATENT + 2 * lane) = static_cast<uint16_t>(rope);
+      *reinterpret_cast<uint16_t*>(rec + MLA_D_LATENT + 2 * lane) = static_cast<uint16_t>(two);
     } else {
-      rec[MLA_D_LATENT + lane] = static_cast<uint8_t>(rope);
-      rec[MLA_D_LATENT + 32 + lane] = static_cast<uint8_t>(rope >> 8);
+      rec[MLA_D_LATENT + lane] = static_cast<uint8_t>(two);
+      rec[MLA_D_LATENT + 32 + lane] = static_cast<uint8_t>(two >> 8);
     }
   }
 }
@@ -264,12 +320,9 @@ int launch_fp8_append(const Fp8AppendArgs& a, cudaStream_t stream) {
   if (grid > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   Fp8AppendArgs p = a;
   p.max_new = static_cast<int>(n);
-  if (a.interleaved)
-    fp8_append_kernel<true><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p, static_cast<int>(n_kv),
-                                                                                  static_cast<int>(n_q));
-  else
-    fp8_append_kernel<false><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p, static_cast<int>(n_kv),
-                                                                                   static_cast<int>(n_q));
+  auto* kern = a.interleaved ? fp8_append_kernel<true> : fp8_append_kernel<false>;
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), kSmemBytes, a.interleaved ? 21 : 22)) return st;
+  kern<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(p, static_cast<int>(n_kv), static_cast<int>(n_q));
   return launch_status();
 }
 

@@ -18,61 +18,88 @@ constexpr int kGroup = MLA_FP8_GROUP;
 
 // ---------------------------------------------------------------------------
 // Quantiser: bf16 [M, K] -> e4m3 codes and one fp32 scale per 128 features.
-// 16 lanes hold a group, 8 features each (one 16-byte load, one 8-byte
-// store); four groups in flight per half-warp.
+// 8 lanes hold a group, 16 features each (two 16-byte loads, one 16-byte
+// store; 8 features where K asks for it); two groups in flight per 8 lanes.
+// HBM-bound, but only with few instructions an element: maxima on bf16
+// pairs, quotients on pairs of floats.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 4;
-constexpr int kQuantGroups = kQuantThreads / 16 * kQuantUnroll;  // groups per CTA
+constexpr int kQuantUnroll = 2;
+constexpr int kQuantGroups = kQuantThreads / 8 * kQuantUnroll;  // groups per CTA
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_bfloat16* __restrict__ x,
                                                                      int64_t x_stride, int64_t K, int n_groups,
                                                                      int row_groups, uint32_t magic, int shift,
                                                                      uint8_t* __restrict__ codes,
                                                                      float* __restrict__ scales) {
-  const int sub = threadIdx.x & 15;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kQuantGroups + (threadIdx.x >> 4);
-  uint4 v[kQuantUnroll];
-  int64_t at[kQuantUnroll];  // offset of this thread's codes, or -1
+  const int sub = threadIdx.x & 7;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kQuantGroups + (threadIdx.x >> 3);
+  uint4 v[kQuantUnroll][2];
+  int64_t at[kQuantUnroll];  // offset of this thread's codes
+  int have[kQuantUnroll];    // 8-feature halves it holds
 #pragma unroll
   for (int i = 0; i < kQuantUnroll; ++i) {
-    const int64_t g = first + i * (kQuantThreads / 16);
-    v[i] = make_uint4(0, 0, 0, 0);
-    at[i] = -1;
+    const int64_t g = first + i * (kQuantThreads / 8);
+    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+    at[i] = 0;
+    have[i] = 0;
     if (g < n_groups) {
       const int64_t m = div_magic(static_cast<uint32_t>(g), magic, shift), j = g - m * row_groups;
-      const int64_t k = j * kGroup + 8 * sub;
-      if (k < K) {
-        v[i] = *reinterpret_cast<const uint4*>(x + m * x_stride + k);
-        at[i] = m * K + k;
-      }
+      const int64_t k = j * kGroup + 16 * sub;
+      const uint4* src = reinterpret_cast<const uint4*>(x + m * x_stride + k);
+      have[i] = k + 16 <= K ? 2 : k + 8 <= K ? 1 : 0;
+      if (have[i] > 0) v[i][0] = src[0];
+      if (have[i] > 1) v[i][1] = src[1];
+      at[i] = m * K + k;
     }
   }
 #pragma unroll
   for (int i = 0; i < kQuantUnroll; ++i) {
-    const int64_t g = first + i * (kQuantThreads / 16);
-    float f[8];
-    bf16x2_to_f32(v[i].x, f[0], f[1]);
-    bf16x2_to_f32(v[i].y, f[2], f[3]);
-    bf16x2_to_f32(v[i].z, f[4], f[5]);
-    bf16x2_to_f32(v[i].w, f[6], f[7]);
-    float am = amax8(f);
+    const int64_t g = first + i * (kQuantThreads / 8);
+    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    uint32_t m2 = 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    // both quotients rounded to nearest: the scale by a division, the codes
-    // by the correctly rounded reciprocal (div_rn)
-    const float scale = fmaxf(__fdiv_rn(am, 448.f), 1.1754943508222875e-38f);
+    for (int k = 0; k < 8; ++k) m2 = max_abs2(m2, w[k] & 0x7FFF7FFFu);  // NaN gives the other operand
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m2 = max_abs2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    float lo, hi;
+    bf16x2_to_f32(m2, lo, hi);
+    const float am = fmaxf(lo, hi);
+    // both quotients rounded to nearest, from correctly rounded reciprocals
+    // (div_rn); 1 / 448 rounded is a constant
+    const float scale = isinf(am) ? am : fmaxf(div_rn(am, 448.f, 0.0022321429569274187f), 1.1754943508222875e-38f);
     const float inv = __frcp_rn(scale);
-    uint32_t w[2];
+    const uint64_t inv2 = pack2(inv, inv), neg2 = pack2(-scale, -scale);
+    uint32_t out[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float q[4];
+    for (int k = 0; k < 4; ++k) {
+      uint32_t code = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[e] = isinf(scale) ? __fmul_rn(f[4 * k + e], inv) : div_rn(f[4 * k + e], scale, inv);
-      w[k] = cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16);
+      for (int j = 0; j < 2; ++j) {
+        float a, b;
+        bf16x2_to_f32(w[2 * k + j], a, b);
+        const uint64_t num = pack2(a, b);
+        const uint64_t q0 = mul2(num, inv2);
+        uint64_t r = num;
+        fma2(r, q0, neg2);  // the exact remainder
+        uint64_t q = q0;
+        fma2(q, r, inv2);
+        unpack2(isinf(scale) ? q0 : q, a, b);
+        code |= cvt_e4m3x2(a, b) << (16 * j);
+      }
+      out[k] = code;
     }
-    if (at[i] >= 0) *reinterpret_cast<uint2*>(codes + at[i]) = make_uint2(w[0], w[1]);
+    if (have[i] == 2 && (K & 15) == 0) {
+      *reinterpret_cast<uint4*>(codes + at[i]) = make_uint4(out[0], out[1], out[2], out[3]);
+    } else {
+      if (have[i] > 0) *reinterpret_cast<uint2*>(codes + at[i]) = make_uint2(out[0], out[1]);
+      if (have[i] > 1) *reinterpret_cast<uint2*>(codes + at[i] + 8) = make_uint2(out[2], out[3]);
+    }
     if (sub == 0 && g < n_groups) scales[g] = scale;
   }
 }
@@ -611,13 +638,17 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
   if (sn > 65535 || sm > 65535) return MLA_ERR_INVALID_ARG;
   p.tiles_m = static_cast<int>(sm);
   p.tiles_n = static_cast<int>(sn);
-  // Split K so that the busiest SM has the fewest K blocks to stream; a
-  // CTA's start and end cost about as much as kOverhead of them.
+  // Split K so that the busiest SM has the fewest K blocks to stream; a wave
+  // of CTAs costs kOverhead blocks more.  Clusters of several CTAs do not fill
+  // every place an SM offers: nine tenths count.  (64 rows, N 7168, K 16384:
+  // 25 us with 4 parts, one wave; 30 with 8, two.  16 rows: 23 with 5 or 6.)
   constexpr int kOverhead = 3;
+  const int64_t places = static_cast<int64_t>(num_sms) * (kt <= 32 ? 3 : kt == 64 ? 2 : 1) * 9 / 10;
   int splits = 1;
   int64_t best = INT64_MAX;
   for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
-    const int64_t cost = (sn * sm * s + num_sms - 1) / num_sms * ((kb + s - 1) / s + kOverhead);
+    const int64_t ctas = sn * sm * s, wave = ctas < places ? ctas : places;
+    const int64_t cost = (ctas + places - 1) / places * ((wave + num_sms - 1) / num_sms * ((kb + s - 1) / s) + kOverhead);
     if (cost < best) {
       best = cost;
       splits = s;
