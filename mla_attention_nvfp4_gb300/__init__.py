@@ -11,6 +11,7 @@ device is not sm_103, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -647,86 +648,30 @@ def mla_nvfp4_prefill_quantized(q, k, v, cu_seqlens, max_seqlen, softmax_scale, 
                                        sparse24=sparse24, return_lse=return_lse, error_word=error_word)
 
 
-# The calls of the 8-bit path check each tensor once, with few Python calls:
-# on the smallest calls the host's time is the larger part.
-_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_FP8 = None
 
 
-def _index(t, name, dtype):
-    """Device index of the call: that of its first tensor."""
-    if not t.is_cuda or t.dtype is not dtype:
-        _need(t, name, dtype)
-    return t.get_device()
+def _fp8():
+    """The native binding of the 8-bit calls (csrc/binding.cpp), which checks
+    the arguments, allocates outputs and launches: on the smallest calls the
+    same steps in Python would take several times the GPU's time."""
+    global _FP8
+    if _FP8 is None:
+        load_library()  # builds both if needed
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"_mla_fp8.so not found at {_build.BINDING}; run the package build")
+        spec = importlib.util.spec_from_file_location("_mla_fp8", _build.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _FP8 = module
+    return _FP8
 
 
-def _same(t, name, dtype, idx):
-    if t.dtype is not dtype or t.get_device() != idx:
-        _need(t, name, dtype, torch.device("cuda", idx))
-        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{idx}")
-
-
-def _optional(t, name, dtype, idx):
-    """Pointer of an optional contiguous tensor, or None."""
-    if t is None:
-        return None
-    _same(t, name, dtype, idx)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _output(t, name, shape, dtype, dev, idx):
-    """A new output tensor, or the given one checked."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _same(t, name, dtype, idx)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}")
-    return t
-
-
-def _call(name, idx, *args):
-    """A library call on device idx, the arguments followed by its current stream."""
-    fn = getattr(load_library(), name)
-    if torch._C._cuda_getDevice() == idx:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
-    else:
-        with torch.cuda.device(idx):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(idx))
-    if st != 0:
-        raise MLAError(name, st)
-
-
-def _rows_contiguous(t):
-    """Last dimension contiguous (a tensor without elements, or a last dimension of one, may have any stride)."""
-    return t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0
-
-
-def _fp8_cache(cache, scales, idx):
-    """The e4m3 cache's two tensors: codes [num_slots, 576], scales fp32 [num_slots / 64]; returns num_slots."""
-    _same(cache, "cache", _F8, idx)
-    _same(scales, "scales", _F32, idx)
-    if cache.dim() != 2 or cache.shape[1] != 576 or not cache.is_contiguous():
-        raise ValueError("cache must be contiguous [num_slots, 576]")
-    slots = cache.shape[0]
-    if slots % FP8_BLOCK != 0:
-        raise ValueError(f"num_slots must be a multiple of {FP8_BLOCK}")
-    if scales.dim() != 1 or scales.shape[0] != slots // FP8_BLOCK or not scales.is_contiguous():
-        raise ValueError(f"scales must be contiguous [num_slots / {FP8_BLOCK}]")
-    return slots
-
-
-def _fp8_pages(page_table, batch, page_size, idx):
-    """(row stride, pages a row) of the page table."""
-    _same(page_table, "page_table", _I32, idx)
-    if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.shape[1] < 1:
-        raise ValueError("page_table must be [batch, max_pages]")
-    if not _rows_contiguous(page_table):
-        raise ValueError("page_table rows must be contiguous")
-    if page_size < FP8_BLOCK or page_size % FP8_BLOCK != 0:
-        raise ValueError(f"page_size must be a multiple of {FP8_BLOCK}")
-    pages = page_table.shape[1]
-    return (page_table.stride(0) if batch > 1 else pages), pages  # one row: any stride
+def _result(name, r):
+    """A binding call's outputs; it returns the status of a failed one."""
+    if type(r) is int:
+        raise MLAError(name, r)
+    return r
 
 
 def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, *,
@@ -741,53 +686,9 @@ def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, pa
     rotated too, into q_out (default: a new tensor; q_pe itself rotates in
     place), which is returned.  max_new_tokens bounds the tokens of one
     sequence (default T; a tighter bound starts fewer CTAs)."""
-    idx = _index(cache, "cache", _F8)
-    slots = _fp8_cache(cache, scales, idx)
-    _same(kv_c, "kv_c", _BF16, idx)
-    _same(k_pe, "k_pe", _BF16, idx)
-    if kv_c.dim() != 2 or kv_c.shape[1] != 512 or not _rows_contiguous(kv_c):
-        raise ValueError("kv_c must be [T, 512] with a contiguous last dimension")
-    T = kv_c.shape[0]
-    if k_pe.dim() != 2 or k_pe.shape[0] != T or k_pe.shape[1] != 64 or not _rows_contiguous(k_pe):
-        raise ValueError("k_pe must be [T, 64] with a contiguous last dimension")
-    _same(cos_sin, "cos_sin", _F32, idx)
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous [max_position, 64]")
-    _same(cu_seqlens, "cu_seqlens", _I32, idx)
-    _same(context_lens, "context_lens", _I32, idx)
-    if cu_seqlens.dim() != 1 or context_lens.dim() != 1 or not cu_seqlens.is_contiguous() \
-            or not context_lens.is_contiguous():
-        raise ValueError("cu_seqlens and context_lens must be contiguous and one-dimensional")
-    B = context_lens.shape[0]
-    if cu_seqlens.shape[0] != B + 1:
-        raise ValueError("cu_seqlens must have one entry more than context_lens")
-    pt_stride, pages = _fp8_pages(page_table, B, page_size, idx)
-    H, q_ptr, q_st, q_sh, o_ptr, o_st, o_sh = 0, None, 0, 0, None, 0, 0
-    if q_pe is not None:
-        _same(q_pe, "q_pe", _BF16, idx)
-        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or q_pe.shape[1] < 1 \
-                or not _rows_contiguous(q_pe):
-            raise ValueError("q_pe must be [T, H, 64] with a contiguous last dimension")
-        if q_out is None:
-            q_out = torch.empty(q_pe.shape, dtype=_BF16, device=q_pe.device)
-        else:
-            _same(q_out, "q_out", _BF16, idx)
-            if q_out.shape != q_pe.shape or not _rows_contiguous(q_out):
-                raise ValueError("q_out must have q_pe's shape and a contiguous last dimension")
-        H = q_pe.shape[1]
-        # a dimension of one element may have any stride
-        q_sh, o_sh = (q_pe.stride(1), q_out.stride(1)) if H > 1 else (64, 64)
-        q_st, o_st = (q_pe.stride(0), q_out.stride(0)) if T > 1 else (max(64, q_sh) * H, max(64, o_sh) * H)
-        q_ptr, o_ptr = q_pe.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out goes with q_pe")
-    kv_st, pe_st = (kv_c.stride(0), k_pe.stride(0)) if T > 1 else (512, 64)  # one row: any stride
-    _call("mla_nvfp4_fp8_cache_append", idx, kv_c.data_ptr(), kv_st, k_pe.data_ptr(), pe_st, T, cos_sin.data_ptr(),
-          cos_sin.shape[0], 1 if interleaved else 0, cu_seqlens.data_ptr(), context_lens.data_ptr(), B,
-          T if max_new_tokens is None else int(max_new_tokens), page_table.data_ptr(), pt_stride, pages, page_size,
-          cache.data_ptr(), slots, scales.data_ptr(), q_ptr, q_st, q_sh, o_ptr, o_st, o_sh, H,
-          _optional(error_word, "error_word", _I32, idx))
-    return q_out
+    return _result("mla_nvfp4_fp8_cache_append", _fp8().append(
+        kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, page_size, interleaved, q_pe, q_out,
+        max_new_tokens, error_word))
 
 
 def mla_nvfp4_fp8_decode_workspace_size(batch: int, num_heads: int) -> int:
@@ -801,71 +702,19 @@ def mla_nvfp4_fp8_decode(q, cache, scales, softmax_scale, *, page_table, seq_len
     scales [num_slots / 64]): q [B,H,576] bf16 -> out [B,H,512] bf16 (and lse
     [B,H] fp32).  split=False works through each sequence without cutting it
     and needs no workspace; otherwise one is allocated unless given."""
-    idx = _index(q, "q", _BF16)
-    slots = _fp8_cache(cache, scales, idx)
-    if q.dim() != 3 or q.shape[2] != 576 or not q.is_contiguous():
-        raise ValueError("q must be contiguous [B, H, 576]")
-    B, H, _ = q.shape
-    pt_stride, pages = _fp8_pages(page_table, B, page_size, idx)
-    _same(seq_lens, "seq_lens", _I32, idx)
-    if seq_lens.dim() != 1 or seq_lens.shape[0] != B or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous [B]")
-    dev = q.device
-    out = _output(out, "out", (B, H, 512), _BF16, dev, idx)
-    if return_lse or lse is not None:
-        lse = _output(lse, "lse", (B, H), _F32, dev, idx)
-    if workspace is not None and not split:
-        raise ValueError("split=False takes no workspace")
-    if split and workspace is None and B > 0 and H > 0:
-        with torch.cuda.device(idx):
-            need = load_library().mla_nvfp4_fp8_decode_workspace_size(B, H)
-        workspace = torch.empty(need, dtype=_U8, device=dev)
-    _call("mla_nvfp4_fp8_decode", idx, q.data_ptr(), B, H, cache.data_ptr(), slots, scales.data_ptr(),
-          page_table.data_ptr(), pt_stride, pages, page_size, seq_lens.data_ptr(), float(softmax_scale),
-          out.data_ptr(), lse.data_ptr() if lse is not None else None, _optional(workspace, "workspace", _U8, idx),
-          workspace.numel() if workspace is not None else 0,
-          _optional(error_word, "error_word", _I32, idx))
-    return (out, lse) if return_lse else out
+    return _result("mla_nvfp4_fp8_decode", _fp8().decode(
+        q, cache, scales, softmax_scale, page_table, seq_lens, page_size, out, lse, workspace, split, error_word,
+        return_lse))
 
 
 def mla_nvfp4_fp8_quantize(x, *, codes=None, scales=None):
     """bf16 [M, K] -> (float8_e4m3fn [M, K], fp32 scales [M, ceil(K / 128)]),
     one scale per 128 features of a row."""
-    idx = _index(x, "x", _BF16)
-    if x.dim() != 2 or not _rows_contiguous(x):
-        raise ValueError("x must be [M, K] with a contiguous last dimension")
-    M, K = x.shape
-    groups = (K + FP8_GROUP - 1) // FP8_GROUP
-    dev = x.device
-    codes = _output(codes, "codes", (M, K), _F8, dev, idx)
-    scales = _output(scales, "scales", (M, groups), _F32, dev, idx)
-    _call("mla_nvfp4_fp8_quantize", idx, x.data_ptr(), x.stride(0) if M > 1 else K, M, K, codes.data_ptr(),
-          scales.data_ptr())
-    return codes, scales
+    return _result("mla_nvfp4_fp8_quantize", _fp8().quantize(x, codes, scales))
 
 
 def mla_nvfp4_fp8_gemm(a, a_scales, w, w_scales, *, out=None, error_word=None):
     """e4m3 x e4m3 -> bf16 [M, N]: a float8_e4m3fn [M, K] with a_scales fp32
     [M, ceil(K / 128)], w float8_e4m3fn [N, K] with w_scales fp32
     [ceil(N / 128), ceil(K / 128)]."""
-    idx = _index(a, "a", _F8)
-    _same(w, "w", _F8, idx)
-    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1] or not _rows_contiguous(a) or not _rows_contiguous(w):
-        raise ValueError("a [M, K] and w [N, K] must share K, with a contiguous last dimension")
-    (M, K), N = a.shape, w.shape[0]
-    kb = (K + FP8_GROUP - 1) // FP8_GROUP
-    if a_scales.shape != (M, kb):
-        raise ValueError(f"a_scales must be contiguous {[M, kb]}")
-    if w_scales.shape != ((N + FP8_GROUP - 1) // FP8_GROUP, kb):
-        raise ValueError(f"w_scales must be contiguous {[(N + FP8_GROUP - 1) // FP8_GROUP, kb]}")
-    if out is None:
-        out = torch.empty((M, N), dtype=_BF16, device=a.device)
-    else:
-        _same(out, "out", _BF16, idx)
-        if out.shape != (M, N) or not _rows_contiguous(out):
-            raise ValueError("out must be [M, N] with a contiguous last dimension")
-    # one row: any stride
-    _call("mla_nvfp4_fp8_gemm", idx, a.data_ptr(), a.stride(0) if M > 1 else K, _optional(a_scales, "a_scales", _F32, idx),
-          M, w.data_ptr(), w.stride(0) if N > 1 else K, _optional(w_scales, "w_scales", _F32, idx), N, K, out.data_ptr(),
-          out.stride(0) if M > 1 else N, _optional(error_word, "error_word", _I32, idx))
-    return out
+    return _result("mla_nvfp4_fp8_gemm", _fp8().gemm(a, a_scales, w, w_scales, out, error_word))

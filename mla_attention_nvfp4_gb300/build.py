@@ -1,9 +1,10 @@
-"""Build libmla_nvfp4.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmla_nvfp4.so in-tree with nvcc for sm_103a (GB300), and the
+Python binding of its 8-bit calls with the host compiler.
 
-Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
-the shared library.  Output: mla_attention_nvfp4_gb300/_build/libmla_nvfp4.so
-(git-ignored).  Rebuilds only when a source or header is newer than the
-library.
+Each .cu file under csrc/ compiles to an object in parallel (binding.cpp
+meanwhile), then nvcc links the shared library.  Output:
+mla_attention_nvfp4_gb300/_build/libmla_nvfp4.so and _mla_fp8.so
+(git-ignored).  Rebuilds only when a source or header is newer than either.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmla_nvfp4.so")
+BINDING = os.path.join(BUILD, "_mla_fp8.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,13 +41,13 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(ROOT, "include", "mla_nvfp4.h"), os.path.abspath(__file__)]
+        glob.glob(os.path.join(CSRC, "*.cpp")) + [os.path.join(ROOT, "include", "mla_nvfp4.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -65,15 +67,48 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
+
+
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    """binding.cpp against this interpreter's and this PyTorch's headers."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    obj = os.path.join(BUILD, "binding.o")
+    _run([os.environ.get("CXX", "g++"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj, "-O2", "-std=c++17", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(root, "include"),
+          "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
+          "-I" + sysconfig.get_paths()["include"]])
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+          "-ltorch", "-ltorch_cpu", "-ltorch_python", "-L" + BUILD, "-lmla_nvfp4", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -113,3 +113,10 @@ def test_python_calls_want_cuda_tensors():
         mla.mla_nvfp4_fp8_quantize(torch.zeros(2, 128).bfloat16())
     with pytest.raises(ValueError, match="CUDA"):
         mla.mla_nvfp4_fp8_gemm(f8, sc[None], f8, sc[None])
+
+
+def test_python_calls_want_tensors_and_arguments_of_the_right_kind():
+    with pytest.raises(TypeError, match="tensor"):
+        mla.mla_nvfp4_fp8_quantize([1.0])
+    with pytest.raises(TypeError):
+        mla.mla_nvfp4_fp8_gemm(None, None, None, None)

@@ -633,3 +633,51 @@ def test_a_layer_in_8_bits():
         y = mla.mla_nvfp4_fp8_gemm(oa, os_, d(w_o).view(F8), d(s_o))
         check_gemm(f32(y), u8(oa), os_.cpu().numpy(), w_o, s_o, "output projection")
     assert int(e.item()) == 0
+
+
+# ----------------------------------------------------------------- refusals
+def test_calls_refuse_wrong_tensors():
+    """Shapes, types, strides and pairs the calls do not take; nothing runs."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)  # noqa: E731
+    i32 = torch.int32
+    cache, scales = z(128, 576, dt=torch.uint8).view(F8), z(2, dt=torch.float32)
+    good = dict(kv_c=z(3, 512), k_pe=z(3, 64), cos_sin=z(8, 64, dt=torch.float32), cu_seqlens=z(2, dt=i32),
+                context_lens=z(1, dt=i32), page_table=z(1, 2, dt=i32), cache=cache, scales=scales)
+    for name, bad in dict(kv_c=z(3, 500), k_pe=z(2, 64), cos_sin=z(8, 32, dt=torch.float32), cu_seqlens=z(3, dt=i32),
+                          context_lens=z(1, dt=torch.int64), page_table=z(2, 2, dt=i32), cache=z(100, 576, dt=torch.uint8).view(F8),
+                          scales=z(3, dt=torch.float32)).items():
+        with pytest.raises(ValueError):
+            mla.mla_nvfp4_fp8_cache_append(**dict(good, **{name: bad}))
+    for kw in (dict(q_out=z(3, 4, 64)), dict(q_pe=z(3, 4, 32)), dict(q_pe=z(2, 4, 64)), dict(page_size=96),
+               dict(q_pe=z(3, 4, 64), q_out=z(3, 5, 64)), dict(kv_c=z(512, 3).t()), dict(error_word=z(1))):
+        with pytest.raises(ValueError):
+            mla.mla_nvfp4_fp8_cache_append(**dict(good, **kw))
+    with pytest.raises(mla.MLAError):  # rows that are not 16-byte aligned
+        mla.mla_nvfp4_fp8_cache_append(**dict(good, kv_c=z(3, 513)[:, :512]))
+    dec = dict(q=z(1, 16, 576), cache=cache, scales=scales, softmax_scale=0.1, page_table=z(1, 2, dt=i32), seq_lens=z(1, dt=i32))
+    for kw in (dict(q=z(1, 16, 512)), dict(q=z(1, 16, 1152)[:, :, :576]), dict(seq_lens=z(2, dt=i32)), dict(page_size=0),
+               dict(out=z(1, 16, 576)), dict(lse=z(1, 8, dt=torch.float32)), dict(workspace=z(8, dt=torch.float32)),
+               dict(split=False, workspace=z(1 << 20, dt=torch.uint8))):
+        with pytest.raises(ValueError):
+            mla.mla_nvfp4_fp8_decode(**dict(dec, **kw))
+    for kw in (dict(softmax_scale=0.0), dict(softmax_scale=math.nan), dict(workspace=z(64, dt=torch.uint8))):
+        with pytest.raises(mla.MLAError):
+            mla.mla_nvfp4_fp8_decode(**dict(dec, **kw))
+    for bad in (z(4), z(4, 8, dt=torch.float16), z(8, 4).t()):
+        with pytest.raises(ValueError):
+            mla.mla_nvfp4_fp8_quantize(bad)
+    with pytest.raises(mla.MLAError):
+        mla.mla_nvfp4_fp8_quantize(z(4, 12))
+    a, sa = z(4, 256, dt=torch.uint8).view(F8), z(4, 2, dt=torch.float32)
+    w, sw = z(130, 256, dt=torch.uint8).view(F8), z(2, 2, dt=torch.float32)
+    for args in ((a, sa, w[:, :240], sw), (a, sa[:, :1], w, sw), (a, sa, w, sw[:1]), (a, sa.t(), w, sw)):
+        with pytest.raises(ValueError):
+            mla.mla_nvfp4_fp8_gemm(*args)
+    with pytest.raises(ValueError):
+        mla.mla_nvfp4_fp8_gemm(a, sa, w, sw, out=z(4, 131))
+    # nothing to do
+    assert mla.mla_nvfp4_fp8_gemm(a[:0], sa[:0], w, sw).shape == (0, 130)
+    assert mla.mla_nvfp4_fp8_quantize(z(0, 128))[1].shape == (0, 1)
+    assert mla.mla_nvfp4_fp8_decode(**dict(dec, q=z(0, 16, 576), page_table=z(0, 2, dt=i32), seq_lens=z(0, dt=i32))).shape == (0, 16, 512)
+    mla.mla_nvfp4_fp8_cache_append(**dict(good, kv_c=z(0, 512), k_pe=z(0, 64)))
+    torch.cuda.synchronize()
