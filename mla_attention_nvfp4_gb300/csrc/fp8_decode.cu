@@ -255,14 +255,20 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
     scan[2 * warp + 1] = most;
   }
   __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[2 * w];
-    total += scan[2 * w];
-    most = max(most, static_cast<int>(scan[2 * w + 1]));
+  int64_t all = lane < kThreads / 32 ? scan[2 * lane] : 0;
+  most = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? static_cast<int>(scan[2 * lane + 1]) : 0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += v;
   }
-  const int64_t per = (total + p.ranges - 1) / p.ranges;
+  const int64_t total = __shfl_sync(0xffffffffu, all, 31);
+  const int64_t before = warp > 0 ? __shfl_sync(0xffffffffu, all, max(warp - 1, 0)) : 0;
+  // (64-bit division only where it is needed)
+  auto divide = [](int64_t a, int64_t b) {
+    return (a | b) >> 31 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+  };
+  const int64_t per = divide(total + p.ranges - 1, p.ranges);
   // A CTA each for whole sequences, where that takes no longer than equal
   // ranges: those begin two pieces (of one sequence's end and the next one's
   // start), and the cut ones are merged.
@@ -278,7 +284,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   for (int b = first; b < last; ++b) {
     const int n = tiles_of(clipped_len(p.a, b));
     if (publish) {
-      const int r0 = n > 0 ? static_cast<int>(off / per) : 0, r1 = n > 0 ? static_cast<int>((off + n - 1) / per) : -1;
+      const int r0 = n > 0 ? static_cast<int>(divide(off, per)) : 0, r1 = n > 0 ? static_cast<int>(divide(off + n - 1, per)) : -1;
       p.cuts[b] = uncut ? make_int2(b, n > 0 ? 1 : 0) : make_int2(r0, (r1 - r0 + 1) | (r0 * per < off ? 1 << 30 : 0));
     }
     if (!uncut && t0 >= off && t0 < off + n) {
@@ -370,12 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = page_of(i + 32);
           y = static_cast<int>(slot < 0 ? p.a.num_slots : slot);
           scale = slot < 0 ? 0.f : p.a.scales[slot / kBlock];
-          const bool good = scale >= kScaleMin && scale <= kScaleMax;
-          if (i < n_blocks && !good) flag_error(err, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
-          if (!good) scale = 0.f;
         }
         const int y0 = __shfl_sync(0xffffffffu, y, at), y1 = __shfl_sync(0xffffffffu, y, at + 1);
-        const float sc0 = __shfl_sync(0xffffffffu, scale, at), sc1 = __shfl_sync(0xffffffffu, scale, at + 1);
         if (lane == 0) {
 #pragma unroll 1
           for (int d = 0; d < 4 && ok; ++d) {
@@ -385,13 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(&ms.full[i], kChunkBytes);
             tma_load_bytes(slot_addr(i), &tm_lat, 128 * d, y0, &ms.full[i]);
             tma_load_bytes(slot_addr(i) + kChunkBytes / 2, &tm_lat, 128 * d, y1, &ms.full[i]);
-            if (d == 0) {
-              // tile n - 4, whose place this is, is done: this chunk took
-              // the place of one of tile n - 3 or a later one
-              ms.scale[n % C::info][0] = sc0;
-              ms.scale[n % C::info][1] = sc1;
-              mbar_arrive(&ms.info_full[n % C::info]);
-            }
           }
           if (ok) {
             const int i = n % C::ropes;
@@ -403,6 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_bytes(dst + kRopeBytes / 2, &tm_rope, MLA_D_LATENT, y1, &ms.rfull[i]);
             }
           }
+        }
+        // the blocks' scales (waited for after the copies); tile n - 4, whose
+        // place they take, is done: this tile's chunks took those of tile n - 3
+        // or a later one
+        if (at == 0) {
+          const bool block = 2 * t + lane < n_blocks, good = scale >= kScaleMin && scale <= kScaleMax;
+          if (block && !good) flag_error(err, y == p.a.num_slots ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
+          if (!good) scale = 0.f;
+        }
+        const float sc0 = __shfl_sync(0xffffffffu, scale, at), sc1 = __shfl_sync(0xffffffffu, scale, at + 1);
+        if (lane == 0 && ok) {
+          ms.scale[n % C::info][0] = sc0;
+          ms.scale[n % C::info][1] = sc1;
+          mbar_arrive(&ms.info_full[n % C::info]);
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       }
@@ -532,68 +541,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < 8) v[2] = src[lane + 64];
         }
       };
-      uint4 v_next[3], v_after[3];
-      load_head(hb + quad, v_next);
-      load_head(hb + quad + 4, v_after);
+      // two heads at a time, the next two's loads in flight
+      uint4 v_next[2][3];
+      load_head(hb + quad, v_next[0]);
+      load_head(hb + quad + 4, v_next[1]);
 #pragma unroll 1
-      for (int h = hb + quad; h < hb + kMine; h += 4) {
-        uint4 v[3];
+      for (int h2 = hb + quad; h2 < hb + kMine; h2 += 8) {
+        uint4 v_now[2][3];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          v[k] = v_next[k];
-          v_next[k] = v_after[k];
-        }
-        load_head(h + 8, v_after);
-        // amax from the bf16 bits (sign dropped, they order like integers)
-        uint32_t m2 = 0;
+        for (int i = 0; i < 6; ++i) v_now[i / 3][i % 3] = v_next[i / 3][i % 3];
+        load_head(h2 + 8, v_next[0]);
+        load_head(h2 + 12, v_next[1]);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            m2 = max(m2, w[j] & 0x7FFF0000u);
-            m2 = max(m2, (w[j] << 16) & 0x7FFF0000u);
+        for (int two = 0; two < 2; ++two) {
+          const int h = h2 + 4 * two;
+          const uint4(&v)[3] = v_now[two];
+          // amax from the bf16 bits (sign dropped, they order like integers)
+          uint32_t m2 = 0;
+  #pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              m2 = max(m2, w[j] & 0x7FFF0000u);
+              m2 = max(m2, (w[j] << 16) & 0x7FFF0000u);
+            }
           }
-        }
-        m2 = __reduce_max_sync(0xffffffffu, m2);
-        // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8)
-        int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        ex = max(-60, min(60, ex));
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-        if (lane == 0)
-          ms.c[h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          // in f16 pairs: 8 significant bits down to 2^-17, then steps of 2^-24
-          uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x0, x1;
-            bf16x2_to_f32(w[j], x0, x1);
-            const __half2 xh = __floats2half2_rn(x0 * inv, x1 * inv);
-            const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
-            const uint32_t a = cvt_e4m3x2_h2(xu);
-            w1[j >> 1] |= a << (16 * (j & 1));
-            w2[j >> 1] |= cvt_e4m3x2_h2(h2_sub(xu, e4m3x2_to_f16x2_pair(a))) << (16 * (j & 1));
-          }
-          // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
-          uint32_t a1, a2;
-          if (k < 2) {
-            const int feature = 256 * k + 8 * lane;
-            const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
-            const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
-            a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
-            a2 = a1 + kH * 128;
-          } else {
-            const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
-            const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
-            a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
-            a2 = a1 + kH * 64;
-          }
-          if (k < 2 || lane < 8) {
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a1), "r"(w1[0]), "r"(w1[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a2), "r"(w2[0]), "r"(w2[1]) : "memory");
+          m2 = __reduce_max_sync(0xffffffffu, m2);
+          // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8)
+          int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+          ex = max(-60, min(60, ex));
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          if (lane == 0)
+            ms.c[h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+  #pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            // in f16 pairs: 8 significant bits down to 2^-17, then steps of 2^-24
+            uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float x0, x1;
+              bf16x2_to_f32(w[j], x0, x1);
+              const __half2 xh = __floats2half2_rn(x0 * inv, x1 * inv);
+              const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
+              const uint32_t a = cvt_e4m3x2_h2(xu);
+              w1[j >> 1] |= a << (16 * (j & 1));
+              w2[j >> 1] |= cvt_e4m3x2_h2(h2_sub(xu, e4m3x2_to_f16x2_pair(a))) << (16 * (j & 1));
+            }
+            // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
+            uint32_t a1, a2;
+            if (k < 2) {
+              const int feature = 256 * k + 8 * lane;
+              const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
+              const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
+              a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
+              a2 = a1 + kH * 128;
+            } else {
+              const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
+              const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
+              a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
+              a2 = a1 + kH * 64;
+            }
+            if (k < 2 || lane < 8) {
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a1), "r"(w1[0]), "r"(w1[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a2), "r"(w2[0]), "r"(w2[1]) : "memory");
+            }
           }
         }
       }
@@ -688,10 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < kMine; h += 4) {
             const float4 mv = *reinterpret_cast<const float4*>(&ms.move[k & 1][hb + h]);
             const float by[4] = {mv.x, mv.y, mv.z, mv.w};
+            if (by[0] != 0.f || by[1] != 0.f || by[2] != 0.f || by[3] != 0.f) {  // the same in all threads
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[h + j] -= by[j];
-              l[h + j] = set ? l[h + j] * ex2_approx(-by[j]) : 0.f;
+              for (int j = 0; j < 4; ++j) {
+                x[h + j] -= by[j];
+                l[h + j] = set ? l[h + j] * ex2_approx(-by[j]) : 0.f;
+              }
             }
           }
           set = true;

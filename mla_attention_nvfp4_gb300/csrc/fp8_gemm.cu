@@ -614,11 +614,36 @@ bool encode_byte_map(CUtensorMap* map, const void* base, int64_t width, int64_t 
 int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
   const int kb = static_cast<int>((a.K + kGroup - 1) / kGroup);
   const int64_t tm = (a.M + kBM - 1) / kBM, tn = (a.N + kBN - 1) / kBN;
-  // Large tiles where they fill the SMs, the streaming form otherwise.
-  const bool large = a.M > 128 && tm * tn >= num_sms;
-  const int kt = large ? kBM : a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  const int kt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;  // tokens of the streaming form's tile
+  const int64_t sn = (a.N + 127) / 128, sm = (a.M + kt - 1) / kt;
+
+  // Which form, and into how many parts K is cut, by an estimate in K blocks
+  // of one CTA's time.  A CTA of either form takes about as long for a K block
+  // (0.57 us), however many share its SM, until together they take what HBM
+  // gives (kPerBlock blocks of 128 weights x 128 in the time of one); a wave
+  // of CTAs costs kOverhead blocks more.  Clusters do not fill every place an
+  // SM offers: nine tenths count.  Measured, N 7168, K 16384: 64 rows, 34 us
+  // with 2 parts, 25 with 4 (one wave each), 30 with 8 (two waves); 16 rows,
+  // 24 with 4, 28 with 8; 512 rows, 116 us streaming in 2 parts, 74 as large
+  // tiles; 128 rows, 39 us streaming, and large tiles would take 74.
+  constexpr int kOverhead = 6, kPerBlock = 200;
+  const int64_t places = static_cast<int64_t>(num_sms) * (kt <= 32 ? 3 : kt == 64 ? 2 : 1) * 9 / 10;
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
+    const int64_t waves = (sn * sm * s + places - 1) / places;
+    int64_t cost = waves * ((kb + s - 1) / s);
+    if (cost < sn * sm * kb / kPerBlock) cost = sn * sm * kb / kPerBlock;
+    cost += waves * kOverhead;
+    if (cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  // More tiles than a grid's second and third dimensions hold are large ones.
+  const bool large = sn > 65535 || sm > 65535 || (a.M > 64 && (tm * tn + num_sms - 1) / num_sms * kb + kOverhead < best);
   CUtensorMap tm_a, tm_w;
-  if (!encode_byte_map(&tm_a, a.a, a.K, a.M, a.lda, kGroup, static_cast<uint32_t>(kt), false) ||
+  if (!encode_byte_map(&tm_a, a.a, a.K, a.M, a.lda, kGroup, static_cast<uint32_t>(large ? kBM : kt), false) ||
       !encode_byte_map(&tm_w, a.w, a.K, a.N, a.ldw, kGroup, large ? kBN : 128, false)) {
     set_last_error("cuTensorMapEncodeTiled failed for the GEMM operands");
     return MLA_ERR_LAUNCH;
@@ -634,26 +659,8 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
     fp8_gemm_kernel<<<grid, kThreads, kSmAlloc, stream>>>(tm_a, tm_w, p);
     return launch_status();
   }
-  const int64_t sn = (a.N + 127) / 128, sm = (a.M + kt - 1) / kt;
-  if (sn > 65535 || sm > 65535) return MLA_ERR_INVALID_ARG;
   p.tiles_m = static_cast<int>(sm);
   p.tiles_n = static_cast<int>(sn);
-  // Split K so that the busiest SM has the fewest K blocks to stream; a wave
-  // of CTAs costs kOverhead blocks more.  Clusters of several CTAs do not fill
-  // every place an SM offers: nine tenths count.  (64 rows, N 7168, K 16384:
-  // 25 us with 4 parts, one wave; 30 with 8, two.  16 rows: 23 with 5 or 6.)
-  constexpr int kOverhead = 3;
-  const int64_t places = static_cast<int64_t>(num_sms) * (kt <= 32 ? 3 : kt == 64 ? 2 : 1) * 9 / 10;
-  int splits = 1;
-  int64_t best = INT64_MAX;
-  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
-    const int64_t ctas = sn * sm * s, wave = ctas < places ? ctas : places;
-    const int64_t cost = (ctas + places - 1) / places * ((wave + num_sms - 1) / num_sms * ((kb + s - 1) / s) + kOverhead);
-    if (cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
   switch (kt) {
     case 16: return launch_small<16>(tm_a, tm_w, p, splits, 15, stream);
     case 32: return launch_small<32>(tm_a, tm_w, p, splits, 16, stream);
