@@ -67,6 +67,11 @@ constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest we
 constexpr float kGain = 16.f;   // 32 heads: the first term's rounding error, at most 16, becomes 256
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
+// The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
+// a sequence on.  1 x 65536 keys, 128 heads: 37.5 us in all (49.2 with 2 warps
+// a row; kSub 4: 38.3, 16: 37.5); 2 x 32768: 41.3 (48.6); 4 x 16384, at 19
+// ranges a sequence: 42.7 (41.1).
+constexpr int kSub = 8, kManyPieces = 24;
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64;
 constexpr uint32_t kColS = 256;  // TMEM: O^T in columns 0..255 (64 per value chunk), then two S^T of 2 kH (q1 | q2)
 
@@ -914,12 +919,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of the pieces of cut sequences, in range order, by LSE; sequences
-// without keys get their zeros here.  Warp = half the features of one
-// (sequence, head), 8 a lane.
-template <int kH>
-__global__ void __launch_bounds__(256) fp8_decode_merge_kernel(const Params p) {
+// without keys get their zeros here.  kSub warps = half the features of one
+// (sequence, head), 8 a lane; each takes every kSub-th piece.
+template <int kSub>
+constexpr int merge_threads = kSub > 1 ? 64 * kSub : 256;
+template <int kH, int kSub>
+__global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
-  const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * merge_threads<kSub> + threadIdx.x) / (32 * kSub);
+  const int sub = kSub > 1 ? (threadIdx.x >> 5) % kSub : 0;
   const int64_t row = id >> 1;
   if (row >= static_cast<int64_t>(p.a.batch) * p.a.num_heads) return;
   const int b = static_cast<int>(row / p.a.num_heads), h = static_cast<int>(row - static_cast<int64_t>(b) * p.a.num_heads);
@@ -942,7 +950,7 @@ __global__ void __launch_bounds__(256) fp8_decode_merge_kernel(const Params p) {
     const float w_mine = ex2_approx(lse_of(base + lane) - ref);
     const int count = min(32, n - base);
 #pragma unroll 4
-    for (int j = 0; j < count; ++j) {
+    for (int j = sub; j < count; j += kSub) {
       const float w = __shfl_sync(0xffffffffu, w_mine, j);
       const int i = base + j;
       const float4* o = reinterpret_cast<const float4*>(
@@ -953,6 +961,20 @@ __global__ void __launch_bounds__(256) fp8_decode_merge_kernel(const Params p) {
       acc[2] = fmaf(w, u.z, acc[2]), acc[3] = fmaf(w, u.w, acc[3]);
       acc[4] = fmaf(w, v.x, acc[4]), acc[5] = fmaf(w, v.y, acc[5]);
       acc[6] = fmaf(w, v.z, acc[6]), acc[7] = fmaf(w, v.w, acc[7]);
+    }
+  }
+  if (kSub > 1) {  // (one row a CTA: its warps left above together or are all here)
+    __shared__ float part[2 * kSub][9][32];
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[warp][k][lane] = acc[k];
+    part[warp][8][lane] = sum;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int s = 1; s < kSub; ++s) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += part[warp + s][k][lane];
+      sum += part[warp + s][8][lane];
     }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
@@ -992,8 +1014,12 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   fp8_decode_kernel<kH><<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
   if (const int st = launch_status()) return st;
   if (!p.split) return MLA_OK;
-  const int64_t warps = 2 * static_cast<int64_t>(p.a.num_heads) * p.a.batch;
-  fp8_decode_merge_kernel<kH><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(p);
+  // A CTA a row where the rows are cut into many pieces.
+  const int64_t rows = static_cast<int64_t>(p.a.num_heads) * p.a.batch;
+  if (p.ranges >= kManyPieces * p.a.batch)
+    fp8_decode_merge_kernel<kH, kSub><<<static_cast<unsigned>(rows), merge_threads<kSub>, 0, stream>>>(p);
+  else
+    fp8_decode_merge_kernel<kH, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(p);
   return launch_status();
 }
 
