@@ -43,6 +43,25 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// One lane of a converged warp.  Loops that issue products are run by the
+// whole warp, their descriptors made of values that the compiler knows to be
+// the warp's (uniform), and only the issue itself is one lane's: in a branch
+// of one lane each operand is moved to a uniform register by itself, which
+// takes longer than a product of 64 columns.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // Instruction descriptor of kind::f8f6f4, e4m3 operands (format 0), fp32
 // accumulator: the fields of idesc_f32acc.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {

@@ -99,8 +99,9 @@ struct Misc {
   alignas(16) float move[2][kH];  // what a tile raises the references by, in turn
   alignas(16) float inv[kH];      // a piece's references, then 1 / its sums
   alignas(16) float sums[4][kH];
-  int top[kH];            // a head's maximum, as an integer that orders like it
+  int top[kH];            // a hit head's maximum, as an integer that orders like it
   uint32_t raised[2][2];  // heads (of either half) whose part of O is to be rescaled
+  uint32_t hits[2], moves[2];  // heads (of either half) that may have to be raised; that are
   float scale[C::info][2];  // of a tile's two blocks; 0: the block is no part of the sequence
   int64_t t0, t1, off0;
   int b0;
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     ms.abort = 0;
+    ms.hits[0] = ms.hits[1] = 0;
     ms.b0 = 0;  // a range without tiles has no first sequence
     ms.off0 = 0;
 #pragma unroll 1
@@ -423,74 +425,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- score products
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, 2 * kH, false, false);
-      const uint64_t dq = smem_desc_sw128(s0 + C::off_q, 0, 1024);
-      const uint64_t dq_rope = smem_desc_sw64(s0 + C::off_q + 4 * C::q_chunk, 512);
-      bool ok = true;
-      auto ready = [&](uint64_t* bar, int parity) {
-        ok = ok && wait(bar, parity, err, &ms.abort);
-        return ok;
-      };
-      int n = 0, piece = 0;
-      for (Pieces it(p, ms, range); ok && it.next(p);) {
-        const int s = it.s, e = it.e;
-        if (s >= e) continue;
-        if (!ready(&ms.q_ready, piece & 1)) break;
+    constexpr uint32_t idesc = idesc_e4m3(128, 2 * kH, false, false);
+    const uint64_t dq = smem_desc_sw128(s0 + C::off_q, 0, 1024);
+    const uint64_t dq_rope = smem_desc_sw64(s0 + C::off_q + 4 * C::q_chunk, 512);
+    bool ok = true;
+    auto ready = [&](uint64_t* bar, int parity) {
+      ok = __all_sync(0xffffffffu, ok && wait(bar, parity, err, &ms.abort));
+      return ok;
+    };
+    int n = 0, piece = 0;
+    for (Pieces it(p, ms, range); ok && it.next(p);) {
+      const int s = it.s, e = it.e;
+      if (s >= e) continue;
+      if (!ready(&ms.q_ready, piece & 1)) break;
 #pragma unroll 1
-        for (int t = s; t < e; ++t, ++n) {
-          const uint32_t d = tmem + kColS + (n & 1) * 2 * kH;
-          if (!ready(&ms.s_free[n & 1], ((n >> 1) & 1) ^ 1)) break;
+      for (int t = s; t < e; ++t, ++n) {
+        const uint32_t d = uniform(tmem + kColS + (n & 1) * 2 * kH);
+        if (!ready(&ms.s_free[n & 1], ((n >> 1) & 1) ^ 1)) break;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const int k = 4 * n + c, i = k % C::slots;
-            if (!ready(&ms.full[i], (k / C::slots) & 1)) break;
-            tc_fence_after();
-            const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024), db = dq + c * (C::q_chunk >> 4);
+        for (int c = 0; c < 4; ++c) {
+          const int k = 4 * n + c, i = uniform(k % C::slots);
+          if (!ready(&ms.full[i], (k / C::slots) & 1)) break;
+          tc_fence_after();
+          const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024), db = dq + uniform(c) * (C::q_chunk >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
           }
-          const int i = n % C::ropes;
-          if (!ready(&ms.rfull[i], (n / C::ropes) & 1)) break;
-          tc_fence_after();
-          const uint64_t da = smem_desc_sw64(s0 + C::off_rope + i * kRopeBytes, 512);
+          __syncwarp();
+        }
+        const int i = uniform(n % C::ropes);
+        if (!ready(&ms.rfull[i], (n / C::ropes) & 1)) break;
+        tc_fence_after();
+        const uint64_t da = smem_desc_sw64(s0 + C::off_rope + i * kRopeBytes, 512);
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, dq_rope + 2 * j, idesc, 1u);
           mma_commit(&ms.rempty[i]);
           mma_commit(&ms.s_full[n & 1]);
         }
-        ++piece;
+        __syncwarp();
       }
+      ++piece;
     }
   } else if (warp == 14) {
     // -------------------------------------------------------- value products
-    if (lane == 0) {
-      const uint64_t dp = smem_desc_sw64(s0 + C::off_p, 512);
-      bool ok = true;
-      int n = 0, piece = 0, k = 0;  // tiles, pieces, tiles that are no piece's first
-      for (Pieces it(p, ms, range); ok && it.next(p);) {
-        const int s = it.s, e = it.e;
-        if (s >= e) continue;
+    const uint64_t dp = smem_desc_sw64(s0 + C::off_p, 512);
+    bool ok = true;
+    auto ready = [&](uint64_t* bar, int parity) {
+      ok = __all_sync(0xffffffffu, ok && wait(bar, parity, err, &ms.abort));
+    };
+    int n = 0, piece = 0, k = 0;  // tiles, pieces, tiles that are no piece's first
+    for (Pieces it(p, ms, range); ok && it.next(p);) {
+      const int s = it.s, e = it.e;
+      if (s >= e) continue;
 #pragma unroll 1
-        for (int t = s; t < e; ++t, ++n) {
-          ok = ok && wait(&ms.p_ready, n & 1, err, &ms.abort);
-          // O as it is to be added to: the previous piece's read, this one's
-          // rescaled
-          if (t > s) {
-            ok = ok && wait(&ms.rescaled[k & 1], (k >> 1) & 1, err, &ms.abort);
-            ++k;
-          } else if (piece > 0) {
-            ok = ok && wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
-          }
-          if (!ok) break;
-          tc_fence_after();
+      for (int t = s; t < e; ++t, ++n) {
+        ready(&ms.p_ready, n & 1);
+        // O as it is to be added to: the previous piece's read, this one's
+        // rescaled
+        if (t > s) {
+          ready(&ms.rescaled[k & 1], (k >> 1) & 1);
+          ++k;
+        } else if (piece > 0) {
+          ready(&ms.o_free, (piece - 1) & 1);
+        }
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const int i = (4 * n + c) % C::slots;
-            // V^T: 128 features of the chunk as rows, 32 keys (4096 bytes) a
-            // step.  The scores of this tile are done (P came of them), so
-            // the chunk is free after these.
-            const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
+        for (int c = 0; c < 4; ++c) {
+          const int i = uniform((4 * n + c) % C::slots);
+          // V^T: 128 features of the chunk as rows, 32 keys (4096 bytes) a
+          // step.  The scores of this tile are done (P came of them), so
+          // the chunk is free after these.
+          const uint64_t da = smem_desc_sw128(slot_addr(i), 0, 1024);
+          const uint32_t d = uniform(tmem + 64 * c);
+          if (elect_one()) {
 #pragma unroll
             for (int term = 0; term < C::terms; ++term) {
               // e4m3 x e4m3, or e4m3 x e5m2 (format 1) for the second term
@@ -498,14 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t db = dp + term * (kTile * 64 >> 4);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_e4m3(tmem + 64 * c, da + 256 * j, db + 128 * j, idesc, (t > s || term > 0 || j > 0) ? 1u : 0u);
+                mma_e4m3(d, da + 256 * j, db + 128 * j, idesc, (t > s || term > 0 || j > 0) ? 1u : 0u);
             }
             mma_commit(&ms.empty[i]);
+            if (c == 3) mma_commit(&ms.pv_done);
           }
-          mma_commit(&ms.pv_done);
+          __syncwarp();
         }
-        ++piece;
       }
+      ++piece;
     }
   } else if (warp < 10) {
     // ---------------------------------------------------- queries, softmax
@@ -667,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int h = 0; h < kMine; ++h) top = fmaxf(top, x[h]);
-        if (half_any(wg, top + lsb > kTop || (!set && valid))) {
-          // Raise the references of the heads that need it.  A head's
-          // maximum: halves exchanged until lane i holds head
+        // Raise the references of the heads that need it.
+        const bool any = __any_sync(0xffffffffu, top + lsb > kTop || (!set && valid));
+        if (any) {
+          // A head's maximum: halves exchanged until lane i holds head
           // i * kMine / 32 of the warp's keys, then over the warps.
           float f[kMine / 2];
 #pragma unroll
@@ -685,28 +697,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          atomicMax(&ms.top[hb + lane * kMine / 32], ordered(f[0] + lsb));
-          half_bar(wg);
+          if (!set || f[0] + lsb > kTop) {
+            const int h = lane * kMine / 32;
+            atomicMax(&ms.top[hb + h], ordered(f[0] + lsb));
+            atomicOr(&ms.hits[wg], 1u << h);
+          }
+        }
+        if (half_any(wg, any)) {
           if (tid < 32) {
-            bool raise = false;
-            if (tid < kMine) {
-              const float mx = from_ordered(ms.top[hb + tid]);
-              raise = isfinite(mx) && (!set || mx > kTop);
-              const float by = raise ? mx - kReset : 0.f;
-              ms.move[k & 1][hb + tid] = by;
-              mr[tid] += by;
-              ms.top[hb + tid] = ordered(-INFINITY);
+            const bool hit = (ms.hits[wg] >> lane & 1) != 0;
+            const float mx = hit ? from_ordered(ms.top[hb + lane]) : 0.f;
+            const bool raise = hit && isfinite(mx) && (!set || mx > kTop);
+            const float by = raise ? mx - kReset : 0.f;
+            if (lane < kMine) ms.move[k & 1][hb + lane] = by;
+            if (raise) mr[lane] += by;
+            if (hit) ms.top[hb + lane] = ordered(-INFINITY);
+            const uint32_t raised = __ballot_sync(0xffffffffu, raise);
+            if (lane == 0) {
+              ms.hits[wg] = 0;
+              ms.moves[wg] = raised;
+              // without earlier keys O is zero (or yet to be written)
+              ms.raised[k & 1][wg] = set ? raised : 0;
             }
-            // without earlier keys O is zero (or yet to be written)
-            const uint32_t raised = __ballot_sync(0xffffffffu, raise && set);
-            if (lane == 0) ms.raised[k & 1][wg] = raised;
           }
           half_bar(wg);
+          const uint32_t moves = ms.moves[wg];
 #pragma unroll
           for (int h = 0; h < kMine; h += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(&ms.move[k & 1][hb + h]);
-            const float by[4] = {mv.x, mv.y, mv.z, mv.w};
-            if (by[0] != 0.f || by[1] != 0.f || by[2] != 0.f || by[3] != 0.f) {  // the same in all threads
+            if (moves >> h & 15) {
+              const float4 mv = *reinterpret_cast<const float4*>(&ms.move[k & 1][hb + h]);
+              const float by[4] = {mv.x, mv.y, mv.z, mv.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 x[h + j] -= by[j];
