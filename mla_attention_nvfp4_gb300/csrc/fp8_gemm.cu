@@ -206,27 +206,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_bytes(s0 + s * kStageBytes + kABytes, &tm_w, kb * kGroup, nt * kBN, &bars.full[s]);
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 || warp == 2) {
+      // An issuer for each accumulator, every other K block: one alone takes
+      // longer to get from one block's products to the next one's (its waits
+      // and commits, about 900 cycles) than these run (520).
       constexpr uint32_t idesc = idesc_e4m3(kBM, kBN, false, false);
-      int it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
-          const int s = it % kStages, buf = it & 1;
-          if (!mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s) ||
-              !mbar_wait(&bars.full[s], (it / kStages) & 1, err, &abort_s)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t da = smem_desc_sw128(s0 + s * kStageBytes, 0, 1024);
-          const uint64_t db = smem_desc_sw128(s0 + s * kStageBytes + kABytes, 0, 1024);
+      const int buf = uniform(warp - 1);
+      const uint32_t d = uniform(tmem + buf * kBN);
+      const int mine = n_tiles > static_cast<int>(blockIdx.x) ? (n_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+      const int64_t blocks = static_cast<int64_t>(mine) * p.kb;
+      for (int64_t i = buf; i < blocks; i += 2) {
+        const uint32_t it = static_cast<uint32_t>(i);
+        const int s = uniform(it % kStages);
+        const uint64_t da = smem_desc_sw128(s0 + s * kStageBytes, 0, 1024);
+        const uint64_t db = smem_desc_sw128(s0 + s * kStageBytes + kABytes, 0, 1024);
+        // (a stage is always the same issuer's, so its phases come in turn)
+        static_assert(kStages % 2 == 0, "stages alternate between the issuers");
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.full[s], (it / kStages) & 1, err, &abort_s) &&
+                                         mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s)))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)  // 32 bytes a step along the swizzled row
-            mma_e4m3(tmem + buf * kBN, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
-          mma_commit(&bars.empty[s]);
+            mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
           mma_commit(&bars.acc_full[buf]);
+          mma_commit(&bars.empty[s]);
         }
+        __syncwarp();
       }
     }
   } else {
@@ -249,31 +256,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // scales two blocks ahead of their use (multiplied only there)
       const int last = p.kb - 1;
       float a0 = as[0], w0 = ws[0], a1 = as[min(1, last)], w1 = ws[min(1, last)];
-      for (int kb = 0; kb < p.kb; ++kb, ++it) {
-        const int buf = it & 1;
-        const float a2 = as[min(kb + 2, last)], w2 = ws[min(kb + 2, last)];
-        if (!mbar_wait(&bars.acc_full[buf], (it >> 1) & 1, err, &abort_s)) {
-          ok = false;
-          break;
-        }
+      // 32 columns at a time, the next ones' load under the current ones' sums
+      // (the next block's too)
+      uint32_t v[32], u[32];
+      auto add = [&](const uint32_t(&x)[32], int c, float sc) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(x[i]), sc, acc[32 * c + i]);
+      };
+      auto filled = [&](int at) {
+        if (!mbar_wait(&bars.acc_full[at & 1], (at >> 1) & 1, err, &abort_s)) return false;
         tc_fence_after();
+        return true;
+      };
+      ok = filled(it);
+      if (ok) {
+        tmem_ld32(src + (it & 1) * kBN, v);
+        tmem_ld_wait(v);
+      }
+      for (int kb = 0; ok && kb < p.kb; ++kb, ++it) {
+        const uint32_t at = src + (it & 1) * kBN;
+        const float a2 = as[min(kb + 2, last)], w2 = ws[min(kb + 2, last)];
         const float sc = a0 * w0;
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t v[32], u[32];
-          tmem_ld32(src + buf * kBN + 32 * c, v);
-          tmem_ld32(src + buf * kBN + 32 * c + 32, u);
-          tmem_ld_wait();
-          if (c == 2) {  // the accumulator may be filled again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), sc, acc[32 * c + i]);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + 32 + i] = fmaf(__uint_as_float(u[i]), sc, acc[32 * c + 32 + i]);
+        tmem_ld32(at + 32, u);
+        add(v, 0, sc);
+        tmem_ld_wait(u);
+        tmem_ld32(at + 64, v);
+        add(u, 1, sc);
+        tmem_ld_wait(v);
+        tmem_ld32(at + 96, u);
+        add(v, 2, sc);
+        tmem_ld_wait(u);
+        tc_fence_before();  // the accumulator may be filled again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.acc_empty[it & 1]);
+        const bool more = kb < last;
+        if (more) {
+          ok = filled(it + 1);
+          if (ok) tmem_ld32(src + ((it + 1) & 1) * kBN, v);
         }
+        add(u, 3, sc);
+        if (more) tmem_ld_wait(v);
         a0 = a1;
         w0 = w1;
         a1 = a2;
@@ -310,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // weights stream through; the K blocks of a tile are split over a cluster's
 // CTAs, whose fp32 sums are added through distributed shared memory in rank
 // order.
-//   warp 0 producer, warp 1 MMA issuer, then four warps of sums per 64 tokens:
-//   thread = weight row.
+//   warp 0 producer, warp 1 and the last one MMA issuers, between them four
+//   warps of sums per 64 tokens: thread = weight row.
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplits = 8;   // portable cluster size
 constexpr int kScaleBlocks = 16;  // K blocks whose scales are staged at a time
@@ -319,7 +341,7 @@ constexpr int kScaleBlocks = 16;  // K blocks whose scales are staged at a time
 template <int kT>
 struct Small {
   static constexpr int halves = kT == 128 ? 2 : 1, tokens = kT / halves;  // groups of sum warps, tokens of each
-  static constexpr int threads = 64 + 128 * halves;
+  static constexpr int sum_threads = 128 * halves, threads = 96 + sum_threads;
   static constexpr int resident = kT <= 32 ? 3 : kT == 64 ? 2 : 1;  // CTAs an SM holds
   static constexpr int stages = kT == 16 ? 4 : kT == 32 ? 3 : kT == 64 ? 4 : 6;
   static constexpr uint32_t w_bytes = 128 * kGroup, t_bytes = kT * kGroup, stage_bytes = w_bytes + t_bytes;
@@ -402,25 +424,33 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
         tma_load_bytes(s0 + s * S::stage_bytes + S::w_bytes, &tm_a, kb * kGroup, m0, &bars.full[s]);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, kT, false, false);
-      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-        const int s = it % S::stages, buf = it & 1;
-        if (!mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s) ||
-            !mbar_wait(&bars.full[s], (it / S::stages) & 1, err, &abort_s))
-          break;
-        tc_fence_after();
-        const uint64_t da = smem_desc_sw128(s0 + s * S::stage_bytes, 0, 1024);
-        const uint64_t db = smem_desc_sw128(s0 + s * S::stage_bytes + S::w_bytes, 0, 1024);
+  } else if (warp == 1 || warp == S::threads / 32 - 1) {
+    // an issuer for each accumulator, as above
+    constexpr uint32_t idesc = idesc_e4m3(128, kT, false, false);
+    const int buf = uniform(warp == 1 ? 0 : 1);
+    const uint32_t d = uniform(tmem + buf * kT);
+    for (int it = buf; it < kb1 - kb0; it += 2) {
+      const int s = uniform(it % S::stages);
+      const uint64_t da = smem_desc_sw128(s0 + s * S::stage_bytes, 0, 1024);
+      const uint64_t db = smem_desc_sw128(s0 + s * S::stage_bytes + S::w_bytes, 0, 1024);
+      // The accumulator first: that block it - 2 is summed says that every
+      // earlier block is in, so that the stage's phase is this block's or the
+      // one before (an odd number of stages gives a stage to both issuers in
+      // turn, and a wait tells phases apart by their parity alone).
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.acc_empty[buf], ((it >> 1) & 1) ^ 1, err, &abort_s) &&
+                                       mbar_wait(&bars.full[s], (it / S::stages) & 1, err, &abort_s)))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_e4m3(tmem + buf * kT, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
-        mma_commit(&bars.empty[s]);
+        for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
         mma_commit(&bars.acc_full[buf]);
+        mma_commit(&bars.empty[s]);
       }
+      __syncwarp();
     }
   } else {
-    constexpr int kSumThreads = S::threads - 64;
+    constexpr int kSumThreads = S::sum_threads;
     const int quad = warp & 3, tid = threadIdx.x - 64;
     const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kTok;
     const float* ws = p.w_scales + static_cast<int64_t>(blockIdx.y) * p.kb;
@@ -479,8 +509,9 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
   // a warp writes 32 neighbouring columns of one output row.
   const int r = (warp & 3) * 32 + lane;
   const int64_t n = static_cast<int64_t>(n0) + r;
+  const bool sums = warp >= 2 && threadIdx.x < 64 + S::sum_threads;
   if (splits == 1) {
-    if (warp >= 2 && n < p.N) {
+    if (sums && n < p.N) {
 #pragma unroll
       for (int i = 0; i < kTok / 2; ++i) {
         float lo, hi;
@@ -494,7 +525,7 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
     // every product has read its operands (each sum waited for them), so the
     // stages' memory holds the sums [token][row]
     __syncthreads();
-    if (warp >= 2) {
+    if (sums) {
       const uint32_t at = s0 + (half * kTok * 128 + r) * 4;
 #pragma unroll
       for (int i = 0; i < kTok / 2; ++i) {
