@@ -125,9 +125,10 @@ constexpr int kThreads = 384;
 constexpr int kRegsIssue = 40, kRegsSum = 232;  // of 168 x 3 warpgroups at launch
 constexpr uint32_t kABytes = kBM * kGroup, kWBytes = kBN * kGroup;
 constexpr uint32_t kStageBytes = kABytes + kWBytes;
-constexpr uint32_t kSmAlloc = kStages * kStageBytes + 1024;
+constexpr uint32_t kRowBytes = 32 * 128;  // a sum warp's rows on their way out
+constexpr uint32_t kSmAlloc = kStages * kStageBytes + 1024, kSmAllocRows = kSmAlloc + 8 * kRowBytes;
 constexpr int kRaster = 8;  // row tiles that share the weights passing through L2
-static_assert(kSmAlloc + 512 <= 232448, "shared memory budget");
+static_assert(kSmAllocRows + 512 <= 232448, "shared memory budget");
 
 struct Params {
   const float* a_scales;
@@ -157,6 +158,10 @@ struct alignas(8) Barriers {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
 };
 
+// kSectors: the output's rows begin at multiples of 32 bytes.  (The other
+// form's staging takes memory that the scales are cached in otherwise:
+// 4096 x 7168 x 16384 in it, 386 us, not 357.)
+template <bool kSectors>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -301,21 +306,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         a1 = a2;
         w1 = w2;
       }
-      if (!ok || !live) continue;
-      __nv_bfloat16* dst = p.c + row * p.ldc + col0;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || col0 >= p.N) continue;
       const int n = p.N - col0 < 128 ? static_cast<int>(p.N - col0) : 128;
-      // 16-byte stores where the row allows them (address and whole group)
-      const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+      if constexpr (kSectors) {
+        // whole sectors, 32 bytes a store
+        __nv_bfloat16* dst = p.c + row * p.ldc + col0;
+        if (row < p.M) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float* f = acc + 8 * i;
-        if (vec && 8 * i + 8 <= n) {
-          *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(bf16x2_pack(f[0], f[1]), bf16x2_pack(f[2], f[3]),
-                                                              bf16x2_pack(f[4], f[5]), bf16x2_pack(f[6], f[7]));
-        } else {
+          for (int i = 0; i < 8; ++i) {
+            const float* f = acc + 16 * i;
+            if (16 * i + 16 <= n) {
+              uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (8 * i + j < n) dst[8 * i + j] = __float2bfloat16_rn(f[j]);
+              for (int j = 0; j < 8; ++j) w[j] = bf16x2_pack(f[2 * j], f[2 * j + 1]);
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * i), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (16 * i + j < n) dst[16 * i + j] = __float2bfloat16_rn(f[j]);
+            }
+          }
+        }
+      } else {
+        // Rows at any address: 64 columns at a time through shared memory
+        // (16-byte units swizzled by the row), so that a warp writes
+        // neighbouring columns of one row (4096 x 7160 x 512: one thread's
+        // row by itself, 187 us).
+        const uint32_t stage = s0 + kStages * kStageBytes + (warp - 4) * kRowBytes;
+        const int rows = static_cast<int>(min(int64_t{32}, p.M - (row - lane)));
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          __syncwarp();  // the part before has been read
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* f = acc + 64 * part + 8 * i;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                         "r"(bf16x2_pack(f[0], f[1])), "r"(bf16x2_pack(f[2], f[3])), "r"(bf16x2_pack(f[4], f[5])),
+                         "r"(bf16x2_pack(f[6], f[7]))
+                         : "memory");
+          }
+          __syncwarp();
+          const int c = 64 * part + 2 * lane;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(p.c) + (row - lane) * p.ldc + col0 + c;
+          for (int r = 0; r < rows; ++r, dst += p.ldc) {
+            uint32_t w;
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(w)
+                         : "r"(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)
+                         : "memory");
+            if (c + 1 < n && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+              *reinterpret_cast<uint32_t*>(dst) = w;
+            } else {
+              if (c < n) dst[0] = static_cast<uint16_t>(w);
+              if (c + 1 < n) dst[1] = static_cast<uint16_t>(w >> 16);
+            }
+          }
         }
       }
     }
@@ -672,7 +720,8 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
     }
   }
   // More tiles than a grid's second and third dimensions hold are large ones.
-  const bool large = sn > 65535 || sm > 65535 || (a.M > 64 && (tm * tn + num_sms - 1) / num_sms * kb + kOverhead < best);
+  const int64_t waves = (tm * tn + num_sms - 1) / num_sms;
+  const bool large = sn > 65535 || sm > 65535 || (a.M > 64 && waves * kb * 7 / 8 + kOverhead < best);
   CUtensorMap tm_a, tm_w;
   if (!encode_byte_map(&tm_a, a.a, a.K, a.M, a.lda, kGroup, static_cast<uint32_t>(large ? kBM : kt), false) ||
       !encode_byte_map(&tm_w, a.w, a.K, a.N, a.ldw, kGroup, large ? kBN : 128, false)) {
@@ -685,9 +734,13 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
     p.tiles_m = static_cast<int>(tm);
     p.tiles_n = static_cast<int>(tn);
     const int grid = static_cast<int>(tm * tn < num_sms ? tm * tn : num_sms);
-    if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_gemm_kernel), static_cast<int>(kSmAlloc), 14))
+    const bool sectors = ((reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.ldc * 2)) & 31u) == 0;
+    const auto kern = sectors ? fp8_gemm_kernel<true> : fp8_gemm_kernel<false>;
+    const uint32_t smem = sectors ? kSmAlloc : kSmAllocRows;
+    if (const int st =
+            smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem), sectors ? 14 : 23))
       return st;
-    fp8_gemm_kernel<<<grid, kThreads, kSmAlloc, stream>>>(tm_a, tm_w, p);
+    kern<<<grid, kThreads, smem, stream>>>(tm_a, tm_w, p);
     return launch_status();
   }
   p.tiles_m = static_cast<int>(sm);

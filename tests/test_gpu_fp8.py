@@ -552,6 +552,36 @@ def test_gemm_strides_and_neighbours(M, N, K):
         assert torch.all(rest == 7.0)
 
 
+@pytest.mark.parametrize("N,wide,left", [(2104, 2112, 0), (2093, 2112, 16), (2104, 2104, 0), (2103, 2104, 1),
+                                         (2101, 2103, 1)])
+def test_gemm_large_tiles_outputs(N, wide, left):
+    # rows of the output at multiples of 32 bytes, of 16, of 2: many rows, one
+    # wave of large tiles, whose last ones are ragged in both directions
+    M, K = 1300, 272
+    rng = np.random.default_rng(N + left)
+    a, sa, w, sw = make_gemm(rng, M, N, K)
+    d = [torch.from_numpy(x).to(DEV) for x in (a, sa, w, sw)]
+    out = torch.full((M + 2, wide), 7.0, dtype=torch.bfloat16, device=DEV)
+    got = mla.mla_nvfp4_fp8_gemm(d[0].view(F8), d[1], d[2].view(F8), d[3], out=out[:M, left:left + N])
+    torch.cuda.synchronize()
+    check_gemm(f32(got), a, sa, w, sw, f"{M}x{N}x{K}, rows of {wide}")
+    rest = out.clone()
+    rest[:M, left:left + N] = 7.0
+    assert torch.all(rest == 7.0)
+
+
+@pytest.mark.parametrize("M", [16, 32, 64, 128, 640])
+def test_gemm_many_blocks(M):
+    # many K blocks a CTA in every form, so that each stage is filled several
+    # times; ten tiles of weights, repeated
+    rng = np.random.default_rng(M)
+    a, sa, w, sw = make_gemm(rng, M, 1280, 4112)
+    got = run_gemm(a, sa, np.tile(w, (20, 1)), np.tile(sw, (20, 1)))
+    check_gemm(got[:, :1280], a, sa, w, sw, f"{M}x25600x4112")
+    for i in range(1, 20):
+        assert np.array_equal(got[:, :1280], got[:, 1280 * i:1280 * (i + 1)])
+
+
 def test_gemm_graph_and_streams():
     rng = np.random.default_rng(21)
     ps = [make_gemm(rng, 9, 700, 1024), make_gemm(rng, 260, 520, 512)]
