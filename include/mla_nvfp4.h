@@ -566,7 +566,7 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  *                  256-byte aligned, contents ignored: the keys of a sequence
  *                  are then cut so that all SMs get the same work, and the
  *                  parts merged by LSE in a fixed order.  NULL: one SM (per
- *                  32 heads) works through all keys of a sequence.  Calls
+ *                  32 or 64 heads) works through all keys of a sequence.  Calls
  *                  that may run at once need a workspace each.
  * scores = softmax_scale * q . key, out = softmax . key[:512].
  * Rows of the cache that hold no key of the sequence are never used,

@@ -26,8 +26,8 @@ __all__ = [
     "mla_nvfp4_quantize_rows", "mla_nvfp4_gemm", "mla_nvfp4_gather_latent", "mla_nvfp4_prefill_partial",
     "mla_nvfp4_merge_fused_out", "mla_nvfp4_prefill_qdq", "mla_nvfp4_prefill_fakequant",
     "mla_nvfp4_prefill_quantized", "mla_nvfp4_fp8_cache_append", "mla_nvfp4_fp8_decode",
-    "mla_nvfp4_fp8_decode_workspace_size", "mla_nvfp4_fp8_quantize", "mla_nvfp4_fp8_gemm", "abi_symbols", "RECORD_BF16_ROPE", "RECORD_FP8_ROPE",
-    "LAUNCHES_PER_CALL",
+    "mla_nvfp4_fp8_decode_workspace_size", "mla_nvfp4_fp8_quantize", "mla_nvfp4_fp8_gemm", "abi_symbols",
+    "RECORD_BF16_ROPE", "RECORD_FP8_ROPE", "FP8_BLOCK", "FP8_GROUP", "LAUNCHES_PER_CALL",
 ]
 
 RECORD_BF16_ROPE = 432
@@ -38,17 +38,18 @@ DEVERR_BOUNDS, DEVERR_TIMEOUT, DEVERR_SCALE, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8
 # Kernels each entry point launches (for launch accounting in the benchmark);
 # decode launches one kernel with one key split, two (plus the merge) with
 # uniform splits and three (plan, decode, merge) when planned, see
-# decode_launches().
+# decode_launches(); the e4m3 decode launches its merge unless split is False.
 LAUNCHES_PER_CALL = {"cache_write": 1, "decode": 3, "prefill": 1, "global_scale": 2, "gemm": 1,
                      "gather_latent": 1, "prefill_partial": 1, "merge_fused_out": 1, "prefill_qdq": 2,
-                     "prefill_fakequant": 1}
+                     "prefill_fakequant": 1, "fp8_cache_append": 1, "fp8_decode": 2, "fp8_quantize": 1, "fp8_gemm": 1}
 # What bounds each hot kernel as built: "hbm", "tensor" (tcgen05 MMA) or
 # "alu" (CUDA-core arithmetic).
-KERNEL_BOUND = {"cache_write": "hbm", "decode": "tensor", "prefill": "tensor", "gemm": "tensor"}
+KERNEL_BOUND = {"cache_write": "hbm", "decode": "tensor", "prefill": "tensor", "gemm": "tensor",
+                "fp8_cache_append": "hbm", "fp8_decode": "tensor", "fp8_quantize": "hbm", "fp8_gemm": "tensor"}
 # Operand type of each kernel's tensor-core products (fp32 accumulation):
 # the decode multiplies f16 operands (the dequantised latent c*s is exact in
 # f16), the prefill bf16 inputs as given.
-OPERAND_DTYPE = {"decode": "f16", "prefill": "bf16", "gemm": "nvfp4"}
+OPERAND_DTYPE = {"decode": "f16", "prefill": "bf16", "gemm": "nvfp4", "fp8_decode": "e4m3", "fp8_gemm": "e4m3"}
 
 
 def kernel_kind(name: str) -> str:

@@ -51,6 +51,15 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// After a wait gave up: the last copies into a ring of stages (full: their
+// barriers; issued: all that were) are waited for, with a limit, so that none
+// lands in memory that its CTA has left.
+__device__ __noinline__ inline void drain_copies(uint64_t* full, uint32_t stages, uint32_t issued) {
+  for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+    for (int n = 0; n < 4096 && !mbar_test(&full[i % stages], (i / stages) & 1); ++n) {
+    }
+}
+
 // One lane of a converged warp.  Loops that issue products are run by the
 // whole warp, their descriptors made of values that the compiler knows to be
 // the warp's (uniform), and only the issue itself is one lane's: in a branch

@@ -44,6 +44,17 @@
 //                goes on; a piece's output, while the next one starts.
 // The code of each role is kept short (rolled loops, one copy): unrolled
 // further, the warps waited for instructions more than for anything else.
+// Times: 64 x 4096 keys, 128 heads 87 us, 64 heads 63, 16 heads 44; 128
+// sequences of 1k to 32k, 16 heads 136 us (5.0 TB/s), 128 heads 315 (1040
+// TFLOP/s); 1 x 65536, 128 heads 36; 1 x 100, 16 heads 12, launches and one
+// chain of latencies.  With 64 heads a CTA, shared memory bounds a tile: the
+// operands of its products (18 x 8 KB and 32 x 6 KB), the copies in (72 KB) and
+// P take 3300 cycles at 128 bytes a cycle, of about 4400.  CTAs of 32 heads
+// read every key twice as often (64 x 4096, 128 heads: 131 us).  What was
+// tried beside that: the next tile into L2 ahead (no faster), the merge put in
+// place before the decode ends (1 x 65536: 58 us, not 50), two value chunks'
+// scores issued at once (90 us, not 88), references found by votes instead of
+// exchanges (111 us, not 94).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -277,8 +288,9 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   const int64_t per = divide(total + p.ranges - 1, p.ranges);
   // A CTA each for whole sequences, where that takes no longer than equal
   // ranges: those begin two pieces (of one sequence's end and the next one's
-  // start), and the cut ones are merged.
-  const bool uncut = B <= p.ranges && most + kPiece <= per + 2 * kPiece + kMerge;
+  // start; one, if they are of a tile or the batch of a sequence), and the cut
+  // ones are merged.
+  const bool uncut = B <= p.ranges && most + kPiece <= per + (per > 1 && B > 1 ? 2 : 1) * kPiece + kMerge;
   const int64_t t0 = uncut ? 0 : range * per;
   int64_t off = before + incl - sum;
   if (tid == 0) {
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tm_lat);
       prefetch_tmap(&tm_rope);
     }
-    int n = 0;
+    int n = 0, chunks = 0, ropes = 0;  // tiles; copies issued
     bool ok = true;
     for (Pieces it(p, ms, range); it.next(p);) {
       const int b = it.b, len = it.len, s = it.s, e = it.e;
@@ -394,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(&ms.full[i], kChunkBytes);
             tma_load_bytes(slot_addr(i), &tm_lat, 128 * d, y0, &ms.full[i]);
             tma_load_bytes(slot_addr(i) + kChunkBytes / 2, &tm_lat, 128 * d, y1, &ms.full[i]);
+            chunks = k + 1;
           }
           if (ok) {
             const int i = n % C::ropes;
@@ -403,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_expect_tx(&ms.rfull[i], kRopeBytes);
               tma_load_bytes(dst, &tm_rope, MLA_D_LATENT, y0, &ms.rfull[i]);
               tma_load_bytes(dst + kRopeBytes / 2, &tm_rope, MLA_D_LATENT, y1, &ms.rfull[i]);
+              ropes = n + 1;
             }
           }
         }
@@ -422,6 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       }
+    }
+    if (!ok && lane == 0) {
+      drain_copies(ms.full, C::slots, chunks);
+      drain_copies(ms.rfull, C::ropes, ropes);
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- score products
@@ -1064,7 +1082,12 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
   uint32_t magic;
   int shift;
   magic_divisor(a.page_size / kBlock, &magic, &shift);
-  Params p{a, magic, shift, l.ranges, l.groups, ws != nullptr, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),
+  // Where the page table holds too few keys for a sequence to be cut (as
+  // make_plan decides, with one tile or more a range), plan and merge are left
+  // out: 1 x 100 keys, 16 heads, 9.7 us, not 12.0.
+  const bool split =
+      ws != nullptr && (a.batch > l.ranges || a.max_pages * a.page_size > (1 + kMerge) * kTile);
+  Params p{a, magic, shift, l.ranges, l.groups, split, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),
            reinterpret_cast<float*>(ws + l.o)};
   if (static_cast<int64_t>(a.batch) * a.num_heads > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   CUtensorMap lat, rope;

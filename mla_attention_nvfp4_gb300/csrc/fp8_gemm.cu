@@ -21,7 +21,11 @@ constexpr int kGroup = MLA_FP8_GROUP;
 // 8 lanes hold a group, 16 features each (two 16-byte loads, one 16-byte
 // store; 8 features where K asks for it); two groups in flight per 8 lanes.
 // HBM-bound, but only with few instructions an element: maxima on bf16
-// pairs, quotients on pairs of floats.
+// pairs, quotients on pairs of floats.  8192 x 16384: 64 us (6.4 TB/s; 75 with
+// one element at a time); 64 x 7168: 2.1 us.
+// x / scale is rounded to nearest by Markstein's method: with y = 1 / scale
+// rounded to nearest and q0 = x y, the remainder x - q0 scale is exact in one
+// fused multiply-add, and q0 + y remainder is the quotient, rounded once.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 constexpr int kQuantUnroll = 2;
@@ -113,11 +117,19 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 // Large: 128 x 256 outputs per tile, persistent CTAs.
 //   warp 0        TMA producer: A and W tiles of one K block, 128-byte swizzle,
 //                 kStages in flight;
-//   warp 1        MMA issuer: four products of K = 32 per block;
+//   warps 1, 2    MMA issuers, one an accumulator: four products of K = 32 per
+//                 block;
 //   warps 4..11   sums: warps 4..7 columns 0..127, warps 8..11 columns 128..255
 //                 (each half has one weight scale per block), thread = row;
 //                 they take the registers the first warpgroup gives up
-//                 (128 sums and two TMEM loads of 32 columns in flight each).
+//                 (128 sums, 32 columns being added and 32 being loaded each).
+// 4096 x 7168 x 16384: 352 us, 2730 TFLOP/s (457 us with one issuer and each
+// load waited for before its sums).  A K block takes 520 cycles of products;
+// an accumulator's way from its products through eight warps' sums back to
+// the issuer is what bounds it (850 cycles a block, two accumulators taking
+// turns).  Sixteen sum warps of 64 columns, with one issuer: 481 us, not 457;
+// sums on pairs (f32x2): 527, not 454; a CTA pair's 256 x 256 tile: 511, its
+// hand-over between the CTAs taking longer than what it saves.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 4;
@@ -211,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_bytes(s0 + s * kStageBytes + kABytes, &tm_w, kb * kGroup, nt * kBN, &bars.full[s]);
         }
       }
+      if (abort_s) drain_copies(bars.full, kStages, it);
     } else if (warp == 1 || warp == 2) {
       // An issuer for each accumulator, every other K block: one alone takes
       // longer to get from one block's products to the next one's (its waits
@@ -382,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order.
 //   warp 0 producer, warp 1 and the last one MMA issuers, between them four
 //   warps of sums per 64 tokens: thread = weight row.
+// N 7168, K 16384: 16 rows 23.5 us, 64 rows 25.4 (4.7 TB/s), 128 rows 36;
+// 1 x 576 x 7168: 5.0 us, of which the launch takes half.
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplits = 8;   // portable cluster size
 constexpr int kScaleBlocks = 16;  // K blocks whose scales are staged at a time
@@ -464,13 +479,15 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
     if (lane == 0) {
       prefetch_tmap(&tm_a);
       prefetch_tmap(&tm_w);
-      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const int s = it % S::stages;
         if (!mbar_wait(&bars.empty[s], ((it / S::stages) & 1) ^ 1, err, &abort_s)) break;
         mbar_expect_tx(&bars.full[s], S::stage_bytes);
         tma_load_bytes(s0 + s * S::stage_bytes, &tm_w, kb * kGroup, n0, &bars.full[s]);
         tma_load_bytes(s0 + s * S::stage_bytes + S::w_bytes, &tm_a, kb * kGroup, m0, &bars.full[s]);
       }
+      if (abort_s) drain_copies(bars.full, S::stages, it);
     }
   } else if (warp == 1 || warp == S::threads / 32 - 1) {
     // an issuer for each accumulator, as above
@@ -697,14 +714,15 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t sn = (a.N + 127) / 128, sm = (a.M + kt - 1) / kt;
 
   // Which form, and into how many parts K is cut, by an estimate in K blocks
-  // of one CTA's time.  A CTA of either form takes about as long for a K block
-  // (0.57 us), however many share its SM, until together they take what HBM
-  // gives (kPerBlock blocks of 128 weights x 128 in the time of one); a wave
-  // of CTAs costs kOverhead blocks more.  Clusters do not fill every place an
-  // SM offers: nine tenths count.  Measured, N 7168, K 16384: 64 rows, 34 us
-  // with 2 parts, 25 with 4 (one wave each), 30 with 8 (two waves); 16 rows,
-  // 24 with 4, 28 with 8; 512 rows, 116 us streaming in 2 parts, 74 as large
-  // tiles; 128 rows, 39 us streaming, and large tiles would take 74.
+  // of one streaming CTA's time (0.5 us), however many share its SM, until
+  // together they take what HBM gives (kPerBlock blocks of 128 weights x 128
+  // in the time of one); a wave of CTAs costs kOverhead blocks more, and a
+  // large tile's block 7/8 of one.  Clusters do not fill every place an SM
+  // offers: nine tenths count.  Measured, N 7168, K 16384: 64 rows, 34 us with
+  // 2 parts, 25 with 4 (one wave each), 30 with 8 (two waves); 16 rows, 24 with
+  // 4, 28 with 8; 128 rows, 36 us streaming, 58 as large tiles; 256 rows, 66
+  // and 58; 512 rows, 127 and 59.  Over 77 shapes of 65 to 2048 rows the form
+  // chosen was within 7 % of the faster one.
   constexpr int kOverhead = 6, kPerBlock = 200;
   const int64_t places = static_cast<int64_t>(num_sms) * (kt <= 32 ? 3 : kt == 64 ? 2 : 1) * 9 / 10;
   int splits = 1;
@@ -730,7 +748,7 @@ int launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t stream, int num_sms) {
   }
   Params p{a.a_scales, a.w_scales, a.M, a.N, a.ldc, kb, static_cast<__nv_bfloat16*>(a.out), 0, 0, a.error_word};
   if (large) {
-    if (tm * tn > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
+    if (tm * tn > int64_t(1) << 30) return MLA_ERR_INVALID_ARG;  // (a tile's index and a grid more fit an int)
     p.tiles_m = static_cast<int>(tm);
     p.tiles_n = static_cast<int>(tn);
     const int grid = static_cast<int>(tm * tn < num_sms ? tm * tn : num_sms);

@@ -33,6 +33,7 @@ Modules:
   attention  absorbed decode (paged and top-k), LSE merge, causal prefill.
   swizzle    the 128x4 scale-factor layout and the fused prefill output.
   gemm       the NVFP4 x NVFP4 product of packed codes and swizzled scales.
+  fp8        the 8-bit path: e4m3 cache append and decode, quantiser, GEMM.
   fakequant  the causal prefill with NVFP4 fake-quantised Q, K, P, V and
              2:4 score sparsity.
 

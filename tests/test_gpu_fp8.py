@@ -8,8 +8,9 @@ Tolerances, for each output element:
                     sum |a w| (fp32 sums of K exact products and one scaled
                     sum a block).
   decode            2^-8 |o| (bf16) + 2^-8 * sum p |v| / sum p (probabilities
-                    carried as two e4m3 terms: each at most half a step of
-                    half a step, 2^-4 * 2^-4, off) + the scores' fp32 sums:
+                    carried as two 8-bit terms: for p in [2^e, 2^(e+1)) the
+                    first leaves at most 2^(e-4), of which the second, e4m3 or
+                    e5m2, leaves at most 2^(e-8)) + the scores' fp32 sums:
                     a score off by d moves p by a factor e^d, so
                     2 (e^d - 1) * sum p |v| / sum p with
                     d = 2^-24 (576 + 8) * max sum |q k| * scale
