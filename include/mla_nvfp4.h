@@ -570,7 +570,8 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  *                  that may run at once need a workspace each.
  * scores = softmax_scale * q . key, out = softmax . key[:512].
  * Rows of the cache that hold no key of the sequence are never used,
- * whatever their bytes.  Errors: MLA_DEVERR_BOUNDS for a length past the page
+ * whatever their bytes.  A NaN or an infinity in a query makes that head's
+ * out and lse NaN, a NaN code in a key those of its sequence.  Errors: MLA_DEVERR_BOUNDS for a length past the page
  * table or a page outside the cache, MLA_DEVERR_SCALE for a block scale out
  * of range: those keys are skipped.
  */

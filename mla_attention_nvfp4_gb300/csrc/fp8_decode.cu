@@ -138,7 +138,8 @@ struct Params {
 };
 
 __device__ __forceinline__ int clipped_len(const Fp8DecodeArgs& a, int b) {
-  const int64_t room = a.max_pages * a.page_size;
+  const int64_t table = a.max_pages * a.page_size, most = (int64_t{1} << 31) - 2 * kTile;  // (lengths are rounded up)
+  const int64_t room = table < most ? table : most;
   const int n = a.seq_lens[b];
   return n <= 0 ? 0 : n <= room ? n : static_cast<int>(room);
 }
@@ -611,12 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           m2 = __reduce_max_sync(0xffffffffu, m2);
-          // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8)
+          // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8); a
+          // head with an infinity or a NaN has NaN scores
           int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-          ex = max(-60, min(60, ex));
+          ex = max(-126, min(120, ex));
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
           if (lane == 0)
-            ms.c[h] = p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+            ms.c[h] = m2 >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                        : p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
   #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -1063,7 +1066,7 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   if (!p.split) return MLA_OK;
   // A CTA a row where the rows are cut into many pieces.
   const int64_t rows = static_cast<int64_t>(p.a.num_heads) * p.a.batch;
-  if (p.ranges >= kManyPieces * p.a.batch)
+  if (p.ranges / kManyPieces >= p.a.batch)
     fp8_decode_merge_kernel<kH, kSub><<<static_cast<unsigned>(rows), merge_threads<kSub>, 0, stream>>>(p);
   else
     fp8_decode_merge_kernel<kH, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(p);

@@ -390,6 +390,70 @@ def test_decode_query_ranges():
     check_decode(got, q, cache, scales, table, lens, 64, what="query ranges")
 
 
+@pytest.mark.parametrize("heads", [16, 40])
+def test_decode_nan_and_infinity_stay_where_they_are(heads):
+    # a query's make its head's results NaN, a key's those of its sequence
+    rng = np.random.default_rng(23)
+    lens = (300, 20000, 100, 65)
+    cache, scales, table = make_cache(rng, lens, 64)
+    q = torch.from_numpy(rng.standard_normal((4, heads, 576))).bfloat16()
+    clean = run_decode(q, cache, scales, table, lens, 64)
+    bad = q.clone()
+    bad[0, 1, 3], bad[0, 2, 575], bad[1, 5, 0], bad[3, 0, 100] = math.nan, math.inf, -math.inf, math.nan
+    cache[table[2][1] * 64 + 5, 570] = 0x7F  # the RoPE part of key 69
+    got = run_decode(bad, cache, scales, table, lens, 64)
+    nan = np.zeros((4, heads), bool)
+    nan[0, 1] = nan[0, 2] = nan[1, 5] = nan[3, 0] = True
+    nan[2] = True
+    assert np.array_equal(np.isnan(got[1]), nan) and np.array_equal(np.isnan(got[0]), np.repeat(nan[..., None], 512, 2))
+    assert np.array_equal(got[0][~nan], clean[0][~nan]) and np.array_equal(got[1][~nan], clean[1][~nan])
+    assert got[2] == 0
+
+
+@pytest.mark.parametrize("power", [-126, -100, 100, 126])
+def test_decode_queries_near_the_ends_of_the_range(power):
+    # scaled by a power of two, and the softmax's scale by its inverse (as far
+    # as fp32 goes): the same results, within the bound
+    rng = np.random.default_rng(24)
+    lens = (200, 77)
+    cache, scales, table = make_cache(rng, lens, 64)
+    q = torch.from_numpy(rng.standard_normal((2, 20, 576))).bfloat16()
+    up = 2.0 ** (power if power > 0 else power + 6)
+    big = (q.double() * up).bfloat16()
+    out, lse, flags = run_decode(big, cache, scales, table, lens, 64, scale=SCALE / up)
+    assert flags == 0
+    finite = torch.isfinite(big).all(2)  # (4 * 2^126 is an infinity)
+    assert finite.float().mean() > 0.8 and np.array_equal(~np.isnan(lse), finite.numpy())
+    h = finite.all(0).numpy()
+    check_decode((out[:, h], lse[:, h]), big[:, h], cache, scales, table, lens, 64, scale=SCALE / up,
+                 what=f"queries 2^{power}")
+
+
+def test_decode_lengths_near_the_largest_integer():
+    # pages of 2^30 tokens: the lengths and the blocks' indexes stay in range,
+    # and what the cache does not hold is flagged and skipped
+    rng = np.random.default_rng(26)
+    cache, scales, _ = make_cache(rng, (128,), 64)
+    cache, scales = cache[:128], scales[:2]
+    cache[:] = fp8.encode(rng.standard_normal((128, 576)) * 100)
+    table = np.array([[0, -1, 7], [0, 1, 2]], dtype=np.int32)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 576))).bfloat16()
+    got = run_decode(q, cache, scales, table, (2 ** 31 - 1, 100), 2 ** 30)
+    assert got[2] == 1
+    check_decode(got, q, cache, scales, np.array([[0], [0]]), (128, 100), 128, what="2^31 - 1 keys")
+
+
+def test_decode_more_sequences_than_threads():
+    rng = np.random.default_rng(25)
+    lens = tuple(int(x) for x in rng.integers(0, 70, 1100))
+    cache, scales, table = make_cache(rng, lens, 64)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 2, 576))).bfloat16()
+    for split in (True, False):
+        got = run_decode(q, cache, scales, table, lens, 64, split=split)
+        assert got[2] == 0
+        check_decode(got, q, cache, scales, table, lens, 64, what=f"1100 sequences split={split}")
+
+
 def test_decode_bad_entries_are_flagged_and_skipped():
     rng = np.random.default_rng(16)
     lens = (300, 200, 64)
