@@ -125,11 +125,12 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 //                 (128 sums, 32 columns being added and 32 being loaded each).
 // 4096 x 7168 x 16384: 352 us, 2730 TFLOP/s (457 us with one issuer and each
 // load waited for before its sums).  A K block takes 520 cycles of products;
-// an accumulator's way from its products through eight warps' sums back to
-// the issuer is what bounds it (850 cycles a block, two accumulators taking
-// turns).  Sixteen sum warps of 64 columns, with one issuer: 481 us, not 457;
-// sums on pairs (f32x2): 527, not 454; a CTA pair's 256 x 256 tile: 511, its
-// hand-over between the CTAs taking longer than what it saves.
+// the sums bound it, at 930 (a warp's 128 multiply-adds a thread, four TMEM
+// loads and a wait, whose answer alone takes 100 to 140 cycles; without the
+// multiply-adds, 700).  Sixteen sum warps of 64 columns: 413 us, not 360; sums
+// on pairs (f32x2): 527, not 454; accumulators freed before two thirds of the
+// sums: the same; the next accumulator asked for ahead: 389; a CTA pair's 256
+// x 256 tile: 511, its hand-over between the CTAs taking more than it saves.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 4;
