@@ -39,6 +39,13 @@ def test_append_alignment(kw):
     assert _append(**kw) == 3
 
 
+@pytest.mark.parametrize("pages", [2**31, 2**62])
+def test_page_tables_too_wide_are_refused(pages):
+    # (a table's tokens, pages times page size, stay in 64 bits)
+    assert _append(pages=pages, pt_st=pages) == 1
+    assert _decode(pages=pages, pt_st=pages) == 1
+
+
 @pytest.mark.parametrize("kw", [dict(T=0), dict(seqs=0), dict(new=0)])
 def test_append_nothing_to_do(kw):
     assert _append(**kw) == 0
