@@ -124,13 +124,16 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 //                 they take the registers the first warpgroup gives up
 //                 (128 sums, 32 columns being added and 32 being loaded each).
 // 4096 x 7168 x 16384: 352 us, 2730 TFLOP/s (457 us with one issuer and each
-// load waited for before its sums).  A K block takes 520 cycles of products;
-// the sums bound it, at 930 (a warp's 128 multiply-adds a thread, four TMEM
-// loads and a wait, whose answer alone takes 100 to 140 cycles; without the
-// multiply-adds, 700).  Sixteen sum warps of 64 columns: 413 us, not 360; sums
-// on pairs (f32x2): 527, not 454; accumulators freed before two thirds of the
-// sums: the same; the next accumulator asked for ahead: 389; a CTA pair's 256
-// x 256 tile: 511, its hand-over between the CTAs taking more than it saves.
+// load waited for before its sums).  A K block takes 520 cycles of products
+// by themselves, and 920 here, where 48 KB are copied into shared memory as 48
+// are read from it: 512 rows take 59 us with the sums and without them.  A CTA
+// pair's 256 x 256 tile halves the weights' part of that and takes as long (60
+// us; its products alone 45), for then the sums bound it: 128 multiply-adds a
+// thread and block beside the scales' loads and waits of 100 to 140 cycles.
+// Sixteen sum warps of 64 columns: 413 us, not 360; sums on pairs (f32x2) and
+// accumulators freed before two thirds of the sums: the same; the next
+// accumulator asked for ahead: 389; row scales staged in shared memory: 73, not
+// 59, for 512 rows.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 4;
@@ -171,9 +174,8 @@ struct alignas(8) Barriers {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
 };
 
-// kSectors: the output's rows begin at multiples of 32 bytes.  (The other
-// form's staging takes memory that the scales are cached in otherwise:
-// 4096 x 7168 x 16384 in it, 386 us, not 357.)
+// kSectors: the output's rows begin at multiples of 32 bytes.  (Both endings
+// in one kernel: 4096 x 7168 x 16384 386 us, not 357.)
 template <bool kSectors>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Params p) {
