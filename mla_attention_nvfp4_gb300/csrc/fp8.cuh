@@ -60,11 +60,12 @@ __device__ __noinline__ inline void drain_copies(uint64_t* full, uint32_t stages
     }
 }
 
-// One lane of a converged warp.  Loops that issue products are run by the
-// whole warp, their descriptors made of values that the compiler knows to be
-// the warp's (uniform), and only the issue itself is one lane's: in a branch
-// of one lane each operand is moved to a uniform register by itself, which
-// takes longer than a product of 64 columns.
+// One lane of a converged warp, the same one each time (a commit follows the
+// products of its own thread).  Loops that issue products are run by the whole
+// warp, their descriptors made of values that the compiler knows to be the
+// warp's (uniform), and only the issue itself is one lane's: the operands are
+// uniform registers, and values of a one-lane branch are moved there one by
+// one (e4m3 decode, 64 x 4096 keys, 128 heads: 94 us so, 88 in this way).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
