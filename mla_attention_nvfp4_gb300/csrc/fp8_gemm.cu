@@ -285,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(x[i]), sc, acc[32 * c + i]);
       };
       auto filled = [&](int at) {
-        if (!mbar_wait(&bars.acc_full[at & 1], (at >> 1) & 1, err, &abort_s)) return false;
+        const bool in = mbar_wait(&bars.acc_full[at & 1], (at >> 1) & 1, err, &abort_s);
         tc_fence_after();
-        return true;
+        return __all_sync(0xffffffffu, in) != 0;  // (a wait may give up in some lanes only)
       };
       ok = filled(it);
       if (ok) {
@@ -322,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         a1 = a2;
         w1 = w2;
       }
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok || col0 >= p.N) continue;
       const int n = p.N - col0 < 128 ? static_cast<int>(p.N - col0) : 128;
       if constexpr (kSectors) {
