@@ -569,6 +569,8 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  *                  32 or 64 heads) works through all keys of a sequence.  Calls
  *                  that may run at once need a workspace each.
  * scores = softmax_scale * q . key, out = softmax . key[:512].
+ * Held in fewer bits than float32: a query's features, exactly as given down
+ * to 2^-13 of their head's largest and within 2^-21 of that below.
  * Rows of the cache that hold no key of the sequence are never used,
  * whatever their bytes.  A NaN or an infinity in a query makes that head's
  * out and lse NaN, a NaN code in a key those of its sequence.  Errors: MLA_DEVERR_BOUNDS for a length past the page

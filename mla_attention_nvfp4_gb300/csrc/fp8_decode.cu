@@ -10,10 +10,14 @@
 // that masking a key masks a thread.
 //
 // Two 8-bit terms carry 8 significant bits:
-//   q = 2^e (q1 + q2) with q1 = e4m3(q 2^-e), q2 = e4m3(q 2^-e - q1): a bf16
-//       query exactly (its 8 bits split 4 + 4), down to 2^-17 of the head's
-//       largest feature, below which it is held to an absolute 2^-19 of it.
-//       The terms are 2 kH columns of one product, added as S^T is read.
+//   q = 2^e (q1 + q2 / 16) with q1 = e4m3(q 2^-e), q2 = e4m3(16 (q 2^-e - q1)):
+//       a bf16 query exactly (its 8 bits split 4 + 4), down to 2^-13 of the
+//       head's largest feature: there q 2^-e is 2^-6, from where on q1's rest
+//       is a multiple of 2^-13 and 16 times it one of e4m3's smallest step,
+//       2^-9.  Features below that are held to half a step, 2^-21 of the
+//       largest.  (16 times the rest, at most 256, still fits; without the
+//       factor both limits lie 2^4 higher.)  The terms are 2 kH columns of one
+//       product, added as S^T is read.
 //   p = p1 + p2 with p1 = e4m3(p), at most 2^-8 off relative (what bf16 would
 //       be).  The largest p lies between 2^kReset and 2^kTop, and the terms'
 //       absolute floor, 2^-13, 2^17 or more below it:
@@ -75,7 +79,7 @@ constexpr int kSoftmax = 256, kOutput = 128, kThreads = 96 + kSoftmax + kOutput;
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
 constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
 constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest weight at 2^4
-constexpr float kGain = 16.f;   // 32 heads: the first term's rounding error, at most 16, becomes 256
+constexpr float kGain = 16.f;   // queries' and 32 heads' weights' second terms: at most 16 becomes 256
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 // The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
               const uint32_t a = cvt_e4m3x2_h2(xu);
               w1[j >> 1] |= a << (16 * (j & 1));
-              w2[j >> 1] |= cvt_e4m3x2_h2(h2_sub(xu, e4m3x2_to_f16x2_pair(a))) << (16 * (j & 1));
+              w2[j >> 1] |= cvt_e4m3x2_h2(h2_fma(h2_sub(xu, e4m3x2_to_f16x2_pair(a)), kGain, 0)) << (16 * (j & 1));
             }
             // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
             uint32_t a1, a2;
@@ -696,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, mv[4] = {mm.x, mm.y, mm.z, mm.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              x[h + j] = fmaf((__uint_as_float(v[i + j]) + __uint_as_float(u[i + j])) * sb, cv[j], -mv[j]);
+              x[h + j] =
+                  fmaf(fmaf(__uint_as_float(u[i + j]), 1.f / kGain, __uint_as_float(v[i + j])) * sb, cv[j], -mv[j]);
           }
         }
         tc_fence_before();
