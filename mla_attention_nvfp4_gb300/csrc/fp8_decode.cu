@@ -19,16 +19,18 @@
 //       factor both limits lie 2^4 higher.)  The terms are 2 kH columns of one
 //       product, added as S^T is read.
 //   p = p1 + p2 with p1 = e4m3(p), at most 2^-8 off relative (what bf16 would
-//       be).  The largest p lies between 2^kReset and 2^kTop, and the terms'
-//       absolute floor, 2^-13, 2^17 or more below it:
+//       be; f16, to which p is rounded before, adds 2^-12).  The largest p lies
+//       between 2^kReset and 2^kTop; p2 has a step of 2^-13 or more, 2^17 or
+//       more below it:
 //         32 heads: p2 = e4m3(16 (p - p1)), both terms in one product, with
 //           accumulators of their own;
 //         64 heads: one accumulator (TMEM holds no more), two products, and
-//           p2 = e5m2(p - p1), which reaches as far down by itself.
-//       There the second term is rounded with an offset that runs evenly
-//       through a step over 32 neighbouring keys: a long tail of equal, tiny
-//       weights, which rounding to nearest would push to one side, keeps its
-//       sum.
+//           p2 = e5m2 of p - p1 in steps of 2^-13 (e5m2's own steps are
+//           smaller below 2^-11, and change from one power of two to the next).
+//       Before either rounding comes an offset that runs evenly through such a
+//       step over 32 neighbouring keys: a long tail of equal, tiny weights,
+//       which rounding to nearest would push to one side, keeps its sum.  The
+//       offsets stay below half a step: a weight of zero is zero.
 //
 // Scales: with s the block's scale, x = log2(e) softmax_scale s q.k8,
 // l = sum 2^(x - m) and O = sum (s 2^(x - m)) k8; m is a per-head reference
@@ -227,6 +229,13 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, float s, uint32_t b) {
   const __half2 r =
       __hfma2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(s), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Rounded to multiples of 2^-13 where below 2^-4: the steps of f16 numbers in
+// [2^-3, 2^-2).  (Larger ones lose what is far below their step in e5m2.)
+__device__ __forceinline__ uint32_t h2_steps(uint32_t a) {
+  const __half2 mid = __float2half2_rn(0.1875f);
+  const __half2 r = __hsub2(__hadd2(*reinterpret_cast<const __half2*>(&a), mid), mid);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // Floats as integers of the same order, for an integer maximum.
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = quad * 32 + lane;  // of the tile: a TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     // offset of the second term's rounding: (j + 1/2) / 32 - 1/2, j the
-    // lane's bits reversed, of a step 2^-13 (2^-9 times the gain)
+    // lane's bits reversed, of a step 2^-13 (32 heads: 2^-9, after the gain)
     const float off = ((__brev(lane) >> 27) + 0.5f) * (1.f / 32) - 0.5f;
     const __half2 dither_h = __float2half2_rn(off * (kH == 32 ? kGain : 1.f) * 0.0001220703125f);
     const uint32_t dither = *reinterpret_cast<const uint32_t*>(&dither_h);
@@ -792,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t pu = *reinterpret_cast<const uint32_t*>(&ph);
             a[j] = cvt_e4m3x2_h2(pu);
             const uint32_t rest = h2_sub(pu, e4m3x2_to_f16x2_pair(a[j]));
-            r[j] = kH == 32 ? cvt_e4m3x2_h2(h2_fma(rest, kGain, dither)) : cvt_e5m2x2_h2(h2_fma(rest, 1.f, dither));
+            r[j] = kH == 32 ? cvt_e4m3x2_h2(h2_fma(rest, kGain, dither)) : cvt_e5m2x2_h2(h2_steps(h2_fma(rest, 1.f, dither)));
           }
           w1[h / 4] = a[0] | (a[1] << 16);
           w2[h / 4] = r[0] | (r[1] << 16);

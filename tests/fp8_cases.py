@@ -2,7 +2,11 @@
 float64 model of those terms.
 
 The kernel holds a query feature x (divided by 2^e, the smallest power that
-brings its head's largest to at most 448) as e4m3(x) + e4m3(16 (x - e4m3(x))) / 16.
+brings its head's largest to at most 448) as e4m3(x) + e4m3(16 (x - e4m3(x))) / 16,
+and a weight p = s 2^(x - m), rounded to f16, whose largest is 2^4 or more, as p1 = e4m3(p) and
+  up to 32 heads: e4m3(16 (p - p1 + o)) / 16,
+  more heads:     e5m2 of p - p1 + o rounded to a multiple of 2^-13 (where below 2^-4),
+with an offset o that runs evenly through a step of 2^-13 over 32 keys.
 """
 import math
 
@@ -21,6 +25,10 @@ def _cast(x, dtype):
 
 def e4m3(x):
     return _cast(x, torch.float8_e4m3fn)
+
+
+def e5m2(x):
+    return _cast(x, torch.float8_e5m2)
 
 
 def f16(x):
@@ -42,6 +50,34 @@ def query_floor(q):
     amax = np.abs(q).max(-1, keepdims=True)
     up = 2.0 ** np.ceil(np.log2(np.maximum(amax, 1e-300) / 448))
     return np.where(np.abs(q) < 2.0 ** -6 * up, (2.0 ** -14 + 2.0 ** -25) * up, 0)
+
+
+# the kernel's order: the lane's five bits reversed
+OFFSET = (np.array([int(f"{i:05b}"[::-1], 2) for i in range(32)]) + 0.5) / 32 - 0.5
+
+
+def weight_model(p, heads, steps=True, offsets=True):
+    """What the terms hold of p [heads, n] (key j in lane j % 32).  steps False: without the multiples of 2^-13; offsets
+    False: without o."""
+    o = OFFSET[np.arange(p.shape[-1]) % 32] * (2.0 ** -13 if offsets else 0)
+    p = f16(p)
+    p1 = e4m3(p)
+    if heads <= 32:
+        return p1 + e4m3(f16(16 * (p - p1) + 16 * o)) / 16
+    r = f16(p - p1 + o)
+    if steps:
+        r = f16(f16(r + 0.1875) - 0.1875)
+    return p1 + e5m2(r)
+
+
+def decode_model(q, k, s, heads, tail=None, **kw):
+    """Attention of q [heads, 576] over codes k [n, 576] of one scale s, its weights through their terms; out in bf16."""
+    x = (q @ k.T) * (s * SCALE)
+    w = np.exp(x - x.max(1, keepdims=True))
+    p = weight_model(16 * w, heads, **kw) / 16
+    if tail is not None:  # key 17 is the peak
+        p = np.where(np.arange(p.shape[1]) == 17, p, tail * p)
+    return torch.from_numpy(p @ k[:, :512] * s / w.sum(1, keepdims=True)).bfloat16().double().numpy()
 
 
 def wide_query(heads, ratio):
@@ -80,4 +116,31 @@ def check_scores(out, q, k, s, heads, what):
     tol = tol + 2.0 ** -17 * p.max(1)[:, None] * np.abs(v).sum(0)
     worst = float(np.max(np.abs(out - o) / tol))
     print(f"[fp8 decode] {what}: {worst:.3f} of the tolerance, relative 2-norm {np.linalg.norm(out - o) / np.linalg.norm(o):.2e}")
+    assert worst <= 1, f"{what}: {worst:.2f} times the tolerance"
+
+
+def alternating_tail(heads, n, gap):
+    """One key `gap` above n - 1 whose values follow the sign of their lane's offset; (q, codes, scale)."""
+    k = np.zeros((n, 576))
+    k[:, :512] = np.where(OFFSET[np.arange(n) % 32] > 0, 448.0, -448.0)[:, None]
+    k[17, :512] = e4m3(np.random.default_rng(n).uniform(1, 2, 512))
+    k[17, 512] = 448
+    s = 2.0 ** -7
+    q = np.zeros((1, heads, 576))
+    q[:, :, 512] = gap / (448 * s * SCALE)
+    return torch.from_numpy(q).bfloat16(), k, s
+
+
+def check_alternating(out, q, k, s, what):
+    """out [heads, 512] of such keys.  A weight w (of a largest of 2^4) is within 2^-8 of itself and f16's rounding, and
+    where the terms' step is absolute within that step, 2^-13: half of it by rounding, half by the offset.  One below
+    2^-19 is zero: the largest offset, 31/64 of the step, does not take it to half of one."""
+    x = (q @ k.T) * (s * SCALE)
+    w = 16 * np.exp(x - x.max(1, keepdims=True))
+    v = k[:, :512] * s
+    o = w @ v / w.sum(1, keepdims=True)
+    off = np.where(w < 2.0 ** -19, w, (2.0 ** -8 + 2.0 ** -12) * w + 2.0 ** -25 + np.where(w < 2.0 ** -5, 2.0 ** -13, 0))
+    tol = np.maximum(bf16_half_ulp(o), bf16_half_ulp(out)) + off @ np.abs(v) / w.sum(1, keepdims=True)
+    worst = float(np.max(np.abs(out - o) / tol))
+    print(f"[fp8 decode] {what}: {worst:.3f} of the tolerance")
     assert worst <= 1, f"{what}: {worst:.2f} times the tolerance"

@@ -40,3 +40,14 @@ def test_a_second_term_without_its_factor_is_told(ratio):
     c.check_scores(scores_through(q, k, 2.0 ** -6, 16), q, k, 2.0 ** -6, 40, "two terms")
     with pytest.raises(AssertionError, match="times the tolerance"):
         c.check_scores(scores_through(q, k, 2.0 ** -6, 1), q, k, 2.0 ** -6, 40, "no factor")
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+@pytest.mark.parametrize("n,gap", [(2000, 9.0), (2000, 16.5), (8192, 30.0), (8192, 60.0)])
+def test_offsets_leave_weights_of_zero_alone(n, gap, heads):
+    q, k, s = c.alternating_tail(heads, n, gap)
+    q = q[0].double().numpy()
+    c.check_alternating(c.decode_model(q, k, s, heads), q, k, s, "two terms")
+    if heads > 32 and gap > 16:
+        with pytest.raises(AssertionError, match="times the tolerance"):
+            c.check_alternating(c.decode_model(q, k, s, heads, steps=False), q, k, s, "e5m2's own steps")

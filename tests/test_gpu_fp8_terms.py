@@ -35,3 +35,11 @@ def test_decode_features_spread_over_2_to_the_14(heads):
     q = torch.from_numpy(rng.standard_normal((2, heads, 576)) * np.exp2(rng.integers(-14, 1, (2, heads, 576)))).bfloat16()
     got = run_decode(q, cache, scales, table, lens, 64)
     check_decode(got, q, cache, scales, table, lens, 64, what=f"{heads} heads, spread 2^14")
+
+
+@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("n,gap", [(500, 9.0), (2000, 14.0), (2000, 16.5), (8192, 30.0), (8192, 60.0)])
+def test_decode_weights_of_zero_add_nothing(n, gap, heads):
+    q, k, s = c.alternating_tail(heads, n, gap)
+    for split in (True, False):
+        c.check_alternating(decode(q, k, s, split=split), q[0].double().numpy(), k, s, f"{heads} heads, gap {gap}, split={split}")
