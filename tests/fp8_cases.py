@@ -119,6 +119,46 @@ def check_scores(out, q, k, s, heads, what):
     assert worst <= 1, f"{what}: {worst:.2f} times the tolerance"
 
 
+def peak_over_tail(heads, n, gap):
+    """Key 17 `gap` above n - 1 of equal score, all values around a common vector; (q, codes, scale)."""
+    rng = np.random.default_rng(n + heads)
+    k = np.zeros((n, 576))
+    k[:, :512] = e4m3(rng.standard_normal((1, 512)) * 60 + rng.standard_normal((n, 512)) * 20)
+    k[17, 512] = 448
+    s = 2.0 ** -7
+    q = np.zeros((1, heads, 576))
+    q[:, :, 512] = gap / (448 * s * SCALE)
+    return torch.from_numpy(q).bfloat16(), k, s
+
+
+def check_tail(out, q, k, s, what):
+    """The tail's part P of the softmax, from what of out [heads, 512] the peak's part p0 does not explain, along the
+    tail's mean value u: (out - p0 v0) . u / u . u.  Off by at most
+      the output's rounding     sum |u_i| half_ulp(out_i) / u . u
+      relative errors           2^-8 + 2^-12 (two terms, f16) and 2 (e^d - 1) (scores off by d) of P and p0 |v0 . u| / u . u
+      the terms' absolute step  2^-13 of a largest weight of 2^4 or more.  Of 32 equal weights the 32 offsets take the
+                                nearest number up: their sum is within half a step.  The last 32 keys and the peak's count
+                                a step each, and a key's own error, a step at most, counts as far as its value along u
+                                differs from the mean's."""
+    x = (q @ k.T) * (s * SCALE)
+    p = np.exp(x - x.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    v = k[:, :512] * s
+    tail = np.delete(np.arange(len(k)), 17)
+    u = v[tail].mean(0)
+    along = v @ u / (u @ u)
+    part, peak = p[:, tail].sum(1), p[:, 17]
+    got = out @ u / (u @ u) - peak * along[17]
+    d = (np.abs(q) @ np.abs(k).T).max(1) * (s * SCALE) * 2.0 ** -24 * 584
+    tol = (np.maximum(bf16_half_ulp(out), bf16_half_ulp(p @ v)) @ np.abs(u) / (u @ u)
+           + (2.0 ** -8 + 2.0 ** -12 + 2 * np.expm1(d)) * (part + peak * abs(along[17]))
+           + 2.0 ** -17 * peak * (len(k) / 64 + 64 + np.abs(along[tail] - 1).sum()))
+    worst = float(np.max(np.abs(got - part) / tol))
+    print(f"[fp8 decode] {what}: a tail of {part[0]:.4f} off by {float(np.max(np.abs(got / part - 1))):.4f} of it, tolerance "
+          f"{float(np.max(tol / part)):.4f}, {worst:.3f} of the tolerance")
+    assert worst <= 1, f"{what}: the tail is off by {worst:.2f} times the tolerance"
+
+
 def alternating_tail(heads, n, gap):
     """One key `gap` above n - 1 whose values follow the sign of their lane's offset; (q, codes, scale)."""
     k = np.zeros((n, 576))

@@ -51,3 +51,21 @@ def test_offsets_leave_weights_of_zero_alone(n, gap, heads):
     if heads > 32 and gap > 16:
         with pytest.raises(AssertionError, match="times the tolerance"):
             c.check_alternating(c.decode_model(q, k, s, heads, steps=False), q, k, s, "e5m2's own steps")
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+@pytest.mark.parametrize("n,gap", [(3000, 6.0), (3000, 9.0), (20000, 12.0)])
+def test_a_tail_dropped_halved_or_raised_is_told(n, gap, heads):
+    q, k, s = c.peak_over_tail(heads, n, gap)
+    q = q[0].double().numpy()
+    c.check_tail(c.decode_model(q, k, s, heads), q, k, s, "two terms")
+    for factor in (0, 0.5, 1.5):
+        with pytest.raises(AssertionError, match="times the tolerance"):
+            c.check_tail(c.decode_model(q, k, s, heads, tail=factor), q, k, s, f"tail times {factor}")
+
+
+def test_a_tail_rounded_to_nearest_is_told():
+    q, k, s = c.peak_over_tail(16, 20000, 12.0)
+    q = q[0].double().numpy()
+    with pytest.raises(AssertionError, match="times the tolerance"):
+        c.check_tail(c.decode_model(q, k, s, 16, offsets=False), q, k, s, "no offsets")

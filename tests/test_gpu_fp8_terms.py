@@ -43,3 +43,11 @@ def test_decode_weights_of_zero_add_nothing(n, gap, heads):
     q, k, s = c.alternating_tail(heads, n, gap)
     for split in (True, False):
         c.check_alternating(decode(q, k, s, split=split), q[0].double().numpy(), k, s, f"{heads} heads, gap {gap}, split={split}")
+
+
+@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("n,gap", [(3000, 6.0), (3000, 9.0), (20000, 10.4), (20000, 11.1), (20000, 12.0), (20000, 13.0)])
+def test_decode_keeps_a_flat_tail(n, gap, heads):
+    q, k, s = c.peak_over_tail(heads, n, gap)
+    for split in (True, False):
+        c.check_tail(decode(q, k, s, split=split), q[0].double().numpy(), k, s, f"{heads} heads, {gap} over {n}, split={split}")
