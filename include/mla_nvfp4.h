@@ -622,7 +622,9 @@ int mla_nvfp4_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int
  * its kernel with a status instead of holding the GPU.  This call launches
  * one CTA whose first wait, on a barrier nothing arrives on, runs out after
  * limit_ns, and whose second wait, with the kernels' full 2 s limit, must
- * then end through the abort flag.
+ * then end through the abort flag; and one CTA that waits as a whole, half of
+ * whose threads give up after limit_ns, whereupon the barrier completes for
+ * the rest: no thread may go on (MLA_DEVERR_BOUNDS if one does).
  *   error_word   : device uint32, receives MLA_DEVERR_TIMEOUT.
  *   limit_ns     : the first wait's limit, 1 us .. 1 s.
  *   elapsed_ns   : device uint64 [2] or NULL: how long each wait ran.

@@ -8,6 +8,7 @@
 // chain of loads (lengths, page, scale and codes, store).
 #include <cuda_runtime.h>
 
+#include "fp8.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -213,7 +214,10 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8Append
       sine[i] = cs[lane + 32];
     }
   }
-  if (!mbar_wait(&bar, 0, p.error_word, nullptr)) return;
+  if (!mbar_wait_cta(&bar, 0, p.error_word)) {
+    if (tid == 0) drain_copies(&bar, 1, 1);
+    return;  // nothing is written
+  }
   auto latent = [&](int r, int half) { return *reinterpret_cast<const uint4*>(smem + r * kKvBytes + 512 * half + 16 * lane); };
   auto rope = [&](int r, int i, float& a, float& b) {  // the rotated pair
     const uint8_t* pe = smem + kBlock * kKvBytes + r * kPeBytes;

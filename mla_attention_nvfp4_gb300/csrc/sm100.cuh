@@ -88,6 +88,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// The same wait by every thread of the CTA: true in all of them, or, where one
+// has given up, false in all (each has a timer of its own, and a thread that
+// left by itself would be missing at the next barrier).
+__device__ __forceinline__ bool mbar_wait_cta(uint64_t* bar, uint32_t parity, uint32_t* error_word,
+                                              uint64_t limit_ns = kWaitLimitNs) {
+  return __syncthreads_and(mbar_wait(bar, parity, error_word, nullptr, limit_ns)) != 0;
+}
+
 // --------------------------------------------------------- tensor maps
 // Pull a kernel-parameter tensor map into the descriptor cache ahead of its
 // first TMA copy.

@@ -2,6 +2,8 @@
 (status codes: 1 invalid, 3 alignment, 5 workspace), and empty work is a
 no-op.  The pointers are never followed."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -127,3 +129,12 @@ def test_python_calls_want_tensors_and_arguments_of_the_right_kind():
         mla.mla_nvfp4_fp8_quantize([1.0])
     with pytest.raises(TypeError):
         mla.mla_nvfp4_fp8_gemm(None, None, None, None)
+
+
+def test_no_thread_leaves_a_wait_of_the_append_by_itself():
+    # (a lane that returned alone would be missing at the warp's shuffles and the CTA's barriers)
+    path = os.path.join(os.path.dirname(mla.__file__), "csrc", "fp8_cache.cu")
+    with open(path) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "mbar_wait_cta(" in code and "drain_copies(" in code
+    assert not re.search(r"\bmbar_wait\(", code)

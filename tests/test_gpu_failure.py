@@ -41,3 +41,12 @@ def test_wait_timeout_is_flagged_and_aborts_the_cta():
     torch.cuda.synchronize()
     assert int(err2.item()) == 0
     assert np.array_equal(cache.cpu().numpy(), oracle_cache(w, gs))
+
+
+def test_a_whole_ctas_wait_ends_for_all_its_threads_alike():
+    # half the threads give up, half see the barrier complete: none goes on
+    for limit in (1_000_000, 20_000_000):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        mla.mla_nvfp4_selftest_wait(err, limit)
+        torch.cuda.synchronize()
+        assert int(err.item()) == mla.DEVERR_TIMEOUT
