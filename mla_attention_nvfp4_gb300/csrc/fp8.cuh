@@ -51,9 +51,11 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
                : "memory");
 }
 
-// After a wait gave up: the last copies into a ring of stages (full: their
-// barriers; issued: all that were) are waited for, with a limit, so that none
-// lands in memory that its CTA has left.
+// What a CTA has in flight when it ends, after a wait that gave up too, would
+// touch memory that is no longer its own.  So an issuer waits for its products
+// (below), which have waited for their copies; and, where a role gave up, one
+// thread waits, with a limit, at the CTA's end for the last copies into each
+// ring of stages (full: their barriers; issued: all that were).
 __device__ __noinline__ inline void drain_copies(uint64_t* full, uint32_t stages, uint32_t issued) {
   for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
     for (int n = 0; n < 4096 && !mbar_test(&full[i % stages], (i / stages) & 1); ++n) {
@@ -78,6 +80,15 @@ __device__ __forceinline__ bool elect_one() {
 template <typename T>
 __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// An issuer (a whole warp) waits for its products, before it leaves; retired: a
+// barrier of its own, of one arrival.
+__device__ __forceinline__ void retire_products(uint64_t* retired, uint32_t* error_word) {
+  __syncwarp();
+  if (elect_one()) mma_commit(retired);
+  __syncwarp();
+  mbar_wait(retired, 0, error_word, nullptr);
 }
 
 // Instruction descriptor of kind::f8f6f4, e4m3 operands (format 0), fp32

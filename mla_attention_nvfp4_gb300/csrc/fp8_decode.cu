@@ -111,7 +111,7 @@ template <int kH>
 struct Misc {
   using C = Cfg<kH>;
   uint64_t full[C::slots], empty[C::slots], rfull[C::ropes], rempty[C::ropes], info_full[C::info];
-  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready, sums_ready, o_free, moved[2], rescaled[2];
+  uint64_t s_full[2], s_free[2], p_ready, pv_done, q_ready, sums_ready, o_free, moved[2], rescaled[2], retired[2];
   alignas(16) float c[kH], m[kH];
   alignas(16) float move[2][kH];  // what a tile raises the references by, in turn
   alignas(16) float inv[kH];      // a piece's references, then 1 / its sums
@@ -123,6 +123,7 @@ struct Misc {
   int64_t t0, t1, off0;
   int b0;
   uint32_t tmem;
+  int chunks, ropes;  // copies issued
   volatile int abort;
 };
 
@@ -368,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.moved[i], kSoftmax / 32);
       mbar_init(&ms.rescaled[i], kOutput / 32);
+      mbar_init(&ms.retired[i], 1);
     }
     fence_mbar_init();
   }
@@ -451,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       }
     }
-    if (!ok && lane == 0) {
-      drain_copies(ms.full, C::slots, chunks);
-      drain_copies(ms.rfull, C::ropes, ropes);
+    if (lane == 0) {
+      ms.chunks = chunks;
+      ms.ropes = ropes;
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- score products
@@ -500,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++piece;
     }
+    retire_products(&ms.retired[0], err);
   } else if (warp == 14) {
     // -------------------------------------------------------- value products
     const uint64_t dp = smem_desc_sw64(s0 + C::off_p, 512);
@@ -559,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++piece;
     }
+    retire_products(&ms.retired[1], err);
   } else if (warp < 10) {
     // ---------------------------------------------------- queries, softmax
     // A wait that gives up leaves these warps running through their loops
@@ -980,6 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 0 && lane == 0 && ms.abort) {
+    drain_copies(ms.full, C::slots, ms.chunks);
+    drain_copies(ms.rfull, C::ropes, ms.ropes);
+  }
 }
 
 // Merge of the pieces of cut sequences, in range order, by LSE; sequences

@@ -171,7 +171,7 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& mt
 }
 
 struct alignas(8) Barriers {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], retired[2];
 };
 
 // kSectors: the output's rows begin at multiples of 32 bytes.  (Both endings
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
+  __shared__ int issued_s;  // K blocks whose copies were
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int n_tiles = p.tiles_m * p.tiles_n;
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], 8);
+      mbar_init(&bars.retired[i], 1);
     }
     fence_mbar_init();
   }
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_bytes(s0 + s * kStageBytes + kABytes, &tm_w, kb * kGroup, nt * kBN, &bars.full[s]);
         }
       }
-      if (abort_s) drain_copies(bars.full, kStages, it);
+      issued_s = it;
     } else if (warp == 1 || warp == 2) {
       // An issuer for each accumulator, every other K block: one alone takes
       // longer to get from one block's products to the next one's (its waits
@@ -256,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      retire_products(&bars.retired[buf], err);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
@@ -387,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 0 && lane == 0 && abort_s) drain_copies(bars.full, kStages, issued_s);
 }
 
 // ---------------------------------------------------------------------------
@@ -439,11 +443,12 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
   constexpr int kTok = S::tokens;
   extern __shared__ uint8_t smem_raw[];
   __shared__ struct alignas(8) {
-    uint64_t full[S::stages], empty[S::stages], acc_full[2], acc_empty[2];
+    uint64_t full[S::stages], empty[S::stages], acc_full[2], acc_empty[2], retired[2];
   } bars;
   __shared__ alignas(16) float scale_s[kScaleBlocks][kT];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
+  __shared__ int issued_s;  // K blocks whose copies were
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int splits = gridDim.x, rank = blockIdx.x;
@@ -461,6 +466,7 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], 4 * S::halves);
+      mbar_init(&bars.retired[i], 1);
     }
     fence_mbar_init();
   }
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
         tma_load_bytes(s0 + s * S::stage_bytes, &tm_w, kb * kGroup, n0, &bars.full[s]);
         tma_load_bytes(s0 + s * S::stage_bytes + S::w_bytes, &tm_a, kb * kGroup, m0, &bars.full[s]);
       }
-      if (abort_s) drain_copies(bars.full, S::stages, it);
+      issued_s = it;
     }
   } else if (warp == 1 || warp == S::threads / 32 - 1) {
     // an issuer for each accumulator, as above
@@ -516,6 +522,7 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
       }
       __syncwarp();
     }
+    retire_products(&bars.retired[buf], err);
   } else {
     constexpr int kSumThreads = S::sum_threads;
     const int quad = warp & 3, tid = threadIdx.x - 64;
@@ -635,6 +642,7 @@ __global__ void __launch_bounds__(Small<kT>::threads, Small<kT>::resident)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, S::cols);
+  if (warp == 0 && lane == 0 && abort_s) drain_copies(bars.full, S::stages, issued_s);
 }
 
 template <int kT>

@@ -138,3 +138,15 @@ def test_no_thread_leaves_a_wait_of_the_append_by_itself():
         code = re.sub(r"//[^\n]*", "", f.read())
     assert "mbar_wait_cta(" in code and "drain_copies(" in code
     assert not re.search(r"\bmbar_wait\(", code)
+
+
+@pytest.mark.parametrize("name,issuers,rings", [("fp8_decode.cu", 2, 2), ("fp8_gemm.cu", 2, 2)])
+def test_no_cta_leaves_copies_or_products_in_flight(name, issuers, rings):
+    path = os.path.join(os.path.dirname(mla.__file__), "csrc", name)
+    with open(path) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert len(re.findall(r"^ +retire_products\(", code, re.M)) == issuers
+    # rings are waited for once all roles have ended, when it is known whether one gave up
+    ends = [part for part in re.split(r"tmem_dealloc\(", code)[1:]]
+    assert sum(len(re.findall(r"drain_copies\(", part.split("__global__")[0])) for part in ends) == rings
+    assert len(re.findall(r"drain_copies\(", code)) == rings
