@@ -138,8 +138,11 @@ def load_library(path: str | None = None, build_if_missing: bool = True) -> ctyp
     if _LIB is not None and path is None:
         return _LIB
     lib_path = path or _build.LIB
-    if path is None and build_if_missing and not _build.up_to_date():
-        _build.build()
+    if path is None and build_if_missing and not _build.library_up_to_date():
+        try:
+            _build.build()
+        except _build.BindingError:  # said by the 8-bit calls, which alone need it
+            pass
     if not os.path.exists(lib_path):
         raise RuntimeError(f"libmla_nvfp4.so not found at {lib_path}; run the package build")
     lib = ctypes.CDLL(lib_path)
@@ -658,9 +661,9 @@ def _fp8():
     same steps in Python would take several times the GPU's time."""
     global _FP8
     if _FP8 is None:
-        load_library()  # builds both if needed
-        if not os.path.exists(_build.BINDING):
-            raise RuntimeError(f"_mla_fp8.so not found at {_build.BINDING}; run the package build")
+        load_library()
+        if not _build.binding_up_to_date():
+            _build.build()
         spec = importlib.util.spec_from_file_location("_mla_fp8", _build.BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

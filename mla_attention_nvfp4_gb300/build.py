@@ -4,7 +4,9 @@ Python binding of its 8-bit calls with the host compiler.
 Each .cu file under csrc/ compiles to an object in parallel (binding.cpp
 meanwhile), then nvcc links the shared library.  Output:
 mla_attention_nvfp4_gb300/_build/libmla_nvfp4.so and _mla_fp8.so
-(git-ignored).  Rebuilds only when a source or header is newer than either.
+(git-ignored).  Either is rebuilt only when a source or header of it is newer.
+The library needs neither Python nor PyTorch, and is built where the binding
+cannot be.
 """
 from __future__ import annotations
 
@@ -41,21 +43,41 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(CSRC, "*.cpp")) + [os.path.join(ROOT, "include", "mla_nvfp4.h"), os.path.abspath(__file__)]
+        [os.path.join(ROOT, "include", "mla_nvfp4.h"), os.path.abspath(__file__)]
+
+
+def _binding_deps():
+    return glob.glob(os.path.join(CSRC, "*.cpp")) + [os.path.join(ROOT, "include", "mla_nvfp4.h"), os.path.abspath(__file__)]
+
+
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, _binding_deps())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and binding_up_to_date()
+
+
+class BindingError(RuntimeError):
+    """The library is built, its Python binding of the 8-bit calls is not."""
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Build what is out of date.  The library needs nvcc alone: it is linked
+    whatever becomes of the binding, whose failure raises BindingError after
+    that."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
+    srcs = _sources() if force or not library_up_to_date() else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -68,16 +90,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if force or not binding_up_to_date() else None
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if objs:
+        tmp = LIB + ".tmp"
+        cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if binding is not None:
+        try:
+            _link_binding(binding.result())
+        except Exception as e:  # no compiler, no PyTorch, no headers
+            raise BindingError(f"{LIB} is built; its Python binding of the 8-bit calls is not: {e}") from e
     return LIB
 
 
@@ -112,5 +138,9 @@ def _link_binding(obj: str) -> None:
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
-                extra_flags=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))
+    try:
+        print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
+                    extra_flags=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))
+    except BindingError as e:  # the C library is what this was asked for
+        sys.stderr.write(f"warning: {e}\n")
+        print(LIB)
