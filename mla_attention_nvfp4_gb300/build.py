@@ -3,7 +3,7 @@ Python binding of its 8-bit calls with the host compiler.
 
 Each .cu file under csrc/ compiles to an object in parallel (binding.cpp
 meanwhile), then nvcc links the shared library.  Output:
-mla_attention_nvfp4_gb300/_build/libmla_nvfp4.so and _mla_fp8.so
+mla_attention_nvfp4_gb300/_build/libmla_nvfp4.so and _mla_fp8.torch-*.so
 (git-ignored).  Either is rebuilt only when a source or header of it is newer.
 The library needs neither Python nor PyTorch, and is built where the binding
 cannot be.
@@ -11,9 +11,12 @@ cannot be.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,8 +24,23 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmla_nvfp4.so")
-BINDING = os.path.join(BUILD, "_mla_fp8.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+
+
+def binding_name() -> str:
+    """The binding is of one interpreter's and one PyTorch's ABI: its file
+    name holds both, so that a tree that meets others builds another one.
+    (PyTorch's version is read from its files: a C user's build imports none.)"""
+    version = "none"
+    spec = importlib.util.find_spec("torch")
+    if spec is not None and spec.origin:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            found = re.search(r"^__version__ = ['\"]([^'\"]+)['\"]", f.read(), re.M)
+        version = found.group(1) if found else "unknown"
+    return f"_mla_fp8.torch-{version}{sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+BINDING = os.path.join(BUILD, binding_name())
 
 
 def nvcc() -> str:
@@ -115,8 +133,6 @@ def _run(cmd):
 
 def _compile_binding() -> str:
     """binding.cpp against this interpreter's and this PyTorch's headers."""
-    import sysconfig
-
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))) if os.path.isabs(nvcc()) else "/usr/local/cuda"

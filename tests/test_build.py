@@ -2,6 +2,7 @@
 (no GPU, nothing of the package's own build is touched)."""
 import os
 import stat
+import sysconfig
 
 import pytest
 import torch
@@ -49,3 +50,22 @@ def test_calls_without_the_binding_load_the_library(tmp_path, monkeypatch):
     assert mla.load_library().mla_nvfp4_status_string(0)
     with pytest.raises(RuntimeError, match="8-bit"):
         mla.mla_nvfp4_fp8_quantize(torch.zeros(2, 128).bfloat16())
+
+
+def test_the_binding_is_of_this_interpreter_and_this_pytorch(tmp_path, monkeypatch):
+    # a tree built beside another PyTorch or Python is not taken for current
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert torch.__version__ in os.path.basename(b.BINDING) and b.BINDING.endswith(suffix)
+    assert b.binding_name() == os.path.basename(b.BINDING)
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "__init__.py").write_text("")
+    (other / "version.py").write_text("__version__ = '9.9.0'\n")
+
+    class Spec:
+        origin = str(other / "__init__.py")
+
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: Spec)
+    assert b.binding_name() == f"_mla_fp8.torch-9.9.0{suffix}"
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: None)
+    assert "torch-none" in b.binding_name()
