@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
     // (div_rn); 1 / 448 rounded is a constant
     const float scale = isinf(am) ? am : fmaxf(div_rn(am, 448.f, 0.0022321429569274187f), 1.1754943508222875e-38f);
     const float inv = __frcp_rn(scale);
-    const uint64_t inv2 = pack2(inv, inv), neg2 = pack2(-scale, -scale);
+    const uint64_t ninv2 = pack2(-inv, -inv), den2 = pack2(scale, scale);
     uint32_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -87,14 +87,16 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
       for (int j = 0; j < 2; ++j) {
         float a, b;
         bf16x2_to_f32(w[2 * k + j], a, b);
+        // everything with 1 / -scale, the quotient's sign turned at the end: a
+        // remainder of zero then leaves -0 as it is
         const uint64_t num = pack2(a, b);
-        const uint64_t q0 = mul2(num, inv2);
+        const uint64_t q0 = mul2(num, ninv2);
         uint64_t r = num;
-        fma2(r, q0, neg2);  // the exact remainder
+        fma2(r, q0, den2);  // the exact remainder
         uint64_t q = q0;
-        fma2(q, r, inv2);
+        fma2(q, r, ninv2);
         unpack2(isinf(scale) ? q0 : q, a, b);
-        code |= cvt_e4m3x2(a, b) << (16 * j);
+        code |= cvt_e4m3x2(-a, -b) << (16 * j);
       }
       out[k] = code;
     }

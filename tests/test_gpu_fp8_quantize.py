@@ -1,0 +1,31 @@
+"""The e4m3 quantiser where its quotients are delicate: codes and scales equal
+the oracle's, which divides in float32."""
+import numpy as np
+import pytest
+import torch
+
+import mla_attention_nvfp4_gb300 as mla
+from oracle import fp8
+from tests.helpers import f32
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+DEV = "cuda:0"
+
+
+def check(t):
+    codes, scales = mla.mla_nvfp4_fp8_quantize(t.to(DEV))
+    rc, rs = fp8.quantize(f32(t))
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    got = codes.cpu().view(torch.uint8).numpy()
+    assert np.array_equal(got, rc), f"{int((got != rc).sum())} codes differ"
+
+
+def test_quantize_keeps_the_sign_of_zero():
+    # among other numbers, alone in a group, and beside an infinity
+    x = torch.randn(6, 512).bfloat16()
+    x[:, ::3] = -0.0
+    x[:, 1::3] = 0.0
+    x[1, :128] = -0.0
+    x[2, 5] = float("inf")
+    check(x)
