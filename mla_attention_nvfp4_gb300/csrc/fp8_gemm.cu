@@ -21,11 +21,12 @@ constexpr int kGroup = MLA_FP8_GROUP;
 // 8 lanes hold a group, 16 features each (two 16-byte loads, one 16-byte
 // store; 8 features where K asks for it); two groups in flight per 8 lanes.
 // HBM-bound, but only with few instructions an element: maxima on bf16
-// pairs, quotients on pairs of floats.  8192 x 16384: 64 us (6.4 TB/s; 75 with
+// pairs, quotients on pairs of floats.  8192 x 16384: 64.5 us (6.3 TB/s; 75 with
 // one element at a time); 64 x 7168: 2.1 us.
 // x / scale is rounded to nearest by Markstein's method: with y = 1 / scale
 // rounded to nearest and q0 = x y, the remainder x - q0 scale is exact in one
-// fused multiply-add, and q0 + y remainder is the quotient, rounded once.
+// fused multiply-add (tiny groups are scaled up for that), and q0 + y remainder
+// is the quotient, rounded once.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 constexpr int kQuantUnroll = 2;
@@ -33,6 +34,12 @@ constexpr int kQuantGroups = kQuantThreads / 8 * kQuantUnroll;  // groups per CT
 
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t times_2_64(uint32_t a) {
+  const __nv_bfloat162 r =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), __float2bfloat162_rn(18446744073709551616.f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -65,7 +72,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 #pragma unroll
   for (int i = 0; i < kQuantUnroll; ++i) {
     const int64_t g = first + i * (kQuantThreads / 8);
-    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
     uint32_t m2 = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m2 = max_abs2(m2, w[k] & 0x7FFF7FFFu);  // NaN gives the other operand
@@ -73,12 +80,22 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
     for (int o = 4; o > 0; o >>= 1) m2 = max_abs2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
     float lo, hi;
     bf16x2_to_f32(m2, lo, hi);
-    const float am = fmaxf(lo, hi);
+    float am = fmaxf(lo, hi), least = 1.1754943508222875e-38f, down = 1.f;
+    if (__builtin_expect(am < 2.42861286636753e-17f, 0)) {  // 448 * 2^-64
+      // A tiny group times 2^64, exactly, with the same quotients: the exact
+      // remainder reaches 2^-46 below a numerator, and fp32 ends at 2^-149.
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = times_2_64(w[k]);
+      am *= 18446744073709551616.f;
+      least *= 18446744073709551616.f;
+      down = 5.421010862427522e-20f;
+    }
     // both quotients rounded to nearest, from correctly rounded reciprocals
     // (div_rn); 1 / 448 rounded is a constant
-    const float scale = isinf(am) ? am : fmaxf(div_rn(am, 448.f, 0.0022321429569274187f), 1.1754943508222875e-38f);
-    const float inv = __frcp_rn(scale);
-    const uint64_t ninv2 = pack2(-inv, -inv), den2 = pack2(scale, scale);
+    const float den = isinf(am) ? am : fmaxf(div_rn(am, 448.f, 0.0022321429569274187f), least);
+    const float scale = den * down;
+    const float inv = __frcp_rn(den);
+    const uint64_t ninv2 = pack2(-inv, -inv), den2 = pack2(den, den);
     uint32_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -95,7 +112,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
         fma2(r, q0, den2);  // the exact remainder
         uint64_t q = q0;
         fma2(q, r, ninv2);
-        unpack2(isinf(scale) ? q0 : q, a, b);
+        unpack2(isinf(den) ? q0 : q, a, b);
         code |= cvt_e4m3x2(-a, -b) << (16 * j);
       }
       out[k] = code;
