@@ -135,7 +135,7 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
   return Py_BuildValue("(NN)", x, y);
 }
 int int32_of(int64_t v, const char* what) {
-  need(v <= INT32_MAX, what);
+  need(v >= INT32_MIN && v <= INT32_MAX, what);
   return static_cast<int>(v);
 }
 
@@ -187,7 +187,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int st = mla_nvfp4_fp8_cache_append(
       kv.data_ptr(), T > 1 ? kv.stride(0) : MLA_D_LATENT, pe.data_ptr(), T > 1 ? pe.stride(0) : MLA_D_ROPE, T,
       data<float>(cs), cs.size(0), interleaved ? 1 : 0, data<int32_t>(cu), data<int32_t>(ctx),
-      int32_of(B, "too many sequences"), int32_of(max_new, "max_new_tokens too large"), data<int32_t>(pt), pt_stride,
+      int32_of(B, "too many sequences"), int32_of(max_new, "max_new_tokens out of range"), data<int32_t>(pt), pt_stride,
       pt.size(1), static_cast<int>(page_size), data<uint8_t>(cache), slots, data<float>(scales),
       H > 0 ? q.data_ptr() : nullptr, q_st, q_sh, H > 0 ? o.data_ptr() : nullptr, o_st, o_sh, int32_of(H, "too many heads"), err, at.stream);
   if (st != MLA_OK) return status(st);

@@ -1,0 +1,32 @@
+"""Calls of the 8-bit path's Python functions that their documentation allows
+or forbids, beside those of tests/test_gpu_fp8.py."""
+import numpy as np
+import pytest
+import torch
+
+import mla_attention_nvfp4_gb300 as mla
+from tests.helpers import f32
+from tests.test_gpu_fp8 import F8, SCALE, check_append, check_decode, errw, make_append, make_cache, run_decode, u8
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+DEV = "cuda:0"
+
+
+def append(c, q=None, q_out=None, **kw):
+    d = {k: torch.from_numpy(c[k]).to(DEV) for k in ("cu", "ctx", "cs", "table", "cache", "scales")}
+    e = errw()
+    got = mla.mla_nvfp4_fp8_cache_append(c["kv"].to(DEV), c["pe"].to(DEV), d["cs"], d["cu"], d["ctx"], d["table"],
+                                         d["cache"].view(F8), d["scales"], page_size=c["page"], q_pe=q, q_out=q_out,
+                                         error_word=e, **kw)
+    torch.cuda.synchronize()
+    assert int(e.item()) == 0
+    return u8(d["cache"]), d["scales"].cpu().numpy(), None if got is None else f32(got)
+
+
+@pytest.mark.parametrize("bad", [-1, -(2 ** 31), -(2 ** 31) - 1, 3 - 2 ** 32, 2 ** 31, 2 ** 32 + 3, 2 ** 63 - 1])
+def test_append_refuses_max_new_tokens_out_of_range(bad):
+    # (3 - 2^32 and 2^32 + 3 have the low 32 bits of 3)
+    c = make_append(np.random.default_rng(0), (3,), (0,), 64, 0)
+    with pytest.raises((ValueError, mla.MLAError)):
+        append(c, max_new_tokens=bad)
