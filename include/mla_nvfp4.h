@@ -526,8 +526,9 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
  *                  sequence of the call (blocks of a shared prefix are full
  *                  and so never written).
  *   q_pe, q_out  : bf16 [num_tokens, num_heads, 64], element strides per token
- *                  and head; q_out may be q_pe with the same strides, or both
- *                  NULL with num_heads 0.  Rounded once, to bf16.
+ *                  and head, in either order (rows of 64 that do not overlap);
+ *                  q_out may be q_pe with the same strides, or both NULL
+ *                  with num_heads 0.  Rounded once, to bf16.
  * A block's scale is the smallest power of two s = 2^e, -60 <= e <= 60, with
  * |key| <= 448 s over the block.  It only grows until the block's first
  * token is written again, which starts it anew; where it grows, the codes of

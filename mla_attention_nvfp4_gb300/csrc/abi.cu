@@ -506,9 +506,12 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
   if (num_tokens > (int64_t(1) << 31) - 1 || kv_c_stride < MLA_D_LATENT || k_pe_stride < MLA_D_ROPE ||
       max_pages < 1 || max_pages > INT32_MAX || page_table_stride < max_pages)
     return MLA_ERR_INVALID_ARG;
-  if (num_heads > 0 && (q_stride_h < MLA_D_ROPE || q_out_stride_h < MLA_D_ROPE ||
-                        q_stride_t < q_stride_h * (num_heads - 1) + MLA_D_ROPE ||
-                        q_out_stride_t < q_out_stride_h * (num_heads - 1) + MLA_D_ROPE))
+  // (token, head) rows that do not overlap: a token's heads inside its stride, or a head's tokens inside that one's
+  const auto apart = [&](int64_t t, int64_t h) {
+    return t >= MLA_D_ROPE && h >= MLA_D_ROPE &&
+           ((t - MLA_D_ROPE) / h >= num_heads - 1 || (h - MLA_D_ROPE) / t >= num_tokens - 1);
+  };
+  if (num_heads > 0 && (!apart(q_stride_t, q_stride_h) || !apart(q_out_stride_t, q_out_stride_h)))
     return MLA_ERR_INVALID_ARG;
   if (num_heads > 0 && q_pe == q_out && (q_stride_t != q_out_stride_t || q_stride_h != q_out_stride_h))
     return MLA_ERR_INVALID_ARG;

@@ -30,3 +30,32 @@ def test_append_refuses_max_new_tokens_out_of_range(bad):
     c = make_append(np.random.default_rng(0), (3,), (0,), 64, 0)
     with pytest.raises((ValueError, mla.MLAError)):
         append(c, max_new_tokens=bad)
+
+
+@pytest.mark.parametrize("new,ctx", [((5, 70, 1), (60, 3, 128)), ((1,), (7,)), ((1, 1), (0, 64))])
+@pytest.mark.parametrize("heads", [1, 4, 33])
+@pytest.mark.parametrize("order", ["head-major", "head-major inside wider rows", "head-major out only"])
+def test_append_rotates_queries_of_either_order(order, heads, new, ctx):
+    c = make_append(np.random.default_rng(heads), new, ctx, 64, heads)
+    T, q = sum(new), c["q"].to(DEV)
+    by_head = torch.zeros(heads, T, 72 if "wider" in order else 64, dtype=torch.bfloat16, device=DEV)
+    view = by_head[:, :, :64].transpose(0, 1)
+    if order == "head-major out only":
+        got = append(c, q=q, q_out=view)
+    else:
+        view.copy_(q)
+        got = append(c, q=view, q_out=view)
+        assert not by_head[:, :, 64:].any()
+    check_append(c, got, True, T)
+
+
+def test_append_refuses_queries_that_overlap():
+    c = make_append(np.random.default_rng(1), (3,), (0,), 64, 4)
+    q = c["q"].to(DEV)
+    flat = torch.zeros(3 * 4 * 64 + 64, dtype=torch.bfloat16, device=DEV)
+    for strides in ((64, 64, 1), (128, 64, 1), (64, 128, 1), (0, 64, 1), (256, 0, 1), (256, 56, 1)):
+        bad = flat.as_strided((3, 4, 64), strides)
+        with pytest.raises(mla.MLAError):
+            append(c, q=q, q_out=bad)
+        with pytest.raises(mla.MLAError):
+            append(c, q=bad, q_out=bad)
