@@ -558,7 +558,8 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  * mla_nvfp4_fp8_decode: absorbed MLA decode over that cache.
  *   q            : bf16 [batch, num_heads, 576] contiguous = [q_nope.W_UK (512),
  *                  rotated q_pe (64)] per head.
- *   page_table   : int32 [batch, max_pages], row stride page_table_stride;
+ *   page_table   : int32 [batch, max_pages], row stride page_table_stride (0:
+ *                  one row for all sequences);
  *   seq_lens     : int32 [batch], keys of sequence b (its newest token's too).
  *   out, lse     : bf16 [batch, num_heads, 512]; fp32 [batch, num_heads] natural
  *                  log, or NULL.  A sequence with no keys gives out = 0 and

@@ -542,7 +542,7 @@ int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t*
                          float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream) {
   if (batch < 0 || num_heads < 1 || num_slots < 0 || page_size < MLA_FP8_BLOCK || page_size % MLA_FP8_BLOCK != 0 ||
       num_slots % MLA_FP8_BLOCK != 0 || num_slots > (int64_t(1) << 31) - MLA_FP8_BLOCK || max_pages < 1 ||
-      max_pages > INT32_MAX || page_table_stride < max_pages)
+      max_pages > INT32_MAX || (page_table_stride < max_pages && page_table_stride != 0))
     return MLA_ERR_INVALID_ARG;
   if (batch == 0) return MLA_OK;
   if (q == nullptr || cache == nullptr || scales == nullptr || page_table == nullptr || seq_lens == nullptr ||

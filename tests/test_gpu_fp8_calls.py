@@ -59,3 +59,26 @@ def test_append_refuses_queries_that_overlap():
             append(c, q=q, q_out=bad)
         with pytest.raises(mla.MLAError):
             append(c, q=bad, q_out=bad)
+
+
+@pytest.mark.parametrize("split", [True, False])
+def test_decode_reads_one_page_table_for_all_sequences(split):
+    # several queries of one cached text: an expanded row
+    rng = np.random.default_rng(3)
+    n, lens = 700, (700, 1, 513, 700)
+    cache, scales, table = make_cache(rng, (n,), 64)
+    q = torch.from_numpy(rng.standard_normal((4, 16, 576))).bfloat16()
+    e = errw()
+    out, lse = mla.mla_nvfp4_fp8_decode(
+        q.to(DEV), torch.from_numpy(cache).to(DEV).view(F8), torch.from_numpy(scales).to(DEV), SCALE,
+        page_table=torch.from_numpy(table).to(DEV).expand(4, -1), seq_lens=torch.tensor(lens, dtype=torch.int32, device=DEV),
+        return_lse=True, split=split, error_word=e)
+    torch.cuda.synchronize()
+    assert int(e.item()) == 0
+    check_decode((f32(out), f32(lse)), q, cache, scales, np.repeat(table, 4, 0), lens, 64, what="one page table")
+    own = run_decode(q, cache, scales, np.repeat(table, 4, 0), lens, 64, split=split)
+    assert np.array_equal(own[0], f32(out)) and np.array_equal(own[1], f32(lse))
+    with pytest.raises(mla.MLAError):  # rows that overlap in part
+        mla.mla_nvfp4_fp8_decode(q.to(DEV), torch.from_numpy(cache).to(DEV).view(F8), torch.from_numpy(scales).to(DEV), SCALE,
+                                 page_table=torch.zeros(20, dtype=torch.int32, device=DEV).as_strided((4, 5), (3, 1)),
+                                 seq_lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
