@@ -574,9 +574,10 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  * Held in fewer bits than float32: a query's features, exactly as given down
  * to 2^-13 of their head's largest and within 2^-21 of that below.
  * Rows of the cache that hold no key of the sequence are never used,
- * whatever their bytes.  A NaN or an infinity in a query makes that head's
- * out and lse NaN, a NaN code in a key those of its sequence.  Errors: MLA_DEVERR_BOUNDS for a length past the page
- * table or a page outside the cache, MLA_DEVERR_SCALE for a block scale out
+ * whatever their bytes.  A NaN or an infinity in a query, or a score above
+ * fp32's range (or all of them below it), makes that head's out and lse NaN, a
+ * NaN code in a key those of its sequence.  Errors: MLA_DEVERR_BOUNDS for a length past the page table
+ * or a page outside the cache, MLA_DEVERR_SCALE for a block scale out
  * of range: those keys are skipped.
  */
 int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,

@@ -82,6 +82,7 @@ constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.15292150460684
 constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
 constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest weight at 2^4
 constexpr float kGain = 16.f;   // queries' and 32 heads' weights' second terms: at most 16 becomes 256
+constexpr float kBelow = -3.402823466e38f;  // a piece's LSE where all its scores are below fp32's range
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 // The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (piece > 0) wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
       ms.sums[quad][hb + lane * kMine / 32] = l[0];
-      if (tid < kMine) ms.inv[hb + tid] = mr[tid];
+      if (tid < kMine) ms.inv[hb + tid] = set ? mr[tid] : -INFINITY;  // -inf: no keys
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.sums_ready);
       half_bar(wg);  // c is free for the next piece
@@ -917,9 +918,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&ms.sums_ready, piece & 1, err, &ms.abort);
       if (tid < kH) {
         const float m = ms.inv[tid];
-        const float sum = (ms.sums[0][tid] + ms.sums[1][tid]) + (ms.sums[2][tid] + ms.sums[3][tid]);
+        float sum = (ms.sums[0][tid] + ms.sums[1][tid]) + (ms.sums[2][tid] + ms.sums[3][tid]);
+        // a score above fp32's range, or all of a sequence's below it (of a
+        // piece's: kBelow, and the merge decides)
+        const bool below = sum == 0.f && m != -INFINITY;
+        if (isinf(sum) || (below && whole)) sum = __uint_as_float(0x7FC00000u);
         ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-        const float l2 = sum != 0.f ? m + log2f(sum) : -INFINITY;
+        const float l2 = sum != 0.f ? m + log2f(sum) : below ? kBelow : -INFINITY;
         if (!whole)
           p.part_lse[part_row + tid] = l2;
         else if (p.a.lse != nullptr && tid < heads)
@@ -1049,6 +1054,7 @@ __global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(c
       sum += part[warp + s][8][lane];
     }
   }
+  if (m == kBelow) sum = __uint_as_float(0x7FC00000u);
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

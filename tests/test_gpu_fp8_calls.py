@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import mla_attention_nvfp4_gb300 as mla
+from oracle import fp8
 from tests.helpers import f32
 from tests.test_gpu_fp8 import F8, SCALE, check_append, check_decode, errw, make_append, make_cache, run_decode, u8
 
@@ -82,3 +83,73 @@ def test_decode_reads_one_page_table_for_all_sequences(split):
         mla.mla_nvfp4_fp8_decode(q.to(DEV), torch.from_numpy(cache).to(DEV).view(F8), torch.from_numpy(scales).to(DEV), SCALE,
                                  page_table=torch.zeros(20, dtype=torch.int32, device=DEV).as_strided((4, 5), (3, 1)),
                                  seq_lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("heads", [16, 40])
+@pytest.mark.parametrize("n", [300, 20000])
+def test_decode_scores_above_the_range_give_nan(n, heads, split):
+    # 2^120 times 448 times a block scale of 2^8: the head's results are NaN whether its sequence is cut or not, the
+    # others' as ever; with the sign turned the key has no weight
+    rng = np.random.default_rng(n)
+    cache, scales, table = make_cache(rng, (n,), 64)
+    at = table[0][np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64
+    cache[at, 3] = 0
+    cache[int(table[0][1]) * 64 + 7, 3] = 0x7E  # key 71
+    scales[table[0][1]] = 2.0 ** 8
+    q = torch.from_numpy(rng.standard_normal((1, heads, 576)) * 2.0 ** -10).bfloat16()
+    q[:, :, 3] = 0
+    clean = run_decode(q, cache, scales, table, (n,), 64, split=split)
+    for sign in (1, -1):
+        big = q.clone()
+        big[0, 2] = 0
+        big[0, 2, 3] = sign * 2.0 ** 120
+        out, lse, flags = run_decode(big, cache, scales, table, (n,), 64, split=split)
+        assert flags == 0
+        if sign > 0:
+            assert np.all(np.isnan(out[0, 2])) and np.isnan(lse[0, 2])
+        else:
+            assert np.all(np.isfinite(out[0, 2])) and abs(lse[0, 2] - np.log(n - 1)) < 1e-5
+        other = np.arange(heads) != 2
+        assert np.array_equal(out[:, other], clean[0][:, other]) and np.array_equal(lse[:, other], clean[1][:, other])
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+def test_decode_scores_all_below_the_range_give_nan(heads):
+    # (a head without keys gives zeros and -inf; this one has keys)
+    cache, scales, table = make_cache(np.random.default_rng(6), (1, 0), 64)
+    cache[int(table[0][0]) * 64, 3] = 0x7E
+    scales[:] = 2.0 ** 8
+    q = torch.zeros(2, heads, 576, dtype=torch.bfloat16)
+    q[0, 1, 3] = -(2.0 ** 120)
+    for split in (True, False):
+        out, lse, flags = run_decode(q, cache, scales, table, (1, 0), 64, split=split)
+        assert flags == 0 and np.all(np.isnan(out[0, 1])) and np.isnan(lse[0, 1])
+        assert np.all(np.isfinite(np.delete(out[0], 1, 0))) and np.allclose(np.delete(lse[0], 1), 0, atol=1e-6)
+        assert np.all(out[1] == 0) and np.all(np.isneginf(lse[1]))
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+def test_decode_scores_below_the_range_in_a_part_of_a_sequence(heads):
+    # the first 6000 keys' scores are below fp32's range: they have no weight, though whole pieces of a cut sequence
+    # consist of them; with all keys' below it the head is NaN
+    rng = np.random.default_rng(7)
+    n = 20000
+    cache, scales, table = make_cache(rng, (n,), 64)
+    at = table[0][np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64
+    cache[at, 3] = np.where(np.arange(n) < 6000, 0x7E, 0)
+    scales[table[0][:-(-n // 64)]] = 2.0 ** 8
+    q = torch.zeros(1, heads, 576, dtype=torch.bfloat16)
+    q[0, 1, 3] = -(2.0 ** 120)
+    v = fp8.decode_codes(cache[at, :512]) * 2.0 ** 8
+    for split in (True, False):
+        out, lse, flags = run_decode(q, cache, scales, table, (n,), 64, split=split)
+        assert flags == 0 and np.all(np.isfinite(out)) and abs(lse[0, 1] - np.log(n - 6000)) < 1e-4
+        # a mean of n - 6000 values: bf16's rounding and the weights' 2^-8 (of 2^4, exact) of their magnitude
+        ref, mag = v[6000:].mean(0), np.abs(v[6000:]).mean(0)
+        assert np.all(np.abs(out[0, 1] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * mag)
+        cache2 = cache.copy()
+        cache2[at, 3] = 0x7E
+        out, lse, flags = run_decode(q, cache2, scales, table, (n,), 64, split=split)
+        assert flags == 0 and np.all(np.isnan(out[0, 1])) and np.isnan(lse[0, 1])
+        assert np.all(np.isfinite(out[0, 0])) and abs(lse[0, 0] - np.log(n)) < 1e-4
