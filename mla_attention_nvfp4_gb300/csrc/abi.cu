@@ -570,7 +570,7 @@ int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K
   if (!aligned16(x) || (x_stride * 2) % 16 || !aligned16(codes)) return MLA_ERR_ALIGNMENT;
   const int sms = device_sms();
   if (sms < 0) return -sms;
-  return mla::launch_fp8_quantize(x, x_stride, M, K, codes, scales, static_cast<cudaStream_t>(stream), sms);
+  return mla::launch_fp8_quantize(x, x_stride, M, K, codes, scales, static_cast<cudaStream_t>(stream));
 }
 
 int mla_nvfp4_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int64_t M, const uint8_t* w,

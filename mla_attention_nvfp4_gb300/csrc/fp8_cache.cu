@@ -42,11 +42,6 @@ __device__ __forceinline__ float block_scale_pow2(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ uint32_t bf16x2_pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // One pair turned by an angle: products and sums each rounded to float32, as
 // the plain formula evaluates (no contraction), so that the rounding of the
 // result to 8 or 16 bits sees the same value.

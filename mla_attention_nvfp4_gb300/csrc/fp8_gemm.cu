@@ -2,8 +2,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
+#include "encode_tiled.h"
 #include "fp8.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
@@ -174,11 +173,6 @@ struct Params {
   int tiles_m, tiles_n;
   uint32_t* error_word;
 };
-
-__device__ __forceinline__ uint32_t bf16x2_pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Tile t: groups of kRaster row tiles, inside a group column by column.
 __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& mt, int& nt) {
@@ -684,33 +678,10 @@ int launch_small(const CUtensorMap& tm_a, const CUtensorMap& tm_w, const Params&
   return cuda_status(cudaLaunchKernelEx(&cfg, fp8_gemm_small_kernel<kT>, tm_a, tm_w, p));
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled from the driver at run time (the library links only
-// the CUDA runtime).
-EncodeTiledFn encode_fn() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      f = reinterpret_cast<EncodeTiledFn>(ptr);
-      fn.store(f, std::memory_order_release);
-    }
-  }
-  return f;
-}
-
 }  // namespace
 
 int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
-                        cudaStream_t stream, int num_sms) {
-  (void)num_sms;
+                        cudaStream_t stream) {
   const int row_groups = static_cast<int>((K + kGroup - 1) / kGroup);
   const int64_t groups = M * row_groups;  // < 2^31 (checked by the caller)
   uint32_t magic;
@@ -725,7 +696,7 @@ int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, u
 
 bool encode_byte_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t stride, uint32_t box_x,
                      uint32_t box_rows, bool swizzle64) {
-  const EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = encode_tiled_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};

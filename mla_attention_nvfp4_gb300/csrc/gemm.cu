@@ -35,8 +35,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
+#include "encode_tiled.h"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -295,32 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// cuTensorMapEncodeTiled from the driver at run time (the library links
-// only the CUDA runtime).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn gemm_encode_fn() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      f = reinterpret_cast<EncodeTiledFn>(ptr);
-      fn.store(f, std::memory_order_release);
-    }
-  }
-  return f;
-}
-
 // Packed codes [rows, K/2] bytes as a 2-D byte map; box = 128 bytes x
 // box_rows rows, 128-byte swizzle (rows past the end read as zero).
 bool make_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t K, uint32_t box_rows) {
-  auto fn = gemm_encode_fn();
+  auto fn = encode_tiled_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};

@@ -224,7 +224,7 @@ size_t fp8_decode_workspace_bytes(int batch, int num_heads, int num_sms);
 int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms);
 
 int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
-                        cudaStream_t stream, int num_sms);
+                        cudaStream_t stream);
 
 struct Fp8GemmArgs {
   const uint8_t* a;

@@ -178,4 +178,10 @@ __device__ __forceinline__ void bf16x2_to_f32(uint32_t v, float& lo, float& hi) 
   hi = __uint_as_float(v & 0xFFFF0000u);
 }
 
+// two floats -> bf16x2 (packed in a u32), rounded to nearest
+__device__ __forceinline__ uint32_t bf16x2_pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 }  // namespace mla

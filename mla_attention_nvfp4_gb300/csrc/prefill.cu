@@ -64,6 +64,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "encode_tiled.h"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -798,30 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------- host side
-// cuTensorMapEncodeTiled, fetched from the driver at run time (the library
-// links only the CUDA runtime).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
 
 // [T, H, D] bf16 with element strides (st, sh, 1) as a 4-D map
 // (64 features, H, T, D/64 chunks of 128 bytes); box = 64 features x 1 head x
 // 128 tokens x all chunks, 128-byte swizzle: one copy per Q, K or V tile.
 bool make_map(CUtensorMap* m, const void* base, int64_t D, int64_t H, int64_t T, int64_t st, int64_t sh) {
-  auto fn = encode_fn();
+  auto fn = encode_tiled_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(D / 64)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(sh * 2), static_cast<cuuint64_t>(st * 2), 128};
