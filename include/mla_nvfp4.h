@@ -533,7 +533,8 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
  * |key| <= 448 s over the block.  It only grows until the block's first
  * token is written again, which starts it anew; where it grows, the codes of
  * the block's earlier tokens are multiplied by s_old / s_new and rounded
- * again (exact but for results below 2^-6, where e4m3 is subnormal).  Codes
+ * again (exact but for results below 2^-6, where e4m3 is subnormal).  (A
+ * caller's own scale that is no power of two: by 1 / s rounded to fp32.)  Codes
  * round to nearest even and saturate at +-448; a NaN feature gives the NaN
  * code and no amax.
  *   Errors       : MLA_DEVERR_BOUNDS for cu_seqlens out of range, a negative
@@ -572,7 +573,10 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  *                  that may run at once need a workspace each.
  * scores = softmax_scale * q . key, out = softmax . key[:512].
  * Held in fewer bits than float32: a query's features, exactly as given down
- * to 2^-13 of their head's largest and within 2^-21 of that below.
+ * to 2^-13 of their head's largest and within 2^-21 of that below; a key's
+ * weight in the sum of the values, within 2^-8 + 2^-12 of itself plus 2^-17 of
+ * the largest (long tails of equal weights keep their sum).  Scores, the
+ * weights' own sum and lse are fp32.
  * Rows of the cache that hold no key of the sequence are never used,
  * whatever their bytes.  A NaN or an infinity in a query, or a score above
  * fp32's range (or all of them below it), makes that head's out and lse NaN, a
@@ -605,7 +609,8 @@ int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K
 /*
  * mla_nvfp4_fp8_gemm: out[m, n] = sum over blocks j of 128 features of
  *     a_scales[m, j] * w_scales[n / 128, j] * sum_{k in j} a[m, k] * w[n, k],
- * summed in fp32 and rounded once to bf16.
+ * summed in fp32 and rounded once to bf16.  A block's two scales are
+ * multiplied first, in fp32, whose range their product must not leave.
  *   a : e4m3 [M, K], row stride lda bytes;  a_scales : fp32 [M, ceil(K / 128)].
  *   w : e4m3 [N, K], row stride ldw bytes;  w_scales : fp32
  *       [ceil(N / 128), ceil(K / 128)].

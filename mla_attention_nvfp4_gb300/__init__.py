@@ -38,7 +38,8 @@ DEVERR_BOUNDS, DEVERR_TIMEOUT, DEVERR_SCALE, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8
 # Kernels each entry point launches (for launch accounting in the benchmark);
 # decode launches one kernel with one key split, two (plus the merge) with
 # uniform splits and three (plan, decode, merge) when planned, see
-# decode_launches(); the e4m3 decode launches its merge unless split is False.
+# decode_launches(); the e4m3 decode launches its merge too, unless split is
+# False or the page table is at most 384 keys wide.
 LAUNCHES_PER_CALL = {"cache_write": 1, "decode": 3, "prefill": 1, "global_scale": 2, "gemm": 1,
                      "gather_latent": 1, "prefill_partial": 1, "merge_fused_out": 1, "prefill_qdq": 2,
                      "prefill_fakequant": 1, "fp8_cache_append": 1, "fp8_decode": 2, "fp8_quantize": 1, "fp8_gemm": 1}
@@ -689,7 +690,10 @@ def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, pa
     [num_slots / 64]), in place.  With q_pe [T,H,64] the queries' RoPE part is
     rotated too, into q_out (default: a new tensor; q_pe itself rotates in
     place), which is returned.  max_new_tokens bounds the tokens of one
-    sequence (default T; a tighter bound starts fewer CTAs)."""
+    sequence (default T).  The grid is one for num_seqs sequences of that many
+    tokens, and CTAs past a sequence's end return at once: for a batch of
+    prompts give the longest one's length, or over T / 64 CTAs a sequence
+    start for nothing."""
     return _result("mla_nvfp4_fp8_cache_append", _fp8().append(
         kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, page_size, interleaved, q_pe, q_out,
         max_new_tokens, error_word))

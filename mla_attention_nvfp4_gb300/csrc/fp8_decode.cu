@@ -50,10 +50,11 @@
 //                goes on; a piece's output, while the next one starts.
 // The code of each role is kept short (rolled loops, one copy): unrolled
 // further, the warps waited for instructions more than for anything else.
-// Times: 64 x 4096 keys, 128 heads 87 us, 64 heads 63, 16 heads 44; 128
-// sequences of 1k to 32k, 16 heads 136 us (5.0 TB/s), 128 heads 315 (1040
-// TFLOP/s); 1 x 65536, 128 heads 36; 1 x 100, 16 heads 12, launches and one
-// chain of latencies.  With 64 heads a CTA, shared memory bounds a tile: the
+// Times (merge included; pairs below compare two forms at one time): 64 x 4096
+// keys, 128 heads 88.5 us, 64 heads 65, 16 heads 46; 128 sequences of 1k to
+// 32k, 16 heads 138 us (5.0 TB/s), 128 heads 324 (1020 TFLOP/s); 1 x 65536, 128
+// heads 37.4; 1 x 100, 16 heads 9.9 (12.3 with the merge), launches and one chain
+// of latencies.  With 64 heads a CTA, shared memory bounds a tile: the
 // operands of its products (18 x 8 KB and 32 x 6 KB), the copies in (72 KB) and
 // P take 3300 cycles at 128 bytes a cycle, of about 4400.  CTAs of 32 heads
 // read every key twice as often (64 x 4096, 128 heads: 131 us).  What was
@@ -86,7 +87,7 @@ constexpr float kBelow = -3.402823466e38f;  // a piece's LSE where all its score
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 // The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
-// a sequence on.  1 x 65536 keys, 128 heads: 37.5 us in all (49.2 with 2 warps
+// a sequence on.  1 x 65536 keys, 128 heads: 37.4 us in all (49.2 with 2 warps
 // a row; kSub 4: 38.3, 16: 37.5); 2 x 32768: 41.3 (48.6); 4 x 16384, at 19
 // ranges a sequence: 42.7 (41.1).
 constexpr int kSub = 8, kManyPieces = 24;
@@ -1115,7 +1116,9 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
   magic_divisor(a.page_size / kBlock, &magic, &shift);
   // Where the page table holds too few keys for a sequence to be cut (as
   // make_plan decides, with one tile or more a range), plan and merge are left
-  // out: 1 x 100 keys, 16 heads, 9.7 us, not 12.0.
+  // out: 1 x 100 keys, 16 heads, 9.9 us, not 12.3.  (The table's width decides,
+  // since lengths are on the device: a wider one costs the 12.3, however few keys
+  // it is used for.)
   const bool split =
       ws != nullptr && (a.batch > l.ranges || a.max_pages * a.page_size > (1 + kMerge) * kTile);
   Params p{a, magic, shift, l.ranges, l.groups, split, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),

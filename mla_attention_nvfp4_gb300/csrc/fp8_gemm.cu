@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 //                 (each half has one weight scale per block), thread = row;
 //                 they take the registers the first warpgroup gives up
 //                 (128 sums, 32 columns being added and 32 being loaded each).
-// 4096 x 7168 x 16384: 352 us, 2730 TFLOP/s (457 us with one issuer and each
-// load waited for before its sums).  A K block takes 520 cycles of products
+// 4096 x 7168 x 16384: 363 to 384 us from run to run, as power allows, 2500 to
+// 2650 TFLOP/s (457 us with one issuer and each load waited for before its sums;
+// the pairs below compare two forms at one time).  A K block takes 520 cycles of products
 // by themselves, and 920 here, where 48 KB are copied into shared memory as 48
 // are read from it: 512 rows take 59 us with the sums and without them.  A CTA
 // pair's 256 x 256 tile halves the weights' part of that and takes as long (60
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const __nv_
 // thread and block beside the scales' loads and waits of 100 to 140 cycles.
 // Sixteen sum warps of 64 columns: 413 us, not 360; sums on pairs (f32x2) and
 // accumulators freed before two thirds of the sums: the same; the next
-// accumulator asked for ahead: 389; row scales staged in shared memory: 73, not
+// accumulator asked for ahead: 389, not 360; row scales staged in shared memory: 73, not
 // 59, for 512 rows.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128, kBN = 256;
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order.
 //   warp 0 producer, warp 1 and the last one MMA issuers, between them four
 //   warps of sums per 64 tokens: thread = weight row.
-// N 7168, K 16384: 16 rows 23.5 us, 64 rows 25.4 (4.7 TB/s), 128 rows 36;
-// 1 x 576 x 7168: 5.0 us, of which the launch takes half.
+// N 7168, K 16384: 16 rows 23 us, 64 rows 25.8 (4.6 TB/s), 128 rows 36;
+// 1 x 576 x 7168: 5.3 us, of which the launch takes half.
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplits = 8;   // portable cluster size
 constexpr int kScaleBlocks = 16;  // K blocks whose scales are staged at a time
