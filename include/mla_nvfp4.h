@@ -580,9 +580,10 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
  * Rows of the cache that hold no key of the sequence are never used,
  * whatever their bytes.  A NaN or an infinity in a query, or a score above
  * fp32's range (or all of them below it), makes that head's out and lse NaN, a
- * NaN code in a key those of its sequence.  Errors: MLA_DEVERR_BOUNDS for a length past the page table
- * or a page outside the cache, MLA_DEVERR_SCALE for a block scale out
- * of range: those keys are skipped.
+ * NaN code in a key those of its sequence.
+ *   Errors       : MLA_DEVERR_BOUNDS for a length past the page table or a page
+ *                  outside the cache, MLA_DEVERR_SCALE for a block scale out of
+ *                  range: those keys are skipped.
  */
 int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
                          const float* scales, const int32_t* page_table, int64_t page_table_stride,
