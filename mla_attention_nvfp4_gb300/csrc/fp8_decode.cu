@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l[kMine];
 #pragma unroll
       for (int h = 0; h < kMine; ++h) l[h] = 0.f;
-      bool set = false;  // the references follow some key
+      bool seen = false;  // there was a key
+      uint32_t unset = static_cast<uint32_t>((uint64_t{1} << kMine) - 1);  // heads whose reference follows no key yet
 #pragma unroll 1
       for (int t = s; t < e; ++t, ++n) {
         wait(&ms.info_full[n % C::info], (n / C::info) & 1, err, &ms.abort);
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kMine; ++h) top = fmaxf(top, x[h]);
         // Raise the references of the heads that need it.
-        const bool any = __any_sync(0xffffffffu, top + lsb > kTop || (!set && valid));
+        const bool any = __any_sync(0xffffffffu, top + lsb > kTop || (unset != 0 && valid));
         if (any) {
           // A head's maximum: halves exchanged until lane i holds head
           // i * kMine / 32 of the warp's keys, then over the warps.
@@ -747,8 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (!set || f[0] + lsb > kTop) {
-            const int h = lane * kMine / 32;
+          const int h = lane * kMine / 32;
+          if ((unset >> h & 1) != 0 || f[0] + lsb > kTop) {
             atomicMax(&ms.top[hb + h], ordered(f[0] + lsb));
             atomicOr(&ms.hits[wg], 1u << h);
           }
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tid < 32) {
             const bool hit = (ms.hits[wg] >> lane & 1) != 0;
             const float mx = hit ? from_ordered(ms.top[hb + lane]) : 0.f;
-            const bool raise = hit && isfinite(mx) && (!set || mx > kTop);
+            const bool raise = hit && isfinite(mx) && ((unset >> lane & 1) != 0 || mx > kTop);
             const float by = raise ? mx - kReset : 0.f;
             if (lane < kMine) ms.move[k & 1][hb + lane] = by;
             if (raise) mr[lane] += by;
@@ -766,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               ms.hits[wg] = 0;
               ms.moves[wg] = raised;
-              // without earlier keys O is zero (or yet to be written)
-              ms.raised[k & 1][wg] = set ? raised : 0;
+              // without earlier weights O is zero (or yet to be written)
+              ms.raised[k & 1][wg] = raised & ~unset;
             }
           }
           half_bar(wg);
@@ -780,11 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 x[h + j] -= by[j];
-                l[h + j] = set ? l[h + j] * ex2_approx(-by[j]) : 0.f;
+                if ((unset >> (h + j) & 1) == 0) l[h + j] *= ex2_approx(-by[j]);  // (else 0, or NaN)
               }
             }
           }
-          set = true;
+          seen = true;
+          unset &= ~moves;
         } else if (tid == 0) {
           ms.raised[k & 1][wg] = 0;
         }
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (piece > 0) wait(&ms.o_free, (piece - 1) & 1, err, &ms.abort);
       ms.sums[quad][hb + lane * kMine / 32] = l[0];
-      if (tid < kMine) ms.inv[hb + tid] = set ? mr[tid] : -INFINITY;  // -inf: no keys
+      if (tid < kMine) ms.inv[hb + tid] = seen ? mr[tid] : -INFINITY;  // -inf: no keys
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.sums_ready);
       half_bar(wg);  // c is free for the next piece

@@ -153,3 +153,29 @@ def test_decode_scores_below_the_range_in_a_part_of_a_sequence(heads):
         out, lse, flags = run_decode(q, cache2, scales, table, (n,), 64, split=split)
         assert flags == 0 and np.all(np.isnan(out[0, 1])) and np.isnan(lse[0, 1])
         assert np.all(np.isfinite(out[0, 0])) and abs(lse[0, 0] - np.log(n)) < 1e-4
+
+
+@pytest.mark.parametrize("heads", [16, 40])
+@pytest.mark.parametrize("n", [1000, 30000])
+@pytest.mark.parametrize("feature", [-448.0, -1.0, 0.0, 448.0])
+def test_decode_references_follow_the_first_key_within_the_range(feature, n, heads):
+    # the first 320 keys' scores are below fp32's range (2^64 * 448 * 2^60 / 14) and have no weight; the others' are all
+    # the same, 0.29 times `feature`: -129 to 129
+    rng = np.random.default_rng(8)
+    cache, scales, table = make_cache(rng, (n,), 64)
+    at = table[0][np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64
+    first = np.arange(n) < 320
+    cache[at, 3] = np.where(first, 0x7E, 0)
+    cache[at, 4] = np.where(first, 0, fp8.encode(np.array([feature]))[0])
+    scales[:] = 2.0 ** -60
+    scales[table[0][:5]] = 2.0 ** 60
+    q = torch.zeros(1, heads, 576, dtype=torch.bfloat16)
+    q[0, 1, 3], q[0, 1, 4] = -(2.0 ** 64), 2.0 ** 62
+    v = fp8.decode_codes(cache[at[320:], :512]) * 2.0 ** -60
+    ref, mag = v.mean(0), np.abs(v).mean(0)
+    for split in (True, False):
+        out, lse, flags = run_decode(q, cache, scales, table, (n,), 64, split=split)
+        score = 4 * feature * SCALE
+        assert flags == 0 and abs(lse[0, 1] - score - np.log(n - 320)) < 1e-4 + 2.0 ** -20 * abs(score)
+        # equal weights: bf16's rounding, and the weights' 2^-8 and f16's of their magnitude
+        assert np.all(np.abs(out[0, 1] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag), split
