@@ -51,9 +51,9 @@
 // The code of each role is kept short (rolled loops, one copy): unrolled
 // further, the warps waited for instructions more than for anything else.
 // Times (merge included; pairs below compare two forms at one time): 64 x 4096
-// keys, 128 heads 88.5 us, 64 heads 65, 16 heads 46; 128 sequences of 1k to
-// 32k, 16 heads 138 us (5.0 TB/s), 128 heads 324 (1020 TFLOP/s); 1 x 65536, 128
-// heads 37.4; 1 x 100, 16 heads 9.9 (12.3 with the merge), launches and one chain
+// keys, 128 heads 88.9 us, 64 heads 65, 16 heads 46; 128 sequences of 1k to
+// 32k, 16 heads 139 us (5.0 TB/s), 128 heads 324 (1020 TFLOP/s); 1 x 65536, 128
+// heads 37.5; 1 x 100, 16 heads 9.9 (12.3 with the merge), launches and one chain
 // of latencies.  With 64 heads a CTA, shared memory bounds a tile: the
 // operands of its products (18 x 8 KB and 32 x 6 KB), the copies in (72 KB) and
 // P take 3300 cycles at 128 bytes a cycle, of about 4400.  CTAs of 32 heads
@@ -87,7 +87,7 @@ constexpr float kBelow = -3.402823466e38f;  // a piece's LSE where all its score
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 // The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
-// a sequence on.  1 x 65536 keys, 128 heads: 37.4 us in all (49.2 with 2 warps
+// a sequence on.  1 x 65536 keys, 128 heads: 37.5 us in all (49.2 with 2 warps
 // a row; kSub 4: 38.3, 16: 37.5); 2 x 32768: 41.3 (48.6); 4 x 16384, at 19
 // ranges a sequence: 42.7 (41.1).
 constexpr int kSub = 8, kManyPieces = 24;
