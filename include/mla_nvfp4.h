@@ -489,6 +489,31 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
                    void* out, int64_t ldc, uint32_t* error_word, void* stream);
 
 /*
+ * NVFP4 matrix-vector products: the projections of a decode step of few rows,
+ * activations in bf16 as they are (mla_nvfp4_gemm wants them in NVFP4), and
+ * weights as mla_nvfp4_gemm reads them, one matrix or one a group (a head's
+ * part of W_UK or W_UV):
+ *     out[m, g, n] = gs_w * sum_k x[m, g, k] * code[g, n, k] * scale[g, n, k / 16].
+ * The pages define no such call; they name the weights' format ("#8").
+ *   x        : bf16 [M, groups, K], element strides per row and group (either
+ *              order; rows of K that do not overlap).
+ *   w_codes  : uint8 [groups, N, K/2] contiguous.
+ *   w_scales : groups x the 128x4-swizzled e4m3 scales of a [N, K/16] matrix
+ *              (layout and padding as for out_scales of the prefill), one
+ *              after another; padding readable, its bytes of no effect.
+ *   gs_w     : device fp32 global scale of all groups.
+ *   out      : bf16 [M, groups, N], element strides likewise; 2-byte aligned.
+ * K a multiple of 32, any M, groups and N.  x, its strides (in bytes), w_codes
+ * and w_scales are 16-byte aligned.  A stride of a dimension of one is not read.
+ * M == 0, groups == 0 or N == 0 is a no-op, K == 0 an error.
+ * Sums are fp32, rounded once to bf16.  Made for few rows: every 16 rows of x
+ * read the weights again.
+ */
+int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_t M, const uint8_t* w_codes,
+                   const uint8_t* w_scales, int groups, int64_t N, int64_t K, const float* gs_w, void* out,
+                   int64_t out_stride_m, int64_t out_stride_g, void* stream);
+
+/*
  * The 8-bit path: a latent cache held in e4m3 with one scale per block of
  * tokens, and an e4m3 GEMM with scales per block of 128.  The source pages
  * name an 8-bit MLA cache as the baseline their NVFP4 cache is compared with
@@ -556,6 +581,25 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
                                uint32_t* error_word, void* stream);
 
 /*
+ * mla_nvfp4_fp8_cache_append_at: mla_nvfp4_fp8_cache_append for sequences
+ * whose tokens are no more at their position's place in the page table
+ * (mla_nvfp4_fp8_cache_evict has taken some out).
+ *   positions : int32 [num_seqs]: new token i of sequence b is token
+ *               context_lens[b] + i of its page table and is turned by the
+ *               angles of position positions[b] + i, as its queries are.  NULL:
+ *               context_lens.  A negative one skips the sequence
+ *               (MLA_DEVERR_BOUNDS).
+ */
+int mla_nvfp4_fp8_cache_append_at(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                                  int64_t num_tokens, const float* cos_sin, int64_t max_position, int interleaved,
+                                  const int32_t* cu_seqlens, const int32_t* context_lens, const int32_t* positions,
+                                  int num_seqs, int max_new_tokens, const int32_t* page_table,
+                                  int64_t page_table_stride, int64_t max_pages, int page_size, uint8_t* cache,
+                                  int64_t num_slots, float* scales, const void* q_pe, int64_t q_stride_t,
+                                  int64_t q_stride_h, void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+                                  int num_heads, uint32_t* error_word, void* stream);
+
+/*
  * mla_nvfp4_fp8_decode: absorbed MLA decode over that cache.
  *   q            : bf16 [batch, num_heads, 576] contiguous = [q_nope.W_UK (512),
  *                  rotated q_pe (64)] per head.
@@ -592,6 +636,96 @@ int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t*
 
 /* Bytes of workspace for mla_nvfp4_fp8_decode; 0 for invalid sizes. */
 size_t mla_nvfp4_fp8_decode_workspace_size(int batch, int num_heads);
+
+/*
+ * mla_nvfp4_fp8_decode_shared: mla_nvfp4_fp8_decode for a batch whose
+ * sequences begin with the same tokens, which are read and multiplied once for
+ * all of them: the rows of as many sequences as fit are one operand, where
+ * mla_nvfp4_fp8_decode gives every sequence CTAs of its own.
+ *   shared_len : a multiple of MLA_FP8_BLOCK, at most max_pages * page_size:
+ *                tokens [0, shared_len) of every sequence of at least that
+ *                length hold the same keys.  They are read through row 0 of
+ *                the page table, whatever its sequence's length; the others'
+ *                entries for them are not read.  A shorter sequence (an empty
+ *                one of a padded batch) is attended to by itself, through its
+ *                own row.
+ *   seq_lens   : int32 [batch], all keys of sequence b, the shared ones too.
+ *   workspace  : mla_nvfp4_fp8_decode_shared_workspace_size(batch, num_heads)
+ *                bytes, 256-byte aligned, contents ignored; needed.  Calls that
+ *                may run at once need a workspace each.
+ * Everything else, roundings and errors too, as mla_nvfp4_fp8_decode; the sums
+ * are in another order than its.
+ */
+int mla_nvfp4_fp8_decode_shared(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                                const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                                int64_t max_pages, int page_size, const int32_t* seq_lens, int64_t shared_len,
+                                float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                uint32_t* error_word, void* stream);
+
+/* Bytes of workspace for mla_nvfp4_fp8_decode_shared; 0 for invalid sizes. */
+size_t mla_nvfp4_fp8_decode_shared_workspace_size(int batch, int num_heads);
+
+/*
+ * mla_nvfp4_fp8_key_weights: the attention weight that a decode step's queries
+ * give to every key, summed over the heads and added to what it had:
+ *   out[b, t] = weights[b, t] + sum_h exp(softmax_scale * q[b, h] . key_t - lse[b, h]).
+ *   q, page_table, seq_lens, softmax_scale : as of mla_nvfp4_fp8_decode, and
+ *   lse          : fp32 [batch, num_heads], its lse.
+ *   weights, out : fp32 [batch, row_len], row strides in elements; weights
+ *                  NULL: zeros; out may be weights (with the same stride).
+ *                  Entries from seq_lens[b] on are left as they are.
+ * Sums are fp32, over the heads in order; a query's features are held as
+ * mla_nvfp4_fp8_decode holds them.  A head whose lse is NaN makes its
+ * sequence's weights NaN, a NaN code in a key that key's.
+ *   Errors       : MLA_DEVERR_BOUNDS for a length past row_len or the page
+ *                  table (those keys are left out) or a page outside the
+ *                  cache, MLA_DEVERR_SCALE for a block scale out of range:
+ *                  those keys' out is weights alone.
+ */
+int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                              const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                              int64_t max_pages, int page_size, const int32_t* seq_lens, float softmax_scale,
+                              const float* lse, const float* weights, int64_t weights_stride, float* out,
+                              int64_t out_stride, int64_t row_len, uint32_t* error_word, void* stream);
+
+/*
+ * mla_nvfp4_fp8_cache_evict: of every sequence the `recent` last tokens and
+ * those of greatest weight, `keep` in all, moved in order to new pages.
+ *   cache, scales   : as above.  The new pages are written; the old ones are
+ *                     only read, and may be given to others after the call
+ *                     (pages of a shared prefix stay).  No new page may be an
+ *                     old one of the call or stand twice in new_page_table.
+ *   weights         : fp32 [batch, row_len], row stride in elements.  Of equal
+ *                     weights the earlier token stays; -0 equals 0, a NaN is
+ *                     below all others.
+ *   page_table, seq_lens : of the sequences as they are.
+ *   new_page_table  : int32 [batch, new_max_pages], row stride in elements.
+ *   keep, recent    : 1 <= keep, 0 <= recent <= keep.  A sequence of at most
+ *                     keep tokens is moved whole.
+ *   kept            : int32 [batch, keep] out: the tokens that stay, ascending,
+ *                     then -1.
+ *   new_lens        : int32 [batch] out: how many.  Not seq_lens itself.
+ *   new_weights     : fp32 [batch, new_row_len >= keep] out or NULL, row stride
+ *                     in elements: their weights, then zeros; apart from weights.
+ * A new block's scale is the one that mla_nvfp4_fp8_cache_append would give it
+ * for these keys, and their codes are rounded again in it (exact but for
+ * results below 2^-6, where e4m3 is subnormal).  Slots of a new page behind the
+ * last token are left as they are.  Keys stay turned by their old position:
+ * append to them with mla_nvfp4_fp8_cache_append_at.
+ *   Errors          : MLA_DEVERR_BOUNDS for a length past row_len or the page
+ *                     table (clipped), more tokens than the new table holds
+ *                     (fewer stay), a page outside the cache; MLA_DEVERR_SCALE
+ *                     for an old block's scale out of range.  A token whose old
+ *                     page or scale is bad becomes a key of zeros; a block
+ *                     whose new page is bad is not written.
+ */
+int mla_nvfp4_fp8_cache_evict(uint8_t* cache, int64_t num_slots, float* scales, const float* weights,
+                              int64_t weights_stride, int64_t row_len, int batch, const int32_t* page_table,
+                              int64_t page_table_stride, int64_t max_pages, const int32_t* new_page_table,
+                              int64_t new_page_table_stride, int64_t new_max_pages, int page_size,
+                              const int32_t* seq_lens, int keep, int recent, int32_t* kept, int32_t* new_lens,
+                              float* new_weights, int64_t new_weights_stride, int64_t new_row_len,
+                              uint32_t* error_word, void* stream);
 
 /*
  * mla_nvfp4_fp8_quantize: activations to e4m3 with one scale per 128 features

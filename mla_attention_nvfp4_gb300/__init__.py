@@ -26,7 +26,9 @@ __all__ = [
     "mla_nvfp4_quantize_rows", "mla_nvfp4_gemm", "mla_nvfp4_gather_latent", "mla_nvfp4_prefill_partial",
     "mla_nvfp4_merge_fused_out", "mla_nvfp4_prefill_qdq", "mla_nvfp4_prefill_fakequant",
     "mla_nvfp4_prefill_quantized", "mla_nvfp4_fp8_cache_append", "mla_nvfp4_fp8_decode",
-    "mla_nvfp4_fp8_decode_workspace_size", "mla_nvfp4_fp8_quantize", "mla_nvfp4_fp8_gemm", "abi_symbols",
+    "mla_nvfp4_fp8_decode_workspace_size", "mla_nvfp4_fp8_quantize", "mla_nvfp4_fp8_gemm",
+    "mla_nvfp4_fp8_decode_shared", "mla_nvfp4_fp8_decode_shared_workspace_size", "mla_nvfp4_fp8_key_weights",
+    "mla_nvfp4_fp8_cache_evict", "mla_nvfp4_gemv", "abi_symbols",
     "RECORD_BF16_ROPE", "RECORD_FP8_ROPE", "FP8_BLOCK", "FP8_GROUP", "LAUNCHES_PER_CALL",
 ]
 
@@ -42,15 +44,18 @@ DEVERR_BOUNDS, DEVERR_TIMEOUT, DEVERR_SCALE, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8
 # False or the page table is at most 384 keys wide.
 LAUNCHES_PER_CALL = {"cache_write": 1, "decode": 3, "prefill": 1, "global_scale": 2, "gemm": 1,
                      "gather_latent": 1, "prefill_partial": 1, "merge_fused_out": 1, "prefill_qdq": 2,
-                     "prefill_fakequant": 1, "fp8_cache_append": 1, "fp8_decode": 2, "fp8_quantize": 1, "fp8_gemm": 1}
+                     "prefill_fakequant": 1, "fp8_cache_append": 1, "fp8_decode": 2, "fp8_quantize": 1, "fp8_gemm": 1,
+                     "fp8_decode_shared": 2, "fp8_key_weights": 1, "fp8_cache_evict": 2, "gemv": 1}
 # What bounds each hot kernel as built: "hbm", "tensor" (tcgen05 MMA) or
 # "alu" (CUDA-core arithmetic).
 KERNEL_BOUND = {"cache_write": "hbm", "decode": "tensor", "prefill": "tensor", "gemm": "tensor",
-                "fp8_cache_append": "hbm", "fp8_decode": "tensor", "fp8_quantize": "hbm", "fp8_gemm": "tensor"}
+                "fp8_cache_append": "hbm", "fp8_decode": "tensor", "fp8_quantize": "hbm", "fp8_gemm": "tensor",
+                "fp8_decode_shared": "tensor", "fp8_key_weights": "hbm", "fp8_cache_evict": "hbm", "gemv": "hbm"}
 # Operand type of each kernel's tensor-core products (fp32 accumulation):
 # the decode multiplies f16 operands (the dequantised latent c*s is exact in
 # f16), the prefill bf16 inputs as given.
-OPERAND_DTYPE = {"decode": "f16", "prefill": "bf16", "gemm": "nvfp4", "fp8_decode": "e4m3", "fp8_gemm": "e4m3"}
+OPERAND_DTYPE = {"decode": "f16", "prefill": "bf16", "gemm": "nvfp4", "fp8_decode": "e4m3", "fp8_gemm": "e4m3",
+                 "fp8_decode_shared": "e4m3", "fp8_key_weights": "e4m3", "gemv": "f16"}
 
 
 def kernel_kind(name: str) -> str:
@@ -106,6 +111,20 @@ _SIGS = {
     "mla_nvfp4_fp8_cache_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp, _c_vp,
                                             _c_int, _c_int, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_vp,
                                             _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_cache_append_at": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_int, _c_vp,
+                                               _c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_i64, _c_int, _c_vp,
+                                               _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64, _c_int,
+                                               _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_decode_shared_workspace_size": (ctypes.c_size_t, [_c_int, _c_int]),
+    "mla_nvfp4_fp8_decode_shared": (_c_int, [_c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
+                                             _c_vp, _c_i64, _c_f, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_key_weights": (_c_int, [_c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
+                                           _c_vp, _c_f, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "mla_nvfp4_fp8_cache_evict": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_i64,
+                                           _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_vp,
+                                           _c_i64, _c_i64, _c_vp, _c_vp]),
+    "mla_nvfp4_gemv": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp,
+                                _c_i64, _c_i64, _c_vp]),
     "mla_nvfp4_fp8_decode_workspace_size": (ctypes.c_size_t, [_c_int, _c_int]),
     "mla_nvfp4_fp8_decode": (_c_int, [_c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
                                       _c_vp, _c_f, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp, _c_vp]),
@@ -681,7 +700,7 @@ def _result(name, r):
 
 def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, *,
                                page_size=64, interleaved=True, q_pe=None, q_out=None, max_new_tokens=None,
-                               error_word=None):
+                               error_word=None, positions=None):
     """Append every sequence's new tokens to the e4m3 latent cache, the RoPE
     key rotated by its position: kv_c [T,512], k_pe [T,64] (bf16, unrotated),
     cos_sin fp32 [max_position, 64] (32 cosines, 32 sines), rows
@@ -693,10 +712,12 @@ def mla_nvfp4_fp8_cache_append(kv_c, k_pe, cos_sin, cu_seqlens, context_lens, pa
     sequence (default T).  The grid is one for num_seqs sequences of that many
     tokens, and CTAs past a sequence's end return at once: for a batch of
     prompts give the longest one's length, or over T / 64 CTAs a sequence
-    start for nothing."""
+    start for nothing.  positions (int32 [B], default context_lens): the
+    position of each sequence's first new token, where eviction has left fewer
+    tokens in the cache than there were."""
     return _result("mla_nvfp4_fp8_cache_append", _fp8().append(
         kv_c, k_pe, cos_sin, cu_seqlens, context_lens, page_table, cache, scales, page_size, interleaved, q_pe, q_out,
-        max_new_tokens, error_word))
+        max_new_tokens, error_word, positions))
 
 
 def mla_nvfp4_fp8_decode_workspace_size(batch: int, num_heads: int) -> int:
@@ -726,3 +747,54 @@ def mla_nvfp4_fp8_gemm(a, a_scales, w, w_scales, *, out=None, error_word=None):
     [M, ceil(K / 128)], w float8_e4m3fn [N, K] with w_scales fp32
     [ceil(N / 128), ceil(K / 128)]."""
     return _result("mla_nvfp4_fp8_gemm", _fp8().gemm(a, a_scales, w, w_scales, out, error_word))
+
+
+def mla_nvfp4_fp8_decode_shared_workspace_size(batch: int, num_heads: int) -> int:
+    """Bytes of workspace on the current device; the contents need no preparation."""
+    return int(load_library().mla_nvfp4_fp8_decode_shared_workspace_size(batch, num_heads))
+
+
+def mla_nvfp4_fp8_decode_shared(q, cache, scales, softmax_scale, *, page_table, seq_lens, shared_len, page_size=64,
+                                out=None, lse=None, workspace=None, error_word=None, return_lse=False):
+    """mla_nvfp4_fp8_decode for a batch whose sequences begin with the same
+    shared_len tokens (a multiple of 64), read once for all of them through
+    row 0 of the page table; seq_lens counts them too, and a sequence shorter
+    than shared_len is attended to by itself.  It pays where a sequence has
+    few heads (64 x 16384 shared keys, 16 heads) and costs the batch a merge
+    where it has many.  A workspace is allocated unless given."""
+    return _result("mla_nvfp4_fp8_decode_shared", _fp8().decode_shared(
+        q, cache, scales, softmax_scale, page_table, seq_lens, shared_len, page_size, out, lse, workspace, error_word,
+        return_lse))
+
+
+def mla_nvfp4_fp8_key_weights(q, cache, scales, softmax_scale, lse, *, page_table, seq_lens, page_size=64, weights=None,
+                              out=None, error_word=None):
+    """The attention weight of every key under a decode step's queries, summed
+    over the heads, with the decode's lse [B,H]: out = weights + that sum, fp32
+    [B, n] (n tokens a sequence at most; without weights and out n is what the
+    page table holds).  weights None: zeros.  out may be weights; a new one is
+    made unless given, zero from seq_lens on.  Returns out."""
+    return _result("mla_nvfp4_fp8_key_weights", _fp8().key_weights(
+        q, cache, scales, softmax_scale, lse, page_table, seq_lens, page_size, weights, out, error_word))
+
+
+def mla_nvfp4_fp8_cache_evict(cache, scales, weights, *, page_table, seq_lens, new_page_table, keep, recent=0, page_size=64,
+                              kept=None, new_lens=None, new_weights=None, error_word=None):
+    """Of every sequence the `recent` last tokens and those of greatest weight
+    (fp32 [B, n]; the earlier of equal ones), `keep` in all, moved in order to
+    the pages of new_page_table, which must be none of the old ones.  Returns
+    (kept int32 [B, keep]: their tokens, then -1; new_lens int32 [B];
+    new_weights fp32 [B, keep] or the wider tensor given: their weights, then
+    zeros).  Append to what is left with positions=the tokens there were."""
+    return _result("mla_nvfp4_fp8_cache_evict", _fp8().evict(
+        cache, scales, weights, page_table, seq_lens, new_page_table, keep, recent, page_size, kept, new_lens, new_weights,
+        error_word))
+
+
+def mla_nvfp4_gemv(x, w_codes, w_scales, gs_w, *, out=None):
+    """bf16 x times NVFP4 weights, laid out as mla_nvfp4_gemm's: x [M, K] with
+    w_codes [N, K/2] and w_scales -> [M, N], or x [M, G, K] with w_codes
+    [G, N, K/2] and w_scales [G, ...] (one matrix a group, e.g. a head's part
+    of W_UK) -> [M, G, N]; gs_w a device fp32 [1] for all groups.  For few
+    rows: every 16 read the weights again."""
+    return _result("mla_nvfp4_gemv", _fp8().gemv(x, w_codes, w_scales, gs_w, out))

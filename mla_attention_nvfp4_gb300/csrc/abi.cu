@@ -33,6 +33,23 @@ int device_sms() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The e4m3 cache's size and its pages'; a page table of one row for all
+// sequences has stride 0.
+bool cache_shape_ok(int64_t num_slots, int page_size) {
+  return num_slots >= 0 && num_slots % MLA_FP8_BLOCK == 0 && num_slots <= (int64_t(1) << 31) - MLA_FP8_BLOCK &&
+         page_size >= MLA_FP8_BLOCK && page_size % MLA_FP8_BLOCK == 0;
+}
+bool table_ok(int64_t max_pages, int64_t stride) {
+  return max_pages >= 1 && max_pages <= INT32_MAX && (stride >= max_pages || stride == 0);
+}
+
+// Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.
+bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
+                  int64_t rows) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + ((rows - 1) * b_stride + b_len) * sizeof(float) && q < p + ((rows - 1) * a_stride + a_len) * sizeof(float);
+}
+
 thread_local const char* t_last_error = "";
 
 }  // namespace
@@ -340,6 +357,32 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
   return mla::launch_gemm(a, static_cast<cudaStream_t>(stream), sms);
 }
 
+int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_t M, const uint8_t* w_codes,
+                   const uint8_t* w_scales, int groups, int64_t N, int64_t K, const float* gs_w, void* out,
+                   int64_t out_stride_m, int64_t out_stride_g, void* stream) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 512;
+  if (M < 0 || groups < 0 || N < 0 || K < 0 || K % 32 != 0) return MLA_ERR_INVALID_ARG;
+  if (M == 0 || groups == 0 || N == 0) return MLA_OK;
+  if (K == 0 || x == nullptr || w_codes == nullptr || w_scales == nullptr || gs_w == nullptr || out == nullptr ||
+      M > kMax || N > kMax || K > kMax || N > kMax / groups)
+    return MLA_ERR_INVALID_ARG;
+  // rows of x and out that do not overlap: a row's groups inside its stride, or a group's rows inside that one's
+  const auto apart = [&](int64_t m, int64_t g, int64_t n) {
+    return (M == 1 || m >= n) && (groups == 1 || g >= n) &&
+           (M == 1 || groups == 1 || (m - n) / g >= groups - 1 || (g - n) / m >= M - 1);
+  };
+  if (!apart(x_stride_m, x_stride_g, K) || !apart(out_stride_m, out_stride_g, N)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_codes) || !aligned16(w_scales) || (M > 1 && x_stride_m % 8 != 0) ||
+      (groups > 1 && x_stride_g % 8 != 0) || (reinterpret_cast<uintptr_t>(out) & 1u) != 0 ||
+      (reinterpret_cast<uintptr_t>(gs_w) & 3u) != 0)
+    return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  const mla::GemvArgs a{x, M > 1 ? x_stride_m : 0, groups > 1 ? x_stride_g : 0, M, w_codes, w_scales, groups, N, K, gs_w,
+                        out, M > 1 ? out_stride_m : 0, groups > 1 ? out_stride_g : 0};
+  return mla::launch_gemv(a, static_cast<cudaStream_t>(stream), sms);
+}
+
 int mla_nvfp4_prefill_partial(const void* q, const void* k, const void* v, int64_t q_stride_t,
                               int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t,
                               int64_t v_stride_h, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k,
@@ -485,10 +528,10 @@ int mla_nvfp4_quantize_rows(const float* x, int64_t M, int64_t N, const float* g
                                    static_cast<cudaStream_t>(stream));
 }
 
-int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+int mla_nvfp4_fp8_cache_append_at(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
                                int64_t num_tokens, const float* cos_sin, int64_t max_position, int interleaved,
-                               const int32_t* cu_seqlens, const int32_t* context_lens, int num_seqs,
-                               int max_new_tokens, const int32_t* page_table, int64_t page_table_stride,
+                               const int32_t* cu_seqlens, const int32_t* context_lens, const int32_t* positions,
+                               int num_seqs, int max_new_tokens, const int32_t* page_table, int64_t page_table_stride,
                                int64_t max_pages, int page_size, uint8_t* cache, int64_t num_slots, float* scales,
                                const void* q_pe, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
                                int64_t q_out_stride_t, int64_t q_out_stride_h, int num_heads,
@@ -524,10 +567,25 @@ int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void
   const int sms = device_sms();
   if (sms < 0) return -sms;
   const mla::Fp8AppendArgs a{kv_c, kv_c_stride, k_pe, k_pe_stride, num_tokens, cos_sin, max_position, interleaved,
-                             cu_seqlens, context_lens, num_seqs, max_new_tokens, page_table, page_table_stride,
-                             max_pages, page_size, cache, num_slots, scales, q_pe, q_stride_t, q_stride_h, q_out,
+                             cu_seqlens, context_lens, positions, num_seqs, max_new_tokens, page_table,
+                             page_table_stride, max_pages, page_size, cache, num_slots, scales, q_pe, q_stride_t, q_stride_h, q_out,
                              q_out_stride_t, q_out_stride_h, num_heads, error_word};
   return mla::launch_fp8_append(a, static_cast<cudaStream_t>(stream));
+}
+
+int mla_nvfp4_fp8_cache_append(const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+                               int64_t num_tokens, const float* cos_sin, int64_t max_position, int interleaved,
+                               const int32_t* cu_seqlens, const int32_t* context_lens, int num_seqs,
+                               int max_new_tokens, const int32_t* page_table, int64_t page_table_stride,
+                               int64_t max_pages, int page_size, uint8_t* cache, int64_t num_slots, float* scales,
+                               const void* q_pe, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
+                               int64_t q_out_stride_t, int64_t q_out_stride_h, int num_heads,
+                               uint32_t* error_word, void* stream) {
+  return mla_nvfp4_fp8_cache_append_at(kv_c, kv_c_stride, k_pe, k_pe_stride, num_tokens, cos_sin, max_position,
+                                       interleaved, cu_seqlens, context_lens, nullptr, num_seqs, max_new_tokens,
+                                       page_table, page_table_stride, max_pages, page_size, cache, num_slots, scales,
+                                       q_pe, q_stride_t, q_stride_h, q_out, q_out_stride_t, q_out_stride_h, num_heads,
+                                       error_word, stream);
 }
 
 size_t mla_nvfp4_fp8_decode_workspace_size(int batch, int num_heads) {
@@ -558,6 +616,94 @@ int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t*
   const mla::Fp8DecodeArgs a{q, batch, num_heads, cache, num_slots, scales, page_table, page_table_stride, max_pages,
                              page_size, seq_lens, softmax_scale, out, lse, workspace, error_word};
   return mla::launch_fp8_decode(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+size_t mla_nvfp4_fp8_decode_shared_workspace_size(int batch, int num_heads) {
+  if (batch < 1 || num_heads < 1) return 0;
+  const int sms = device_sms();
+  return mla::fp8_shared_workspace_bytes(batch, num_heads, sms > 0 ? sms : 152);
+}
+
+int mla_nvfp4_fp8_decode_shared(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                                const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                                int64_t max_pages, int page_size, const int32_t* seq_lens, int64_t shared_len,
+                                float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                uint32_t* error_word, void* stream) {
+  if (batch < 0 || num_heads < 1 || !cache_shape_ok(num_slots, page_size) || !table_ok(max_pages, page_table_stride) ||
+      shared_len < 0 || shared_len % MLA_FP8_BLOCK != 0 || shared_len > max_pages * page_size)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (q == nullptr || cache == nullptr || scales == nullptr || page_table == nullptr || seq_lens == nullptr ||
+      out == nullptr || num_slots == 0 || static_cast<int64_t>(batch) * num_heads > (int64_t(1) << 31) - 128)
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < mla::fp8_shared_workspace_bytes(batch, num_heads, sms))
+    return MLA_ERR_WORKSPACE;
+  const mla::Fp8DecodeArgs a{q, batch, num_heads, cache, num_slots, scales, page_table, page_table_stride, max_pages,
+                             page_size, seq_lens, softmax_scale, out, lse, workspace, error_word};
+  return mla::launch_fp8_shared(a, shared_len, static_cast<cudaStream_t>(stream), sms);
+}
+
+int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uint8_t* cache, int64_t num_slots,
+                              const float* scales, const int32_t* page_table, int64_t page_table_stride,
+                              int64_t max_pages, int page_size, const int32_t* seq_lens, float softmax_scale,
+                              const float* lse, const float* weights, int64_t weights_stride, float* out,
+                              int64_t out_stride, int64_t row_len, uint32_t* error_word, void* stream) {
+  if (batch < 0 || num_heads < 1 || !cache_shape_ok(num_slots, page_size) || !table_ok(max_pages, page_table_stride) ||
+      row_len < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0 || row_len == 0) return MLA_OK;
+  if (q == nullptr || cache == nullptr || scales == nullptr || page_table == nullptr || seq_lens == nullptr ||
+      lse == nullptr || out == nullptr || num_slots == 0 || out_stride < row_len ||
+      (weights != nullptr && weights_stride < row_len))
+    return MLA_ERR_INVALID_ARG;
+  if (weights != nullptr && (weights != out || weights_stride != out_stride) &&
+      rows_overlap(weights, weights_stride, row_len, out, out_stride, row_len, batch))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache)) return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  const mla::Fp8WeightsArgs a{q, batch, num_heads, cache, num_slots, scales, page_table, page_table_stride, max_pages,
+                              page_size, seq_lens, softmax_scale, lse, weights, weights_stride, out, out_stride,
+                              row_len, error_word};
+  return mla::launch_fp8_key_weights(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+int mla_nvfp4_fp8_cache_evict(uint8_t* cache, int64_t num_slots, float* scales, const float* weights,
+                              int64_t weights_stride, int64_t row_len, int batch, const int32_t* page_table,
+                              int64_t page_table_stride, int64_t max_pages, const int32_t* new_page_table,
+                              int64_t new_page_table_stride, int64_t new_max_pages, int page_size,
+                              const int32_t* seq_lens, int keep, int recent, int32_t* kept, int32_t* new_lens,
+                              float* new_weights, int64_t new_weights_stride, int64_t new_row_len,
+                              uint32_t* error_word, void* stream) {
+  if (batch < 0 || !cache_shape_ok(num_slots, page_size) || !table_ok(max_pages, page_table_stride) ||
+      max_pages > page_table_stride || new_max_pages < 1 || new_max_pages > INT32_MAX ||
+      new_page_table_stride < new_max_pages || row_len < 0 || keep < 1 || recent < 0 || recent > keep ||
+      keep > (1 << 30))
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0) return MLA_OK;
+  if (cache == nullptr || scales == nullptr || (weights == nullptr && row_len > 0) || page_table == nullptr ||
+      new_page_table == nullptr || seq_lens == nullptr || kept == nullptr || new_lens == nullptr || num_slots == 0 ||
+      weights_stride < row_len)
+    return MLA_ERR_INVALID_ARG;
+  if (new_lens == seq_lens || new_lens == kept) return MLA_ERR_INVALID_ARG;
+  if (new_weights != nullptr &&
+      (new_row_len < keep || new_weights_stride < new_row_len ||
+       rows_overlap(weights, weights_stride, row_len, new_weights, new_weights_stride, new_row_len, batch)))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache)) return MLA_ERR_ALIGNMENT;
+  const int sms = device_sms();
+  if (sms < 0) return -sms;
+  const mla::Fp8EvictArgs a{cache, num_slots, scales, weights, weights_stride, row_len, batch, page_table,
+                            page_table_stride, max_pages, new_page_table, new_page_table_stride, new_max_pages,
+                            page_size, seq_lens, keep, recent, kept, new_lens, new_weights, new_weights_stride,
+                            new_row_len, error_word};
+  return mla::launch_fp8_evict(a, static_cast<cudaStream_t>(stream));
 }
 
 int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,

@@ -1,4 +1,4 @@
-// Python binding of the 8-bit calls: checks, outputs, device and stream in
+// Python binding of the 8-bit calls and the matrix-vector products: checks, outputs, device and stream in
 // one native call each.  The smallest of these calls take 2 to 6 us on the
 // GPU; the same steps in Python take 10 to 20 us of the host.  Arguments are
 // those of the functions of the package's __init__.py, by position, None
@@ -8,6 +8,7 @@
 
 #include <ATen/core/TensorBody.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -183,11 +184,17 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int64_t max_new = args.skip_none() ? T : args.integer();
   uint32_t* err = args.error_word();
+  const int32_t* positions = nullptr;
+  if (!args.skip_none()) {
+    const Tensor& t = args.tensor("positions", kI32);
+    need(t.dim() == 1 && t.size(0) == B && t.is_contiguous(), "positions must be contiguous with context_lens' shape");
+    positions = data<int32_t>(t);
+  }
   const Launch at(args.device);
-  const int st = mla_nvfp4_fp8_cache_append(
+  const int st = mla_nvfp4_fp8_cache_append_at(
       kv.data_ptr(), T > 1 ? kv.stride(0) : MLA_D_LATENT, pe.data_ptr(), T > 1 ? pe.stride(0) : MLA_D_ROPE, T,
       data<float>(cs), cs.size(0), interleaved ? 1 : 0, data<int32_t>(cu), data<int32_t>(ctx),
-      int32_of(B, "too many sequences"), int32_of(max_new, "max_new_tokens out of range"), data<int32_t>(pt), pt_stride,
+      positions, int32_of(B, "too many sequences"), int32_of(max_new, "max_new_tokens out of range"), data<int32_t>(pt), pt_stride,
       pt.size(1), static_cast<int>(page_size), data<uint8_t>(cache), slots, data<float>(scales),
       H > 0 ? q.data_ptr() : nullptr, q_st, q_sh, H > 0 ? o.data_ptr() : nullptr, o_st, o_sh, int32_of(H, "too many heads"), err, at.stream);
   if (st != MLA_OK) return status(st);
@@ -284,8 +291,167 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args args{a, n};
+  const Tensor &q = args.tensor("q", kBF16), &cache = args.tensor("cache", kF8), &scales = args.tensor("scales", kF32);
+  const float softmax_scale = static_cast<float>(args.number());
+  const Tensor &pt = args.tensor("page_table", kI32), &lens = args.tensor("seq_lens", kI32);
+  const int64_t shared_len = args.integer(), page_size = args.integer();
+  const int64_t slots = check_cache(cache, scales);
+  need(q.dim() == 3 && q.size(2) == MLA_D_QK_DECODE && q.is_contiguous(), "q must be contiguous [B, H, 576]");
+  const int64_t B = q.size(0), H = q.size(1);
+  const int64_t pt_stride = check_pages(pt, B, page_size);
+  need(lens.dim() == 1 && lens.size(0) == B && lens.is_contiguous(), "seq_lens must be contiguous [B]");
+  need(shared_len >= 0 && shared_len % MLA_FP8_BLOCK == 0, "shared_len must be a multiple of 64");
+  const int b = int32_of(B, "batch too large"), h = int32_of(H, "too many heads");
+  const Tensor out = args.output("out", kBF16, {B, H, MLA_D_LATENT});
+  PyObject* lse_given = args.next();
+  PyObject* ws_given = args.next();
+  uint32_t* err = args.error_word();
+  const bool return_lse = args.flag();
+  Tensor lse, ws;
+  if (return_lse || lse_given != Py_None) {
+    Args one{&lse_given, 1, 0, args.device};
+    lse = one.output("lse", kF32, {B, H});
+  }
+  const Launch at(args.device);
+  if (ws_given != Py_None) {
+    Args one{&ws_given, 1, 0, args.device};
+    ws = one.tensor("workspace", at::kByte);
+    need(ws.is_contiguous(), "workspace must be contiguous");
+  } else if (B > 0 && H > 0) {
+    ws = at::empty({static_cast<int64_t>(mla_nvfp4_fp8_decode_shared_workspace_size(b, h))}, q.options().dtype(at::kByte));
+  }
+  const int st = mla_nvfp4_fp8_decode_shared(
+      q.data_ptr(), b, h, bytes(cache), slots, data<float>(scales), data<int32_t>(pt), pt_stride, pt.size(1),
+      static_cast<int>(page_size), data<int32_t>(lens), shared_len, softmax_scale, out.data_ptr(),
+      lse.defined() ? data<float>(lse) : nullptr, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0,
+      err, at.stream);
+  if (st != MLA_OK) return status(st);
+  return return_lse ? pair(out, lse) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// fp32 [batch, n]; returns its row stride.
+int64_t check_rows(const Tensor& t, int64_t batch, const char* what) {
+  need(t.dim() == 2 && t.size(0) == batch && rows_contiguous(t), what);
+  return batch > 1 ? t.stride(0) : t.size(1);  // one row: any stride
+}
+
+PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args args{a, n};
+  const Tensor &q = args.tensor("q", kBF16), &cache = args.tensor("cache", kF8), &scales = args.tensor("scales", kF32);
+  const float softmax_scale = static_cast<float>(args.number());
+  const Tensor &lse = args.tensor("lse", kF32), &pt = args.tensor("page_table", kI32), &lens = args.tensor("seq_lens", kI32);
+  const int64_t page_size = args.integer();
+  const int64_t slots = check_cache(cache, scales);
+  need(q.dim() == 3 && q.size(2) == MLA_D_QK_DECODE && q.is_contiguous(), "q must be contiguous [B, H, 576]");
+  const int64_t B = q.size(0), H = q.size(1);
+  const int64_t pt_stride = check_pages(pt, B, page_size);
+  need(lens.dim() == 1 && lens.size(0) == B && lens.is_contiguous(), "seq_lens must be contiguous [B]");
+  need(lse.dim() == 2 && lse.size(0) == B && lse.size(1) == H && lse.is_contiguous(), "lse must be contiguous [B, H]");
+  Tensor w, out;
+  int64_t w_stride = 0, row = pt.size(1) * page_size;
+  if (!args.skip_none()) {
+    w = args.tensor("weights", kF32);
+    w_stride = check_rows(w, B, "weights must be [B, n] with a contiguous last dimension");
+    row = w.size(1);
+  }
+  PyObject* out_given = args.next();
+  uint32_t* err = args.error_word();
+  const Launch at(args.device);
+  int64_t out_stride = 0;
+  if (out_given != Py_None) {
+    Args one{&out_given, 1, 0, args.device};
+    out = one.tensor("out", kF32);
+    out_stride = check_rows(out, B, "out must be [B, n] with a contiguous last dimension");
+    need(!w.defined() || out.size(1) == row, "out must have weights' shape");
+    row = out.size(1);
+  } else {
+    out = at::zeros({B, row}, lse.options());
+    out_stride = row;
+  }
+  const int st = mla_nvfp4_fp8_key_weights(
+      q.data_ptr(), int32_of(B, "batch too large"), int32_of(H, "too many heads"), bytes(cache), slots, data<float>(scales),
+      data<int32_t>(pt), pt_stride, pt.size(1), static_cast<int>(page_size), data<int32_t>(lens), softmax_scale,
+      data<float>(lse), w.defined() ? data<float>(w) : nullptr, w_stride, data<float>(out), out_stride, row, err, at.stream);
+  return st != MLA_OK ? status(st) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args args{a, n};
+  const Tensor &cache = args.tensor("cache", kF8), &scales = args.tensor("scales", kF32), &w = args.tensor("weights", kF32);
+  const Tensor &pt = args.tensor("page_table", kI32), &lens = args.tensor("seq_lens", kI32);
+  const Tensor& npt = args.tensor("new_page_table", kI32);
+  const int64_t keep = args.integer(), recent = args.integer(), page_size = args.integer();
+  const int64_t slots = check_cache(cache, scales);
+  need(lens.dim() == 1 && lens.is_contiguous(), "seq_lens must be contiguous [B]");
+  const int64_t B = lens.size(0);
+  const int64_t pt_stride = check_pages(pt, B, page_size), npt_stride = check_pages(npt, B, page_size);
+  const int64_t w_stride = check_rows(w, B, "weights must be [B, n] with a contiguous last dimension");
+  need(keep >= 1 && keep <= 1 << 30, "keep must be 1 or more");
+  need(recent >= 0 && recent <= keep, "recent must lie between 0 and keep");
+  const Tensor kept = args.output("kept", kI32, {B, keep}), new_lens = args.output("new_lens", kI32, {B});
+  Tensor nw;
+  int64_t nw_stride = keep;
+  if (args.skip_none()) {
+    nw = at::empty({B, keep}, w.options());
+  } else {
+    nw = args.tensor("new_weights", kF32);
+    nw_stride = check_rows(nw, B, "new_weights must be [B, n] with a contiguous last dimension");
+    need(nw.size(1) >= keep, "new_weights must have room for keep tokens");
+  }
+  uint32_t* err = args.error_word();
+  const Launch at(args.device);
+  const int st = mla_nvfp4_fp8_cache_evict(
+      data<uint8_t>(cache), slots, data<float>(scales), data<float>(w), w_stride, w.size(1), int32_of(B, "batch too large"),
+      data<int32_t>(pt), pt_stride, pt.size(1), data<int32_t>(npt), npt_stride, npt.size(1), static_cast<int>(page_size),
+      data<int32_t>(lens), static_cast<int>(keep), static_cast<int>(recent), data<int32_t>(kept), data<int32_t>(new_lens),
+      data<float>(nw), nw_stride, nw.size(1), err, at.stream);
+  if (st != MLA_OK) return status(st);
+  PyObject* x = THPVariable_Wrap(kept);
+  PyObject* y = THPVariable_Wrap(new_lens);
+  PyObject* z = THPVariable_Wrap(nw);
+  return Py_BuildValue("(NNN)", x, y, z);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args args{a, n};
+  const Tensor &x = args.tensor("x", kBF16), &w = args.tensor("w_codes", at::kByte), &ws = args.tensor("w_scales", at::kByte);
+  const Tensor& gs = args.tensor("gs_w", kF32);
+  const int64_t d = x.dim();
+  need((d == 2 || d == 3) && w.dim() == d, "x [M, K] goes with w_codes [N, K/2], x [M, G, K] with [G, N, K/2]");
+  const int64_t M = x.size(0), G = d == 3 ? x.size(1) : 1, K = x.size(d - 1), N = w.size(d - 2);
+  need(2 * w.size(d - 1) == K && (d == 2 || w.size(0) == G), "x and w_codes must share K and their groups");
+  need(rows_contiguous(x) && w.is_contiguous() && ws.is_contiguous(),
+       "w_codes and w_scales must be contiguous, and x have a contiguous last dimension");
+  need(ws.numel() == G * ((N + 127) / 128 * 128) * ((K / 16 + 3) / 4 * 4), "w_scales must hold the padded scales of every group");
+  need(gs.numel() >= 1, "gs_w must hold the global scale");
+  Tensor out;
+  if (args.skip_none()) {
+    out = d == 3 ? at::empty({M, G, N}, x.options()) : at::empty({M, N}, x.options());
+  } else {
+    out = args.tensor("out", kBF16);
+    need(out.dim() == d && out.size(0) == M && (d == 2 || out.size(1) == G) && out.size(d - 1) == N && rows_contiguous(out),
+         "out must be [M, N] or [M, G, N] with a contiguous last dimension");
+  }
+  const Launch at(args.device);
+  const int st = mla_nvfp4_gemv(x.data_ptr(), x.stride(0), d == 3 ? x.stride(1) : 0, M, bytes(w), bytes(ws),
+                                int32_of(G, "too many groups"), N, K, data<float>(gs), out.data_ptr(), out.stride(0),
+                                d == 3 ? out.stride(1) : 0, at.stream);
+  return st != MLA_OK ? status(st) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(append), METHOD(decode), METHOD(quantize), METHOD(gemm), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(append), METHOD(decode), METHOD(quantize), METHOD(gemm), METHOD(decode_shared),
+                         METHOD(key_weights), METHOD(evict), METHOD(gemv), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_fp8", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
+#include "fp8_paged.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -24,22 +25,13 @@ constexpr int kKey = MLA_D_LATENT + MLA_D_ROPE;
 constexpr int kQPairs = kThreads;  // (token, head) rows of 64 per query CTA
 constexpr int kPeBytes = MLA_D_ROPE * 2, kKvBytes = MLA_D_LATENT * 2;
 constexpr int kSmemBytes = kBlock * (kKvBytes + kPeBytes);  // 72 KB: three CTAs an SM
-constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
+constexpr float kScaleMin = kFp8ScaleMin, kScaleMax = kFp8ScaleMax;
 
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
-}
-
-// The smallest 2^e, -60 <= e <= 60, with amax <= 448 * 2^e (448 = 1.75 * 2^8):
-// from amax's exponent and whether its fraction is above .75.
-__device__ __forceinline__ float block_scale_pow2(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = e < -60 ? -60 : e > 60 ? 60 : e;  // amax 0 and subnormal: -60; inf: 60
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
 // One pair turned by an angle: products and sums each rounded to float32, as
@@ -51,17 +43,19 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// Sequence b's new tokens: rows a.. of the batch, positions ctx .. ctx + n.
-// False when its entries are out of range (flagged) or it has none.
+// Sequence b's new tokens: rows a.. of the batch, its tokens ctx .. ctx + n,
+// whose angles are those of rows `ahead` further on.  False when its entries
+// are out of range (flagged) or it has none.
 struct Span {
-  int64_t row, ctx, end;  // first row; first position; one past the last
+  int64_t row, ctx, end, ahead;  // first row; first token; one past the last; position less token
 };
 __device__ __forceinline__ bool sequence_span(const Fp8AppendArgs& p, int b, Span& s, bool flag) {
   const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1], ctx = p.context_lens[b];
+  const int64_t position = p.positions != nullptr ? p.positions[b] : ctx;
   uint32_t bits = 0;
   int64_t n = e - a;
   bool ok = true;
-  if (a < 0 || e > p.num_tokens || n < 0 || ctx < 0) {
+  if (a < 0 || e > p.num_tokens || n < 0 || ctx < 0 || position < 0) {
     bits = MLA_DEVERR_BOUNDS;
     ok = false;
   } else {
@@ -70,13 +64,13 @@ __device__ __forceinline__ bool sequence_span(const Fp8AppendArgs& p, int b, Spa
       n = p.max_new;
     }
     int64_t end = ctx + n;
-    const int64_t room = p.max_pages * p.page_size;
-    const int64_t most = room < p.max_position ? room : p.max_position;
+    const int64_t room = p.max_pages * p.page_size, angles = p.max_position - (position - ctx);
+    const int64_t most = room < angles ? room : angles;
     if (end > most) {
       bits = MLA_DEVERR_BOUNDS;
       end = most;
     }
-    s = Span{a, ctx, end};
+    s = Span{a, ctx, end, position - ctx};
     ok = end > ctx;
   }
   if (bits != 0 && flag) flag_error(p.error_word, bits);
@@ -127,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8Append
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       if (row_of[i] < 0) break;
-      const float* cs = p.cos_sin + (sp.ctx + row_of[i]) * 64;
+      const float* cs = p.cos_sin + (sp.ctx + sp.ahead + row_of[i]) * 64;
       __nv_bfloat16* dst = o + (sp.row + row_of[i]) * p.qo_st + head_of[i] * p.qo_sh + 8 * c;
       uint32_t* w = reinterpret_cast<uint32_t*>(&v[i][0]);
       if constexpr (kInterleaved) {
@@ -168,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8Append
   }
 
   // ------------------------------------------------------------------ keys
-  const int64_t pos0 = (sp.ctx / kBlock + part) * kBlock;  // position of the block's first token
+  const int64_t pos0 = (sp.ctx / kBlock + part) * kBlock;  // the block's first token
   if (pos0 >= sp.end) return;
   const int lo = sp.ctx > pos0 ? static_cast<int>(sp.ctx - pos0) : 0;  // the block's rows written here
   const int hi = sp.end < pos0 + kBlock ? static_cast<int>(sp.end - pos0) : kBlock;
@@ -204,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8Append
     const int r = warp + i * kWarps;
     cosine[i] = sine[i] = 0.f;
     if (r >= lo && r < hi) {
-      const float* cs = p.cos_sin + (pos0 + r) * 64;
+      const float* cs = p.cos_sin + (pos0 + sp.ahead + r) * 64;
       cosine[i] = cs[lane];
       sine[i] = cs[lane + 32];
     }
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_append_kernel(const Fp8Append
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) am = fmaxf(am, red[i]);
 
-  const float need = block_scale_pow2(am);
+  const float need = fp8_block_scale(am);
   const bool keep = lo > 0 && was >= kScaleMin && was <= kScaleMax;
   if (lo > 0 && !keep && tid == 0) flag_error(p.error_word, MLA_DEVERR_SCALE);
   const float scale = keep ? fmaxf(was, need) : need;

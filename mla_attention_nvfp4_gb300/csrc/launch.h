@@ -172,6 +172,19 @@ struct GemmArgs {
 
 int launch_gemm(const GemmArgs& a, cudaStream_t stream, int num_sms);
 
+struct GemvArgs {
+  const void* x;  // bf16, strides in elements per row and group
+  int64_t x_sm, x_sg;
+  int64_t M;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  int64_t groups, N, K;
+  const float* gs_w;
+  void* out;
+  int64_t out_sm, out_sg;
+};
+int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms);
+
 // The 8-bit path (e4m3 cache and GEMM).
 struct Fp8AppendArgs {
   const void* kv_c;
@@ -184,6 +197,7 @@ struct Fp8AppendArgs {
   int interleaved;
   const int32_t* cu_seqlens;
   const int32_t* context_lens;
+  const int32_t* positions;  // of each sequence's first new token, or nullptr: context_lens
   int num_seqs;
   int max_new;
   const int32_t* page_table;
@@ -222,6 +236,61 @@ struct Fp8DecodeArgs {
 };
 size_t fp8_decode_workspace_bytes(int batch, int num_heads, int num_sms);
 int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms);
+
+// The decode of a batch whose sequences' first shared_len tokens (a multiple
+// of 64) are the same; the workspace is needed.
+size_t fp8_shared_workspace_bytes(int batch, int num_heads, int num_sms);
+int launch_fp8_shared(const Fp8DecodeArgs& a, int64_t shared_len, cudaStream_t stream, int num_sms);
+
+struct Fp8WeightsArgs {
+  const void* q;
+  int batch;
+  int num_heads;
+  const uint8_t* cache;
+  int64_t num_slots;
+  const float* scales;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  int64_t max_pages;
+  int page_size;
+  const int32_t* seq_lens;
+  float softmax_scale;
+  const float* lse;
+  const float* weights;  // nullptr: zeros
+  int64_t weights_stride;
+  float* out;
+  int64_t out_stride;
+  int64_t row_len;
+  uint32_t* error_word;
+};
+int launch_fp8_key_weights(const Fp8WeightsArgs& a, cudaStream_t stream, int num_sms);
+
+struct Fp8EvictArgs {
+  uint8_t* cache;
+  int64_t num_slots;
+  float* scales;
+  const float* weights;
+  int64_t weights_stride;
+  int64_t row_len;
+  int batch;
+  const int32_t* page_table;
+  int64_t pt_stride;
+  int64_t max_pages;
+  const int32_t* new_page_table;
+  int64_t new_pt_stride;
+  int64_t new_max_pages;
+  int page_size;
+  const int32_t* seq_lens;
+  int keep;
+  int recent;
+  int32_t* kept;  // [batch, keep]
+  int32_t* new_lens;
+  float* new_weights;  // or nullptr
+  int64_t new_weights_stride;
+  int64_t new_row_len;
+  uint32_t* error_word;
+};
+int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream);
 
 int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
                         cudaStream_t stream);

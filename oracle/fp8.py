@@ -50,13 +50,14 @@ def block_scale(amax: float) -> float:
     return 2.0 ** e
 
 
-def append(cache, scales, kv_c, k_pe, cos_sin, cu, ctx, table, page_size, interleaved) -> None:
+def append(cache, scales, kv_c, k_pe, cos_sin, cu, ctx, table, page_size, interleaved, positions=None) -> None:
     """In place on cache (uint8 [slots, 576]) and scales (float32)."""
     for b in range(len(ctx)):
         n = int(cu[b + 1] - cu[b])
         pos = int(ctx[b]) + np.arange(n)
+        turn = pos if positions is None else int(positions[b]) + np.arange(n)
         key = np.concatenate([np.asarray(kv_c[cu[b]:cu[b + 1]], np.float32),
-                              rotate(k_pe[cu[b]:cu[b + 1]], cos_sin[pos], interleaved)], 1)
+                              rotate(k_pe[cu[b]:cu[b + 1]], cos_sin[turn], interleaved)], 1)
         for blk in sorted(set((pos // BLOCK).tolist())):
             rows = key[pos // BLOCK == blk]
             first = int(pos[pos // BLOCK == blk][0])
@@ -99,6 +100,70 @@ def decode(q, cache, scales, softmax_scale, table, lens, page_size):
         s = np.asarray(scales, np.float64)[keys // BLOCK]
         flat[b] = np.max(p / z * s, 1)[:, None] * np.abs(k[:, :512] / s[:, None]).sum(0)
     return out, lse, oabs, flat
+
+
+def key_slots(table_row, n, page_size, scales):
+    """(slots of tokens 0 .. n, which of them can be read)."""
+    t = np.arange(n)
+    page = np.asarray(table_row, np.int64)[t // page_size]
+    slot = page * page_size + t % page_size
+    ok = (page >= 0) & (slot // BLOCK < len(scales))
+    s = np.asarray(scales, np.float64)[np.where(ok, slot // BLOCK, 0)]
+    return slot, ok & (s >= 2.0 ** -60) & (s <= 2.0 ** 60)
+
+
+def key_weights(q, cache, scales, softmax_scale, lse, table, lens, page_size, weights):
+    """(weights + each key's part of the softmax summed over the heads, how far fp32 sums may be off), float64; q float
+    [B, H, 576].  Off by at most, of a head's part p at score x: 2 (e^d - 1) p with d = 2^-24 584 |q| |k| scale (the
+    score's sum) + 2^-22 (|x| + |lse|) (log2 units and their difference) + 2^-21 (exp2); and 2^-24 (H + 2) of the sum."""
+    B, H, _ = q.shape
+    out, tol = np.array(weights, np.float64), np.zeros(np.shape(weights))
+    for b in range(B):
+        slot, ok = key_slots(table[b], int(lens[b]), page_size, scales)
+        t = np.nonzero(ok)[0]
+        if not len(t):
+            continue
+        k = decode_codes(cache[slot[t]]) * np.asarray(scales, np.float64)[slot[t] // BLOCK][:, None]
+        qb, ln = np.asarray(q[b], np.float64), np.asarray(lse[b], np.float64)[:, None]
+        x = qb @ k.T * softmax_scale
+        p = np.exp(x - ln)
+        d = (np.abs(qb) @ np.abs(k).T) * softmax_scale * 2.0 ** -24 * 584 + 2.0 ** -22 * (np.abs(x) + np.abs(ln)) + 2.0 ** -21
+        out[b, t] += p.sum(0)
+        tol[b, t] = (2 * np.expm1(d) * p).sum(0) + 2.0 ** -24 * (H + 2) * (p.sum(0) + np.abs(out[b, t]))
+    return out, tol
+
+
+def choose(weights, n, keep, recent):
+    """The tokens of n that stay: the last `recent`, then by weight (the earlier of equal ones, NaN last), ascending."""
+    w = np.asarray(weights[:n], np.float64)
+    old = n - min(n, recent)
+    order = sorted(range(old), key=lambda t: (math.isnan(w[t]), -w[t] if not math.isnan(w[t]) else 0, t))
+    m = min(n, keep)
+    return np.array(sorted(order[:m - (n - old)]) + list(range(old, n)), np.int64)
+
+
+def evict(cache, scales, weights, table, lens, new_table, keep, recent, page_size):
+    """In place on cache and scales; (kept, new lengths, new weights [B, keep])."""
+    B = len(lens)
+    kept, new_lens, new_w = np.full((B, keep), -1, np.int32), np.zeros(B, np.int32), np.zeros((B, keep), np.float32)
+    old_cache, old_scales = cache.copy(), scales.copy()
+    for b in range(B):
+        t = choose(weights[b], int(lens[b]), keep, recent)
+        kept[b, :len(t)], new_lens[b], new_w[b, :len(t)] = t, len(t), np.asarray(weights[b])[t]
+        slot, ok = key_slots(table[b], int(lens[b]), page_size, old_scales)
+        slot, ok = slot[t], ok[t]
+        at = np.where(ok, slot, 0)
+        value = np.where(ok[:, None], decode_codes(old_cache[at]) * np.asarray(old_scales, np.float64)[at // BLOCK][:, None], 0)
+        for i in range(0, len(t), BLOCK):
+            part = value[i:i + BLOCK]
+            page = int(new_table[b][i // page_size])
+            to = page * page_size + i % page_size
+            if page < 0 or to // BLOCK >= len(scales):
+                continue
+            a = np.abs(part)
+            scales[to // BLOCK] = block_scale(float(np.max(np.where(np.isnan(a), 0, a))))
+            cache[to:to + len(part)] = encode(part / float(scales[to // BLOCK]))
+    return kept, new_lens, new_w
 
 
 def quantize(x):

@@ -44,3 +44,13 @@ def nvfp4_gemm_entries(a_codes, a_scales, w_codes, w_scales, K: int, gs_a, gs_w,
 
     return rows_hat(a_codes, a_scales, rows, gs_a) @ rows_hat(w_codes, w_scales, cols, gs_w).T
 
+
+def gemv(x, w_codes, w_scales, N: int, K: int, gs_w):
+    """(product, product of magnitudes, sum of |w| a column) of x [M, G, K] with G packed matrices, float64: the first two
+    [M, G, N], the last [G, N]."""
+    x = np.asarray(x, np.float64)
+    G = x.shape[1]
+    sizes = np.asarray(w_scales).reshape(G, -1)
+    w = np.stack([swizzle.dequantize_rows(np.asarray(w_codes).reshape(G, N, K // 2)[g], sizes[g], N, K, gs_w)
+                  for g in range(G)]).astype(np.float64)
+    return np.einsum("mgk,gnk->mgn", x, w), np.einsum("mgk,gnk->mgn", np.abs(x), np.abs(w)), np.abs(w).sum(2)
