@@ -43,6 +43,8 @@ bool table_ok(int64_t max_pages, int64_t stride) {
   return max_pages >= 1 && max_pages <= INT32_MAX && (stride >= max_pages || stride == 0);
 }
 
+constexpr int kSharedRows = 1 << 30;  // sequences times heads of a batch with a shared prefix
+
 // Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.
 bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
                   int64_t rows) {
@@ -619,7 +621,7 @@ int mla_nvfp4_fp8_decode(const void* q, int batch, int num_heads, const uint8_t*
 }
 
 size_t mla_nvfp4_fp8_decode_shared_workspace_size(int batch, int num_heads) {
-  if (batch < 1 || num_heads < 1) return 0;
+  if (batch < 1 || num_heads < 1 || batch > kSharedRows / num_heads) return 0;
   const int sms = device_sms();
   return mla::fp8_shared_workspace_bytes(batch, num_heads, sms > 0 ? sms : 152);
 }
@@ -634,7 +636,7 @@ int mla_nvfp4_fp8_decode_shared(const void* q, int batch, int num_heads, const u
     return MLA_ERR_INVALID_ARG;
   if (batch == 0) return MLA_OK;
   if (q == nullptr || cache == nullptr || scales == nullptr || page_table == nullptr || seq_lens == nullptr ||
-      out == nullptr || num_slots == 0 || static_cast<int64_t>(batch) * num_heads > (int64_t(1) << 31) - 128)
+      out == nullptr || num_slots == 0 || batch > kSharedRows / num_heads)
     return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return MLA_ERR_ALIGNMENT;

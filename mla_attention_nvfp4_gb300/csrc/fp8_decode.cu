@@ -135,6 +135,18 @@ constexpr uint32_t smem_bytes() {
 }
 static_assert(smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448, "shared memory budget");
 
+// A batch with a shared prefix (groups is 1, cuts one entry a list): lists of
+// keys with up to kH query rows each, one after another.  First the prefix, once
+// for every kH of the batch's rows (sequence, head); then the keys that are each
+// sequence's own, once for every kH of its heads.  A list in a range has its
+// partial results at list + range: pieces follow each other in both.
+struct SharedPlan {
+  int64_t len;                 // of the prefix
+  int prefix, lists, groups;   // lists of the prefix, of all; per sequence
+  int own_rows;                // rows of an own list's partial results
+  int64_t own;                 // the first of those rows
+};
+
 struct Params {
   Fp8DecodeArgs a;
   uint32_t page_magic;  // division by page_size / 64
@@ -144,6 +156,7 @@ struct Params {
   int2* cuts;      // [batch]: a sequence's first range, and its pieces | (1 << 30 where the first is part 1)
   float* part_lse;   // log2 units, [range][group][2][kH]
   float* part_o;     // the same rows of 512
+  SharedPlan sh;
 };
 
 __device__ __forceinline__ int clipped_len(const Fp8DecodeArgs& a, int b) {
@@ -166,15 +179,23 @@ __device__ __forceinline__ int block_slot(const Params& p, int page, int i) {
 }
 
 // The pieces of a CTA's work, one after another: tiles [s, e) of sequence b
-// (len keys, n tiles).  Cut form: the pieces of a range of tiles; part is 0
-// for the one the range begins with, else 1.  Whole form: sequences range,
+// (len keys, n tiles, from block `block` of its page table), query rows row ..
+// row + rows of the batch's.  Cut form: the pieces of a range of tiles; part is
+// 0 for the one the range begins with, else 1.  Whole form: sequences range,
 // range + ranges, ..., those without keys too.
+template <int kH, bool kShared>
 struct Pieces {
   int b = 0, len = 0, s = 0, e = 0, n = 0, part = 0;
+  const int rows;
+  static constexpr int block = 0;
+  __device__ __forceinline__ int64_t row(const Params& p) const { return static_cast<int64_t>(b) * p.a.num_heads + h0_; }
+  __device__ __forceinline__ int64_t part_row(const Params& p, int range) const {
+    return ((static_cast<int64_t>(range) * p.groups + h0_ / kH) * 2 + part) * kH;
+  }
 
   template <class M>
   __device__ __forceinline__ Pieces(const Params& p, const M& ms, int range)
-      : split_(p.split), step_(p.split ? 1 : p.ranges), next_(p.split ? ms.b0 : range), t_(p.split ? ms.t0 : 0),
+      : rows(min(kH, p.a.num_heads - static_cast<int>(blockIdx.x % p.groups) * kH)), h0_(blockIdx.x % p.groups * kH), split_(p.split), step_(p.split ? 1 : p.ranges), next_(p.split ? ms.b0 : range), t_(p.split ? ms.t0 : 0),
         t0_(t_), t1_(p.split ? ms.t1 : 0), off_(p.split ? ms.off0 : 0) {
     next_len_ = load(p);
   }
@@ -199,12 +220,109 @@ struct Pieces {
 
  private:
   __device__ __forceinline__ int load(const Params& p) const { return next_ < p.a.batch ? clipped_len(p.a, next_) : 0; }
+  const int h0_;
   const bool split_;
   const int step_;
   int next_, next_len_;
   int64_t t_;
   const int64_t t0_, t1_;
   int64_t off_;
+};
+
+// The keys and rows of a list.
+struct KeyList {
+  int b, rows;  // page table row
+  int64_t row;
+  int first, last;  // prefix: the sequences of its rows
+};
+template <int kH>
+__device__ __forceinline__ KeyList key_list(const Params& p, int v) {
+  const int H = p.a.num_heads;
+  KeyList k;
+  if (v < p.sh.prefix) {
+    const int64_t all = static_cast<int64_t>(p.a.batch) * H;
+    k.row = static_cast<int64_t>(v) * kH;
+    k.rows = all - k.row < kH ? static_cast<int>(all - k.row) : kH;
+    k.b = 0;
+    k.first = static_cast<int>(k.row / H);
+    k.last = static_cast<int>((k.row + k.rows - 1) / H);
+  } else {
+    const int u = v - p.sh.prefix, g = u % p.sh.groups;
+    k.b = k.first = k.last = u / p.sh.groups;
+    k.row = static_cast<int64_t>(k.b) * H + g * kH;
+    k.rows = min(kH, H - g * kH);
+  }
+  return k;
+}
+// Its keys, given the longest of its sequences' lengths (an own list's only one).
+__device__ __forceinline__ int list_keys(const Params& p, int v, int longest) {
+  const int shared = static_cast<int>(p.sh.len);
+  if (v < p.sh.prefix) return longest >= shared ? shared : 0;
+  return longest >= shared ? longest - shared : longest;
+}
+// What a list takes, in tiles: its start, where it has any.
+__device__ __forceinline__ int list_cost(int tiles) { return tiles > 0 ? tiles + kPiece : 0; }
+
+// The same for lists: a range is one of their costs, of which the first kPiece
+// of a list are its start and the rest its tiles.
+template <int kH>
+struct Pieces<kH, true> {
+  int b = 0, len = 0, s = 0, e = 0, n = 0, rows = 0, block = 0, list = 0;
+  __device__ __forceinline__ int64_t row(const Params&) const { return row_; }
+  __device__ __forceinline__ int64_t part_row(const Params& p, int range) const {
+    const int64_t prefix = p.sh.prefix;
+    return list < prefix ? (static_cast<int64_t>(list) + range) * kH
+                         : p.sh.own + (list - prefix + range) * static_cast<int64_t>(p.sh.own_rows);
+  }
+  template <class M>
+  __device__ __forceinline__ Pieces(const Params& p, const M& ms, int)
+      : next_(ms.b0), t_(ms.t0), t1_(ms.t1), off_(ms.off0), lane_(threadIdx.x & 31) {
+    longest_ = load(p);
+  }
+  // (called by whole warps)
+  __device__ __forceinline__ bool next(const Params& p) {
+    while (t_ < t1_ && next_ < p.sh.lists) {
+      const int v = next_;
+      const int longest = __reduce_max_sync(0xffffffffu, longest_);
+      len = list_keys(p, v, longest);
+      n = tiles_of(len);
+      const int64_t first = off_ + kPiece, end = off_ + list_cost(n), hi = t1_ < end ? t1_ : end;
+      s = t_ > first ? static_cast<int>(t_ - first) : 0;
+      e = hi > first ? static_cast<int>(hi - first) : 0;
+      t_ = hi;
+      if (hi == end) {
+        off_ = end;
+        ++next_;
+        longest_ = load(p);  // ahead of its use
+      }
+      if (s < e) {
+        const KeyList k = key_list<kH>(p, v);
+        list = v;
+        b = k.b;
+        rows = k.rows;
+        row_ = k.row;
+        block = v >= p.sh.prefix && longest >= p.sh.len ? static_cast<int>(p.sh.len / kBlock) : 0;
+        return true;
+      }
+    }
+    return false;
+  }
+
+ private:
+  __device__ __forceinline__ int load(const Params& p) const {
+    int most = 0;
+    if (next_ < p.sh.lists) {
+      const KeyList k = key_list<kH>(p, next_);
+      for (int i = k.first + lane_; i <= k.last; i += 32) most = max(most, clipped_len(p.a, i));
+    }
+    return most;
+  }
+  int64_t row_ = 0;
+  int next_, longest_;
+  int64_t t_;
+  const int64_t t1_;
+  int64_t off_;
+  const int lane_;
 };
 
 // mbar_wait with the loop kept out of line: one try where it is used.
@@ -262,18 +380,30 @@ __device__ __forceinline__ bool half_any(int wg, bool v) {
   return r != 0;
 }
 
-// The plan: this CTA's range of the batch's tiles, and its first sequence.
-// scan: two words of shared memory a warp.
-template <class M>
+// The plan: this CTA's range of the batch's tiles, and its first sequence; or
+// of the lists' costs, and its first list.  scan: two words of shared memory a
+// warp.
+template <int kH, bool kShared, class M>
 __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan, int range, bool publish) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = kShared ? p.sh.lists : p.a.batch;
+  auto cost_of = [&](int b) {
+    if constexpr (kShared) {
+      const KeyList k = key_list<kH>(p, b);
+      int most = 0;
+#pragma unroll 1
+      for (int i = k.first; i <= k.last; ++i) most = max(most, clipped_len(p.a, i));
+      return list_cost(tiles_of(list_keys(p, b, most)));
+    } else {
+      return tiles_of(clipped_len(p.a, b));
+    }
+  };
   const int per_thread = (B + kThreads - 1) / kThreads;
   const int first = tid * per_thread, last = min(first + per_thread, B);
   int64_t sum = 0;
   int most = 0;
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
-    const int n = tiles_of(clipped_len(p.a, b));
+    const int n = cost_of(b);
     sum += n;
     most = max(most, n);
   }
@@ -307,9 +437,41 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   // ranges: those begin two pieces (of one sequence's end and the next one's
   // start; one, if they are of a tile or the batch of a sequence), and the cut
   // ones are merged.
-  const bool uncut = B <= p.ranges && most + kPiece <= per + (per > 1 && B > 1 ? 2 : 1) * kPiece + kMerge;
+  // (A list's cost has its start; a range begins one more, that of a cut list.)
+  const bool uncut =
+      B <= p.ranges && (kShared ? most <= per + kPiece
+                                : most + kPiece <= per + (per > 1 && B > 1 ? 2 : 1) * kPiece + kMerge);
   const int64_t t0 = uncut ? 0 : range * per;
   int64_t off = before + incl - sum;
+  if constexpr (kShared) {
+    if (tid == 0) {
+      ms.t0 = t0;
+      ms.t1 = uncut ? 0 : t0 + per < total ? t0 + per : total;
+    }
+    __syncthreads();  // (an uncut list's thread writes them again)
+#pragma unroll 1
+    for (int b = first; b < last; ++b) {
+      const int n = cost_of(b);
+      if (publish) {
+        const int r0 = n > 0 ? static_cast<int>(divide(off + kPiece, per)) : 0, r1 = n > 0 ? static_cast<int>(divide(off + n - 1, per)) : -1;
+        p.cuts[b] = uncut ? make_int2(b, n > 0 ? 1 : 0) : make_int2(r0, r1 - r0 + 1);
+        // (by its first list, which may have no keys)
+        const KeyList k = key_list<kH>(p, b);
+        if (b >= p.sh.prefix && (b - p.sh.prefix) % p.sh.groups == 0 && p.a.seq_lens[k.b] > clipped_len(p.a, k.b))
+          flag_error(p.a.error_word, MLA_DEVERR_BOUNDS);
+      }
+      if (uncut ? b == range : t0 >= off && t0 < off + n) {
+        ms.b0 = b;
+        ms.off0 = off;
+        if (uncut) {
+          ms.t0 = off;
+          ms.t1 = off + n;
+        }
+      }
+      off += n;
+    }
+    return;
+  }
   if (tid == 0) {
     ms.t0 = t0;
     ms.t1 = uncut ? (range < B ? tiles_of(clipped_len(p.a, range)) : 0) : t0 + per < total ? t0 + per : total;
@@ -317,7 +479,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   }
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
-    const int n = tiles_of(clipped_len(p.a, b));
+    const int n = cost_of(b);
     if (publish) {
       const int r0 = n > 0 ? static_cast<int>(divide(off, per)) : 0, r1 = n > 0 ? static_cast<int>(divide(off + n - 1, per)) : -1;
       p.cuts[b] = uncut ? make_int2(b, n > 0 ? 1 : 0) : make_int2(r0, (r1 - r0 + 1) | (r0 * per < off ? 1 << 30 : 0));
@@ -330,17 +492,17 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   }
 }
 
-template <int kH>
+template <int kH, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_decode_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const Params p) {
   using C = Cfg<kH>;
+  using Work = Pieces<kH, kShared>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int range = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
-  const int h0 = group * kH, heads = min(kH, p.a.num_heads - h0);
   uint32_t* err = p.a.error_word;
 
   if (threadIdx.x == 0) {
@@ -379,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
-  if (p.split) make_plan(p, ms, reinterpret_cast<int64_t*>(&ms.sums[0][0]), range, blockIdx.x == 0);
+  if (p.split) make_plan<kH, kShared>(p, ms, reinterpret_cast<int64_t*>(&ms.sums[0][0]), range, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -394,14 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int n = 0, chunks = 0, ropes = 0;  // tiles; copies issued
     bool ok = true;
-    for (Pieces it(p, ms, range); it.next(p);) {
+    for (Work it(p, ms, range); it.next(p);) {
       const int b = it.b, len = it.len, s = it.s, e = it.e;
       // 32 blocks (16 tiles) at a time, one a lane: the block's first slot
       // (past the cache where there is none, so that it reads as zeros) and
       // its scale.  The next 32 page table entries are loaded ahead.
-      if (s == 0 && group == 0 && lane == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
+      if (!kShared && s == 0 && group == 0 && lane == 0 && p.a.seq_lens[b] > len) flag_error(err, MLA_DEVERR_BOUNDS);
       const int n_blocks = min((len + kBlock - 1) / kBlock, 2 * e);
-      auto page_of = [&](int i) { return i < n_blocks ? block_page(p, b, i) : -1; };
+      auto page_of = [&](int i) { return i < n_blocks ? block_page(p, b, i + it.block) : -1; };
       int page = page_of(2 * s + lane), y = 0;
       float scale = 0.f;
 #pragma unroll 1
@@ -409,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = (2 * (t - s)) & 31;
         if (at == 0) {
           const int i = 2 * t + lane;
-          const int slot = i < n_blocks ? block_slot(p, page, i) : -1;
+          const int slot = i < n_blocks ? block_slot(p, page, i + it.block) : -1;
           page = page_of(i + 32);
           y = static_cast<int>(slot < 0 ? p.a.num_slots : slot);
           scale = slot < 0 ? 0.f : p.a.scales[slot / kBlock];
@@ -470,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return ok;
     };
     int n = 0, piece = 0;
-    for (Pieces it(p, ms, range); ok && it.next(p);) {
+    for (Work it(p, ms, range); ok && it.next(p);) {
       const int s = it.s, e = it.e;
       if (s >= e) continue;
       if (!ready(&ms.q_ready, piece & 1)) break;
@@ -513,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok && wait(bar, parity, err, &ms.abort));
     };
     int n = 0, piece = 0, k = 0;  // tiles, pieces, tiles that are no piece's first
-    for (Pieces it(p, ms, range); ok && it.next(p);) {
+    for (Work it(p, ms, range); ok && it.next(p);) {
       const int s = it.s, e = it.e;
       if (s >= e) continue;
 #pragma unroll 1
@@ -580,10 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const __half2 dither_h = __float2half2_rn(off * (kH == 32 ? kGain : 1.f) * 0.0001220703125f);
     const uint32_t dither = *reinterpret_cast<const uint32_t*>(&dither_h);
     int n = 0, piece = 0, k = 0;
-    for (Pieces it(p, ms, range); it.next(p);) {
-      const int b = it.b, len = it.len, s = it.s, e = it.e;
-      if (s >= e) {  // no keys
-        const int64_t row = static_cast<int64_t>(b) * p.a.num_heads + h0;
+    for (Work it(p, ms, range); it.next(p);) {
+      const int len = it.len, s = it.s, e = it.e, heads = it.rows;
+      const int64_t row = it.row(p);
+      if (!kShared && s >= e) {  // no keys
         uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT);
         for (int i = threadIdx.x - 64; i < heads * (MLA_D_LATENT / 8); i += kSoftmax) out[i] = make_uint4(0, 0, 0, 0);
         if (p.a.lse != nullptr)
@@ -593,8 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Queries (the previous piece's last scores, which this half has read,
       // were the last to use them): a warp takes every fourth head of its
       // half; lane l features 8 l.., and 256 + 8 l.., lanes 0..7 the RoPE's.
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) +
-                               (static_cast<int64_t>(b) * p.a.num_heads + h0) * kKey;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + row * kKey;
       auto load_head = [&](int h, uint4(&v)[3]) {
         v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
         if (h < heads && h < hb + kMine) {
@@ -877,15 +1038,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;  // of a value chunk: a TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     int piece = 0, n_last = -1, k = 0;  // the piece's last tile; tiles that are no piece's first
-    for (Pieces it(p, ms, range); it.next(p);) {
+    for (Work it(p, ms, range); it.next(p);) {
       if (it.s >= it.e) continue;
-      const int b = it.b;
-      const bool whole = it.e - it.s == it.n;
-      const int64_t out_row = static_cast<int64_t>(b) * p.a.num_heads + h0;
-      const int64_t part_row = ((static_cast<int64_t>(range) * p.groups + group) * 2 + it.part) * kH;
+      const int heads = it.rows;
+      const bool whole = !kShared && it.e - it.s == it.n;
+      const int64_t out_row = it.row(p), part_row = it.part_row(p, range);
       n_last += it.e - it.s;
       // the next sequence's queries, into L2 meanwhile
-      if (b + 1 < p.a.batch) {
+      if (!kShared && it.b + 1 < p.a.batch) {
         const char* q = static_cast<const char*>(p.a.q) + (out_row + p.a.num_heads) * (kKey * 2);
         for (int i = tid; i < heads * (kKey * 2 / 128); i += kOutput)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128 * i));
@@ -928,9 +1088,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (isinf(sum) || (below && whole)) sum = __uint_as_float(0x7FC00000u);
         ms.inv[tid] = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
         const float l2 = sum != 0.f ? m + log2f(sum) : below ? kBelow : -INFINITY;
-        if (!whole)
-          p.part_lse[part_row + tid] = l2;
-        else if (p.a.lse != nullptr && tid < heads)
+        if (!whole) {
+          if (!kShared || tid < heads) p.part_lse[part_row + tid] = l2;
+        } else if (p.a.lse != nullptr && tid < heads)
           p.a.lse[out_row + tid] = l2 * kLn2;
       }
       asm volatile("bar.sync 5, %0;" ::"n"(kOutput) : "memory");
@@ -998,12 +1158,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge of the pieces of cut sequences, in range order, by LSE; sequences
-// without keys get their zeros here.  kSub warps = half the features of one
-// (sequence, head), 8 a lane; each takes every kSub-th piece.
+// Merge of the pieces of cut sequences, in range order, by LSE (of a prefix
+// before those of a sequence's own keys); sequences without keys get their
+// zeros here.  kSub warps = half the features of one (sequence, head), 8 a
+// lane; each takes every kSub-th piece.
 template <int kSub>
 constexpr int merge_threads = kSub > 1 ? 64 * kSub : 256;
-template <int kH, int kSub>
+template <int kH, int kSub, bool kShared>
 __global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
   const int64_t id = (static_cast<int64_t>(blockIdx.x) * merge_threads<kSub> + threadIdx.x) / (32 * kSub);
@@ -1012,14 +1173,33 @@ __global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(c
   if (row >= static_cast<int64_t>(p.a.batch) * p.a.num_heads) return;
   const int b = static_cast<int>(row / p.a.num_heads), h = static_cast<int>(row - static_cast<int64_t>(b) * p.a.num_heads);
   const int half = static_cast<int>(id & 1);
-  const int2 cut = p.cuts[b];
-  const int n = cut.y & ~(1 << 30), first = cut.y >> 30;  // pieces; part of the first
-  if (n == 1) return;                                     // written already
+  // its pieces, and the row of partial results of each
+  int n, n0 = 0, first = 0;
+  int64_t row0, own0 = 0;
+  if constexpr (kShared) {
+    const int own = p.sh.prefix + b * p.sh.groups + h / kH, list = static_cast<int>(row / kH);
+    const int2 mine = p.cuts[own];
+    const bool shares = p.sh.prefix > 0 && clipped_len(p.a, b) >= p.sh.len;
+    const int2 pre = shares ? p.cuts[list] : make_int2(0, 0);
+    n0 = pre.y;
+    n = n0 + mine.y;
+    row0 = (static_cast<int64_t>(list) + pre.x) * kH + row % kH;
+    own0 = p.sh.own + (own - p.sh.prefix + mine.x - static_cast<int64_t>(n0)) * p.sh.own_rows + h % kH;
+  } else {
+    const int2 cut = p.cuts[b];
+    n = cut.y & ~(1 << 30), first = cut.y >> 30;  // pieces; part of the first
+    if (n == 1) return;                           // written already
+    row0 = cut.x * static_cast<int64_t>(p.groups) * 2 * kH + (h / kH) * 2 * kH + h % kH;
+  }
+  auto part_of = [&](int i) {
+    if constexpr (kShared)
+      return i < n0 ? row0 + static_cast<int64_t>(i) * kH : own0 + static_cast<int64_t>(i) * p.sh.own_rows;
+    else
+      return row0 + i * (static_cast<int64_t>(p.groups) * 2 * kH) + (i == 0 ? first * kH : 0);
+  };
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + row * MLA_D_LATENT + 256 * half + 4 * lane;
   // lane i: LSE of piece i, i + 32, ...
-  const int64_t stride = static_cast<int64_t>(p.groups) * 2 * kH;  // rows of partial results a range
-  const int64_t row0 = cut.x * stride + (h / kH) * 2 * kH + h % kH;
-  auto lse_of = [&](int i) { return i < n ? p.part_lse[row0 + i * stride + (i == 0 ? first * kH : 0)] : -INFINITY; };
+  auto lse_of = [&](int i) { return i < n ? p.part_lse[part_of(i)] : -INFINITY; };
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, lse_of(i));
 #pragma unroll
@@ -1033,8 +1213,7 @@ __global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(c
     for (int j = sub; j < count; j += kSub) {
       const float w = __shfl_sync(0xffffffffu, w_mine, j);
       const int i = base + j;
-      const float4* o = reinterpret_cast<const float4*>(
-          p.part_o + (row0 + i * stride + (i == 0 ? first * kH : 0)) * MLA_D_LATENT + 256 * half + 4 * lane);
+      const float4* o = reinterpret_cast<const float4*>(p.part_o + part_of(i) * MLA_D_LATENT + 256 * half + 4 * lane);
       const float4 u = o[0], v = o[32];
       sum += w;
       acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]);
@@ -1088,20 +1267,54 @@ Layout layout(int batch, int num_heads, int num_sms) {
   return l;
 }
 
-template <int kH>
+template <int kH, bool kShared>
 int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int slot, cudaStream_t stream) {
   constexpr int bytes = static_cast<int>(smem_bytes<kH>());
-  if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_decode_kernel<kH>), bytes, slot)) return st;
-  fp8_decode_kernel<kH><<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
+  const auto kern = fp8_decode_kernel<kH, kShared>;
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), bytes, slot)) return st;
+  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
   if (const int st = launch_status()) return st;
   if (!p.split) return MLA_OK;
   // A CTA a row where the rows are cut into many pieces.
   const int64_t rows = static_cast<int64_t>(p.a.num_heads) * p.a.batch;
-  if (p.ranges / kManyPieces >= p.a.batch)
-    fp8_decode_merge_kernel<kH, kSub><<<static_cast<unsigned>(rows), merge_threads<kSub>, 0, stream>>>(p);
+  if (p.ranges / kManyPieces >= (kShared ? p.sh.prefix : p.a.batch))
+    fp8_decode_merge_kernel<kH, kSub, kShared><<<static_cast<unsigned>(rows), merge_threads<kSub>, 0, stream>>>(p);
   else
-    fp8_decode_merge_kernel<kH, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(p);
+    fp8_decode_merge_kernel<kH, 1, kShared><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(p);
   return launch_status();
+}
+
+int cache_maps(const Fp8DecodeArgs& a, CUtensorMap* lat, CUtensorMap* rope) {
+  if (encode_byte_map(lat, a.cache, kKey, a.num_slots, kKey, 128, kBlock, false) &&
+      encode_byte_map(rope, a.cache, kKey, a.num_slots, kKey, 64, kBlock, true))
+    return MLA_OK;
+  set_last_error("cuTensorMapEncodeTiled failed for the cache");
+  return MLA_ERR_LAUNCH;
+}
+
+// Shared prefix: the batch's rows decide on the heads a CTA.
+struct SharedLayout {
+  int kh;
+  SharedPlan plan;
+  size_t lse, o, total;
+};
+SharedLayout shared_layout(int batch, int num_heads, int num_sms, int64_t shared_len) {
+  SharedLayout l;
+  const int64_t rows = static_cast<int64_t>(batch) * num_heads;
+  l.kh = rows <= 32 ? 32 : 64;
+  constexpr int64_t kNever = (int64_t(1) << 31) - kBlock;  // (longer than a sequence can be)
+  l.plan.len = shared_len < kNever ? shared_len : kNever;
+  l.plan.prefix = static_cast<int>((rows + l.kh - 1) / l.kh);
+  l.plan.groups = (num_heads + l.kh - 1) / l.kh;
+  l.plan.lists = l.plan.prefix + batch * l.plan.groups;
+  l.plan.own_rows = num_heads < l.kh ? num_heads : l.kh;
+  l.plan.own = (static_cast<int64_t>(l.plan.prefix) + num_sms) * l.kh;
+  const size_t all = l.plan.own + (static_cast<int64_t>(batch) * l.plan.groups + num_sms) * l.plan.own_rows;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.lse = up(static_cast<size_t>(l.plan.lists) * sizeof(int2));
+  l.o = up(l.lse + all * sizeof(float));
+  l.total = l.o + all * MLA_D_LATENT * sizeof(float);
+  return l;
 }
 
 }  // namespace
@@ -1124,15 +1337,29 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
   const bool split =
       ws != nullptr && (a.batch > l.ranges || a.max_pages * a.page_size > (1 + kMerge) * kTile);
   Params p{a, magic, shift, l.ranges, l.groups, split, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),
-           reinterpret_cast<float*>(ws + l.o)};
+           reinterpret_cast<float*>(ws + l.o), SharedPlan{}};
   if (static_cast<int64_t>(a.batch) * a.num_heads > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   CUtensorMap lat, rope;
-  if (!encode_byte_map(&lat, a.cache, kKey, a.num_slots, kKey, 128, kBlock, false) ||
-      !encode_byte_map(&rope, a.cache, kKey, a.num_slots, kKey, 64, kBlock, true)) {
-    set_last_error("cuTensorMapEncodeTiled failed for the cache");
-    return MLA_ERR_LAUNCH;
-  }
-  return heads_per_cta(a.num_heads) == 64 ? launch<64>(p, lat, rope, 19, stream) : launch<32>(p, lat, rope, 20, stream);
+  if (const int st = cache_maps(a, &lat, &rope)) return st;
+  return heads_per_cta(a.num_heads) == 64 ? launch<64, false>(p, lat, rope, 19, stream)
+                                          : launch<32, false>(p, lat, rope, 20, stream);
+}
+
+size_t fp8_shared_workspace_bytes(int batch, int num_heads, int num_sms) {
+  return shared_layout(batch, num_heads, num_sms, 0).total;
+}
+
+int launch_fp8_shared(const Fp8DecodeArgs& a, int64_t shared_len, cudaStream_t stream, int num_sms) {
+  const SharedLayout l = shared_layout(a.batch, a.num_heads, num_sms, shared_len);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  uint32_t magic;
+  int shift;
+  magic_divisor(a.page_size / kBlock, &magic, &shift);
+  const Params p{a, magic, shift, num_sms, 1, true, reinterpret_cast<int2*>(ws), reinterpret_cast<float*>(ws + l.lse),
+                 reinterpret_cast<float*>(ws + l.o), l.plan};
+  CUtensorMap lat, rope;
+  if (const int st = cache_maps(a, &lat, &rope)) return st;
+  return l.kh == 64 ? launch<64, true>(p, lat, rope, 24, stream) : launch<32, true>(p, lat, rope, 25, stream);
 }
 
 }  // namespace mla
