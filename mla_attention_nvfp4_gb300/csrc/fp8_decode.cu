@@ -260,10 +260,17 @@ __device__ __forceinline__ int list_keys(const Params& p, int v, int longest) {
   if (v < p.sh.prefix) return longest >= shared ? shared : 0;
   return longest >= shared ? longest - shared : longest;
 }
-// What a list takes, in tiles: its start, where it has any.
-__device__ __forceinline__ int list_cost(int tiles) { return tiles > 0 ? tiles + kPiece : 0; }
+// What a list takes, in tiles: its start, where it has any.  (64 rows: 32 x
+// (32768 + 1000) keys, 128 heads, 256 us; with 3 tiles a start, 4, 6: 297, 274,
+// 256: the CTAs of the many short lists were the last to end.)
+template <int kH>
+constexpr int kStart = kH == 64 ? 5 : 3;
+template <int kH>
+__device__ __forceinline__ int list_cost(int tiles) {
+  return tiles > 0 ? tiles + kStart<kH> : 0;
+}
 
-// The same for lists: a range is one of their costs, of which the first kPiece
+// The same for lists: a range is one of their costs, of which the first kStart
 // of a list are its start and the rest its tiles.
 template <int kH>
 struct Pieces<kH, true> {
@@ -286,7 +293,7 @@ struct Pieces<kH, true> {
       const int longest = __reduce_max_sync(0xffffffffu, longest_);
       len = list_keys(p, v, longest);
       n = tiles_of(len);
-      const int64_t first = off_ + kPiece, end = off_ + list_cost(n), hi = t1_ < end ? t1_ : end;
+      const int64_t first = off_ + kStart<kH>, end = off_ + list_cost<kH>(n), hi = t1_ < end ? t1_ : end;
       s = t_ > first ? static_cast<int>(t_ - first) : 0;
       e = hi > first ? static_cast<int>(hi - first) : 0;
       t_ = hi;
@@ -392,7 +399,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
       int most = 0;
 #pragma unroll 1
       for (int i = k.first; i <= k.last; ++i) most = max(most, clipped_len(p.a, i));
-      return list_cost(tiles_of(list_keys(p, b, most)));
+      return list_cost<kH>(tiles_of(list_keys(p, b, most)));
     } else {
       return tiles_of(clipped_len(p.a, b));
     }
@@ -439,7 +446,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   // ones are merged.
   // (A list's cost has its start; a range begins one more, that of a cut list.)
   const bool uncut =
-      B <= p.ranges && (kShared ? most <= per + kPiece
+      B <= p.ranges && (kShared ? most <= per + kStart<kH>
                                 : most + kPiece <= per + (per > 1 && B > 1 ? 2 : 1) * kPiece + kMerge);
   const int64_t t0 = uncut ? 0 : range * per;
   int64_t off = before + incl - sum;
@@ -453,7 +460,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
     for (int b = first; b < last; ++b) {
       const int n = cost_of(b);
       if (publish) {
-        const int r0 = n > 0 ? static_cast<int>(divide(off + kPiece, per)) : 0, r1 = n > 0 ? static_cast<int>(divide(off + n - 1, per)) : -1;
+        const int r0 = n > 0 ? static_cast<int>(divide(off + kStart<kH>, per)) : 0, r1 = n > 0 ? static_cast<int>(divide(off + n - 1, per)) : -1;
         p.cuts[b] = uncut ? make_int2(b, n > 0 ? 1 : 0) : make_int2(r0, r1 - r0 + 1);
         // (by its first list, which may have no keys)
         const KeyList k = key_list<kH>(p, b);
@@ -1298,10 +1305,10 @@ struct SharedLayout {
   SharedPlan plan;
   size_t lse, o, total;
 };
-SharedLayout shared_layout(int batch, int num_heads, int num_sms, int64_t shared_len) {
+SharedLayout shared_layout(int kh, int batch, int num_heads, int num_sms, int64_t shared_len) {
   SharedLayout l;
   const int64_t rows = static_cast<int64_t>(batch) * num_heads;
-  l.kh = rows <= 32 ? 32 : 64;
+  l.kh = kh;
   constexpr int64_t kNever = (int64_t(1) << 31) - kBlock;  // (longer than a sequence can be)
   l.plan.len = shared_len < kNever ? shared_len : kNever;
   l.plan.prefix = static_cast<int>((rows + l.kh - 1) / l.kh);
@@ -1346,11 +1353,19 @@ int launch_fp8_decode(const Fp8DecodeArgs& a, cudaStream_t stream, int num_sms) 
 }
 
 size_t fp8_shared_workspace_bytes(int batch, int num_heads, int num_sms) {
-  return shared_layout(batch, num_heads, num_sms, 0).total;
+  const size_t a = shared_layout(32, batch, num_heads, num_sms, 0).total;
+  const size_t b = shared_layout(64, batch, num_heads, num_sms, 0).total;
+  return a > b ? a : b;
 }
 
 int launch_fp8_shared(const Fp8DecodeArgs& a, int64_t shared_len, cudaStream_t stream, int num_sms) {
-  const SharedLayout l = shared_layout(a.batch, a.num_heads, num_sms, shared_len);
+  // 64 rows a CTA, where the keys are read half as often and a tile of 64 rows
+  // takes little longer than one of 32; 32 where no CTA would have two tiles of
+  // the prefix, and its start counts (but not for heads that fill 64 rows: their
+  // own keys may be many).
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.num_heads;
+  const bool few = a.num_heads <= 32 && (rows + 31) / 32 * ((shared_len + kTile - 1) / kTile) <= num_sms;
+  const SharedLayout l = shared_layout(few ? 32 : 64, a.batch, a.num_heads, num_sms, shared_len);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   uint32_t magic;
   int shift;
