@@ -511,7 +511,7 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
  */
 int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_t M, const uint8_t* w_codes,
                    const uint8_t* w_scales, int groups, int64_t N, int64_t K, const float* gs_w, void* out,
-                   int64_t out_stride_m, int64_t out_stride_g, void* stream);
+                   int64_t out_stride_m, int64_t out_stride_g, uint32_t* error_word, void* stream);
 
 /*
  * The 8-bit path: a latent cache held in e4m3 with one scale per block of

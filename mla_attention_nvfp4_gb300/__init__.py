@@ -124,7 +124,7 @@ _SIGS = {
                                            _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_vp,
                                            _c_i64, _c_i64, _c_vp, _c_vp]),
     "mla_nvfp4_gemv": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp,
-                                _c_i64, _c_i64, _c_vp]),
+                                _c_i64, _c_i64, _c_vp, _c_vp]),
     "mla_nvfp4_fp8_decode_workspace_size": (ctypes.c_size_t, [_c_int, _c_int]),
     "mla_nvfp4_fp8_decode": (_c_int, [_c_vp, _c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_int,
                                       _c_vp, _c_f, _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp, _c_vp]),
@@ -791,10 +791,10 @@ def mla_nvfp4_fp8_cache_evict(cache, scales, weights, *, page_table, seq_lens, n
         error_word))
 
 
-def mla_nvfp4_gemv(x, w_codes, w_scales, gs_w, *, out=None):
+def mla_nvfp4_gemv(x, w_codes, w_scales, gs_w, *, out=None, error_word=None):
     """bf16 x times NVFP4 weights, laid out as mla_nvfp4_gemm's: x [M, K] with
     w_codes [N, K/2] and w_scales -> [M, N], or x [M, G, K] with w_codes
     [G, N, K/2] and w_scales [G, ...] (one matrix a group, e.g. a head's part
     of W_UK) -> [M, G, N]; gs_w a device fp32 [1] for all groups.  For few
     rows: every 16 read the weights again."""
-    return _result("mla_nvfp4_gemv", _fp8().gemv(x, w_codes, w_scales, gs_w, out))
+    return _result("mla_nvfp4_gemv", _fp8().gemv(x, w_codes, w_scales, gs_w, out, error_word))

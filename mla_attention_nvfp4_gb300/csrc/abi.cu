@@ -361,7 +361,7 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
 
 int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_t M, const uint8_t* w_codes,
                    const uint8_t* w_scales, int groups, int64_t N, int64_t K, const float* gs_w, void* out,
-                   int64_t out_stride_m, int64_t out_stride_g, void* stream) {
+                   int64_t out_stride_m, int64_t out_stride_g, uint32_t* error_word, void* stream) {
   constexpr int64_t kMax = (int64_t(1) << 31) - 512;
   if (M < 0 || groups < 0 || N < 0 || K < 0 || K % 32 != 0) return MLA_ERR_INVALID_ARG;
   if (M == 0 || groups == 0 || N == 0) return MLA_OK;
@@ -381,7 +381,7 @@ int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_
   const int sms = device_sms();
   if (sms < 0) return -sms;
   const mla::GemvArgs a{x, M > 1 ? x_stride_m : 0, groups > 1 ? x_stride_g : 0, M, w_codes, w_scales, groups, N, K, gs_w,
-                        out, M > 1 ? out_stride_m : 0, groups > 1 ? out_stride_g : 0};
+                        out, M > 1 ? out_stride_m : 0, groups > 1 ? out_stride_g : 0, error_word};
   return mla::launch_gemv(a, static_cast<cudaStream_t>(stream), sms);
 }
 

@@ -441,10 +441,11 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(out.dim() == d && out.size(0) == M && (d == 2 || out.size(1) == G) && out.size(d - 1) == N && rows_contiguous(out),
          "out must be [M, N] or [M, G, N] with a contiguous last dimension");
   }
+  uint32_t* err = args.error_word();
   const Launch at(args.device);
   const int st = mla_nvfp4_gemv(x.data_ptr(), x.stride(0), d == 3 ? x.stride(1) : 0, M, bytes(w), bytes(ws),
                                 int32_of(G, "too many groups"), N, K, data<float>(gs), out.data_ptr(), out.stride(0),
-                                d == 3 ? out.stride(1) : 0, at.stream);
+                                d == 3 ? out.stride(1) : 0, err, at.stream);
   return st != MLA_OK ? status(st) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }

@@ -182,6 +182,7 @@ struct GemvArgs {
   const float* gs_w;
   void* out;
   int64_t out_sm, out_sg;
+  uint32_t* error_word;
 };
 int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms);
 

@@ -89,7 +89,7 @@ def test_evict_alignment_and_empty():
 
 
 def _gemv(**kw):
-    a = dict(x=P, xm=256, xg=64, M=4, w=P, sf=P, G=4, N=8, K=64, gs=P, out=P, om=32, og=8, stream=None)
+    a = dict(x=P, xm=256, xg=64, M=4, w=P, sf=P, G=4, N=8, K=64, gs=P, out=P, om=32, og=8, err=None, stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
     return mla.load_library().mla_nvfp4_gemv(*a.values())
