@@ -36,12 +36,8 @@ using namespace sm100;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStep = 256;  // features a warp takes at a time: 64 a thread of a quad
 constexpr int kMinStages = 3, kMaxStages = 8;  // of weights in shared memory
-#ifndef KCTAS
-#define KCTAS 2
-#define KSHARE 110
-#endif
-constexpr int kCtas = KCTAS;                       // an SM
-constexpr uint32_t kShare = KSHARE * 1024;         // of an SM's shared memory for each of them
+constexpr int kCtas = 2;                       // an SM
+constexpr uint32_t kShare = 110 * 1024;        // of an SM's shared memory for each of them
 constexpr uint32_t kCodeBytes = 128 * (kStep / 2), kScaleBytes = 4 * 512;
 
 struct Params {
@@ -148,16 +144,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     bulk_load(dst + kCodeBytes, scales + static_cast<int64_t>(step) * 2048, tiles * 512, &full[slot]);
     issued = i + 1;
   };
-  if (tid == 0) {
-    abort = 0;
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    fence_mbar_init();
-    for (int i = 0; i < p.stages && i < count; ++i) load(i);
-  }
-
   // x, a chunk of stages at a time: a warp takes rows of steps (a chunk has a
   // row for each warp at least), 8 features a lane; a unit of 8 is piece u % 8 of
   // the quad's thread u / 8.
@@ -199,20 +185,37 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int piece = unit & 7, thread = unit >> 3;
     sts128(x_base + (buffer * chunk_steps + s) * kXStep + 16 * (piece * (4 * kPad) + 4 * r + thread), v);
   };
-  constexpr int kAhead = kPad > 8 ? 2 : 1;  // rows of x a warp has in registers ahead
+  constexpr int kAhead = kPad > 8 ? 2 : 1;  // rows of x a warp has in registers ahead,
+  constexpr int kDepth = 3;                 // of so many chunks
   const int pairs_x = kPad * chunk_steps;
-  uint4 next[kAhead];
-  auto read_ahead = [&](int i) {
+  uint4 next[kDepth][kAhead];
+  auto read_ahead = [&](uint4 (&v)[kAhead], int i) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) next[j] = read_x(i, warp + kWarps * j);
+    for (int j = 0; j < kAhead; ++j) v[j] = read_x(i, warp + kWarps * j);
   };
   auto stage_all = [&](int i, int buffer) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) stage_x(buffer, warp + kWarps * j, next[j]);
+    for (int j = 0; j < kAhead; ++j) stage_x(buffer, warp + kWarps * j, next[0][j]);
 #pragma unroll 1
     for (int pair = warp + kWarps * kAhead; pair < pairs_x; pair += kWarps) stage_x(buffer, pair, read_x(i, pair));
+#pragma unroll
+    for (int d = 0; d + 1 < kDepth; ++d)
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) next[d][j] = next[d + 1][j];
   };
-  read_ahead(0);
+  // (before the weights are asked for, behind which it would wait)
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) read_ahead(next[d], d * chunk);
+  if (tid == 0) {
+    abort = 0;
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_mbar_init();
+    for (int i = 0; i < p.stages && i < count; ++i) load(i);
+  }
+
   stage_all(0, 0);
 
   float total[kTiles][4] = {};
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll 1
   for (int i0 = 0; i0 < count; i0 += chunk, buffer ^= 1) {
     __syncthreads();  // the chunk's x is there, and the one before has been read
-    read_ahead(i0 + chunk);
+    read_ahead(next[kDepth - 1], i0 + kDepth * chunk);
 #pragma unroll 1
     for (int i = i0; i < min(i0 + chunk, count); ++i) {
       // (A wait that gives up, which the error word tells, leaves the warps
