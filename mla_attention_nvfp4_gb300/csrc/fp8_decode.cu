@@ -66,6 +66,7 @@
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
+#include "fp8_query.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
 #include "sm100.cuh"
@@ -82,9 +83,8 @@ constexpr int kSoftmax = 256, kOutput = 128, kThreads = 96 + kSoftmax + kOutput;
 constexpr float kScaleMin = 8.673617379884035e-19f, kScaleMax = 1.152921504606847e18f;  // 2^-60, 2^60
 constexpr float kTop = 8.5f;    // weights stay at or below 2^8.5 = 362 (e4m3: 448)
 constexpr float kReset = 4.0f;  // a raised reference puts the tile's largest weight at 2^4
-constexpr float kGain = 16.f;   // queries' and 32 heads' weights' second terms: at most 16 becomes 256
 constexpr float kBelow = -3.402823466e38f;  // a piece's LSE where all its scores are below fp32's range
-constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPiece = 3, kMerge = 2;  // what a piece's start and a merge cost, in tiles
 // The merge gives a row of results 2 kSub warps, not 2, from kManyPieces ranges
 // a sequence on.  1 x 65536 keys, 128 heads: 37.5 us in all (49.2 with 2 warps
@@ -340,24 +340,10 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* e
   return mbar_test(bar, parity) || wait_long(bar, parity, err, abort);
 }
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2_h2(uint32_t h2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
-  return r;
-}
 __device__ __forceinline__ uint32_t cvt_e5m2x2_h2(uint32_t h2) {
   uint16_t r;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
-}
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t h2_fma(uint32_t a, float s, uint32_t b) {
-  const __half2 r =
-      __hfma2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(s), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 // Rounded to multiples of 2^-13 where below 2^-4: the steps of f16 numbers in
 // [2^-3, 2^-2).  (Larger ones lose what is far below their step in e5m2.)
@@ -787,60 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int two = 0; two < 2; ++two) {
           const int h = h2 + 4 * two;
           const uint4(&v)[3] = v_now[two];
-          // amax from the bf16 bits (sign dropped, they order like integers)
-          uint32_t m2 = 0;
-  #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              m2 = max(m2, w[j] & 0x7FFF0000u);
-              m2 = max(m2, (w[j] << 16) & 0x7FFF0000u);
-            }
-          }
-          m2 = __reduce_max_sync(0xffffffffu, m2);
-          // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8); a
-          // head with an infinity or a NaN has NaN scores
-          int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-          ex = max(-126, min(120, ex));
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-          if (lane == 0)
-            ms.c[h] = m2 >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                        : p.a.softmax_scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-  #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            // in f16 pairs: 8 significant bits down to 2^-17, then steps of 2^-24
-            uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float x0, x1;
-              bf16x2_to_f32(w[j], x0, x1);
-              const __half2 xh = __floats2half2_rn(x0 * inv, x1 * inv);
-              const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
-              const uint32_t a = cvt_e4m3x2_h2(xu);
-              w1[j >> 1] |= a << (16 * (j & 1));
-              w2[j >> 1] |= cvt_e4m3x2_h2(h2_fma(h2_sub(xu, e4m3x2_to_f16x2_pair(a)), kGain, 0)) << (16 * (j & 1));
-            }
-            // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
-            uint32_t a1, a2;
-            if (k < 2) {
-              const int feature = 256 * k + 8 * lane;
-              const uint32_t base = s0 + C::off_q + (feature >> 7) * C::q_chunk;
-              const uint32_t unit = (feature & 127) >> 4, half = feature & 8;
-              a1 = base + h * 128 + ((unit ^ (h & 7)) << 4) + half;
-              a2 = a1 + kH * 128;
-            } else {
-              const uint32_t base = s0 + C::off_q + 4 * C::q_chunk;
-              const uint32_t unit = lane >> 1, half = (lane & 1) * 8;
-              a1 = base + h * 64 + ((unit ^ ((h >> 1) & 3)) << 4) + half;
-              a2 = a1 + kH * 64;
-            }
-            if (k < 2 || lane < 8) {
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a1), "r"(w1[0]), "r"(w1[1]) : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a2), "r"(w2[0]), "r"(w2[1]) : "memory");
-            }
-          }
+          const float c = query_terms<kH>(v, lane, h, s0 + C::off_q, p.a.softmax_scale);
+          if (lane == 0) ms.c[h] = c;
         }
       }
       fence_async_smem();

@@ -35,7 +35,7 @@ int current_device_sms();
 // Raise `kernel`'s dynamic shared memory limit to `bytes` on the current
 // device, once per device and kernel slot (the attribute persists), so that
 // launches inside a stream capture make no attribute calls.  `slot` names
-// the kernel (0 .. 31).
+// the kernel (0 .. 63).
 int smem_limit_once(const void* kernel, int bytes, int slot);
 
 int launch_cache_write(const void* kv_c, int64_t kv_stride, const void* k_pe, int64_t pe_stride,
