@@ -38,12 +38,9 @@ __device__ __forceinline__ float query_terms(const uint4 (&v)[3], int lane, int 
   for (int k = 0; k < 3; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      m2 = max(m2, w[j] & 0x7FFF0000u);
-      m2 = max(m2, (w[j] << 16) & 0x7FFF0000u);
-    }
+    for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, w[j] & 0x7FFF7FFFu);
   }
-  m2 = __reduce_max_sync(0xffffffffu, m2);
+  m2 = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFF0000u, m2 << 16));
   // 2^e, the smallest with amax <= 448 * 2^e (448 = 1.75 * 2^8); a
   // head with an infinity or a NaN has NaN scores
   int ex = static_cast<int>(m2 >> 23) - 127 - 8 + ((m2 & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -53,17 +50,18 @@ __device__ __forceinline__ float query_terms(const uint4 (&v)[3], int lane, int 
   for (int k = 0; k < 3; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
     // in f16 pairs: 8 significant bits down to 2^-17, then steps of 2^-24
-    uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
+    uint32_t a[4], r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x0, x1;
       bf16x2_to_f32(w[j], x0, x1);
       const __half2 xh = __floats2half2_rn(x0 * inv, x1 * inv);
       const uint32_t xu = *reinterpret_cast<const uint32_t*>(&xh);
-      const uint32_t a = cvt_e4m3x2_h2(xu);
-      w1[j >> 1] |= a << (16 * (j & 1));
-      w2[j >> 1] |= cvt_e4m3x2_h2(h2_fma(h2_sub(xu, e4m3x2_to_f16x2_pair(a)), kGain, 0)) << (16 * (j & 1));
+      a[j] = cvt_e4m3x2_h2(xu);
+      r[j] = cvt_e4m3x2_h2(h2_fma(h2_sub(xu, e4m3x2_to_f16x2_pair(a[j])), kGain, 0));
     }
+    const uint32_t w1[2] = {__byte_perm(a[0], a[1], 0x5410), __byte_perm(a[2], a[3], 0x5410)};
+    const uint32_t w2[2] = {__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410)};
     // row h (q1) and kH + h (q2) of the chunk; 16-byte units swizzled by the row
     uint32_t a1, a2;
     if (k < 2) {

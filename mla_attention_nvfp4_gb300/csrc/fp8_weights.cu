@@ -13,7 +13,7 @@
 // its pieces' starts, a sequence's queries being converted anew):
 //   warp 0      TMA producer; 128-feature chunks and the RoPE's in turn;
 //   warp 1      issues the products, a tile ahead;
-//   warps 2..9  queries to two terms; then every other tile each four of them:
+//   warps 2..   queries to two terms; then a tile each four of them, in turn:
 //               thread = key.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -31,7 +31,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kKey = kFp8Key, kBlock = MLA_FP8_BLOCK, kTile = 128;
-constexpr int kSum = 256, kThreads = 64 + kSum, kWarps = kThreads / 32;
+// Groups of four warps that take a tile each in turn: two keep up with the
+// tiles; with 64 heads and more the queries want four.
+template <int kH>
+constexpr int kGroups = kH >= 64 ? 4 : 2;
+template <int kH>
+constexpr int kThreads = 64 + 128 * kGroups<kH>;
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64, kTileBytes = 4 * kChunkBytes + kRopeBytes;
 constexpr int kStart = 2;  // a piece's start, in tiles
 constexpr int kInfo = 4;   // tiles whose scales are kept
@@ -51,7 +56,7 @@ struct Misc {
   uint64_t s_full[2], s_free[2], q_ready, q_free, retired;
   alignas(16) float2 head[2][kH];  // of a piece, in turn: factor of its scores, log2(e) lse
   float scale[kInfo][2];           // of a tile's two blocks; 0: none of the sequence's
-  int64_t scan[kWarps], t0, t1, off0;
+  int64_t scan[kThreads<kH> / 32], t0, t1, off0;
   int b0;
   uint32_t tmem;
   int copies;
@@ -119,7 +124,7 @@ struct Pieces {
 };
 
 // This CTA's part of the sequences' costs, and its first sequence.
-template <class M>
+template <int kThreads, class M>
 __device__ __forceinline__ void make_plan(const Params& p, M& ms) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
   const int per_thread = (B + kThreads - 1) / kThreads;
@@ -140,7 +145,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms) {
   __syncthreads();
   int64_t total = 0, off = incl - sum;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) off += ms.scan[i];
     total += ms.scan[i];
   }
@@ -161,10 +166,11 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms) {
 }
 
 template <int kH>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kH>, 1)
     fp8_key_weights_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                            const __grid_constant__ Params p) {
   using C = Cfg<kH>;
+  constexpr int kQueryWarps = 4 * kGroups<kH>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
   const uint32_t s0 = smem_u32(smem);
@@ -183,9 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kInfo; ++i) mbar_init(&ms.info_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.s_free[i], kSum / 64);
+      mbar_init(&ms.s_free[i], 4);
     }
-    mbar_init(&ms.q_ready, kSum / 32);
+    mbar_init(&ms.q_ready, kQueryWarps);
     mbar_init(&ms.q_free, 1);
     mbar_init(&ms.retired, 1);
     fence_mbar_init();
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   __syncthreads();  // (b0 is set before the plan)
-  make_plan(p, ms);
+  make_plan<kThreads<kH>>(p, ms);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -336,11 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_head(warp - 2, next);
       if (piece > 0) mbar_wait(&ms.q_free, (piece - 1) & 1, err, &ms.abort);
 #pragma unroll 1
-      for (int h = warp - 2; h < kH; h += kSum / 32) {
+      for (int h = warp - 2; h < kH; h += kQueryWarps) {
         uint4 v[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) v[i] = next[i];
-        load_head(h + kSum / 32, next);
+        load_head(h + kQueryWarps, next);
         const float c = query_terms<kH>(v, lane, h, s0 + C::off_q, p.a.softmax_scale);
         // (no head: its weights are 2^-inf)
         if (lane == 0) head[h] = h < heads ? make_float2(c, p.a.lse[row0 + h] * kLog2e) : make_float2(0.f, INFINITY);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
       for (int t = it.s; t < it.e; ++t, ++n) {
-        if ((n & 1) != group) continue;
+        if (n % kGroups<kH> != group) continue;
         const int at = t * kTile + key;
         float before = 0.f;
         if (p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
@@ -399,7 +405,7 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   constexpr int bytes = static_cast<int>(smem_bytes<kH>());
   const auto kern = fp8_key_weights_kernel<kH>;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), bytes, slot)) return st;
-  kern<<<ctas, kThreads, bytes, stream>>>(lat, rope, p);
+  kern<<<ctas, kThreads<kH>, bytes, stream>>>(lat, rope, p);
   return launch_status();
 }
 
