@@ -705,7 +705,7 @@ int mla_nvfp4_fp8_cache_evict(uint8_t* cache, int64_t num_slots, float* scales, 
                             page_table_stride, max_pages, new_page_table, new_page_table_stride, new_max_pages,
                             page_size, seq_lens, keep, recent, kept, new_lens, new_weights, new_weights_stride,
                             new_row_len, error_word};
-  return mla::launch_fp8_evict(a, static_cast<cudaStream_t>(stream));
+  return mla::launch_fp8_evict(a, static_cast<cudaStream_t>(stream), sms);
 }
 
 int mla_nvfp4_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,

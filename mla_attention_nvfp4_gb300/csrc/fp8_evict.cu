@@ -1,19 +1,30 @@
 // Eviction from the e4m3 cache: of every sequence the most recent tokens and
 // those of greatest weight, in order, moved to new pages.
-//   choose: a CTA a sequence: the weight of rank n from four passes over its
-//           bytes (counts of each byte's values among the weights that agree
-//           above), then the indices in order;
-//   move:   a CTA a new block of 64 tokens, whose scale follows the rule of
-//           the append.
+//
+//   choose  a cluster a sequence, each CTA a part of its tokens, whose weights
+//           wait in shared memory as integers of their order.  The weight of rank
+//           n comes byte by byte: counts of a byte's values among the weights that
+//           agree above it (a histogram a warp, so that equal weights meet in a
+//           warp only; summed over the warps, then over the cluster by every CTA).
+//           Then the tokens above it, and the first of those equal to it, find
+//           their places from counts of the warps and CTAs before.  Latency:
+//           four rounds of five barriers, about a microsecond each.
+//   move    a CTA a new block of 64 tokens, all its rows in registers while the
+//           largest is found: HBM-bound.  Its scale follows the append's rule.
 #include <cuda_runtime.h>
 
 #include "fp8_paged.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 namespace {
 
 constexpr int kBlock = MLA_FP8_BLOCK, kKey = kFp8Key;
-constexpr int kChoose = 1024, kMove = 256;
+constexpr int kChoose = 1024, kWarps = kChoose / 32;
+constexpr int kHeld = 16384;          // weights in shared memory; the others of a longer part are read again
+constexpr int kPart = 2048;           // tokens a CTA of a cluster takes at least, where there are so many
+constexpr int kChooseBytes = (kHeld + kWarps * 256) * 4;
+constexpr int kMove = 256, kUnits = kBlock * kKey / 16 / kMove;  // 16-byte units a thread
 
 // Weights as integers of the same order; NaN comes first, -0 is 0.
 __device__ __forceinline__ uint32_t rank_key(float w) {
@@ -22,74 +33,151 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kChoose) fp8_evict_choose_kernel(const Fp8EvictArgs a) {
-  __shared__ int count[256], warp_sum[2][32];
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(sm100::smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8EvictArgs a, int ctas) {
+  extern __shared__ uint32_t held[];  // weights, then kWarps histograms
+  __shared__ int total[2][256];       // of this CTA, in turn
+  __shared__ int upper[8], counts[2], warp_counts[2][kWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
+  int* hist = reinterpret_cast<int*>(held + kHeld);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-    const float* w = a.weights + b * a.weights_stride;
-    const int64_t room = min(min(a.max_pages * a.page_size, a.row_len), static_cast<int64_t>(1) << 30);
-    const int len = fp8_length(a.seq_lens[b], room, a.error_word, tid == 0);
-    const int n = fp8_length(min(len, a.keep), a.new_max_pages * a.page_size, a.error_word, tid == 0);
-    const int old = len - min(len, min(a.recent, n));  // tokens that may go
-    int left = n - (len - old);                        // of them stay
-    // the smallest key that stays, and how many of those equal to it
-    uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) count[tid] = 0;
+  const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
+  const float* w = a.weights + b * a.weights_stride;
+  const int64_t room = min(min(a.max_pages * a.page_size, a.row_len), static_cast<int64_t>(1) << 30);
+  const bool first = rank == 0 && tid == 0;
+  const int len = fp8_length(a.seq_lens[b], room, a.error_word, first);
+  const int n = fp8_length(min(len, a.keep), a.new_max_pages * a.page_size, a.error_word, first);
+  const int old = len - min(n, a.recent);  // tokens that may go (recent <= keep; a shorter new table keeps fewer)
+  int left = n - (len - old);              // of them stay
+  // this CTA's tokens, and its warps': consecutive ones, in 32s
+  const int per = ((len + ctas - 1) / ctas + kChoose - 1) / kChoose * kChoose;
+  const int t0 = min(rank * per, len), t1 = min(t0 + per, len), per_warp = per / kWarps;
+  auto key_of = [&](int t) { return t - t0 < kHeld ? held[t - t0] : rank_key(w[t]); };
+  for (int t = t0 + tid; t < min(t1, t0 + kHeld); t += kChoose) held[t - t0] = rank_key(w[t]);
+
+  // the smallest key that stays, and how many of those equal to it
+  uint32_t prefix = 0xFFFFFFFFu;  // (no weight's)
+  if (left > 0) {
+    prefix = 0;
+#pragma unroll 1
+    for (int round = 0; round < 4; ++round) {
+      const int shift = 24 - 8 * round;
+      const uint32_t mask = round == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (int i = tid; i < kWarps * 256; i += kChoose) hist[i] = 0;
       __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int t = tid; t < old; t += kChoose) {
-        const uint32_t k = rank_key(w[t]);
-        if ((k & mask) == prefix) atomicAdd(&count[k >> shift & 255], 1);
+      for (int t = t0 + tid; t < min(t1, old); t += kChoose) {
+        const uint32_t k = key_of(t);
+        if ((k & mask) == prefix) atomicAdd(&hist[warp * 256 + (k >> shift & 255)], 1);
       }
       __syncthreads();
-      if (tid == 0) {
-        int v = 255, l = left;
-        while (v > 0 && count[v] < l) l -= count[v--];
-        s_prefix = prefix | static_cast<uint32_t>(v) << shift;
-        s_left = l;
+      int* mine = total[round & 1];
+      if (tid < 256) {
+        int sum = 0;
+#pragma unroll 8
+        for (int i = 0; i < kWarps; ++i) sum += hist[i * 256 + tid];
+        mine[tid] = sum;
+      }
+      if (ctas > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      int count = 0, above = 0;  // weights with this byte; with a larger one
+      if (tid < 256) {
+        if (ctas > 1)
+          for (int c = 0; c < ctas; ++c) count += ld_cluster(&mine[tid], c);
+        else
+          count = mine[tid];
+        int incl = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_down_sync(0xffffffffu, incl, o);
+          if (lane + o < 32) incl += v;
+        }
+        if (lane == 0) upper[warp] = incl;
+        above = incl - count;
+      }
+      __syncthreads();
+      if (tid < 256) {
+        for (int i = warp + 1; i < 8; ++i) above += upper[i];
+        if (above < left && left <= above + count) {
+          s_prefix = prefix | static_cast<uint32_t>(tid) << shift;
+          s_left = left - above;
+        }
       }
       __syncthreads();
       prefix = s_prefix;
       left = s_left;
     }
-    // in order
-    int done = 0, equal = 0;
-    for (int base = 0; base < len; base += kChoose) {
-      const int t = base + tid;
-      const uint32_t k = t < old ? rank_key(w[t]) : 0;
-      const bool tie = t < old && k == prefix, above = t < len && (t >= old || k > prefix);
-      const uint32_t ties = __ballot_sync(0xffffffffu, tie);
-      if (lane == 0) warp_sum[0][warp] = __popc(ties);
-      __syncthreads();
-      int before = equal;
-      for (int i = 0; i < warp; ++i) before += warp_sum[0][i];
-      for (int i = 0; i < 32; ++i) equal += warp_sum[0][i];
-      const bool stays = above || (tie && before + __popc(ties & ((1u << lane) - 1)) < left);
-      const uint32_t all = __ballot_sync(0xffffffffu, stays);
-      if (lane == 0) warp_sum[1][warp] = __popc(all);
-      __syncthreads();
-      int at = done + __popc(all & ((1u << lane) - 1));
-      for (int i = 0; i < warp; ++i) at += warp_sum[1][i];
-      for (int i = 0; i < 32; ++i) done += warp_sum[1][i];
-      if (stays && at < n) {
-        a.kept[static_cast<int64_t>(b) * a.keep + at] = t;
-        if (a.new_weights != nullptr) a.new_weights[b * a.new_weights_stride + at] = w[t];
-      }
-    }
-    for (int i = n + tid; i < a.keep; i += kChoose) a.kept[static_cast<int64_t>(b) * a.keep + i] = -1;
-    if (a.new_weights != nullptr)
-      for (int64_t i = n + tid; i < a.new_row_len; i += kChoose) a.new_weights[b * a.new_weights_stride + i] = 0.f;
-    if (tid == 0) a.new_lens[b] = n;
-    __syncthreads();
   }
+
+  // Places in order: what stays before this CTA, before this warp, and in it.
+  const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
+  auto kind = [&](int t, bool& above, bool& tie) {  // of token t < w1
+    const uint32_t k = t < min(w1, old) ? key_of(t) : 0;
+    tie = t < min(w1, old) && k == prefix;
+    above = t < w1 && (t >= old || k > prefix);
+  };
+  __syncthreads();
+  int n_above = 0, n_tie = 0;
+  for (int t = w0; t < w1; t += 32) {
+    bool above, tie;
+    kind(t + lane, above, tie);
+    n_above += __popc(__ballot_sync(0xffffffffu, above));
+    n_tie += __popc(__ballot_sync(0xffffffffu, tie));
+  }
+  if (lane == 0) warp_counts[0][warp] = n_above, warp_counts[1][warp] = n_tie;
+  __syncthreads();
+  int before_above = 0, before_tie = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) before_above += warp_counts[0][i], before_tie += warp_counts[1][i];
+    n_above = i == 0 ? warp_counts[0][0] : n_above + warp_counts[0][i];
+    n_tie = i == 0 ? warp_counts[1][0] : n_tie + warp_counts[1][i];
+  }
+  if (ctas > 1) {
+    if (tid == 0) counts[0] = n_above, counts[1] = n_tie;
+    cluster_sync();
+    for (int c = 0; c < rank; ++c) before_above += ld_cluster(&counts[0], c), before_tie += ld_cluster(&counts[1], c);
+    cluster_sync();  // (the others' shared memory is read until here)
+  }
+  int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
+  float* new_w = a.new_weights != nullptr ? a.new_weights + b * a.new_weights_stride : nullptr;
+  for (int t = w0; t < w1; t += 32) {
+    bool above, tie;
+    kind(t + lane, above, tie);
+    const uint32_t ties = __ballot_sync(0xffffffffu, tie), under = (1u << lane) - 1;
+    const bool stays = above || (tie && before_tie + __popc(ties & under) < left);
+    const uint32_t aboves = __ballot_sync(0xffffffffu, above);
+    // ties before this token that stay: the first `left`
+    const int at = before_above + __popc(aboves & under) + min(left, before_tie + __popc(ties & under));
+    if (stays && at < n) {
+      kept[at] = t + lane;
+      if (new_w != nullptr) new_w[at] = w[t + lane];
+    }
+    before_above += __popc(aboves);
+    before_tie += __popc(ties);
+  }
+  for (int64_t i = n + rank * kChoose + tid; i < a.keep; i += ctas * kChoose) kept[i] = -1;
+  if (new_w != nullptr)
+    for (int64_t i = n + rank * kChoose + tid; i < a.new_row_len; i += ctas * kChoose) new_w[i] = 0.f;
+  if (first) a.new_lens[b] = n;
 }
 
-__global__ void __launch_bounds__(kMove) fp8_evict_move_kernel(const Fp8EvictArgs a, int blocks) {
+__global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8EvictArgs a, int blocks) {
   const int b = blockIdx.x / blocks, i = blockIdx.x % blocks, tid = threadIdx.x;
-  const int n = a.new_lens[b], rows = min(kBlock, n - i * kBlock);
+  const int rows = min(kBlock, a.new_lens[b] - i * kBlock);
   if (rows <= 0) return;
   __shared__ int64_t from[kBlock];
   __shared__ float scale[kBlock], most[kMove / 32];
@@ -100,35 +188,92 @@ __global__ void __launch_bounds__(kMove) fp8_evict_move_kernel(const Fp8EvictArg
     const bool good = s >= kFp8ScaleMin && s <= kFp8ScaleMax;
     if (!good) flag_error(a.error_word, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
     from[tid] = good ? slot + t % kBlock : -1;
-    scale[tid] = good ? s : 0.f;
+    scale[tid] = good ? s : 1.f;
   }
   __syncthreads();
-  auto value = [&](int r, int j) { return from[r] < 0 ? 0.f : e4m3_to_f32(a.cache[from[r] * kKey + j]) * scale[r]; };
-  float am = 0.f;
-  for (int e = tid; e < rows * kKey; e += kMove) am = fmaxf(am, fabsf(value(e / kKey, e % kKey)));
-  for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  if ((tid & 31) == 0) most[tid >> 5] = am;
-  __syncthreads();
-  for (int k = 0; k < kMove / 32; ++k) am = fmaxf(am, most[k]);
-  const float s = fp8_block_scale(am);
   const int64_t to = fp8_block_slot(a.new_page_table + b * a.new_pt_stride, i, a.page_size, a.num_slots);
   if (to < 0) {
     if (tid == 0) flag_error(a.error_word, MLA_DEVERR_BOUNDS);
     return;
   }
+  uint4 v[kUnits];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const int u = tid + j * kMove, r = u / (kKey / 16);
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (r < rows && from[r] >= 0)
+      v[j] = *reinterpret_cast<const uint4*>(a.cache + from[r] * kKey + u % (kKey / 16) * 16);
+  }
+  float am = 0.f;
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const int r = (tid + j * kMove) / (kKey / 16);
+    uint32_t m = 0;
+    const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t c = q[k] & 0x7F7F7F7Fu;
+      m = __vmaxu4(m, c & ~__vcmpeq4(c, 0x7F7F7F7Fu));  // (a NaN has no amax)
+    }
+    m = __vmaxu4(m, m >> 16);
+    m = max(m & 0xFFu, m >> 8 & 0xFFu);
+    if (r < rows) am = fmaxf(am, e4m3_to_f32(m) * scale[r]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  if ((tid & 31) == 0) most[tid >> 5] = am;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kMove / 32; ++k) am = fmaxf(am, most[k]);
+  const float s = fp8_block_scale(am), inv = 1.f / s;
   if (tid == 0) a.scales[to / kBlock] = s;
-  for (int e = tid; e < rows * kKey; e += kMove)
-    a.cache[to * kKey + e] = static_cast<uint8_t>(cvt_e4m3(value(e / kKey, e % kKey) * (1.f / s)));
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    const int u = tid + j * kMove, r = u / (kKey / 16);
+    if (r >= rows) break;
+    if (scale[r] != s) {
+      // exact for powers of two, but for results below 2^-6 (another scale's product is rounded to fp32 first)
+      const float ratio = scale[r] * inv;
+      uint32_t* q = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t out = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t h2 = e4m3x2_to_f16x2_pair(q[k] >> (16 * h));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          out |= cvt_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+        }
+        q[k] = out;
+      }
+    }
+    *reinterpret_cast<uint4*>(a.cache + to * kKey + 16 * u) = v[j];
+  }
 }
 
 }  // namespace
 
-int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream) {
+int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream, int num_sms) {
   const int blocks = (a.keep + kBlock - 1) / kBlock;
   if (static_cast<int64_t>(a.batch) * blocks > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
-  fp8_evict_choose_kernel<<<a.batch, kChoose, 0, stream>>>(a);
-  if (const int st = launch_status()) return st;
-  fp8_evict_move_kernel<<<a.batch * blocks, kMove, 0, stream>>>(a, blocks);
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_evict_choose_kernel), kChooseBytes, 36)) return st;
+  // a cluster a sequence, as large as the SMs and its tokens allow
+  const int64_t table = a.max_pages * a.page_size, row = a.row_len < table ? a.row_len : table;
+  int ctas = 1;
+  while (ctas < 8 && a.batch * static_cast<int64_t>(ctas) * 2 <= num_sms && row > static_cast<int64_t>(ctas) * kPart) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * ctas);
+  cfg.blockDim = dim3(kChoose);
+  cfg.dynamicSmemBytes = kChooseBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  if (const int st = cuda_status(cudaLaunchKernelEx(&cfg, fp8_evict_choose_kernel, a, ctas))) return st;
+  fp8_evict_move_kernel<<<static_cast<unsigned>(a.batch) * blocks, kMove, 0, stream>>>(a, blocks);
   return launch_status();
 }
 

@@ -291,7 +291,7 @@ struct Fp8EvictArgs {
   int64_t new_row_len;
   uint32_t* error_word;
 };
-int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream);
+int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream, int num_sms);
 
 int launch_fp8_quantize(const void* x, int64_t x_stride, int64_t M, int64_t K, uint8_t* codes, float* scales,
                         cudaStream_t stream);
