@@ -3,12 +3,11 @@
 //
 //   choose  a cluster a sequence, each CTA a part of its tokens, whose weights
 //           wait in shared memory as integers of their order.  The weight of rank
-//           n comes byte by byte: counts of a byte's values among the weights that
-//           agree above it (a histogram a warp, so that equal weights meet in a
-//           warp only; summed over the warps, then over the cluster by every CTA).
+//           n comes 11, 11 and 10 bits at a time: counts of their values among the
+//           weights that agree above them, summed over the cluster by every CTA.
 //           Then the tokens above it, and the first of those equal to it, find
-//           their places from counts of the warps and CTAs before.  Latency:
-//           four rounds of five barriers, about a microsecond each.
+//           their places from counts of the warps and CTAs before.  Bound by its
+//           chain of barriers.
 //   move    a CTA a new block of 64 tokens, all its rows in registers while the
 //           largest is found: HBM-bound.  Its scale follows the append's rule.
 #include <cuda_runtime.h>
@@ -23,7 +22,8 @@ constexpr int kBlock = MLA_FP8_BLOCK, kKey = kFp8Key;
 constexpr int kChoose = 1024, kWarps = kChoose / 32;
 constexpr int kHeld = 16384;          // weights in shared memory; the others of a longer part are read again
 constexpr int kPart = 2048;           // tokens a CTA of a cluster takes at least, where there are so many
-constexpr int kChooseBytes = (kHeld + kWarps * 256) * 4;
+constexpr int kBins = 2048;
+constexpr int kChooseBytes = kHeld * 4;
 constexpr int kMove = 256, kUnits = kBlock * kKey / 16 / kMove;  // 16-byte units a thread
 
 // Weights as integers of the same order; NaN comes first, -0 is 0.
@@ -36,6 +36,15 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+__device__ __forceinline__ int2 ld_cluster2(const int2* p, int rank) {
+  int2 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+      : "=r"(v.x), "=r"(v.y)
+      : "r"(sm100::smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 __device__ __forceinline__ int ld_cluster(const int* p, int rank) {
   int v;
   asm volatile(
@@ -47,12 +56,11 @@ __device__ __forceinline__ int ld_cluster(const int* p, int rank) {
 }
 
 __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8EvictArgs a, int ctas) {
-  extern __shared__ uint32_t held[];  // weights, then kWarps histograms
-  __shared__ int total[2][256];       // of this CTA, in turn
-  __shared__ int upper[8], counts[2], warp_counts[2][kWarps];
+  extern __shared__ uint32_t held[];  // weights
+  __shared__ alignas(16) int hist[2][kBins];  // of this CTA, in turn
+  __shared__ int upper[kWarps], counts[2], warp_counts[2][kWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
-  int* hist = reinterpret_cast<int*>(held + kHeld);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
   const float* w = a.weights + b * a.weights_stride;
@@ -66,56 +74,67 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   const int per = ((len + ctas - 1) / ctas + kChoose - 1) / kChoose * kChoose;
   const int t0 = min(rank * per, len), t1 = min(t0 + per, len), per_warp = per / kWarps;
   auto key_of = [&](int t) { return t - t0 < kHeld ? held[t - t0] : rank_key(w[t]); };
-  for (int t = t0 + tid; t < min(t1, t0 + kHeld); t += kChoose) held[t - t0] = rank_key(w[t]);
+  for (int base = 0; base < min(t1 - t0, kHeld); base += 8 * kChoose) {  // (all loads of eight in flight)
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = base + j * kChoose + tid;
+      v[j] = t0 + i < t1 && i < kHeld ? __ldg(w + t0 + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = base + j * kChoose + tid;
+      if (t0 + i < t1 && i < kHeld) held[i] = rank_key(v[j]);
+    }
+  }
 
   // the smallest key that stays, and how many of those equal to it
   uint32_t prefix = 0xFFFFFFFFu;  // (no weight's)
   if (left > 0) {
     prefix = 0;
 #pragma unroll 1
-    for (int round = 0; round < 4; ++round) {
-      const int shift = 24 - 8 * round;
-      const uint32_t mask = round == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int i = tid; i < kWarps * 256; i += kChoose) hist[i] = 0;
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bins = round == 2 ? 1024 : kBins;
+      const uint32_t mask = round == 0 ? 0u : round == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+      // thread i: bins 2 i and 2 i + 1
+      int2* mine = reinterpret_cast<int2*>(hist[round & 1]) + tid;
+      *mine = make_int2(0, 0);
       __syncthreads();
+#pragma unroll 4
       for (int t = t0 + tid; t < min(t1, old); t += kChoose) {
         const uint32_t k = key_of(t);
-        if ((k & mask) == prefix) atomicAdd(&hist[warp * 256 + (k >> shift & 255)], 1);
+        if ((k & mask) == prefix) atomicAdd(&hist[round & 1][k >> shift & (bins - 1)], 1);
       }
-      __syncthreads();
-      int* mine = total[round & 1];
-      if (tid < 256) {
-        int sum = 0;
-#pragma unroll 8
-        for (int i = 0; i < kWarps; ++i) sum += hist[i * 256 + tid];
-        mine[tid] = sum;
-      }
-      if (ctas > 1)
+      int2 count;
+      if (ctas > 1) {
         cluster_sync();
-      else
+        count = make_int2(0, 0);
+        for (int c = 0; c < ctas; ++c) {
+          const int2 v = ld_cluster2(mine, c);
+          count.x += v.x;
+          count.y += v.y;
+        }
+      } else {
         __syncthreads();
-      int count = 0, above = 0;  // weights with this byte; with a larger one
-      if (tid < 256) {
-        if (ctas > 1)
-          for (int c = 0; c < ctas; ++c) count += ld_cluster(&mine[tid], c);
-        else
-          count = mine[tid];
-        int incl = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_down_sync(0xffffffffu, incl, o);
-          if (lane + o < 32) incl += v;
-        }
-        if (lane == 0) upper[warp] = incl;
-        above = incl - count;
+        count = *mine;
       }
+      // weights in larger bins: of the warp, and of the warps above
+      int incl = count.x + count.y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_down_sync(0xffffffffu, incl, o);
+        if (lane + o < 32) incl += v;
+      }
+      if (lane == 0) upper[warp] = incl;
       __syncthreads();
-      if (tid < 256) {
-        for (int i = warp + 1; i < 8; ++i) above += upper[i];
-        if (above < left && left <= above + count) {
-          s_prefix = prefix | static_cast<uint32_t>(tid) << shift;
-          s_left = left - above;
-        }
+      const int above = __reduce_add_sync(0xffffffffu, lane > warp ? upper[lane] : 0) + incl - count.x - count.y;
+      const int more = above + count.y;  // for the lower of the two
+      if (above < left && left <= more) {
+        s_prefix = prefix | static_cast<uint32_t>(2 * tid + 1) << shift;
+        s_left = left - above;
+      } else if (more < left && left <= more + count.x) {
+        s_prefix = prefix | static_cast<uint32_t>(2 * tid) << shift;
+        s_left = left - more;
       }
       __syncthreads();
       prefix = s_prefix;
@@ -130,8 +149,8 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
     tie = t < min(w1, old) && k == prefix;
     above = t < w1 && (t >= old || k > prefix);
   };
-  __syncthreads();
   int n_above = 0, n_tie = 0;
+#pragma unroll 4
   for (int t = w0; t < w1; t += 32) {
     bool above, tie;
     kind(t + lane, above, tie);
@@ -140,62 +159,60 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   }
   if (lane == 0) warp_counts[0][warp] = n_above, warp_counts[1][warp] = n_tie;
   __syncthreads();
-  int before_above = 0, before_tie = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before_above += warp_counts[0][i], before_tie += warp_counts[1][i];
-    n_above = i == 0 ? warp_counts[0][0] : n_above + warp_counts[0][i];
-    n_tie = i == 0 ? warp_counts[1][0] : n_tie + warp_counts[1][i];
-  }
+  n_above = warp_counts[0][lane], n_tie = warp_counts[1][lane];
+  int before_above = __reduce_add_sync(0xffffffffu, lane < warp ? n_above : 0);
+  int before_tie = __reduce_add_sync(0xffffffffu, lane < warp ? n_tie : 0);
   if (ctas > 1) {
+    n_above = __reduce_add_sync(0xffffffffu, n_above), n_tie = __reduce_add_sync(0xffffffffu, n_tie);
     if (tid == 0) counts[0] = n_above, counts[1] = n_tie;
     cluster_sync();
-    for (int c = 0; c < rank; ++c) before_above += ld_cluster(&counts[0], c), before_tie += ld_cluster(&counts[1], c);
-    cluster_sync();  // (the others' shared memory is read until here)
+    before_above += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&counts[0], lane) : 0);
+    before_tie += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&counts[1], lane) : 0);
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   }
   int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
   float* new_w = a.new_weights != nullptr ? a.new_weights + b * a.new_weights_stride : nullptr;
-  for (int t = w0; t < w1; t += 32) {
-    bool above, tie;
-    kind(t + lane, above, tie);
-    const uint32_t ties = __ballot_sync(0xffffffffu, tie), under = (1u << lane) - 1;
-    const bool stays = above || (tie && before_tie + __popc(ties & under) < left);
-    const uint32_t aboves = __ballot_sync(0xffffffffu, above);
-    // ties before this token that stay: the first `left`
-    const int at = before_above + __popc(aboves & under) + min(left, before_tie + __popc(ties & under));
-    if (stays && at < n) {
-      kept[at] = t + lane;
-      if (new_w != nullptr) new_w[at] = w[t + lane];
+  for (int base = w0; base < w1; base += 128) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = new_w != nullptr && base + 32 * j + lane < w1 ? __ldg(w + base + 32 * j + lane) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = base + 32 * j + lane;
+      bool above, tie;
+      kind(t, above, tie);
+      const uint32_t ties = __ballot_sync(0xffffffffu, tie), aboves = __ballot_sync(0xffffffffu, above), under = (1u << lane) - 1;
+      const int ties_before = before_tie + __popc(ties & under);
+      // (of the ties the first `left` stay)
+      const int at = before_above + __popc(aboves & under) + min(left, ties_before);
+      if ((above || (tie && ties_before < left)) && at < n) {
+        kept[at] = t;
+        if (new_w != nullptr) new_w[at] = v[j];
+      }
+      before_above += __popc(aboves);
+      before_tie += __popc(ties);
     }
-    before_above += __popc(aboves);
-    before_tie += __popc(ties);
   }
   for (int64_t i = n + rank * kChoose + tid; i < a.keep; i += ctas * kChoose) kept[i] = -1;
   if (new_w != nullptr)
     for (int64_t i = n + rank * kChoose + tid; i < a.new_row_len; i += ctas * kChoose) new_w[i] = 0.f;
   if (first) a.new_lens[b] = n;
+  if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // (the others' shared memory is read until then)
 }
 
 __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8EvictArgs a, int blocks) {
   const int b = blockIdx.x / blocks, i = blockIdx.x % blocks, tid = threadIdx.x;
-  const int rows = min(kBlock, a.new_lens[b] - i * kBlock);
-  if (rows <= 0) return;
   __shared__ int64_t from[kBlock];
   __shared__ float scale[kBlock], most[kMove / 32];
-  if (tid < rows) {
-    const int t = a.kept[static_cast<int64_t>(b) * a.keep + i * kBlock + tid];
-    const int64_t slot = fp8_block_slot(a.page_table + b * a.pt_stride, t / kBlock, a.page_size, a.num_slots);
-    const float s = slot < 0 ? 0.f : a.scales[slot / kBlock];
-    const bool good = s >= kFp8ScaleMin && s <= kFp8ScaleMax;
-    if (!good) flag_error(a.error_word, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
-    from[tid] = good ? slot + t % kBlock : -1;
-    scale[tid] = good ? s : 1.f;
+  // a chain of loads: token, page, its rows; the scales come with those
+  const int at = i * kBlock + tid, t = tid < kBlock && at < a.keep ? a.kept[static_cast<int64_t>(b) * a.keep + at] : -1;
+  int64_t slot = -1;
+  if (t >= 0) {
+    slot = fp8_block_slot(a.page_table + b * a.pt_stride, t / kBlock, a.page_size, a.num_slots);
+    from[tid] = slot < 0 ? -1 : slot + t % kBlock;
   }
-  __syncthreads();
-  const int64_t to = fp8_block_slot(a.new_page_table + b * a.new_pt_stride, i, a.page_size, a.num_slots);
-  if (to < 0) {
-    if (tid == 0) flag_error(a.error_word, MLA_DEVERR_BOUNDS);
-    return;
-  }
+  const int rows = __syncthreads_count(t >= 0);
+  if (rows == 0) return;
   uint4 v[kUnits];
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
@@ -203,6 +220,18 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
     v[j] = make_uint4(0, 0, 0, 0);
     if (r < rows && from[r] >= 0)
       v[j] = *reinterpret_cast<const uint4*>(a.cache + from[r] * kKey + u % (kKey / 16) * 16);
+  }
+  const int64_t to = fp8_block_slot(a.new_page_table + b * a.new_pt_stride, i, a.page_size, a.num_slots);
+  if (t >= 0) {
+    const float s = slot < 0 ? 0.f : a.scales[slot / kBlock];
+    const bool good = s >= kFp8ScaleMin && s <= kFp8ScaleMax;
+    if (!good) flag_error(a.error_word, slot < 0 ? MLA_DEVERR_BOUNDS : MLA_DEVERR_SCALE);
+    scale[tid] = good ? s : 0.f;  // a key of zeros
+  }
+  __syncthreads();
+  if (to < 0) {
+    if (tid == 0) flag_error(a.error_word, MLA_DEVERR_BOUNDS);
+    return;
   }
   float am = 0.f;
 #pragma unroll
@@ -217,7 +246,10 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
     }
     m = __vmaxu4(m, m >> 16);
     m = max(m & 0xFFu, m >> 8 & 0xFFu);
-    if (r < rows) am = fmaxf(am, e4m3_to_f32(m) * scale[r]);
+    if (r < rows) {
+      if (scale[r] == 0.f) v[j] = make_uint4(0, 0, 0, 0);
+      am = fmaxf(am, e4m3_to_f32(m) * scale[r]);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
@@ -231,7 +263,7 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
   for (int j = 0; j < kUnits; ++j) {
     const int u = tid + j * kMove, r = u / (kKey / 16);
     if (r >= rows) break;
-    if (scale[r] != s) {
+    if (scale[r] != s && scale[r] != 0.f) {
       // exact for powers of two, but for results below 2^-6 (another scale's product is rounded to fp32 first)
       const float ratio = scale[r] * inv;
       uint32_t* q = reinterpret_cast<uint32_t*>(&v[j]);
