@@ -108,12 +108,12 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
       int2 count;
       if (ctas > 1) {
         cluster_sync();
+        int2 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = c < ctas ? ld_cluster2(mine, c) : make_int2(0, 0);
         count = make_int2(0, 0);
-        for (int c = 0; c < ctas; ++c) {
-          const int2 v = ld_cluster2(mine, c);
-          count.x += v.x;
-          count.y += v.y;
-        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) count.x += v[c].x, count.y += v[c].y;
       } else {
         __syncthreads();
         count = *mine;
@@ -200,6 +200,19 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // (the others' shared memory is read until then)
 }
 
+// |codes| of two bytes; codes times a factor, rounded again.
+__device__ __forceinline__ __half2 magnitudes(uint32_t two) {
+  const uint32_t h2 = e4m3x2_to_f16x2_pair(two);
+  return __habs2(*reinterpret_cast<const __half2*>(&h2));
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t two, __half2 by) {
+  const uint32_t h2 = e4m3x2_to_f16x2_pair(two);
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h2), by);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
+  return r;
+}
+
 __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8EvictArgs a, int blocks) {
   const int b = blockIdx.x / blocks, i = blockIdx.x % blocks, tid = threadIdx.x;
   __shared__ int64_t from[kBlock];
@@ -237,18 +250,13 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     const int r = (tid + j * kMove) / (kKey / 16);
-    uint32_t m = 0;
-    const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t c = q[k] & 0x7F7F7F7Fu;
-      m = __vmaxu4(m, c & ~__vcmpeq4(c, 0x7F7F7F7Fu));  // (a NaN has no amax)
-    }
-    m = __vmaxu4(m, m >> 16);
-    m = max(m & 0xFFu, m >> 8 & 0xFFu);
     if (r < rows) {
       if (scale[r] == 0.f) v[j] = make_uint4(0, 0, 0, 0);
-      am = fmaxf(am, e4m3_to_f32(m) * scale[r]);
+      const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      __half2 m = __float2half2_rn(0.f);  // (a NaN has no amax)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = __hmax2(m, __hmax2(magnitudes(q[k]), magnitudes(q[k] >> 16)));
+      am = fmaxf(am, fmaxf(__low2float(m), __high2float(m)) * scale[r]);
     }
   }
 #pragma unroll
@@ -263,20 +271,28 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
   for (int j = 0; j < kUnits; ++j) {
     const int u = tid + j * kMove, r = u / (kKey / 16);
     if (r >= rows) break;
-    if (scale[r] != s && scale[r] != 0.f) {
-      // exact for powers of two, but for results below 2^-6 (another scale's product is rounded to fp32 first)
-      const float ratio = scale[r] * inv;
+    const float ratio = scale[r] * inv;
+    if (ratio != 1.f && ratio != 0.f) {
       uint32_t* q = reinterpret_cast<uint32_t*>(&v[j]);
+      if ((__float_as_uint(ratio) & 0x7FFFFFu) == 0 && ratio <= 32768.f) {
+        // A power of two: products in f16, exact where e4m3 is not zero (codes have
+        // 4 significant bits; below 2^-24 the factor is zero, and so are they).
+        const __half2 by = __float2half2_rn(ratio);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t out = 0;
+        for (int k = 0; k < 4; ++k) q[k] = scaled(q[k], by) | scaled(q[k] >> 16, by) << 16;
+      } else {
+        // (a caller's own scale: the product is rounded to fp32 first)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t h2 = e4m3x2_to_f16x2_pair(q[k] >> (16 * h));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          out |= cvt_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t out = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t h2 = e4m3x2_to_f16x2_pair(q[k] >> (16 * h));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            out |= cvt_e4m3x2(f.x * ratio, f.y * ratio) << (16 * h);
+          }
+          q[k] = out;
         }
-        q[k] = out;
       }
     }
     *reinterpret_cast<uint4*>(a.cache + to * kKey + 16 * u) = v[j];
