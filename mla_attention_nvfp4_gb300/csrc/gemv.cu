@@ -23,6 +23,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "fp8.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
@@ -37,7 +39,9 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStep = 256;  // features a warp takes at a time: 64 a thread of a quad
 constexpr int kMinStages = 3, kMaxStages = 8;  // of weights in shared memory
 constexpr int kCtas = 2;                       // an SM
-constexpr uint32_t kShare = 110 * 1024;        // of an SM's shared memory for each of them
+constexpr uint32_t kShare = (222 / kCtas) * 1024;  // of an SM's shared memory for each of them
+constexpr uint32_t kLimit = 224 * 1024;        // of 227 KB, where a stage is large
+constexpr int kMaxSplits = 8;
 constexpr uint32_t kCodeBytes = 128 * (kStep / 2), kScaleBytes = 4 * 512;
 
 struct Params {
@@ -144,6 +148,20 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     bulk_load(dst + kCodeBytes, scales + static_cast<int64_t>(step) * 2048, tiles * 512, &full[slot]);
     issued = i + 1;
   };
+  if (tid == 0) {
+    abort = 0;
+    prefetch_tmap(&map);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_mbar_init();
+  }
+  // The next call's CTAs may take the place of those that end; nothing is read
+  // before the work ahead of this call is done.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
   // x, a chunk of stages at a time: a warp takes rows of steps (a chunk has a
   // row for each warp at least), 8 features a lane; a unit of 8 is piece u % 8 of
   // the quad's thread u / 8.
@@ -207,15 +225,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) read_ahead(next[d], d * chunk);
   if (tid == 0) {
-    abort = 0;
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    fence_mbar_init();
     for (int i = 0; i < p.stages && i < count; ++i) load(i);
   }
-
   stage_all(0, 0);
 
   float total[kTiles][4] = {};
@@ -338,18 +349,63 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (p.splits > 1) cluster_sync();  // (the others' shared memory is read until here)
 }
 
+// Clusters of each size that the current device holds at once, asked for once.
 template <int kPad>
-int launch(Params p, int64_t ctas, int64_t m_tiles, int slot, cudaStream_t stream) {
+int64_t resident_clusters(int splits, int num_sms) {
+  static std::atomic<int> known[64][kMaxSplits + 1];
+  int dev = 0;
+  if (splits == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return static_cast<int64_t>(num_sms) * kCtas / splits;
+  int n = known[dev][splits].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(splits * num_sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kShare;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad>, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = num_sms * kCtas / splits;
+    }
+    known[dev][splits].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int kPad>
+int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   const auto kern = nvfp4_gemv_kernel<kPad>;
+  static_assert(kMinStages * kCodeBytes >= kWarps * 16 * kPad * sizeof(float), "the sums fit in the stages of weights");
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLimit), slot)) return st;
+  const auto stage_bytes = [](int subs) { return kCodeBytes + subs * kScaleBytes; };
+  const auto x_bytes = [](int subs) { return 2u * (kPad * subs > kWarps ? kPad * subs : kWarps) * (kStep * 2); };
+
+  // Rows a CTA, and K's parts (a cluster of up to 8; a step a warp at least): the
+  // shortest time, as waves of the clusters that the SMs hold at once, each of a
+  // CTA's stages and of a start and an end that take about as long as four.
+  const int64_t steps = (p.a.K + kStep - 1) / kStep, m_tiles = (p.a.M + kPad - 1) / kPad, units = p.a.groups * p.tiles;
+  int64_t best_time = INT64_MAX, ctas = 0;
+  for (int log = 3; log >= 0; --log) {
+    const int subs = kWarps >> log;
+    if (x_bytes(subs) + kMinStages * stage_bytes(subs) > kLimit) break;
+    const int64_t stages = (steps + subs - 1) / subs;
+    for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
+      const int64_t held = resident_clusters<kPad>(s, num_sms), clusters = units * subs * m_tiles;
+      const int64_t time = (clusters + held - 1) / held * ((stages + s - 1) / s + 4);
+      if (time < best_time) best_time = time, ctas = units * subs * s, p.row_log = log, p.splits = s;
+    }
+  }
+  if (ctas > (int64_t(1) << 31) - 1 || m_tiles > 65535) return MLA_ERR_INVALID_ARG;
   const int subs = kWarps >> p.row_log;
-  const uint32_t stage = kCodeBytes + subs * kScaleBytes, x_bytes = 2 * (kPad * subs > kWarps ? kPad * subs : kWarps) * (kStep * 2);
-  p.stages = x_bytes + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x_bytes) / stage);
+  const uint32_t stage = stage_bytes(subs), x = x_bytes(subs);
+  p.row_stages = static_cast<int>((steps + subs - 1) / subs);
+  p.stages = x + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  static_assert(kMinStages * kCodeBytes >= kWarps * 16 * 16 * sizeof(float), "the sums fit in the stages of weights");
-  constexpr int kMost = kMinStages * (kCodeBytes + kWarps * kScaleBytes) + 2 * kWarps * (kPad > 1 ? kPad : 1) * (kStep * 2);
-  constexpr int kLimit = kMost > static_cast<int>(kShare) ? kMost : static_cast<int>(kShare);
-  static_assert(kLimit <= 232448 - 2048, "shared memory budget");
-  if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), kLimit, slot)) return st;
+
   CUtensorMap map;
   if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, 128, 16 << p.row_log, false)) {
     set_last_error("cuTensorMapEncodeTiled failed for the weights");
@@ -358,54 +414,32 @@ int launch(Params p, int64_t ctas, int64_t m_tiles, int slot, cudaStream_t strea
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(m_tiles));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = x_bytes + p.stages * stage;
+  cfg.dynamicSmemBytes = x + p.stages * stage;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, map, p));
 }
 
 }  // namespace
 
 int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
-  Params p;
+  Params p = {};
   p.a = a;
   p.tiles = static_cast<int>((a.N + 127) / 128);
-  const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
   p.k_tiles = (a.K / 16 + 3) / 4;
   p.scale_bytes = p.tiles * p.k_tiles * 512;
-  // All the rows of a tile a CTA (x is staged once a CTA) and K split over up to
-  // 8 CTAs, so that whole waves of CTAs fill the SMs; fewer rows where that leaves
-  // SMs without work.  A warp has a step of features at least.
-  int pad = 1;
-  while (pad < 16 && pad < a.M) pad *= 2;
-  const int64_t m_tiles = (a.M + pad - 1) / pad;
-  const int64_t slots = static_cast<int64_t>(num_sms) * kCtas;
-  const int64_t units = a.groups * p.tiles * m_tiles;
-  double best_share = 0;
-  int64_t best = 0;
-  for (int log = 3; log >= 0; --log) {
-    const int subs = kWarps >> log;
-    for (int s = 1; s <= 8 && (s == 1 || s * subs <= steps); ++s) {
-      const int64_t ctas = units * subs * s, waves = (ctas + slots - 1) / slots;
-      const double share = static_cast<double>(ctas) / static_cast<double>(waves * slots);
-      if (share > best_share * 1.05) best_share = share, best = ctas / m_tiles, p.row_log = log, p.splits = s;
-    }
-    if (best_share > 0.7) break;
-  }
-  if (best > (int64_t(1) << 31) - 1 || m_tiles > 65535) return MLA_ERR_INVALID_ARG;
-  p.row_stages = (steps + (kWarps >> p.row_log) - 1) >> (3 - p.row_log);
-  switch (pad) {
-    case 1: return launch<1>(p, best, m_tiles, 26, stream);
-    case 2: return launch<2>(p, best, m_tiles, 27, stream);
-    case 4: return launch<4>(p, best, m_tiles, 28, stream);
-    case 8: return launch<8>(p, best, m_tiles, 29, stream);
-    default: return launch<16>(p, best, m_tiles, 30, stream);
-  }
+  if (a.M <= 1) return launch<1>(p, 26, num_sms, stream);
+  if (a.M <= 2) return launch<2>(p, 27, num_sms, stream);
+  if (a.M <= 4) return launch<4>(p, 28, num_sms, stream);
+  if (a.M <= 8) return launch<8>(p, 29, num_sms, stream);
+  return launch<16>(p, 30, num_sms, stream);
 }
 
 }  // namespace mla
