@@ -37,18 +37,31 @@ using namespace sm100;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStep = 256;  // features a warp takes at a time: 64 a thread of a quad
-constexpr int kMinStages = 3, kMaxStages = 8;  // of weights in shared memory
-constexpr int kCtas = 2;                       // an SM
+constexpr int kMaxStages = 8;  // of weights in shared memory
+constexpr int kCtas = 2;       // an SM
 constexpr uint32_t kShare = (222 / kCtas) * 1024;  // of an SM's shared memory for each of them
-constexpr uint32_t kLimit = 224 * 1024;        // of 227 KB, where a stage is large
-constexpr int kMaxSplits = 8;
-constexpr uint32_t kCodeBytes = 128 * (kStep / 2), kScaleBytes = 4 * 512;
+constexpr uint32_t kLimit = 224 * 1024;            // of 227 KB, where a stage is large
+constexpr int kMaxSplits = 10;                     // (above 8: not portable, asked for)
+
+// kGroups: of 16 rows a warp, for which it reads x once.
+template <int kGroups>
+struct Cfg {
+  static constexpr int rows = 16 * kGroups * kWarps;  // of a row tile
+  static constexpr uint32_t code_bytes = rows * (kStep / 2);
+  static constexpr int log = kGroups == 2 ? 5 : 4;    // of a warp's rows
+  static constexpr int min_stages = kGroups == 2 ? 2 : 3;
+  // a stage's bytes, with 2^row_log warps that have rows of their own
+  static constexpr uint32_t stage(int row_log) {
+    return code_bytes + (kWarps >> row_log) * ((1 << (log + row_log)) > 128 ? 2u : 1u) * 2048u;
+  }
+};
 
 struct Params {
   GemvArgs a;
-  int row_log;    // 2^row_log warps with rows of their own, 16 each; the others take further steps of a stage
+  int row_log;    // 2^row_log warps with rows of their own; the others take further steps of a stage
   int splits;     // CTAs a cluster
-  int tiles;      // of 128 rows, a group
+  int tiles;      // of C::rows rows, a group
+  int sf_tiles;   // of 128 rows, a group
   int row_stages;  // of a whole row
   int stages;      // in shared memory
   int64_t k_tiles, scale_bytes;
@@ -107,9 +120,10 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
 }
 
 // kPad: rows of x a CTA takes, at most.
-template <int kPad>
+template <int kPad, int kGroups>
 __global__ void __launch_bounds__(kThreads, kCtas)
     nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
+  using C = Cfg<kGroups>;
   constexpr int kTiles = kPad > 8 ? 2 : 1;  // groups of 8 columns of the products
   constexpr int kXStep = kPad * kStep * 2;  // bytes of x a step
   extern __shared__ __align__(1024) uint8_t smem[];  // stages of weights, two chunks of x; then the CTA's sums
@@ -117,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
   __shared__ volatile int abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, t = lane & 3;
-  const int row_warps = 1 << p.row_log, subs = kWarps >> p.row_log, cta_rows = 16 << p.row_log;
+  const int row_warps = 1 << p.row_log, subs = kWarps >> p.row_log, cta_rows = 1 << (C::log + p.row_log);
   uint32_t id = blockIdx.x / p.splits;
   const int split = blockIdx.x - id * p.splits;
   const int sub = id & (subs - 1);
@@ -128,24 +142,28 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int rows = static_cast<int>(p.a.M - m0 < kPad ? p.a.M - m0 : kPad);
   const int row_warp = warp & (row_warps - 1), k_warp = warp >> p.row_log;
   const int first = p.row_stages * split / p.splits, count = p.row_stages * (split + 1) / p.splits - first;  // count >= 1
-  const uint32_t stage_bytes = kCodeBytes + subs * kScaleBytes;
+  const int sf_tiles = cta_rows > 128 ? 2 : 1;  // this CTA's rows are of
+  const uint32_t stage_bytes = C::code_bytes + sf_tiles * subs * 2048;
   const uint32_t base = smem_u32(smem), x_base = base + p.stages * stage_bytes;
 
   // Weights: lines of 128 bytes, step by step the CTA's rows, their 16-byte
   // pieces swizzled by the row (rows past the matrix: zeros, or the next group's);
   // then the steps' scales as they lie.
-  const int64_t n0 = static_cast<int64_t>(tile) * 128 + sub * cta_rows;
-  const uint8_t* scales = p.a.w_scales + g * p.scale_bytes + tile * p.k_tiles * 512;
+  const int64_t n0 = static_cast<int64_t>(tile) * C::rows + sub * cta_rows;
+  const int sf_there = static_cast<int>(min(p.sf_tiles - n0 / 128, static_cast<int64_t>(sf_tiles)));
+  const uint8_t* scales = p.a.w_scales + g * p.scale_bytes + n0 / 128 * p.k_tiles * 512;
   int issued = 0;
   auto load = [&](int i) {  // by one thread
     const int slot = i % p.stages, step = (first + i) * subs;
     const uint32_t dst = base + slot * stage_bytes;
     const int64_t left = p.k_tiles - static_cast<int64_t>(step) * 4;  // tiles of 4 blocks
     const int tiles = left < 4 * subs ? static_cast<int>(left) : 4 * subs;
-    mbar_expect_tx(&full[slot], kCodeBytes + tiles * 512);
+    mbar_expect_tx(&full[slot], C::code_bytes + max(sf_there, 0) * tiles * 512);
     for (int k = 0; k < subs; ++k)
       tma_load_bytes(dst + k * (cta_rows * 128), &map, (step + k) * (kStep / 2), static_cast<int>(g * p.a.N + n0), &full[slot]);
-    bulk_load(dst + kCodeBytes, scales + static_cast<int64_t>(step) * 2048, tiles * 512, &full[slot]);
+    for (int k = 0; k < sf_there; ++k)
+      bulk_load(dst + C::code_bytes + k * subs * 2048, scales + (k * p.k_tiles + static_cast<int64_t>(step) * 4) * 512, tiles * 512,
+                &full[slot]);
     issued = i + 1;
   };
   if (tid == 0) {
@@ -229,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   stage_all(0, 0);
 
-  float total[kTiles][4] = {};
+  float total[kGroups][kTiles][4] = {};
   // where this thread's weights, scales and x lie in a stage
-  const int r0 = row_warp * 16 + quad, line0 = k_warp * cta_rows + r0, in_tile = sub * cta_rows + r0;
+  const int r0 = row_warp * (16 * kGroups) + quad, line0 = k_warp * cta_rows + r0, in_tile = (sub * cta_rows + r0) & 127;
   const uint32_t code_at = base + line0 * 128 + (((2 * t) ^ (line0 & 7)) << 4);
-  const uint32_t scale_at = base + kCodeBytes + k_warp * kScaleBytes + t * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
-  const uint32_t scale_next = ((in_tile + 8) & 31) * 16 + ((in_tile + 8) >> 5) * 4 - (in_tile & 31) * 16 - (in_tile >> 5) * 4;
+  // (a warp's rows are some of 32 whose scales are 16 bytes apart)
+  const uint32_t scale_at = base + C::code_bytes + ((r0 >> 7) * subs + k_warp) * 2048 + t * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
   uint32_t x_at[kTiles];
 #pragma unroll
   for (int c = 0; c < kTiles; ++c)  // (columns past the rows are whatever they are, and not written)
@@ -252,43 +270,57 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       mbar_wait(&full[slot], phase, p.a.error_word, &abort);
       const uint32_t at = slot * stage_bytes, in_chunk = (buffer * chunk + i - i0) * subs;
       const uint32_t x_in = in_chunk * kXStep;
-      uint32_t lo = lds32(scale_at + at), hi = lds32(scale_at + at + scale_next);
+      uint32_t sf[2 * kGroups];  // of rows r0, r0 + 8, ..
+#pragma unroll
+      for (int r = 0; r < 2 * kGroups; ++r) sf[r] = lds32(scale_at + at + 128 * r);
       const int block = ((first + i) * subs + k_warp) * 16 + 4 * t;
       if (block + 4 > blocks) {  // the last four blocks of a row may be two, or none (the padding may hold NaN)
         const uint32_t mask = blocks - block == 2 ? 0xFFFFu : 0u;
-        lo &= mask;
-        hi &= mask;
+#pragma unroll
+        for (int r = 0; r < 2 * kGroups; ++r) sf[r] &= mask;
       }
-      const uint32_t sc[2][2] = {{e4m3x2_to_f16x2_pair(lo), e4m3x2_to_f16x2_pair(lo >> 16)},
-                                 {e4m3x2_to_f16x2_pair(hi), e4m3x2_to_f16x2_pair(hi >> 16)}};  // of two blocks each
-      float acc[kTiles][4] = {};
+      float acc[kGroups][kTiles][4] = {};
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2) {  // two blocks of 16
-        uint4 v[2];
+        uint4 v[2 * kGroups];
+        uint32_t sc[2 * kGroups];  // f16 pairs of their scales
 #pragma unroll
-        for (int r = 0; r < 2; ++r) v[r] = lds128((code_at ^ (b2 << 4)) + at + r * 1024);
+        for (int r = 0; r < 2 * kGroups; ++r) {
+          v[r] = lds128((code_at ^ (b2 << 4)) + at + r * 1024);
+          sc[r] = e4m3x2_to_f16x2_pair(sf[r] >> (16 * b2));
+        }
 #pragma unroll
         for (int b1 = 0; b1 < 2; ++b1) {
-          uint32_t a[2][8];
+          uint4 u[kTiles][2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t s2 = __byte_perm(sc[r][b2], 0, b1 ? 0x3232 : 0x1010);
-            uint32_t h[4];
-            codes_to_f16(b1 ? v[r].z : v[r].x, h);
+          for (int c = 0; c < kTiles; ++c)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[r][j] = h2_mul(h[j], s2);
-            codes_to_f16(b1 ? v[r].w : v[r].y, h);
+            for (int half = 0; half < 2; ++half)
+              u[c][half] = lds128(x_at[c] + x_in + (4 * b2 + 2 * b1 + half) * (64 * kPad));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[r][4 + j] = h2_mul(h[j], s2);
-          }
+          for (int gr = 0; gr < kGroups; ++gr) {
+            uint32_t a[2][8];
 #pragma unroll
-          for (int c = 0; c < kTiles; ++c) {
+            for (int r = 0; r < 2; ++r) {
+              const uint4 w = v[2 * gr + r];
+              const uint32_t s2 = __byte_perm(sc[2 * gr + r], 0, b1 ? 0x3232 : 0x1010);
+              uint32_t h[4];
+              codes_to_f16(b1 ? w.z : w.x, h);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint4 u = lds128(x_at[c] + x_in + (4 * b2 + 2 * b1 + half) * (64 * kPad));
-              mma_f16(acc[c], a[0][4 * half], a[1][4 * half], a[0][4 * half + 1], a[1][4 * half + 1], u.x, u.y);
-              mma_f16(acc[c], a[0][4 * half + 2], a[1][4 * half + 2], a[0][4 * half + 3], a[1][4 * half + 3], u.z, u.w);
+              for (int j = 0; j < 4; ++j) a[r][j] = h2_mul(h[j], s2);
+              codes_to_f16(b1 ? w.w : w.y, h);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[r][4 + j] = h2_mul(h[j], s2);
             }
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                mma_f16(acc[gr][c], a[0][4 * half], a[1][4 * half], a[0][4 * half + 1], a[1][4 * half + 1], u[c][half].x,
+                        u[c][half].y);
+                mma_f16(acc[gr][c], a[0][4 * half + 2], a[1][4 * half + 2], a[0][4 * half + 3], a[1][4 * half + 3],
+                        u[c][half].z, u[c][half].w);
+              }
           }
         }
       }
@@ -297,9 +329,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
       for (int c = 0; c < kTiles; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = 8 * c + 2 * t + (j & 1);
-          total[c][j] = fmaf(acc[c][j], factor[buffer][(i - i0) * subs + k_warp][min(col, kPad - 1)], total[c][j]);
+        for (int j = 0; j < 2; ++j) {
+          const float f = factor[buffer][(i - i0) * subs + k_warp][min(8 * c + 2 * t + j, kPad - 1)];
+#pragma unroll
+          for (int gr = 0; gr < kGroups; ++gr) {
+            total[gr][c][j] = fmaf(acc[gr][c][j], f, total[gr][c][j]);
+            total[gr][c][j + 2] = fmaf(acc[gr][c][j + 2], f, total[gr][c][j + 2]);
+          }
         }
       // the stage before is free once all warps have read it
       if (tid == 0 && i > 0 && i - 1 + p.stages < count) {
@@ -323,7 +359,11 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = 8 * c + 2 * t + (j & 1);
-      if (col < rows) sums[k_warp * pairs + col * cta_rows + r0 + 8 * (j >> 1)] = total[c][j];
+      if (col < rows) {
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr)
+          sums[k_warp * pairs + col * cta_rows + r0 + 16 * gr + 8 * (j >> 1)] = total[gr][c][j];
+      }
     }
   __syncthreads();
   if (subs > 1 && p.splits > 1) {
@@ -337,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const float gs = *p.a.gs_w;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + m0 * p.a.out_sm + g * p.a.out_sg + n0;
   for (int e = split * kThreads + tid; e < pairs; e += p.splits * kThreads) {
-    const int col = e >> (4 + p.row_log), r = e & (cta_rows - 1);
+    const int col = e >> (C::log + p.row_log), r = e & (cta_rows - 1);
     float v = 0.f;
     if (p.splits > 1) {
       for (int k = 0; k < p.splits; ++k) v += ld_cluster(base + 4 * e, k);
@@ -350,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 }
 
 // Clusters of each size that the current device holds at once, asked for once.
-template <int kPad>
+template <int kPad, int kGroups>
 int64_t resident_clusters(int splits, int num_sms) {
   static std::atomic<int> known[64][kMaxSplits + 1];
   int dev = 0;
@@ -367,22 +407,25 @@ int64_t resident_clusters(int splits, int num_sms) {
     cfg.dynamicSmemBytes = kShare;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad>, &cfg) != cudaSuccess || n < 1) {
+    if ((splits > 8 && cudaFuncSetAttribute(nvfp4_gemv_kernel<kPad, kGroups>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad, kGroups>, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
-      n = num_sms * kCtas / splits;
+      n = splits > 8 ? -1 : num_sms * kCtas / splits;  // -1: none
     }
     known[dev][splits].store(n, std::memory_order_relaxed);
   }
   return n;
 }
 
-template <int kPad>
+template <int kPad, int kGroups>
 int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
-  const auto kern = nvfp4_gemv_kernel<kPad>;
-  static_assert(kMinStages * kCodeBytes >= kWarps * 16 * kPad * sizeof(float), "the sums fit in the stages of weights");
+  using C = Cfg<kGroups>;
+  const auto kern = nvfp4_gemv_kernel<kPad, kGroups>;
+  static_assert(C::min_stages * C::code_bytes >= C::rows * kPad * sizeof(float), "the sums fit in the stages of weights");
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLimit), slot)) return st;
-  const auto stage_bytes = [](int subs) { return kCodeBytes + subs * kScaleBytes; };
   const auto x_bytes = [](int subs) { return 2u * (kPad * subs > kWarps ? kPad * subs : kWarps) * (kStep * 2); };
+
+  p.tiles = static_cast<int>((p.a.N + C::rows - 1) / C::rows);
 
   // Rows a CTA, and K's parts (a cluster of up to 8; a step a warp at least): the
   // shortest time, as waves of the clusters that the SMs hold at once, each of a
@@ -391,23 +434,24 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   int64_t best_time = INT64_MAX, ctas = 0;
   for (int log = 3; log >= 0; --log) {
     const int subs = kWarps >> log;
-    if (x_bytes(subs) + kMinStages * stage_bytes(subs) > kLimit) break;
+    if (x_bytes(subs) + C::min_stages * C::stage(log) > kLimit) break;
     const int64_t stages = (steps + subs - 1) / subs;
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
-      const int64_t held = resident_clusters<kPad>(s, num_sms), clusters = units * subs * m_tiles;
+      const int64_t held = resident_clusters<kPad, kGroups>(s, num_sms), clusters = units * subs * m_tiles;
+      if (held < 1) continue;
       const int64_t time = (clusters + held - 1) / held * ((stages + s - 1) / s + 4);
       if (time < best_time) best_time = time, ctas = units * subs * s, p.row_log = log, p.splits = s;
     }
   }
   if (ctas > (int64_t(1) << 31) - 1 || m_tiles > 65535) return MLA_ERR_INVALID_ARG;
   const int subs = kWarps >> p.row_log;
-  const uint32_t stage = stage_bytes(subs), x = x_bytes(subs);
+  const uint32_t stage = C::stage(p.row_log), x = x_bytes(subs);
   p.row_stages = static_cast<int>((steps + subs - 1) / subs);
-  p.stages = x + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x) / stage);
+  p.stages = x + C::min_stages * stage >= kShare ? C::min_stages : static_cast<int>((kShare - x) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
 
   CUtensorMap map;
-  if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, 128, 16 << p.row_log, false)) {
+  if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, 128, 1 << (C::log + p.row_log), false)) {
     set_last_error("cuTensorMapEncodeTiled failed for the weights");
     return MLA_ERR_LAUNCH;
   }
@@ -432,14 +476,20 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
 int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
   Params p = {};
   p.a = a;
-  p.tiles = static_cast<int>((a.N + 127) / 128);
+  p.sf_tiles = static_cast<int>((a.N + 127) / 128);
   p.k_tiles = (a.K / 16 + 3) / 4;
-  p.scale_bytes = p.tiles * p.k_tiles * 512;
-  if (a.M <= 1) return launch<1>(p, 26, num_sms, stream);
-  if (a.M <= 2) return launch<2>(p, 27, num_sms, stream);
-  if (a.M <= 4) return launch<4>(p, 28, num_sms, stream);
-  if (a.M <= 8) return launch<8>(p, 29, num_sms, stream);
-  return launch<16>(p, 30, num_sms, stream);
+  p.scale_bytes = p.sf_tiles * p.k_tiles * 512;
+  // Two groups of 16 rows a warp where x is much (more than 8 rows) or a row of
+  // weights a stage or two, so that few CTAs and not the depth of the ring count:
+  // 16 x 7168 x 16384 27.3 us, not 28.5; 4 x 128 heads x 512 x 128 4.8, not 6.4.
+  // One where three and more stages are to be in flight: 1 x 7168 x 16384 18.2 us,
+  // not 23.4; 1 x 576 x 7168 4.0, not 4.5.
+  const bool two = a.K <= 2 * kStep;
+  if (a.M <= 1) return two ? launch<1, 2>(p, 26, num_sms, stream) : launch<1, 1>(p, 27, num_sms, stream);
+  if (a.M <= 2) return two ? launch<2, 2>(p, 28, num_sms, stream) : launch<2, 1>(p, 29, num_sms, stream);
+  if (a.M <= 4) return two ? launch<4, 2>(p, 30, num_sms, stream) : launch<4, 1>(p, 31, num_sms, stream);
+  if (a.M <= 8) return two ? launch<8, 2>(p, 37, num_sms, stream) : launch<8, 1>(p, 38, num_sms, stream);
+  return launch<16, 2>(p, 39, num_sms, stream);
 }
 
 }  // namespace mla
