@@ -5,9 +5,12 @@
 // The decode's score product alone, on tcgen05: tiles of 128 keys x 576
 // features arrive by TMA as they lie and are the 128-row operand, the queries'
 // two e4m3 terms (fp8_query.cuh) the other, so that a key is a TMEM lane and
-// the sum over the heads stays in its thread.  HBM-bound: all heads (up to 128,
-// two terms each: 256 columns) meet a tile while it is there, and no result of
-// one tile is needed by another.  More heads take a launch each 128.
+// the sum over the heads stays in its thread.  HBM-bound: all heads meet a tile
+// while it is there, and no result of one tile is needed by another.  Up to 64
+// heads are one CTA's; up to 128 a pair's (a cluster of two), each CTA of which
+// loads one of a tile's two blocks for both, and the second sends its sums to the
+// first.  (All 128 in one CTA leave room for one tile: 64 x 4096 keys 46.5 us.)
+// More heads take a launch each 128.
 //
 // One CTA per SM, persistent over an equal part of the batch's tiles (and of
 // its pieces' starts, a sequence's queries being converted anew):
@@ -32,9 +35,9 @@ using namespace sm100;
 
 constexpr int kKey = kFp8Key, kBlock = MLA_FP8_BLOCK, kTile = 128;
 // Groups of four warps that take a tile each in turn: two keep up with the
-// tiles; with 64 heads and more the queries want four.
+// tiles; with 64 heads the queries want four.
 template <int kH>
-constexpr int kGroups = kH >= 64 ? 4 : 2;
+constexpr int kGroups = kH == 64 ? 4 : 2;
 template <int kH>
 constexpr int kThreads = 64 + 128 * kGroups<kH>;
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64, kTileBytes = 4 * kChunkBytes + kRopeBytes;
@@ -43,7 +46,7 @@ constexpr int kInfo = 4;   // tiles whose scales are kept
 
 template <int kH>
 struct Cfg {
-  static constexpr int tiles = kH == 128 ? 1 : 2;  // in shared memory
+  static constexpr int tiles = 2;  // in shared memory
   static constexpr int slots = 5 * tiles;          // chunks of them
   static constexpr uint32_t off_rope = 4 * tiles * kChunkBytes, off_q = tiles * kTileBytes;
   static constexpr uint32_t off_misc = off_q + 2 * kH * kKey;
@@ -56,6 +59,9 @@ struct Misc {
   uint64_t s_full[2], s_free[2], q_ready, q_free, retired;
   alignas(16) float2 head[2][kH];  // of a piece, in turn: factor of its scores, log2(e) lse
   float scale[kInfo][2];           // of a tile's two blocks; 0: none of the sequence's
+  // Pair: the second CTA's sums of a tile, one place a group; theirs to read, to write.
+  uint64_t peer_full[kGroups<kH>], peer_free[kGroups<kH>];
+  float peer[kGroups<kH>][kTile];
   int64_t scan[kThreads<kH> / 32], t0, t1, off0;
   int b0;
   uint32_t tmem;
@@ -67,7 +73,7 @@ template <int kH>
 constexpr uint32_t smem_bytes() {
   return Cfg<kH>::off_misc + static_cast<uint32_t>(sizeof(Misc<kH>));
 }
-static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
+static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
 
 struct Params {
   Fp8WeightsArgs a;
@@ -125,7 +131,7 @@ struct Pieces {
 
 // This CTA's part of the sequences' costs, and its first sequence.
 template <int kThreads, class M>
-__device__ __forceinline__ void make_plan(const Params& p, M& ms) {
+__device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int parts) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
   const int per_thread = (B + kThreads - 1) / kThreads;
   const int first = min(tid * per_thread, B), last = min(first + per_thread, B);
@@ -149,7 +155,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms) {
     if (i < warp) off += ms.scan[i];
     total += ms.scan[i];
   }
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * per;
+  const int64_t per = (total + parts - 1) / parts, t0 = part * per;
   if (tid == 0) {
     ms.t0 = t0;
     ms.t1 = t0 + per < total ? t0 + per : total;
@@ -165,7 +171,46 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms) {
   }
 }
 
-template <int kH>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Of the other CTA of a pair.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// mbar_wait for arrivals of the other CTA, whose writes before them are seen (by
+// a second look, of the cluster's scope).
+__device__ __forceinline__ void peer_wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
+  mbar_wait(bar, parity, err, abort);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(parity)
+      : "memory");
+}
+// A copy into, and an arrival on a barrier of, both CTAs of a pair.
+__device__ __forceinline__ void tma_load_bytes_pair(uint32_t dst, const void* tmap, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
+      "[%4], %5;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+template <int kH, bool kPair>
 __global__ void __launch_bounds__(kThreads<kH>, 1)
     fp8_key_weights_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                            const __grid_constant__ Params p) {
@@ -175,7 +220,8 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
   Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = min(kH, p.a.num_heads - p.h0);
+  const int rank = kPair ? blockIdx.x & 1 : 0, part = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int h0 = p.h0 + rank * kH, heads = min(kH, p.a.num_heads - h0);
   uint32_t* err = p.a.error_word;
 
   if (threadIdx.x == 0) {
@@ -184,7 +230,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     ms.off0 = 0;
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(&ms.full[i], 1);
-      mbar_init(&ms.empty[i], 1);
+      mbar_init(&ms.empty[i], kPair ? 2 : 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(&ms.info_full[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -194,6 +240,10 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     mbar_init(&ms.q_ready, kQueryWarps);
     mbar_init(&ms.q_free, 1);
     mbar_init(&ms.retired, 1);
+    for (int i = 0; i < kGroups<kH>; ++i) {
+      mbar_init(&ms.peer_full[i], 4);
+      mbar_init(&ms.peer_free[i], 4);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -201,9 +251,10 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     tmem_relinquish();
   }
   __syncthreads();  // (b0 is set before the plan)
-  make_plan<kThreads<kH>>(p, ms);
+  make_plan<kThreads<kH>>(p, ms, part, kPair ? gridDim.x >> 1 : gridDim.x);
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // (the barriers of both are set)
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
   // chunk c of tile n (4: the RoPE)
@@ -241,20 +292,23 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
           scale = there ? p.a.scales[slot / kBlock] : 0.f;
         }
         const int y0 = __shfl_sync(0xffffffffu, y, at), y1 = __shfl_sync(0xffffffffu, y, at + 1);
-        if (lane == 0) {
-#pragma unroll 1
-          for (int c = 0; c < 5; ++c) {
-            const int i = n % C::tiles * 5 + c;
-            ok = mbar_wait(&ms.empty[i], ((n / C::tiles) & 1) ^ 1, err, &ms.abort);
-            if (!ok) break;
+        if (lane < 5) {  // a chunk a lane
+          const int c = lane, i = n % C::tiles * 5 + c;
+          ok = mbar_wait(&ms.empty[i], ((n / C::tiles) & 1) ^ 1, err, &ms.abort);
+          if (ok) {
             const uint32_t bytes = c < 4 ? kChunkBytes : kRopeBytes, dst = slot_addr(n, c);
             const CUtensorMap* map = c < 4 ? &tm_lat : &tm_rope;
             mbar_expect_tx(&ms.full[i], bytes);
-            tma_load_bytes(dst, map, 128 * c, y0, &ms.full[i]);
-            tma_load_bytes(dst + bytes / 2, map, 128 * c, y1, &ms.full[i]);
+            if constexpr (kPair) {  // (the place is free in both)
+              tma_load_bytes_pair(dst + rank * (bytes / 2), map, 128 * c, rank == 0 ? y0 : y1, &ms.full[i]);
+            } else {
+              tma_load_bytes(dst, map, 128 * c, y0, &ms.full[i]);
+              tma_load_bytes(dst + bytes / 2, map, 128 * c, y1, &ms.full[i]);
+            }
             ++copies;
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
         // the scales (waited for after the copies); the place of tile n - 4,
         // whose sums are done: this tile's chunks took those of a later one
         if (at == 0) {
@@ -274,46 +328,48 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     if (lane == 0) ms.copies = copies;
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
+    // The loop is short: all chunks in one copy, descriptors by additions, and
+    // what a wait says told to the warp once a tile (products of chunks that never
+    // came are never read; with a vote a chunk the issue took a microsecond a tile).
     constexpr uint32_t idesc = idesc_e4m3(128, 2 * kH, false, false);
-    const uint64_t dq = smem_desc_sw128(s0 + C::off_q, 0, 1024);
-    const uint64_t dq_rope = smem_desc_sw64(s0 + C::off_q + 4 * 2 * kH * 128, 512);
+    const uint64_t dq = smem_desc_sw128(s0 + C::off_q, 0, 1024), dk = smem_desc_sw128(s0, 0, 1024);
+    const uint64_t dq_rope = smem_desc_sw64(s0 + C::off_q + 4 * 2 * kH * 128, 512), dk_rope = smem_desc_sw64(s0 + C::off_rope, 512);
+    auto ready = [&](uint64_t* bar, int parity) { return mbar_test(bar, parity) || mbar_wait(bar, parity, err, &ms.abort); };
     bool ok = true;
-    auto ready = [&](uint64_t* bar, int parity) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, err, &ms.abort));
-      return ok;
-    };
     int n = 0, piece = 0;
     for (Pieces it(p, ms); ok && it.next(p); ++piece) {
-      if (!ready(&ms.q_ready, piece & 1)) break;
+      ok = __all_sync(0xffffffffu, ready(&ms.q_ready, piece & 1));
+      tc_fence_after();
 #pragma unroll 1
-      for (int t = it.s; t < it.e; ++t, ++n) {
-        const uint32_t d = uniform(tmem + (n & 1) * 2 * kH);
-        if (!ready(&ms.s_free[n & 1], ((n >> 1) & 1) ^ 1)) break;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int i = uniform(n % C::tiles * 5 + c);
-          if (!ready(&ms.full[i], (n / C::tiles) & 1)) break;
-          tc_fence_after();
-          const uint64_t da = smem_desc_sw128(uniform(slot_addr(n, c)), 0, 1024), db = dq + uniform(c) * (2 * kH * 128 >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
-            mma_commit(&ms.empty[i]);
-          }
-          __syncwarp();
-        }
-        const int i = uniform(n % C::tiles * 5 + 4);
-        if (!ready(&ms.full[i], (n / C::tiles) & 1)) break;
+      for (int t = it.s; ok && t < it.e; ++t, ++n) {
+        const int half = uniform(n & 1);
+        static_assert(C::tiles == 2, "tile n in place n & 1");
+        const uint32_t d = tmem + half * 2 * kH;
+        ok = ready(&ms.s_free[half], ((n >> 1) & 1) ^ 1);
         tc_fence_after();
-        const uint64_t da = smem_desc_sw64(uniform(slot_addr(n, 4)), 512);
-        if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, dq_rope + 2 * j, idesc, 1u);
-          mma_commit(&ms.empty[i]);
-          mma_commit(&ms.s_full[n & 1]);
-          if (t + 1 == it.e) mma_commit(&ms.q_free);
+        for (int c = 0; c < 5; ++c) {
+          uint64_t* empty = &ms.empty[5 * half + c];
+          ok &= ready(&ms.full[5 * half + c], (n >> 1) & 1);
+          __syncwarp();
+          if (elect_one()) {
+            if (c < 4) {
+              const uint64_t da = dk + (4 * half + c) * (kChunkBytes >> 4), db = dq + c * (2 * kH * 128 >> 4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
+            } else {
+              const uint64_t da = dk_rope + half * (kRopeBytes >> 4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, dq_rope + 2 * j, idesc, 1u);
+            }
+            kPair ? mma_commit_pair(empty) : mma_commit(empty);
+            if (c == 4) {
+              mma_commit(&ms.s_full[half]);
+              if (t + 1 == it.e) mma_commit(&ms.q_free);
+            }
+          }
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
       }
     }
     retire_products(&ms.retired, err);
@@ -326,7 +382,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     int n = 0, piece = 0;
     for (Pieces it(p, ms); it.next(p); ++piece) {
       const int b = it.b, len = it.len;
-      const int64_t row0 = static_cast<int64_t>(b) * p.a.num_heads + p.h0;
+      const int64_t row0 = static_cast<int64_t>(b) * p.a.num_heads + h0;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + row0 * kKey;
       float2* head = ms.head[piece & 1];
       auto load_head = [&](int h, uint4(&v)[3]) {
@@ -361,7 +417,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
         if (n % kGroups<kH> != group) continue;
         const int at = t * kTile + key;
         float before = 0.f;
-        if (p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
+        if (rank == 0 && p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
         mbar_wait(&ms.info_full[n % kInfo], (n / kInfo) & 1, err, &ms.abort);
         const float scale = ms.scale[n % kInfo][quad >> 1];
         mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
@@ -388,7 +444,21 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
             sum[(i + 1) & 3] += ex2_approx(fmaf(x1, f.z, -f.w));
           }
         }
-        const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if constexpr (kPair) {
+          const int turn = n / kGroups<kH> & 1;
+          if (rank == 1) {
+            peer_wait(&ms.peer_free[group], turn ^ 1, err, &ms.abort);
+            peer_store(peer_addr(&ms.peer[group][key], 0), all);
+            __syncwarp();
+            if (lane == 0) peer_arrive(peer_addr(&ms.peer_full[group], 0));
+            continue;
+          }
+          peer_wait(&ms.peer_full[group], turn, err, &ms.abort);
+          all += ms.peer[group][key];
+          __syncwarp();
+          if (lane == 0) peer_arrive(peer_addr(&ms.peer_free[group], 1));
+        }
         if (at < len) p.a.out[b * p.a.out_stride + at] = before + (scale > 0.f ? all : 0.f);
       }
     }
@@ -398,15 +468,29 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::columns);
   if (warp == 0 && lane == 0 && ms.abort) drain_copies(ms.full, C::slots, ms.copies);
+  if constexpr (kPair) {  // (the other CTA writes here until its end)
+    __syncthreads();
+    cluster_sync();
+  }
 }
 
-template <int kH>
+template <int kH, bool kPair>
 int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int slot, int ctas, cudaStream_t stream) {
   constexpr int bytes = static_cast<int>(smem_bytes<kH>());
-  const auto kern = fp8_key_weights_kernel<kH>;
+  const auto kern = fp8_key_weights_kernel<kH, kPair>;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), bytes, slot)) return st;
-  kern<<<ctas, kThreads<kH>, bytes, stream>>>(lat, rope, p);
-  return launch_status();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? ctas / 2 * 2 : ctas));
+  cfg.blockDim = dim3(kThreads<kH>);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, lat, rope, p));
 }
 
 }  // namespace
@@ -422,10 +506,10 @@ int launch_fp8_key_weights(const Fp8WeightsArgs& a, cudaStream_t stream, int num
   }
   for (; p.h0 < a.num_heads; p.h0 += 128) {
     const int heads = a.num_heads - p.h0;
-    const int st = heads <= 16   ? launch<16>(p, lat, rope, 32, num_sms, stream)
-                   : heads <= 32 ? launch<32>(p, lat, rope, 33, num_sms, stream)
-                   : heads <= 64 ? launch<64>(p, lat, rope, 34, num_sms, stream)
-                                 : launch<128>(p, lat, rope, 35, num_sms, stream);
+    const int st = heads <= 16   ? launch<16, false>(p, lat, rope, 32, num_sms, stream)
+                   : heads <= 32 ? launch<32, false>(p, lat, rope, 33, num_sms, stream)
+                   : heads <= 64 ? launch<64, false>(p, lat, rope, 34, num_sms, stream)
+                                 : launch<64, true>(p, lat, rope, 35, num_sms, stream);
     if (st != MLA_OK) return st;
     // the next heads are added to these
     p.a.weights = a.out;
