@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
+  if constexpr (kShared) asm volatile("griddepcontrol.wait;" ::: "memory");  // for the work ahead of this call
   if (p.split) make_plan<kH, kShared>(p, ms, reinterpret_cast<int64_t*>(&ms.sums[0][0]), range, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
@@ -1107,6 +1108,7 @@ template <int kSub>
 constexpr int merge_threads = kSub > 1 ? 64 * kSub : 256;
 template <int kH, int kSub, bool kShared>
 __global__ void __launch_bounds__(merge_threads<kSub>) fp8_decode_merge_kernel(const Params p) {
+  if constexpr (kShared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the next call's, which wait)
   const int lane = threadIdx.x & 31;
   const int64_t id = (static_cast<int64_t>(blockIdx.x) * merge_threads<kSub> + threadIdx.x) / (32 * kSub);
   const int sub = kSub > 1 ? (threadIdx.x >> 5) % kSub : 0;
@@ -1213,8 +1215,22 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   constexpr int bytes = static_cast<int>(smem_bytes<kH>());
   const auto kern = fp8_decode_kernel<kH, kShared>;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), bytes, slot)) return st;
-  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
-  if (const int st = launch_status()) return st;
+  if constexpr (kShared) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ranges));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (const int st = cuda_status(cudaLaunchKernelEx(&cfg, kern, lat, rope, p))) return st;
+  } else {
+    kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, bytes, stream>>>(lat, rope, p);
+    if (const int st = launch_status()) return st;
+  }
   if (!p.split) return MLA_OK;
   // A CTA a row where the rows are cut into many pieces.
   const int64_t rows = static_cast<int64_t>(p.a.num_heads) * p.a.batch;

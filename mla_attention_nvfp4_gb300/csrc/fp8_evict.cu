@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   __shared__ int s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the work ahead of this call
   const float* w = a.weights + b * a.weights_stride;
   const int64_t room = min(min(a.max_pages * a.page_size, a.row_len), static_cast<int64_t>(1) << 30);
   const bool first = rank == 0 && tid == 0;
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
     before_tie += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&counts[1], lane) : 0);
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move's CTAs, which wait for this grid's end
   int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
   float* new_w = a.new_weights != nullptr ? a.new_weights + b * a.new_weights_stride : nullptr;
   for (int base = w0; base < w1; base += 128) {
@@ -217,6 +219,8 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
   const int b = blockIdx.x / blocks, i = blockIdx.x % blocks, tid = threadIdx.x;
   __shared__ int64_t from[kBlock];
   __shared__ float scale[kBlock], most[kMove / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for what was chosen
   // a chain of loads: token, page, its rows; the scales come with those
   const int at = i * kBlock + tid, t = tid < kBlock && at < a.keep ? a.kept[static_cast<int64_t>(b) * a.keep + at] : -1;
   int64_t slot = -1;
@@ -314,15 +318,20 @@ int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream, int num_sms) {
   cfg.blockDim = dim3(kChoose);
   cfg.dynamicSmemBytes = kChooseBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   if (const int st = cuda_status(cudaLaunchKernelEx(&cfg, fp8_evict_choose_kernel, a, ctas))) return st;
-  fp8_evict_move_kernel<<<static_cast<unsigned>(a.batch) * blocks, kMove, 0, stream>>>(a, blocks);
-  return launch_status();
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * blocks);
+  cfg.blockDim = dim3(kMove);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, fp8_evict_move_kernel, a, blocks));
 }
 
 }  // namespace mla

@@ -250,6 +250,10 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     tmem_alloc(&ms.tmem, C::columns);
     tmem_relinquish();
   }
+  // The next call's CTAs may take the place of those that end; nothing is read
+  // before the work ahead of this call is done.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();  // (b0 is set before the plan)
   make_plan<kThreads<kH>>(p, ms, part, kPair ? gridDim.x >> 1 : gridDim.x);
   tc_fence_before();
@@ -484,12 +488,14 @@ int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int
   cfg.blockDim = dim3(kThreads<kH>);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 1 : 0;
+  cfg.numAttrs = kPair ? 2 : 1;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, lat, rope, p));
 }
 

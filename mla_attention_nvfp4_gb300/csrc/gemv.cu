@@ -119,6 +119,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
   return v;
 }
 
+// mbar_wait with the loop kept out of line: one try where it is used.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
+  return mbar_wait(bar, parity, err, abort);
+}
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
+  if (!mbar_test(bar, parity)) wait_long(bar, parity, err, abort);
+}
+
 // kPad: rows of x a CTA takes, at most.
 template <int kPad, int kGroups>
 __global__ void __launch_bounds__(kThreads, kCtas)
@@ -267,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     for (int i = i0; i < min(i0 + chunk, count); ++i) {
       // (A wait that gives up, which the error word tells, leaves the warps
       // running through their loops; the sums are then whatever they are.)
-      mbar_wait(&full[slot], phase, p.a.error_word, &abort);
+      wait(&full[slot], phase, p.a.error_word, &abort);
       const uint32_t at = slot * stage_bytes, in_chunk = (buffer * chunk + i - i0) * subs;
       const uint32_t x_in = in_chunk * kXStep;
       uint32_t sf[2 * kGroups];  // of rows r0, r0 + 8, ..
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       // the stage before is free once all warps have read it
       if (tid == 0 && i > 0 && i - 1 + p.stages < count) {
         const int before = i - 1;
-        mbar_wait(&empty[before % p.stages], (before / p.stages) & 1, p.a.error_word, &abort);
+        wait(&empty[before % p.stages], (before / p.stages) & 1, p.a.error_word, &abort);
         load(before + p.stages);
       }
       if (++slot == p.stages) slot = 0, phase ^= 1;
