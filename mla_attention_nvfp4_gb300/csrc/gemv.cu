@@ -399,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
 // Clusters of each size that the current device holds at once, asked for once.
 template <int kPad, int kGroups>
-int64_t resident_clusters(int splits, int num_sms) {
+int resident_clusters(int splits, int dev, int num_sms) {
   static std::atomic<int> known[64][kMaxSplits + 1];
-  int dev = 0;
-  if (splits == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return static_cast<int64_t>(num_sms) * kCtas / splits;
+  if (splits == 1 || dev >= 64) return splits > 8 ? -1 : num_sms * kCtas / splits;
   int n = known[dev][splits].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
@@ -435,6 +434,8 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
 
   p.tiles = static_cast<int>((p.a.N + C::rows - 1) / C::rows);
 
+  int dev = 0;
+  if (const int st = cuda_status(cudaGetDevice(&dev))) return st;
   // Rows a CTA, and K's parts (a cluster of up to 8; a step a warp at least): the
   // shortest time, as waves of the clusters that the SMs hold at once, each of a
   // CTA's stages and of a start and an end that take about as long as four.
@@ -445,7 +446,7 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
     if (x_bytes(subs) + C::min_stages * C::stage(log) > kLimit) break;
     const int64_t stages = (steps + subs - 1) / subs;
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
-      const int64_t held = resident_clusters<kPad, kGroups>(s, num_sms), clusters = units * subs * m_tiles;
+      const int64_t held = resident_clusters<kPad, kGroups>(s, dev, num_sms), clusters = units * subs * m_tiles;
       if (held < 1) continue;
       const int64_t time = (clusters + held - 1) / held * ((stages + s - 1) / s + 4);
       if (time < best_time) best_time = time, ctas = units * subs * s, p.row_log = log, p.splits = s;
