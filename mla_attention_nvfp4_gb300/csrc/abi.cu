@@ -366,7 +366,7 @@ int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_
   if (M < 0 || groups < 0 || N < 0 || K < 0 || K % 32 != 0) return MLA_ERR_INVALID_ARG;
   if (M == 0 || groups == 0 || N == 0) return MLA_OK;
   if (K == 0 || x == nullptr || w_codes == nullptr || w_scales == nullptr || gs_w == nullptr || out == nullptr ||
-      M > kMax || N > kMax || K > kMax || N > kMax / groups)
+      M > kMax || N > kMax || K > (int64_t(1) << 30) || N > kMax / groups)
     return MLA_ERR_INVALID_ARG;
   // rows of x and out that do not overlap: a row's groups inside its stride, or a group's rows inside that one's
   const auto apart = [&](int64_t m, int64_t g, int64_t n) {

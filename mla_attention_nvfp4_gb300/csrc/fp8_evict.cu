@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = base + j * kChoose + tid;
-      v[j] = t0 + i < t1 && i < kHeld ? __ldg(w + t0 + i) : 0.f;
+      v[j] = t0 + i < t1 && i < kHeld ? w[t0 + i] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   for (int base = w0; base < w1; base += 128) {
     float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = new_w != nullptr && base + 32 * j + lane < w1 ? __ldg(w + base + 32 * j + lane) : 0.f;
+    for (int j = 0; j < 4; ++j) v[j] = new_w != nullptr && base + 32 * j + lane < w1 ? w[base + 32 * j + lane] : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = base + 32 * j + lane;

@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     fence_mbar_init();
   }
   // The next call's CTAs may take the place of those that end; nothing is read
-  // before the work ahead of this call is done.
+  // before the work ahead of this call is done (and by no load that takes memory
+  // for constant: it was not when these CTAs began).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int unit = (lane & 3) * 8 + (lane >> 2);
   auto read_x = [&](int i, int pair) {  // i: the chunk's first stage
     const int r = pair % kPad, k = ((first + i) * subs + pair / kPad) * kStep + 8 * unit;
-    return i < count && r < rows && k < p.a.K ? __ldg(reinterpret_cast<const uint4*>(x + r * p.a.x_sm + k)) : make_uint4(0, 0, 0, 0);
+    return i < count && r < rows && k < p.a.K ? *reinterpret_cast<const uint4*>(x + r * p.a.x_sm + k) : make_uint4(0, 0, 0, 0);
   };
   auto stage_x = [&](int buffer, int pair, uint4 v) {
     uint32_t* q = reinterpret_cast<uint32_t*>(&v);

@@ -257,6 +257,55 @@ def test_evict_long(n):
         check_evict(c, evict(c, keep, recent), keep, recent, f"{kind} {keep} of {n}")
 
 
+def test_evict_of_a_large_batch_with_one_long_sequence():
+    # one CTA a sequence, which does not hold all its weights at once
+    rng = np.random.default_rng(20)
+    lens = (40000,) + (100, 0, 63) * 30
+    for kind, keep in (("spread", 300), ("ties", 90)):
+        c = make_evict(rng, lens, keep, 64, kind)
+        check_evict(c, evict(c, keep, 10), keep, 10, f"91 sequences, {kind}")
+
+
+def test_calls_in_a_row_read_what_the_work_ahead_wrote():
+    # queries, cache, lengths and weights of every call are written by the kernels just before it
+    rng = np.random.default_rng(21)
+    lens, keep = (700, 64, 3000), 200
+    sets = []
+    for _ in range(3):
+        q, cache, scales, table, lse = step(rng, 16, lens, 64)
+        sets.append((q.to(DEV), t(cache), t(scales), t(lse), t(rng.random((3, 3000)).astype(np.float32))))
+    blocks = sets[0][2].numel()
+    new = torch.arange(blocks, blocks + 3 * 4, dtype=torch.int32, device=DEV).view(3, 4)
+    tab, ln = t(table), i32(lens)
+    grow = lambda s: (s[0], torch.cat([s[1], s[1].new_zeros(3 * 4 * 64, 576)]), torch.cat([s[2], s[2].new_ones(12)]), s[3], s[4])  # noqa: E731
+    # (the sets' page tables differ; every set is read through the last one's)
+    sets = [grow(s) for s in sets]
+    clean = lambda c: torch.where((c & 0x7F) == 0x7F, 0x30, c)  # noqa: E731
+    sets = [(s[0], clean(s[1]), s[2], s[3], s[4]) for s in sets]
+
+    def both(q, cache, scales, lse, w):
+        mla.mla_nvfp4_fp8_key_weights(q, cache.view(F8), scales, SCALE, lse, page_table=tab, seq_lens=ln, weights=w, out=w)
+        return mla.mla_nvfp4_fp8_cache_evict(cache.view(F8), scales, w, page_table=tab, seq_lens=ln, new_page_table=new,
+                                             keep=keep, recent=20)
+
+    ref = []
+    for s in sets:
+        held = [x.clone() for x in s]
+        torch.cuda.synchronize()
+        out = both(*held)
+        torch.cuda.synchronize()
+        ref.append([x.clone() for x in (*out, held[1], held[2], held[4])])
+    held, got = [x.clone() for x in sets[0]], []
+    for i in range(60):
+        for h, s in zip(held, sets[i % 3]):
+            h.copy_(s)
+        out = both(*held)
+        got.append([x.clone() for x in (*out, held[1], held[2], held[4])])
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, ref[i % 3])), i
+
+
 def test_evict_special_weights():
     rng = np.random.default_rng(9)
     c = make_evict(rng, (500, 400), 100, 64)

@@ -195,3 +195,48 @@ def test_gemv_agrees_with_the_gemm_on_activations_that_nvfp4_holds():
     b = f32(mla.mla_nvfp4_gemm(to(xc[0]), to(xsf[0]), to(codes[0]), to(sf[0]), one, one))
     mag = gemm.gemv(f32(x)[:, None], codes, sf, N, K, 1.0)[1][:, 0]
     assert np.all(np.abs(a - b) <= bf16_half_ulp(a) + bf16_half_ulp(b) + 4.0 * K * 2.0 ** -24 * mag)
+
+
+@pytest.mark.parametrize("M", [1, 3, 6, 16])
+def test_gemv_of_the_largest_matrix_sampled(M):
+    # 7168 x 16384: the forms that split K over clusters; 60 columns of it against the oracle
+    rng = np.random.default_rng(M)
+    N, K = 7168, 16384
+    gs = np.float32(0.01)
+    codes, sf = weights(rng, 1, N, K)
+    x = rows(rng, M, 1, K)
+    got = f32(run(x[:, 0].to(DEV), codes[0], sf[0], gs))
+    cols = np.sort(rng.choice(N, 60, replace=False))
+    w = swizzle.unswizzle_scales(sf[0], N, K // 16)[cols]
+    check(got[:, cols][:, None], x, codes[:, cols], swizzle.swizzle_scales(w)[None], gs, f"{M} rows of {N}x{K}")
+
+
+def test_gemv_calls_in_a_row_read_what_the_work_ahead_wrote():
+    # every call's x, weights and scale are written by the kernels just before it
+    rng = np.random.default_rng(9)
+    N, K = 600, 4096
+    sets = [(rows(rng, 2, 1, K)[:, 0].to(DEV), *(to(a[0]) for a in weights(rng, 1, N, K)), torch.tensor([0.1 * (i + 1)], device=DEV))
+            for i in range(4)]
+    ref = []
+    for s in sets:
+        ref.append(mla.mla_nvfp4_gemv(*s))
+        torch.cuda.synchronize()
+    held = [torch.empty_like(t) for t in sets[0]]
+    got = []
+    for i in range(400):
+        for h, t in zip(held, sets[i % 4]):
+            h.copy_(t)
+        got.append(mla.mla_nvfp4_gemv(*held))
+    # and a chain of them, each call's result the next one's x
+    square = [to(a[0]) for a in weights(rng, 1, 512, 512)]
+    one = torch.tensor([2.0 ** -9], device=DEV)
+    chain, steps = rows(rng, 4, 1, 512)[:, 0].to(DEV), []
+    for _ in range(50):
+        steps.append(chain)
+        chain = mla.mla_nvfp4_gemv(chain, *square, one)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, ref[i % 4]) for i, g in enumerate(got))
+    for x, y in zip(steps, steps[1:] + [chain]):
+        again = mla.mla_nvfp4_gemv(x, *square, one)
+        torch.cuda.synchronize()
+        assert torch.equal(again.view(torch.int16), y.view(torch.int16))

@@ -304,6 +304,29 @@ def test_shared_graph_streams_and_repeats():
     check_decode((f32(fresh[0]), f32(fresh[1])), q.cpu(), cache2, sc2, eff2, now, 64, what="other lengths")
 
 
+def test_shared_calls_in_a_row_read_what_the_work_ahead_wrote():
+    rng = np.random.default_rng(12)
+    shared, lens, H = 512, (700, 512, 513, 100), 16
+    c = make(rng, shared, lens, 64)
+    qs = [queries(rng, 4, H).to(DEV) for _ in range(3)]
+    lengths = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, (650, 512, 600, 100), (512, 512, 512, 64))]
+    lengths[1][2] = 513
+    args, kw = (t(c[0]).view(F8), t(c[1]), SCALE), dict(page_table=t(c[2]), shared_len=shared, return_lse=True)
+    ref = []
+    for q, ln in zip(qs, lengths):
+        ref.append(mla.mla_nvfp4_fp8_decode_shared(q, *args, seq_lens=ln, **kw))
+        torch.cuda.synchronize()
+    q, ln, got = torch.empty_like(qs[0]), torch.empty_like(lengths[0]), []
+    ws = torch.empty(mla.mla_nvfp4_fp8_decode_shared_workspace_size(4, H), dtype=torch.uint8, device=DEV)
+    for i in range(90):
+        q.copy_(qs[i % 3])
+        ln.copy_(lengths[i % 3])
+        got.append(mla.mla_nvfp4_fp8_decode_shared(q, *args, seq_lens=ln, workspace=ws, **kw))
+    torch.cuda.synchronize()
+    for i, (o, x) in enumerate(got):
+        assert torch.equal(o, ref[i % 3][0]) and torch.equal(x, ref[i % 3][1]), i
+
+
 def test_shared_agrees_with_the_decode_on_the_same_sequences():
     rng = np.random.default_rng(10)
     shared, lens, H = 512, (700, 512, 513), 128

@@ -97,7 +97,7 @@ def _gemv(**kw):
 
 @pytest.mark.parametrize("kw", [
     dict(M=-1), dict(G=-1), dict(N=-1), dict(K=-32), dict(K=16), dict(K=48), dict(K=0), dict(x=None), dict(w=None),
-    dict(sf=None), dict(gs=None), dict(out=None), dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 31), dict(N=1 << 30),
+    dict(sf=None), dict(gs=None), dict(out=None), dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 31), dict(K=(1 << 30) + 32), dict(N=1 << 30),
     # rows that overlap
     dict(xm=64), dict(xm=248), dict(xg=56), dict(xm=0), dict(xg=0), dict(om=8), dict(om=31), dict(og=7), dict(om=8, og=24),
     dict(xm=64, xg=248)])
