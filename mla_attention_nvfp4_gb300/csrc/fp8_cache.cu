@@ -27,13 +27,6 @@ constexpr int kPeBytes = MLA_D_ROPE * 2, kKvBytes = MLA_D_LATENT * 2;
 constexpr int kSmemBytes = kBlock * (kKvBytes + kPeBytes);  // 72 KB: three CTAs an SM
 constexpr float kScaleMin = kFp8ScaleMin, kScaleMax = kFp8ScaleMax;
 
-// `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // One pair turned by an angle: products and sums each rounded to float32, as
 // the plain formula evaluates (no contraction), so that the rounding of the
 // result to 8 or 16 bits sees the same value.

@@ -332,14 +332,6 @@ struct Pieces<kH, true> {
   const int lane_;
 };
 
-// mbar_wait with the loop kept out of line: one try where it is used.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  return mbar_wait(bar, parity, err, abort);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  return mbar_test(bar, parity) || wait_long(bar, parity, err, abort);
-}
-
 __device__ __forceinline__ uint32_t cvt_e5m2x2_h2(uint32_t h2) {
   uint16_t r;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));

@@ -18,6 +18,8 @@
 namespace mla {
 namespace {
 
+using namespace sm100;
+
 constexpr int kBlock = MLA_FP8_BLOCK, kKey = kFp8Key;
 constexpr int kChoose = 1024, kWarps = kChoose / 32;
 constexpr int kHeld = 16384;          // weights in shared memory; the others of a longer part are read again
@@ -33,32 +35,17 @@ __device__ __forceinline__ uint32_t rank_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int2 ld_cluster2(const int2* p, int rank) {
+__device__ __forceinline__ int2 cluster_load2(const int2* p, int rank) {
   int2 v;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
-      : "=r"(v.x), "=r"(v.y)
-      : "r"(sm100::smem_u32(p)), "r"(rank)
-      : "memory");
-  return v;
-}
-__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
-  int v;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
-      : "=r"(v)
-      : "r"(sm100::smem_u32(p)), "r"(rank)
-      : "memory");
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr(smem_u32(p), rank)) : "memory");
   return v;
 }
 
 __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8EvictArgs a, int ctas) {
   extern __shared__ uint32_t held[];  // weights
   __shared__ alignas(16) int hist[2][kBins];  // of this CTA, in turn
-  __shared__ int upper[kWarps], counts[2], warp_counts[2][kWarps];
+  __shared__ int upper[kWarps], warp_counts[2][kWarps];
+  __shared__ int2 counts;
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -111,7 +98,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
         cluster_sync();
         int2 v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = c < ctas ? ld_cluster2(mine, c) : make_int2(0, 0);
+        for (int c = 0; c < 8; ++c) v[c] = c < ctas ? cluster_load2(mine, c) : make_int2(0, 0);
         count = make_int2(0, 0);
 #pragma unroll
         for (int c = 0; c < 8; ++c) count.x += v[c].x, count.y += v[c].y;
@@ -165,11 +152,12 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   int before_tie = __reduce_add_sync(0xffffffffu, lane < warp ? n_tie : 0);
   if (ctas > 1) {
     n_above = __reduce_add_sync(0xffffffffu, n_above), n_tie = __reduce_add_sync(0xffffffffu, n_tie);
-    if (tid == 0) counts[0] = n_above, counts[1] = n_tie;
+    if (tid == 0) counts = make_int2(n_above, n_tie);
     cluster_sync();
-    before_above += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&counts[0], lane) : 0);
-    before_tie += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&counts[1], lane) : 0);
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    const int2 other = lane < rank ? cluster_load2(&counts, lane) : make_int2(0, 0);
+    before_above += __reduce_add_sync(0xffffffffu, other.x);
+    before_tie += __reduce_add_sync(0xffffffffu, other.y);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move's CTAs, which wait for this grid's end
   int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
@@ -199,7 +187,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   if (new_w != nullptr)
     for (int64_t i = n + rank * kChoose + tid; i < a.new_row_len; i += ctas * kChoose) new_w[i] = 0.f;
   if (first) a.new_lens[b] = n;
-  if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // (the others' shared memory is read until then)
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (the others' shared memory is read until then)
 }
 
 // |codes| of two bytes; codes times a factor, rounded again.

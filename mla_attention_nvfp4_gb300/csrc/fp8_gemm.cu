@@ -434,9 +434,6 @@ struct Small {
   static constexpr uint32_t cols = 2 * kT;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t remote;
   float4 v;

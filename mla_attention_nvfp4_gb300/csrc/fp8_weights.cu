@@ -171,15 +171,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int 
   }
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// Of the other CTA of a pair.
-__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
+// To the other CTA of a pair.
 __device__ __forceinline__ void peer_store(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -453,15 +445,15 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
           const int turn = n / kGroups<kH> & 1;
           if (rank == 1) {
             peer_wait(&ms.peer_free[group], turn ^ 1, err, &ms.abort);
-            peer_store(peer_addr(&ms.peer[group][key], 0), all);
+            peer_store(cluster_addr(smem_u32(&ms.peer[group][key]), 0), all);
             __syncwarp();
-            if (lane == 0) peer_arrive(peer_addr(&ms.peer_full[group], 0));
+            if (lane == 0) peer_arrive(cluster_addr(smem_u32(&ms.peer_full[group]), 0));
             continue;
           }
           peer_wait(&ms.peer_full[group], turn, err, &ms.abort);
           all += ms.peer[group][key];
           __syncwarp();
-          if (lane == 0) peer_arrive(peer_addr(&ms.peer_free[group], 1));
+          if (lane == 0) peer_arrive(cluster_addr(smem_u32(&ms.peer_free[group]), 1));
         }
         if (at < len) p.a.out[b * p.a.out_stride + at] = before + (scale > 0.f ? all : 0.f);
       }

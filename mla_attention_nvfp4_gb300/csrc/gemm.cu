@@ -98,12 +98,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Shared-memory descriptor of one 512-byte scale tile for tcgen05.cp
 // 32x128b: 32 rows of 16 bytes, no swizzle, i.e. four 8-row core matrices
 // 128 bytes apart.

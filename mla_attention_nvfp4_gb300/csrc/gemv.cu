@@ -67,13 +67,6 @@ struct Params {
   int64_t k_tiles, scale_bytes;
 };
 
-// `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // 8 codes to f16 pairs, in order.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -106,27 +99,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
-
-// mbar_wait with the loop kept out of line: one try where it is used.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  return mbar_wait(bar, parity, err, abort);
-}
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  if (!mbar_test(bar, parity)) wait_long(bar, parity, err, abort);
-}
-
 // kPad: rows of x a CTA takes, at most.
 template <int kPad, int kGroups>
 __global__ void __launch_bounds__(kThreads, kCtas)
@@ -389,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int col = e >> (C::log + p.row_log), r = e & (cta_rows - 1);
     float v = 0.f;
     if (p.splits > 1) {
-      for (int k = 0; k < p.splits; ++k) v += ld_cluster(base + 4 * e, k);
+      for (int k = 0; k < p.splits; ++k) v += cluster_load(base + 4 * e, k);
     } else {
       for (int k = 0; k < subs; ++k) v += sums[k * pairs + e];
     }

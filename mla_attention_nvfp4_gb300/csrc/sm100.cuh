@@ -88,6 +88,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// mbar_wait with the loop kept out of line: one try where it is used.
+__device__ __noinline__ inline bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* error_word, volatile int* abort) {
+  return mbar_wait(bar, parity, error_word, abort);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* error_word, volatile int* abort) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, error_word, abort);
+}
+
 // The same wait by every thread of the CTA: true in all of them, or, where one
 // has given up, false in all (each has a timer of its own, and a thread that
 // left by itself would be missing at the next barrier).
@@ -101,6 +109,29 @@ __device__ __forceinline__ bool mbar_wait_cta(uint64_t* bar, uint32_t parity, ui
 // first TMA copy.
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
+// `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// ----------------------------------------------------------------- clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A shared-memory address in CTA `rank` of the cluster, and loads from there.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
+  return v;
 }
 
 // generic-proxy shared-memory writes -> visible to the async proxy (MMA, TMA)
