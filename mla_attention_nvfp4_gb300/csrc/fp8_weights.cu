@@ -390,18 +390,28 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
           if (lane < 8) v[2] = src[lane + 64];
         }
       };
-      uint4 next[3];
-      load_head(warp - 2, next);
+      // two heads at a time, the next two's loads in flight
+      uint4 next[2][3];
+      load_head(warp - 2, next[0]);
+      load_head(warp - 2 + kQueryWarps, next[1]);
+      const float lse = lane < kH / kQueryWarps && warp - 2 + lane * kQueryWarps < heads
+                            ? p.a.lse[row0 + warp - 2 + lane * kQueryWarps] * kLog2e
+                            : INFINITY;  // (no head: its weights are 2^-inf)
       if (piece > 0) mbar_wait(&ms.q_free, (piece - 1) & 1, err, &ms.abort);
 #pragma unroll 1
-      for (int h = warp - 2; h < kH; h += kQueryWarps) {
-        uint4 v[3];
+      for (int i = 0; i < kH / kQueryWarps; i += 2) {
+        uint4 v[2][3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[i] = next[i];
-        load_head(h + kQueryWarps, next);
-        const float c = query_terms<kH>(v, lane, h, s0 + C::off_q, p.a.softmax_scale);
-        // (no head: its weights are 2^-inf)
-        if (lane == 0) head[h] = h < heads ? make_float2(c, p.a.lse[row0 + h] * kLog2e) : make_float2(0.f, INFINITY);
+        for (int j = 0; j < 6; ++j) v[j / 3][j % 3] = next[j / 3][j % 3];
+        load_head(warp - 2 + (i + 2) * kQueryWarps, next[0]);
+        load_head(warp - 2 + (i + 3) * kQueryWarps, next[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int h = warp - 2 + (i + j) * kQueryWarps;
+          const float c = query_terms<kH>(v[j], lane, h, s0 + C::off_q, p.a.softmax_scale);
+          const float ln = __shfl_sync(0xffffffffu, lse, i + j);
+          if (lane == 0) head[h] = make_float2(h < heads ? c : 0.f, ln);
+        }
       }
       fence_async_smem();
       __syncwarp();
