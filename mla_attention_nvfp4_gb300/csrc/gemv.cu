@@ -36,23 +36,30 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kStep = 256;  // features a warp takes at a time: 64 a thread of a quad
 constexpr int kMaxStages = 8;  // of weights in shared memory
 constexpr int kCtas = 2;       // an SM
 constexpr uint32_t kShare = (222 / kCtas) * 1024;  // of an SM's shared memory for each of them
 constexpr uint32_t kLimit = 224 * 1024;            // of 227 KB, where a stage is large
 constexpr int kMaxSplits = 10;                     // (above 8: not portable, asked for)
 
+constexpr int kXBlock = 256;                       // features of a row of x that share a power of two
+constexpr int kMinStages = 3;
+
 // kGroups: of 16 rows a warp, for which it reads x once.
 template <int kGroups>
 struct Cfg {
   static constexpr int rows = 16 * kGroups * kWarps;  // of a row tile
-  static constexpr uint32_t code_bytes = rows * (kStep / 2);
+  static constexpr int step = 256 / kGroups;          // features a warp takes at a time: a quarter a thread of a quad
+  static constexpr uint32_t line = step / 2, code_bytes = rows * line, sf_bytes = step / 64 * 512;
   static constexpr int log = kGroups == 2 ? 5 : 4;    // of a warp's rows
-  static constexpr int min_stages = kGroups == 2 ? 2 : 3;
   // a stage's bytes, with 2^row_log warps that have rows of their own
   static constexpr uint32_t stage(int row_log) {
-    return code_bytes + (kWarps >> row_log) * ((1 << (log + row_log)) > 128 ? 2u : 1u) * 2048u;
+    return code_bytes + (kWarps >> row_log) * ((1 << (log + row_log)) > 128 ? 2u : 1u) * sf_bytes;
+  }
+  // x's, a chunk: a row of a block for each warp at least, in whole stages
+  __host__ __device__ static constexpr int chunk(int pad, int subs) {
+    const int a = kXBlock / step / subs, b = kXBlock / step * kWarps / (pad * subs);
+    return a > b ? (a > 1 ? a : 1) : (b > 1 ? b : 1);
   }
 };
 
@@ -94,6 +101,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -105,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
   using C = Cfg<kGroups>;
   constexpr int kTiles = kPad > 8 ? 2 : 1;  // groups of 8 columns of the products
-  constexpr int kXStep = kPad * kStep * 2;  // bytes of x a step
+  constexpr int kStep = C::step, kXStep = kPad * kStep * 2;  // bytes of x a step
   extern __shared__ __align__(1024) uint8_t smem[];  // stages of weights, two chunks of x; then the CTA's sums
   __shared__ float factor[2][kWarps][kPad];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
@@ -123,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int row_warp = warp & (row_warps - 1), k_warp = warp >> p.row_log;
   const int first = p.row_stages * split / p.splits, count = p.row_stages * (split + 1) / p.splits - first;  // count >= 1
   const int sf_tiles = cta_rows > 128 ? 2 : 1;  // this CTA's rows are of
-  const uint32_t stage_bytes = C::code_bytes + sf_tiles * subs * 2048;
+  const uint32_t stage_bytes = C::code_bytes + sf_tiles * subs * C::sf_bytes;
   const uint32_t base = smem_u32(smem), x_base = base + p.stages * stage_bytes;
 
   // Weights: lines of 128 bytes, step by step the CTA's rows, their 16-byte
@@ -136,14 +148,14 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   auto load = [&](int i) {  // by one thread
     const int slot = i % p.stages, step = (first + i) * subs;
     const uint32_t dst = base + slot * stage_bytes;
-    const int64_t left = p.k_tiles - static_cast<int64_t>(step) * 4;  // tiles of 4 blocks
-    const int tiles = left < 4 * subs ? static_cast<int>(left) : 4 * subs;
+    const int64_t left = p.k_tiles - static_cast<int64_t>(step) * (kStep / 64);  // tiles of 4 blocks
+    const int tiles = left < kStep / 64 * subs ? static_cast<int>(left) : kStep / 64 * subs;
     mbar_expect_tx(&full[slot], C::code_bytes + max(sf_there, 0) * tiles * 512);
     for (int k = 0; k < subs; ++k)
-      tma_load_bytes(dst + k * (cta_rows * 128), &map, (step + k) * (kStep / 2), static_cast<int>(g * p.a.N + n0), &full[slot]);
+      tma_load_bytes(dst + k * (cta_rows * C::line), &map, (step + k) * C::line, static_cast<int>(g * p.a.N + n0), &full[slot]);
     for (int k = 0; k < sf_there; ++k)
-      bulk_load(dst + C::code_bytes + k * subs * 2048, scales + (k * p.k_tiles + static_cast<int64_t>(step) * 4) * 512, tiles * 512,
-                &full[slot]);
+      bulk_load(dst + C::code_bytes + k * subs * C::sf_bytes, scales + (k * p.k_tiles + static_cast<int64_t>(step) * (kStep / 64)) * 512,
+                tiles * 512, &full[slot]);
     issued = i + 1;
   };
   if (tid == 0) {
@@ -161,15 +173,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // x, a chunk of stages at a time: a warp takes rows of steps (a chunk has a
-  // row for each warp at least), 8 features a lane; a unit of 8 is piece u % 8 of
-  // the quad's thread u / 8.
-  const int chunk = kPad * subs >= kWarps ? 1 : kWarps / (kPad * subs);  // stages
-  const int chunk_steps = chunk * subs;
+  // x, a chunk of stages at a time: a warp takes rows of blocks of 256 features (a
+  // chunk has one for each warp at least), 8 features a lane.  A unit of 8 is piece
+  // u % kPieces of the quad's thread u / kPieces, of the step u / (4 kPieces).
+  constexpr int kPieces = kStep / 32;
+  const int chunk = C::chunk(kPad, subs), chunk_steps = chunk * subs;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.a.x) + m0 * p.a.x_sm + g * p.a.x_sg;
-  const int unit = (lane & 3) * 8 + (lane >> 2);
+  const int unit = kPieces == 8 ? (lane & 3) * 8 + (lane >> 2) : (lane & 16) + (lane & 3) * 4 + (lane >> 2 & 3);
   auto read_x = [&](int i, int pair) {  // i: the chunk's first stage
-    const int r = pair % kPad, k = ((first + i) * subs + pair / kPad) * kStep + 8 * unit;
+    const int r = pair % kPad, k = (first + i) * subs * kStep + pair / kPad * kXBlock + 8 * unit;
     return i < count && r < rows && k < p.a.K ? *reinterpret_cast<const uint4*>(x + r * p.a.x_sm + k) : make_uint4(0, 0, 0, 0);
   };
   auto stage_x = [&](int buffer, int pair, uint4 v) {
@@ -199,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const __half2 h = __floats2half2_rn(lo * up, hi * up);
       q[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    const int piece = unit & 7, thread = unit >> 3;
-    sts128(x_base + (buffer * chunk_steps + s) * kXStep + 16 * (piece * (4 * kPad) + 4 * r + thread), v);
+    const int piece = unit % kPieces, thread = unit / kPieces & 3, step = s * (kXBlock / kStep) + unit / (4 * kPieces);
+    sts128(x_base + (buffer * chunk_steps + step) * kXStep + 16 * (piece * (4 * kPad) + 4 * r + thread), v);
   };
   constexpr int kAhead = kPad > 8 ? 2 : 1;  // rows of x a warp has in registers ahead,
   constexpr int kDepth = 3;                 // of so many chunks
-  const int pairs_x = kPad * chunk_steps;
+  const int pairs_x = kPad * chunk_steps * kStep / kXBlock;
   uint4 next[kDepth][kAhead];
   auto read_ahead = [&](uint4 (&v)[kAhead], int i) {
 #pragma unroll
@@ -231,9 +243,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   float total[kGroups][kTiles][4] = {};
   // where this thread's weights, scales and x lie in a stage
   const int r0 = row_warp * (16 * kGroups) + quad, line0 = k_warp * cta_rows + r0, in_tile = (sub * cta_rows + r0) & 127;
-  const uint32_t code_at = base + line0 * 128 + (((2 * t) ^ (line0 & 7)) << 4);
+  const uint32_t code_at = base + line0 * C::line + (kGroups == 1 ? (2 * t) ^ (line0 & 7) : t ^ (line0 >> 1 & 3)) * 16;
   // (a warp's rows are some of 32 whose scales are 16 bytes apart)
-  const uint32_t scale_at = base + C::code_bytes + ((r0 >> 7) * subs + k_warp) * 2048 + t * 512 + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+  const uint32_t scale_at = base + C::code_bytes + ((r0 >> 7) * subs + k_warp) * C::sf_bytes +
+                            (kGroups == 1 ? t * 512 : (t >> 1) * 512 + (t & 1) * 2) + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
   uint32_t x_at[kTiles];
 #pragma unroll
   for (int c = 0; c < kTiles; ++c)  // (columns past the rows are whatever they are, and not written)
@@ -251,23 +264,24 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       wait(&full[slot], phase, p.a.error_word, &abort);
       const uint32_t at = slot * stage_bytes, in_chunk = (buffer * chunk + i - i0) * subs;
       const uint32_t x_in = in_chunk * kXStep;
-      uint32_t sf[2 * kGroups];  // of rows r0, r0 + 8, ..
+      uint32_t sf[2 * kGroups];  // of rows r0, r0 + 8, ..: four or two blocks' of a thread
 #pragma unroll
-      for (int r = 0; r < 2 * kGroups; ++r) sf[r] = lds32(scale_at + at + 128 * r);
-      const int block = ((first + i) * subs + k_warp) * 16 + 4 * t;
-      if (block + 4 > blocks) {  // the last four blocks of a row may be two, or none (the padding may hold NaN)
+      for (int r = 0; r < 2 * kGroups; ++r) sf[r] = kGroups == 1 ? lds32(scale_at + at + 128 * r) : lds16(scale_at + at + 128 * r);
+      constexpr int kBlocks = kStep / 64;
+      const int block = ((first + i) * subs + k_warp) * (kStep / 16) + kBlocks * t;
+      if (block + kBlocks > blocks) {  // the last blocks of a row may be two of four, or none (the padding may hold NaN)
         const uint32_t mask = blocks - block == 2 ? 0xFFFFu : 0u;
 #pragma unroll
         for (int r = 0; r < 2 * kGroups; ++r) sf[r] &= mask;
       }
       float acc[kGroups][kTiles][4] = {};
 #pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2) {  // two blocks of 16
+      for (int b2 = 0; b2 < kStep / 128; ++b2) {  // two blocks of 16
         uint4 v[2 * kGroups];
         uint32_t sc[2 * kGroups];  // f16 pairs of their scales
 #pragma unroll
         for (int r = 0; r < 2 * kGroups; ++r) {
-          v[r] = lds128((code_at ^ (b2 << 4)) + at + r * 1024);
+          v[r] = lds128((code_at ^ (b2 << 4)) + at + r * (8 * C::line));
           sc[r] = e4m3x2_to_f16x2_pair(sf[r] >> (16 * b2));
         }
 #pragma unroll
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       for (int c = 0; c < kTiles; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float f = factor[buffer][(i - i0) * subs + k_warp][min(8 * c + 2 * t + j, kPad - 1)];
+          const float f = factor[buffer][((i - i0) * subs + k_warp) * kStep / kXBlock][min(8 * c + 2 * t + j, kPad - 1)];
 #pragma unroll
           for (int gr = 0; gr < kGroups; ++gr) {
             total[gr][c][j] = fmaf(acc[gr][c][j], f, total[gr][c][j]);
@@ -401,9 +415,9 @@ template <int kPad, int kGroups>
 int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   using C = Cfg<kGroups>;
   const auto kern = nvfp4_gemv_kernel<kPad, kGroups>;
-  static_assert(C::min_stages * C::code_bytes >= C::rows * kPad * sizeof(float), "the sums fit in the stages of weights");
+  static_assert(kMinStages * C::code_bytes >= C::rows * kPad * sizeof(float), "the sums fit in the stages of weights");
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLimit), slot)) return st;
-  const auto x_bytes = [](int subs) { return 2u * (kPad * subs > kWarps ? kPad * subs : kWarps) * (kStep * 2); };
+  const auto x_bytes = [](int subs) { return 2u * C::chunk(kPad, subs) * subs * kPad * C::step * 2; };
 
   p.tiles = static_cast<int>((p.a.N + C::rows - 1) / C::rows);
 
@@ -412,11 +426,11 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   // Rows a CTA, and K's parts (a cluster of up to 8; a step a warp at least): the
   // shortest time, as waves of the clusters that the SMs hold at once, each of a
   // CTA's stages and of a start and an end that take about as long as four.
-  const int64_t steps = (p.a.K + kStep - 1) / kStep, m_tiles = (p.a.M + kPad - 1) / kPad, units = p.a.groups * p.tiles;
+  const int64_t steps = (p.a.K + C::step - 1) / C::step, m_tiles = (p.a.M + kPad - 1) / kPad, units = p.a.groups * p.tiles;
   int64_t best_time = INT64_MAX, ctas = 0;
   for (int log = 3; log >= 0; --log) {
     const int subs = kWarps >> log;
-    if (x_bytes(subs) + C::min_stages * C::stage(log) > kLimit) break;
+    if (x_bytes(subs) + kMinStages * C::stage(log) > kLimit) break;
     const int64_t stages = (steps + subs - 1) / subs;
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
       const int64_t held = resident_clusters<kPad, kGroups>(s, dev, num_sms), clusters = units * subs * m_tiles;
@@ -429,11 +443,11 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   const int subs = kWarps >> p.row_log;
   const uint32_t stage = C::stage(p.row_log), x = x_bytes(subs);
   p.row_stages = static_cast<int>((steps + subs - 1) / subs);
-  p.stages = x + C::min_stages * stage >= kShare ? C::min_stages : static_cast<int>((kShare - x) / stage);
+  p.stages = x + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
 
   CUtensorMap map;
-  if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, 128, 1 << (C::log + p.row_log), false)) {
+  if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, C::line, 1 << (C::log + p.row_log), kGroups == 2)) {
     set_last_error("cuTensorMapEncodeTiled failed for the weights");
     return MLA_ERR_LAUNCH;
   }
@@ -466,7 +480,7 @@ int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
   // 16 x 7168 x 16384 27.3 us, not 28.5; 4 x 128 heads x 512 x 128 4.8, not 6.4.
   // One where three and more stages are to be in flight: 1 x 7168 x 16384 18.2 us,
   // not 23.4; 1 x 576 x 7168 4.0, not 4.5.
-  const bool two = a.K <= 2 * kStep;
+  const bool two = a.K <= 512;
   if (a.M <= 1) return two ? launch<1, 2>(p, 26, num_sms, stream) : launch<1, 1>(p, 27, num_sms, stream);
   if (a.M <= 2) return two ? launch<2, 2>(p, 28, num_sms, stream) : launch<2, 1>(p, 29, num_sms, stream);
   if (a.M <= 4) return two ? launch<4, 2>(p, 30, num_sms, stream) : launch<4, 1>(p, 31, num_sms, stream);
