@@ -41,7 +41,8 @@ DEVERR_BOUNDS, DEVERR_TIMEOUT, DEVERR_SCALE, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8
 # decode launches one kernel with one key split, two (plus the merge) with
 # uniform splits and three (plan, decode, merge) when planned, see
 # decode_launches(); the e4m3 decode launches its merge too, unless split is
-# False or the page table is at most 384 keys wide.
+# False or the page table is at most 384 keys wide; the key weights take a
+# launch each 128 heads.
 LAUNCHES_PER_CALL = {"cache_write": 1, "decode": 3, "prefill": 1, "global_scale": 2, "gemm": 1,
                      "gather_latent": 1, "prefill_partial": 1, "merge_fused_out": 1, "prefill_qdq": 2,
                      "prefill_fakequant": 1, "fp8_cache_append": 1, "fp8_decode": 2, "fp8_quantize": 1, "fp8_gemm": 1,
@@ -50,7 +51,7 @@ LAUNCHES_PER_CALL = {"cache_write": 1, "decode": 3, "prefill": 1, "global_scale"
 # "alu" (CUDA-core arithmetic).
 KERNEL_BOUND = {"cache_write": "hbm", "decode": "tensor", "prefill": "tensor", "gemm": "tensor",
                 "fp8_cache_append": "hbm", "fp8_decode": "tensor", "fp8_quantize": "hbm", "fp8_gemm": "tensor",
-                "fp8_decode_shared": "tensor", "fp8_key_weights": "hbm", "fp8_cache_evict": "hbm", "gemv": "hbm"}
+                "fp8_decode_shared": "tensor", "fp8_key_weights": "hbm", "fp8_cache_evict": "hbm", "gemv": "alu"}
 # Operand type of each kernel's tensor-core products (fp32 accumulation):
 # the decode multiplies f16 operands (the dequantised latent c*s is exact in
 # f16), the prefill bf16 inputs as given.
@@ -760,8 +761,10 @@ def mla_nvfp4_fp8_decode_shared(q, cache, scales, softmax_scale, *, page_table, 
     shared_len tokens (a multiple of 64), read once for all of them through
     row 0 of the page table; seq_lens counts them too, and a sequence shorter
     than shared_len is attended to by itself.  It pays where a sequence has
-    few heads (64 x 16384 shared keys, 16 heads) and costs the batch a merge
-    where it has many.  A workspace is allocated unless given."""
+    few heads (64 sequences, 16384 shared keys and up to 2048 of their own, 16
+    heads: 62 us, not 120), less where its heads fill a CTA's 64 rows (32 x
+    (32768 + 1000), 128 heads: 254 us, not 274), and not for short prefixes.  A
+    workspace is allocated unless given."""
     return _result("mla_nvfp4_fp8_decode_shared", _fp8().decode_shared(
         q, cache, scales, softmax_scale, page_table, seq_lens, shared_len, page_size, out, lse, workspace, error_word,
         return_lse))

@@ -7,9 +7,14 @@
 //           weights that agree above them, summed over the cluster by every CTA.
 //           Then the tokens above it, and the first of those equal to it, find
 //           their places from counts of the warps and CTAs before.  Bound by its
-//           chain of barriers.
+//           chain of loads and barriers: 5.8 us for 1000 tokens, 15 for 32
+//           sequences to 32k.  (Rounds of 8 bits with a histogram a warp: 19; rounds of
+//           11 with 8 copies of the histogram: 22, for clearing and adding them.)
 //   move    a CTA a new block of 64 tokens, all its rows in registers while the
-//           largest is found: HBM-bound.  Its scale follows the append's rule.
+//           largest is found: 128k tokens in 24.7 us, 6.0 TB/s read and written.  Its
+//           scale follows the append's rule.  (Amax and rounding on f16 pairs; with
+//           integer bytes and fp32 29.7 us.  Persistent CTAs with warps that find the
+//           next block's rows meanwhile: 34.)
 #include <cuda_runtime.h>
 
 #include "fp8_paged.cuh"

@@ -9,8 +9,11 @@
 // while it is there, and no result of one tile is needed by another.  Up to 64
 // heads are one CTA's; up to 128 a pair's (a cluster of two), each CTA of which
 // loads one of a tile's two blocks for both, and the second sends its sums to the
-// first.  (All 128 in one CTA leave room for one tile: 64 x 4096 keys 46.5 us.)
+// first.  (All 128 in one CTA leave room for one tile: 64 x 4096 keys 48.9 us.)
 // More heads take a launch each 128.
+// Times: 32 sequences of 1k to 32k, 16 heads 32.2 us (5.7 TB/s); 64 x 4096, 64 heads
+// 31.9, 128 heads 45.8 (3.5 TB/s: the pair's two tiles in flight wait for both CTAs'
+// products, and its pieces' starts); 1 x 1000, 16 heads 4.9, a chain of latencies.
 //
 // One CTA per SM, persistent over an equal part of the batch's tiles (and of
 // its pieces' starts, a sequence's queries being converted anew):

@@ -1,25 +1,30 @@
 // bf16 rows times an NVFP4 weight matrix (one, or one a group):
 //   out[m, g, n] = gs sum_k x[m, g, k] code[g, n, k] scale[g, n, k / 16].
 //
-// HBM-bound: every weight is 9/16 of a byte, read once for up to 16 rows.  The
-// sums run on mma.sync m16n8k16 (f16 operands, fp32 sums): weights are its 16
-// rows, x its 8 columns, and what an instruction could do beyond the bytes' rate
-// counts for nothing here.  (tcgen05 would want the weights unpacked in shared
-// memory first; here they go from global memory to registers, are converted
-// there and multiplied.)
+// Every weight is 9/16 of a byte, read once for up to 16 rows: HBM would bound it
+// (9.9 us for 7168 x 16384).  What does is the conversion of the weights: of some
+// 290 instructions a warp for 16 rows x 256 features 160 are the codes' conversion
+// and the scales' products.  The sums run on mma.sync m16n8k16 (f16 operands, fp32
+// sums): weights are its 16 rows, x its 8 columns.  (tcgen05 wants its operands in
+// shared memory: f16 weights would be written there and read again.)
 //   weights  code * scale has 6 significant bits between 2^-10 and 2688: exact in
-//            f16.  A thread holds 64 weights of two rows (32 bytes each) a step of
-//            256 features: four whole blocks of 16, whose scales are one word.
-//            Which feature of an instruction they are is free, as long as x
-//            agrees: its rows lie in shared memory in the order of the fragments.
-//   x        bf16 in f16, after a power of two a row and 2048 features that brings
+//            f16.  A thread of a quad holds a quarter of a step's features of a row,
+//            whole blocks of 16.  Which feature of an instruction they are is free,
+//            as long as x agrees: its rows lie in shared memory in the order of the
+//            fragments.
+//   x        bf16 in f16, after a power of two a row and 256 features that brings
 //            the largest to 2^14 or more: exact down to 2^-31 of it (f16's steps
 //            are 2^-24), within 2^-39 of it below.  Infinities and NaN are kept.
-//   rows     a warp's 16 are 4 consecutive ones of each 32 of a 128-row tile: so
-//            their scales are 64 consecutive bytes of the swizzled layout.
-// The 8 warps of a CTA take kRows rows of 16 and split the features of a step
-// range over the rest; a cluster of up to 8 CTAs splits K, and its CTAs each add
+// The 8 warps of a CTA take 16 or 32 rows each, or share rows and split the
+// features of a stage; a cluster of up to 10 CTAs splits K, and its CTAs each add
 // up and write a part of the rows: no workspace, and sums in a fixed order.
+// Weights come by TMA into a ring (a box of lines of 128 or 64 bytes, and the
+// scales as they lie), x is read ahead of them (asked for behind 25 MB of weights
+// it came 5 us later).
+// Times: 1 x 7168 x 16384 17.9 us (3.7 TB/s), 16 rows 27.6, 1 x 576 x 7168 4.0,
+// 4 rows of 128 matrices of 512 x 128 3.8.  What was tried beside that: weights
+// from global memory to registers (23.3 us), three CTAs an SM (clusters of 8 then
+// fill the SMs one and a half times: 31 us), 16 warps a CTA (16 rows: 31.8 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -423,7 +428,7 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
 
   int dev = 0;
   if (const int st = cuda_status(cudaGetDevice(&dev))) return st;
-  // Rows a CTA, and K's parts (a cluster of up to 8; a step a warp at least): the
+  // Rows a CTA, and K's parts (a cluster of up to 10; a step a warp at least): the
   // shortest time, as waves of the clusters that the SMs hold at once, each of a
   // CTA's stages and of a start and an end that take about as long as four.
   const int64_t steps = (p.a.K + C::step - 1) / C::step, m_tiles = (p.a.M + kPad - 1) / kPad, units = p.a.groups * p.tiles;
@@ -475,11 +480,10 @@ int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
   p.sf_tiles = static_cast<int>((a.N + 127) / 128);
   p.k_tiles = (a.K / 16 + 3) / 4;
   p.scale_bytes = p.sf_tiles * p.k_tiles * 512;
-  // Two groups of 16 rows a warp where x is much (more than 8 rows) or a row of
-  // weights a stage or two, so that few CTAs and not the depth of the ring count:
-  // 16 x 7168 x 16384 27.3 us, not 28.5; 4 x 128 heads x 512 x 128 4.8, not 6.4.
-  // One where three and more stages are to be in flight: 1 x 7168 x 16384 18.2 us,
-  // not 23.4; 1 x 576 x 7168 4.0, not 4.5.
+  // Two groups of 16 rows a warp, in steps of half the features, where x is much
+  // (more than 8 rows: 16 x 7168 x 16384 27.6 us, with one 28.5) or a row of weights
+  // short (4 x 128 heads x 512 x 128 3.8 us, with one 6.4).  One otherwise: 1 x 7168 x
+  // 16384 17.9 us, with two 20.4; 1 x 576 x 7168 4.0, with two 4.4.
   const bool two = a.K <= 512;
   if (a.M <= 1) return two ? launch<1, 2>(p, 26, num_sms, stream) : launch<1, 1>(p, 27, num_sms, stream);
   if (a.M <= 2) return two ? launch<2, 2>(p, 28, num_sms, stream) : launch<2, 1>(p, 29, num_sms, stream);

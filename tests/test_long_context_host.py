@@ -138,4 +138,4 @@ def test_python_calls_want_cuda_tensors():
 
 def test_launch_accounting_names_them():
     for name in ("fp8_decode_shared", "fp8_key_weights", "fp8_cache_evict", "gemv"):
-        assert mla.LAUNCHES_PER_CALL[name] >= 1 and mla.kernel_kind(name) in ("hbm", "tensor")
+        assert mla.LAUNCHES_PER_CALL[name] >= 1 and mla.kernel_kind(name) in ("hbm", "tensor", "alu")
