@@ -503,7 +503,7 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
  *              after another; padding readable, its bytes of no effect.
  *   gs_w     : device fp32 global scale of all groups.
  *   out      : bf16 [M, groups, N], element strides likewise; 2-byte aligned.
- * K a multiple of 32 up to 2^30, any M, groups and N.  out is no part of x.  x, its strides (in bytes), w_codes
+ * K a multiple of 32 up to 2^30, M up to 1048560, groups * N below 2^31 - 512.  out is no part of x.  x, its strides (in bytes), w_codes
  * and w_scales are 16-byte aligned.  A stride of a dimension of one is not read.
  * M == 0, groups == 0 or N == 0 is a no-op, K == 0 an error.
  * Sums are fp32, rounded once to bf16.  Made for few rows: every 16 rows of x

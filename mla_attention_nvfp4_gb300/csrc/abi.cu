@@ -362,11 +362,11 @@ int mla_nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, c
 int mla_nvfp4_gemv(const void* x, int64_t x_stride_m, int64_t x_stride_g, int64_t M, const uint8_t* w_codes,
                    const uint8_t* w_scales, int groups, int64_t N, int64_t K, const float* gs_w, void* out,
                    int64_t out_stride_m, int64_t out_stride_g, uint32_t* error_word, void* stream) {
-  constexpr int64_t kMax = (int64_t(1) << 31) - 512;
+  constexpr int64_t kMax = (int64_t(1) << 31) - 512, kMostRows = 16 * 65535;  // (16 a grid row)
   if (M < 0 || groups < 0 || N < 0 || K < 0 || K % 32 != 0) return MLA_ERR_INVALID_ARG;
   if (M == 0 || groups == 0 || N == 0) return MLA_OK;
   if (K == 0 || x == nullptr || w_codes == nullptr || w_scales == nullptr || gs_w == nullptr || out == nullptr ||
-      M > kMax || N > kMax || K > (int64_t(1) << 30) || N > kMax / groups)
+      M > kMostRows || N > kMax || K > (int64_t(1) << 30) || N > kMax / groups)
     return MLA_ERR_INVALID_ARG;
   // rows of x and out that do not overlap: a row's groups inside its stride, or a group's rows inside that one's
   const auto apart = [&](int64_t m, int64_t g, int64_t n) {

@@ -432,7 +432,7 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need(rows_contiguous(x) && w.is_contiguous() && ws.is_contiguous(),
        "w_codes and w_scales must be contiguous, and x have a contiguous last dimension");
   need(ws.numel() == G * ((N + 127) / 128 * 128) * ((K / 16 + 3) / 4 * 4), "w_scales must hold the padded scales of every group");
-  need(gs.numel() >= 1, "gs_w must hold the global scale");
+  need(gs.numel() == 1, "gs_w must hold one global scale, for all groups");
   Tensor out;
   if (args.skip_none()) {
     out = d == 3 ? at::empty({M, G, N}, x.options()) : at::empty({M, N}, x.options());

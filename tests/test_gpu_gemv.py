@@ -156,6 +156,16 @@ def test_gemv_strides_and_outputs():
         run(x.to(DEV), codes[:2], sf, gs)
 
 
+def test_gemv_has_one_global_scale():
+    # (one a group is not read as the first for all)
+    rng = np.random.default_rng(16)
+    codes, sf = weights(rng, 2, 16, 32)
+    x = rows(rng, 1, 2, 32).to(DEV)
+    for gs in (torch.ones(2, device=DEV), torch.ones(0, device=DEV)):
+        with pytest.raises(ValueError, match="gs_w"):
+            mla.mla_nvfp4_gemv(x, to(codes), to(sf), gs)
+
+
 def test_gemv_repeats_itself_in_a_graph_and_on_two_streams():
     rng = np.random.default_rng(7)
     N, K = 7168, 2048

@@ -112,6 +112,10 @@ def test_gemv_alignment_and_empty():
     assert _gemv(M=0) == 0 and _gemv(G=0) == 0 and _gemv(N=0) == 0
 
 
+def test_gemv_rows_up_to_the_grid():
+    assert _gemv(M=16 * 65535 + 1, xm=1 << 13, om=1 << 13) == 1
+
+
 def test_append_at_has_the_checks_of_append():
     a = dict(kv_c=P, kv_st=512, k_pe=P, pe_st=64, T=4, cs=P, maxpos=100, il=1, cu=P, ctx=P, pos=P, seqs=2, new=4, pt=P,
              pt_st=2, pages=2, page=64, cache=P, slots=128, scales=P, q=None, qt=0, qh=0, o=None, ot=0, oh=0, H=0,
