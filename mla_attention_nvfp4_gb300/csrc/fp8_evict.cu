@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
     const int2 other = lane < rank ? cluster_load2(&counts, lane) : make_int2(0, 0);
     before_above += __reduce_add_sync(0xffffffffu, other.x);
     before_tie += __reduce_add_sync(0xffffffffu, other.y);
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move's CTAs, which wait for this grid's end
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   if (new_w != nullptr)
     for (int64_t i = n + rank * kChoose + tid; i < a.new_row_len; i += ctas * kChoose) new_w[i] = 0.f;
   if (first) a.new_lens[b] = n;
+  __syncwarp();
   if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (the others' shared memory is read until then)
 }
 
@@ -299,11 +301,13 @@ __global__ void __launch_bounds__(kMove, 4) fp8_evict_move_kernel(const Fp8Evict
 }  // namespace
 
 int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream, int num_sms) {
-  const int blocks = (a.keep + kBlock - 1) / kBlock;
+  // new blocks a sequence, at most: of `keep` tokens, of those there can be, of the new pages
+  const int64_t table = a.max_pages * a.page_size, row = a.row_len < table ? a.row_len : table;
+  const int64_t room = a.new_max_pages * a.page_size < row ? a.new_max_pages * a.page_size : row;
+  const int blocks = static_cast<int>(((a.keep < room ? a.keep : room) + kBlock - 1) / kBlock);
   if (static_cast<int64_t>(a.batch) * blocks > (int64_t(1) << 31) - 1) return MLA_ERR_INVALID_ARG;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(fp8_evict_choose_kernel), kChooseBytes, 36)) return st;
   // a cluster a sequence, as large as the SMs and its tokens allow
-  const int64_t table = a.max_pages * a.page_size, row = a.row_len < table ? a.row_len : table;
   int ctas = 1;
   while (ctas < 8 && a.batch * static_cast<int64_t>(ctas) * 2 <= num_sms && row > static_cast<int64_t>(ctas) * kPart) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -320,6 +324,7 @@ int launch_fp8_evict(const Fp8EvictArgs& a, cudaStream_t stream, int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
   if (const int st = cuda_status(cudaLaunchKernelEx(&cfg, fp8_evict_choose_kernel, a, ctas))) return st;
+  if (blocks == 0) return MLA_OK;  // (weights of no tokens)
   cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * blocks);
   cfg.blockDim = dim3(kMove);
   cfg.dynamicSmemBytes = 0;

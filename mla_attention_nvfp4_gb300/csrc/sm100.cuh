@@ -120,6 +120,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // ----------------------------------------------------------------- clusters
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // (.aligned: whole warps)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A shared-memory address in CTA `rank` of the cluster, and loads from there.

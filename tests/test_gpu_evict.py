@@ -335,6 +335,50 @@ def test_evict_strides_and_given_outputs():
     assert np.all(o[:, :50] == 5) and np.all(o[:, 350:] == 5)
 
 
+def test_evict_keeps_more_than_there_can_be():
+    # new blocks end with the tokens and the new pages, kept's entries with -1
+    rng = np.random.default_rng(31)
+    c = make_evict(rng, (130, 0, 64), 1 << 16, 64)
+    check_evict(c, evict(c, 1 << 16, 3), 1 << 16, 3, "of few")
+    e = errw()
+    pages = i32([0, 1, 2])[:, None]
+    cache, sc = torch.zeros((6 * 64, 576), dtype=torch.uint8, device=DEV), torch.ones(6, device=DEV)
+    kept, n, nw = mla.mla_nvfp4_fp8_cache_evict(
+        cache.view(F8), sc, torch.empty((3, 0), device=DEV), page_table=pages, seq_lens=i32([0, 0, 0]), new_page_table=pages + 3,
+        keep=5, error_word=e)
+    assert kept.eq(-1).all() and n.eq(0).all() and nw.eq(0).all() and int(e.item()) == 0
+
+
+def test_a_cache_past_32_bits_of_bytes():
+    # the same keys in the first pages and beyond 2^32 bytes: the same results
+    rng = np.random.default_rng(32)
+    lens, keep = (300, 129), 100
+    c = make_evict(rng, lens, keep, 64)
+    c["cache"] &= 0xF7  # (no NaN)
+    pages = len(c["cache"]) // 64
+    first = (1 << 32) // (576 * 64) + 1
+    cache = torch.empty(((first + pages) * 64, 576), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(first + pages, device=DEV)
+    cache[first * 64:], scales[first:] = t(c["cache"]), t(c["scales"])
+    far = {**c, "table": c["table"] + first, "new": c["new"] + first}
+    q = torch.from_numpy(rng.standard_normal((2, 16, 576))).bfloat16().to(DEV)
+
+    def calls(cache, scales, c):
+        e = errw()
+        a = dict(page_table=t(c["table"]), seq_lens=i32(lens), error_word=e)
+        out, lse = mla.mla_nvfp4_fp8_decode_shared(q, cache.view(F8), scales, SCALE, shared_len=0, return_lse=True, **a)
+        w = mla.mla_nvfp4_fp8_key_weights(q, cache.view(F8), scales, SCALE, lse, **a)
+        got = evict(c, keep, 10, cache=cache, scales=scales)
+        assert int(e.item()) == 0 and got[5] == 0
+        return f32(out), f32(lse), w.cpu().numpy(), got
+
+    near = calls(t(c["cache"]), t(c["scales"]), c)
+    there = calls(cache, scales, far)
+    for x, y in zip(near[:3] + near[3][:3], there[:3] + there[3][:3]):
+        assert np.all(np.isfinite(x)) and np.array_equal(x, y)
+    assert np.array_equal(near[3][3], there[3][3][first * 64:]) and np.array_equal(near[3][4], there[3][4][first:])
+
+
 def test_evict_bad_entries():
     rng = np.random.default_rng(11)
     lens, keep = (300, 200), 150
