@@ -246,20 +246,21 @@ struct KeyList {
 };
 template <int kH>
 __device__ __forceinline__ KeyList key_list(const Params& p, int v) {
-  const int H = p.a.num_heads;
+  const uint32_t H = p.a.num_heads;  // (rows are at most 2^30)
   KeyList k;
   if (v < p.sh.prefix) {
-    const int64_t all = static_cast<int64_t>(p.a.batch) * H;
-    k.row = static_cast<int64_t>(v) * kH;
-    k.rows = all - k.row < kH ? static_cast<int>(all - k.row) : kH;
+    const uint32_t row = static_cast<uint32_t>(v) * kH;
+    k.row = row;
+    k.rows = min(static_cast<uint32_t>(p.a.batch) * H - row, static_cast<uint32_t>(kH));
     k.b = 0;
-    k.first = static_cast<int>(k.row / H);
-    k.last = static_cast<int>((k.row + k.rows - 1) / H);
+    k.first = static_cast<int>(row / H);
+    k.last = static_cast<int>((row + k.rows - 1) / H);
   } else {
-    const int u = v - p.sh.prefix, g = u % p.sh.groups;
-    k.b = k.first = k.last = u / p.sh.groups;
-    k.row = static_cast<int64_t>(k.b) * H + g * kH;
-    k.rows = min(kH, H - g * kH);
+    const uint32_t u = v - p.sh.prefix, groups = p.sh.groups;
+    k.b = k.first = k.last = static_cast<int>(u / groups);
+    const int g = static_cast<int>(u - k.b * groups);
+    k.row = k.b * H + g * kH;
+    k.rows = min(kH, p.a.num_heads - g * kH);
   }
   return k;
 }
@@ -749,35 +750,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Queries (the previous piece's last scores, which this half has read,
       // were the last to use them): a warp takes every fourth head of its
-      // half; lane l features 8 l.., and 256 + 8 l.., lanes 0..7 the RoPE's.
+      // half, four at a time (of 64 heads two, the next two's loads in flight: 32 x
+      // (32768 + 1000) shared keys, 128 heads 254 us, with four 255; 128 sequences to
+      // 32k of 16 heads 135, with two 139).
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + row * kKey;
-      auto load_head = [&](int h, uint4(&v)[3]) {
-        v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
-        if (h < heads && h < hb + kMine) {
-          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
-          v[0] = src[lane];
-          v[1] = src[lane + 32];
-          if (lane < 8) v[2] = src[lane + 64];
-        }
-      };
-      // two heads at a time, the next two's loads in flight
-      uint4 v_next[2][3];
-      load_head(hb + quad, v_next[0]);
-      load_head(hb + quad + 4, v_next[1]);
+      const int limit = min(heads, hb + kMine);
+      constexpr int kN = kH == 64 ? 2 : 4;
+      QueryHeads<kN> next;
+      next.load(q, lane, hb + quad, 4, limit);
 #pragma unroll 1
-      for (int h2 = hb + quad; h2 < hb + kMine; h2 += 8) {
-        uint4 v_now[2][3];
+      for (int h = hb + quad; h < hb + kMine; h += 4 * kN) {
+        const QueryHeads<kN> now = next;
+        if (kMine > 4 * kN) next.load(q, lane, h + 4 * kN, 4, limit);
+        float c[kN];
+        query_terms<kH>(now, lane, h, 4, s0 + C::off_q, p.a.softmax_scale, c);
 #pragma unroll
-        for (int i = 0; i < 6; ++i) v_now[i / 3][i % 3] = v_next[i / 3][i % 3];
-        load_head(h2 + 8, v_next[0]);
-        load_head(h2 + 12, v_next[1]);
-#pragma unroll
-        for (int two = 0; two < 2; ++two) {
-          const int h = h2 + 4 * two;
-          const uint4(&v)[3] = v_now[two];
-          const float c = query_terms<kH>(v, lane, h, s0 + C::off_q, p.a.softmax_scale);
-          if (lane == 0) ms.c[h] = c;
-        }
+        for (int j = 0; j < kN; ++j)
+          if (lane == j) ms.c[h + 4 * j] = c[j];
       }
       fence_async_smem();
       __syncwarp();
@@ -987,10 +976,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = !kShared && it.e - it.s == it.n;
       const int64_t out_row = it.row(p), part_row = it.part_row(p, range);
       n_last += it.e - it.s;
-      // the next sequence's queries, into L2 meanwhile
-      if (!kShared && it.b + 1 < p.a.batch) {
-        const char* q = static_cast<const char*>(p.a.q) + (out_row + p.a.num_heads) * (kKey * 2);
-        for (int i = tid; i < heads * (kKey * 2 / 128); i += kOutput)
+      // the next sequence's or list's queries, into L2 meanwhile
+      int64_t next_row = out_row + p.a.num_heads;
+      int next_rows = it.b + 1 < p.a.batch ? heads : 0;
+      if constexpr (kShared) {
+        next_rows = 0;
+        if (it.list + 1 < p.sh.lists) {
+          const KeyList k = key_list<kH>(p, it.list + 1);
+          next_row = k.row;
+          next_rows = k.rows;
+        }
+      }
+      if (next_rows > 0) {
+        const char* q = static_cast<const char*>(p.a.q) + next_row * (kKey * 2);
+        for (int i = tid; i < next_rows * (kKey * 2 / 128); i += kOutput)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128 * i));
       }
       // Rescaling: a head's columns of the value chunks (kH 32: of both terms)

@@ -384,37 +384,19 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
       const int64_t row0 = static_cast<int64_t>(b) * p.a.num_heads + h0;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + row0 * kKey;
       float2* head = ms.head[piece & 1];
-      auto load_head = [&](int h, uint4(&v)[3]) {
-        v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
-        if (h < heads) {
-          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(h) * kKey);
-          v[0] = src[lane];
-          v[1] = src[lane + 32];
-          if (lane < 8) v[2] = src[lane + 64];
-        }
-      };
-      // two heads at a time, the next two's loads in flight
-      uint4 next[2][3];
-      load_head(warp - 2, next[0]);
-      load_head(warp - 2 + kQueryWarps, next[1]);
-      const float lse = lane < kH / kQueryWarps && warp - 2 + lane * kQueryWarps < heads
+      constexpr int kMine = kH / kQueryWarps;
+      QueryHeads<kMine> mine;
+      mine.load(q, lane, warp - 2, kQueryWarps, heads);
+      const float lse = lane < kMine && warp - 2 + lane * kQueryWarps < heads
                             ? p.a.lse[row0 + warp - 2 + lane * kQueryWarps] * kLog2e
                             : INFINITY;  // (no head: its weights are 2^-inf)
       if (piece > 0) mbar_wait(&ms.q_free, (piece - 1) & 1, err, &ms.abort);
-#pragma unroll 1
-      for (int i = 0; i < kH / kQueryWarps; i += 2) {
-        uint4 v[2][3];
+      float c[kMine];
+      query_terms<kH>(mine, lane, warp - 2, kQueryWarps, s0 + C::off_q, p.a.softmax_scale, c);
 #pragma unroll
-        for (int j = 0; j < 6; ++j) v[j / 3][j % 3] = next[j / 3][j % 3];
-        load_head(warp - 2 + (i + 2) * kQueryWarps, next[0]);
-        load_head(warp - 2 + (i + 3) * kQueryWarps, next[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int h = warp - 2 + (i + j) * kQueryWarps;
-          const float c = query_terms<kH>(v[j], lane, h, s0 + C::off_q, p.a.softmax_scale);
-          const float ln = __shfl_sync(0xffffffffu, lse, i + j);
-          if (lane == 0) head[h] = make_float2(h < heads ? c : 0.f, ln);
-        }
+      for (int j = 0; j < kMine; ++j) {
+        const int h = warp - 2 + j * kQueryWarps;
+        if (lane == j) head[h] = make_float2(h < heads ? c[j] : 0.f, lse);
       }
       fence_async_smem();
       __syncwarp();
