@@ -174,22 +174,6 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int 
   }
 }
 
-// To the other CTA of a pair.
-__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void peer_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// mbar_wait for arrivals of the other CTA, whose writes before them are seen (by
-// a second look, of the cluster's scope).
-__device__ __forceinline__ void peer_wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  mbar_wait(bar, parity, err, abort);
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(parity)
-      : "memory");
-}
 // A copy into, and an arrival on a barrier of, both CTAs of a pair.
 __device__ __forceinline__ void tma_load_bytes_pair(uint32_t dst, const void* tmap, int x, int y, uint64_t* bar) {
   asm volatile(

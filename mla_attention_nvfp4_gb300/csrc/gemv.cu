@@ -22,7 +22,7 @@
 // scales as they lie), x is read ahead of them (asked for behind 25 MB of weights
 // it came 5 us later).
 // Times: 1 x 7168 x 16384 17.9 us (3.7 TB/s), 16 rows 27.6, 1 x 576 x 7168 4.0,
-// 4 rows of 128 matrices of 512 x 128 3.8.  What was tried beside that: weights
+// 4 rows of 128 matrices of 512 x 128 3.5.  What was tried beside that: weights
 // from global memory to registers (23.3 us), three CTAs an SM (clusters of 8 then
 // fill the SMs one and a half times: 31 us), 16 warps a CTA (16 rows: 31.8 us).
 #include <cuda.h>
@@ -116,11 +116,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-// kPad: rows of x a CTA takes, at most.
-template <int kPad, int kGroups>
+// kPad: rows of x a CTA takes, at most.  kSplit: clusters split K (a kernel without
+// their code ends sooner: 4 x 128 heads x 512 x 128 3.5 us, not 3.8).
+template <int kPad, int kGroups, bool kSplit>
 __global__ void __launch_bounds__(kThreads, kCtas)
     nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
   using C = Cfg<kGroups>;
+  const int splits = kSplit ? p.splits : 1;
   constexpr int kTiles = kPad > 8 ? 2 : 1;  // groups of 8 columns of the products
   constexpr int kStep = C::step, kXStep = kPad * kStep * 2;  // bytes of x a step
   extern __shared__ __align__(1024) uint8_t smem[];  // stages of weights, two chunks of x; then the CTA's sums
@@ -129,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   __shared__ volatile int abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane >> 2, t = lane & 3;
   const int row_warps = 1 << p.row_log, subs = kWarps >> p.row_log, cta_rows = 1 << (C::log + p.row_log);
-  uint32_t id = blockIdx.x / p.splits;
-  const int split = blockIdx.x - id * p.splits;
+  uint32_t id = blockIdx.x / splits;
+  const int split = blockIdx.x - id * splits;
   const int sub = id & (subs - 1);
   id >>= 3 - p.row_log;
   const int64_t g = id / p.tiles;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kPad;
   const int rows = static_cast<int>(p.a.M - m0 < kPad ? p.a.M - m0 : kPad);
   const int row_warp = warp & (row_warps - 1), k_warp = warp >> p.row_log;
-  const int first = p.row_stages * split / p.splits, count = p.row_stages * (split + 1) / p.splits - first;  // count >= 1
+  const int first = p.row_stages * split / splits, count = p.row_stages * (split + 1) / splits - first;  // count >= 1
   const int sf_tiles = cta_rows > 128 ? 2 : 1;  // this CTA's rows are of
   const uint32_t stage_bytes = C::code_bytes + sf_tiles * subs * C::sf_bytes;
   const uint32_t base = smem_u32(smem), x_base = base + p.stages * stage_bytes;
@@ -366,27 +368,27 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
     }
   __syncthreads();
-  if (subs > 1 && p.splits > 1) {
+  if (subs > 1 && splits > 1) {
     for (int e = tid; e < pairs; e += kThreads) {
       float v = sums[e];
       for (int k = 1; k < subs; ++k) v += sums[k * pairs + e];
       sums[e] = v;
     }
   }
-  if (p.splits > 1) cluster_sync();
+  if (splits > 1) cluster_sync();
   const float gs = *p.a.gs_w;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + m0 * p.a.out_sm + g * p.a.out_sg + n0;
-  for (int e = split * kThreads + tid; e < pairs; e += p.splits * kThreads) {
+  for (int e = split * kThreads + tid; e < pairs; e += splits * kThreads) {
     const int col = e >> (C::log + p.row_log), r = e & (cta_rows - 1);
     float v = 0.f;
-    if (p.splits > 1) {
-      for (int k = 0; k < p.splits; ++k) v += cluster_load(base + 4 * e, k);
+    if (splits > 1) {
+      for (int k = 0; k < splits; ++k) v += cluster_load(base + 4 * e, k);
     } else {
       for (int k = 0; k < subs; ++k) v += sums[k * pairs + e];
     }
     if (n0 + r < p.a.N) out[col * p.a.out_sm + r] = __float2bfloat16_rn(v * gs);
   }
-  if (p.splits > 1) cluster_sync();  // (the others' shared memory is read until here)
+  if (splits > 1) cluster_sync();  // (the others' shared memory is read until here)
 }
 
 // Clusters of each size that the current device holds at once, asked for once.
@@ -406,8 +408,8 @@ int resident_clusters(int splits, int dev, int num_sms) {
     cfg.dynamicSmemBytes = kShare;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((splits > 8 && cudaFuncSetAttribute(nvfp4_gemv_kernel<kPad, kGroups>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
-        cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad, kGroups>, &cfg) != cudaSuccess || n < 1) {
+    if ((splits > 8 && cudaFuncSetAttribute(nvfp4_gemv_kernel<kPad, kGroups, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad, kGroups, true>, &cfg) != cudaSuccess || n < 1) {
       (void)cudaGetLastError();
       n = splits > 8 ? -1 : num_sms * kCtas / splits;  // -1: none
     }
@@ -419,9 +421,10 @@ int resident_clusters(int splits, int dev, int num_sms) {
 template <int kPad, int kGroups>
 int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   using C = Cfg<kGroups>;
-  const auto kern = nvfp4_gemv_kernel<kPad, kGroups>;
   static_assert(kMinStages * C::code_bytes >= C::rows * kPad * sizeof(float), "the sums fit in the stages of weights");
-  if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLimit), slot)) return st;
+  const auto split_kern = nvfp4_gemv_kernel<kPad, kGroups, true>, whole_kern = nvfp4_gemv_kernel<kPad, kGroups, false>;
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(split_kern), static_cast<int>(kLimit), slot)) return st;
+  if (const int st = smem_limit_once(reinterpret_cast<const void*>(whole_kern), static_cast<int>(kLimit), slot + 9)) return st;
   const auto x_bytes = [](int subs) { return 2u * C::chunk(kPad, subs) * subs * kPad * C::step * 2; };
 
   p.tiles = static_cast<int>((p.a.N + C::rows - 1) / C::rows);
@@ -469,7 +472,7 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, map, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, p.splits > 1 ? split_kern : whole_kern, map, p));
 }
 
 }  // namespace
@@ -482,14 +485,15 @@ int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
   p.scale_bytes = p.sf_tiles * p.k_tiles * 512;
   // Two groups of 16 rows a warp, in steps of half the features, where x is much
   // (more than 8 rows: 16 x 7168 x 16384 27.6 us, with one 28.5) or a row of weights
-  // short (4 x 128 heads x 512 x 128 3.8 us, with one 6.4).  One otherwise: 1 x 7168 x
+  // short (4 x 128 heads x 512 x 128 3.5 us, with one 6.4).  One otherwise: 1 x 7168 x
   // 16384 17.9 us, with two 20.4; 1 x 576 x 7168 4.0, with two 4.4.
   const bool two = a.K <= 512;
-  if (a.M <= 1) return two ? launch<1, 2>(p, 26, num_sms, stream) : launch<1, 1>(p, 27, num_sms, stream);
-  if (a.M <= 2) return two ? launch<2, 2>(p, 28, num_sms, stream) : launch<2, 1>(p, 29, num_sms, stream);
-  if (a.M <= 4) return two ? launch<4, 2>(p, 30, num_sms, stream) : launch<4, 1>(p, 31, num_sms, stream);
-  if (a.M <= 8) return two ? launch<8, 2>(p, 37, num_sms, stream) : launch<8, 1>(p, 38, num_sms, stream);
-  return launch<16, 2>(p, 39, num_sms, stream);
+  constexpr int kSlot = 37;  // 9 and 9 more
+  if (a.M <= 1) return two ? launch<1, 2>(p, kSlot, num_sms, stream) : launch<1, 1>(p, kSlot + 1, num_sms, stream);
+  if (a.M <= 2) return two ? launch<2, 2>(p, kSlot + 2, num_sms, stream) : launch<2, 1>(p, kSlot + 3, num_sms, stream);
+  if (a.M <= 4) return two ? launch<4, 2>(p, kSlot + 4, num_sms, stream) : launch<4, 1>(p, kSlot + 5, num_sms, stream);
+  if (a.M <= 8) return two ? launch<8, 2>(p, kSlot + 6, num_sms, stream) : launch<8, 1>(p, kSlot + 7, num_sms, stream);
+  return launch<16, 2>(p, kSlot + 8, num_sms, stream);
 }
 
 }  // namespace mla
