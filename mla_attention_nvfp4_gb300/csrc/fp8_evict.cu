@@ -162,8 +162,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
     const int2 other = lane < rank ? cluster_load2(&counts, lane) : make_int2(0, 0);
     before_above += __reduce_add_sync(0xffffffffu, other.x);
     before_tie += __reduce_add_sync(0xffffffffu, other.y);
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_arrive();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move's CTAs, which wait for this grid's end
   int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
@@ -193,8 +192,7 @@ __global__ void __launch_bounds__(kChoose, 1) fp8_evict_choose_kernel(const Fp8E
   if (new_w != nullptr)
     for (int64_t i = n + rank * kChoose + tid; i < a.new_row_len; i += ctas * kChoose) new_w[i] = 0.f;
   if (first) a.new_lens[b] = n;
-  __syncwarp();
-  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // (the others' shared memory is read until then)
+  if (ctas > 1) cluster_wait();  // (the others' shared memory is read until then)
 }
 
 // |codes| of two bytes; codes times a factor, rounded again.

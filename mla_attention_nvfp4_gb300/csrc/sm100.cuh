@@ -119,18 +119,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // ----------------------------------------------------------------- clusters
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();  // (.aligned: whole warps)
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The two halves of it.
 __device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
+  __syncwarp();  // (.aligned: whole warps)
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // A shared-memory address in CTA `rank` of the cluster, and loads from there.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
