@@ -52,7 +52,7 @@
 // further, the warps waited for instructions more than for anything else.
 // Times (merge included; pairs below compare two forms at one time): 64 x 4096
 // keys, 128 heads 88.9 us, 64 heads 65, 16 heads 46; 128 sequences of 1k to
-// 32k, 16 heads 139 us (5.0 TB/s), 128 heads 324 (1020 TFLOP/s); 1 x 65536, 128
+// 32k, 16 heads 135 us (5.2 TB/s), 128 heads 324 (1020 TFLOP/s); 1 x 65536, 128
 // heads 37.5; 1 x 100, 16 heads 9.9 (12.3 with the merge), launches and one chain
 // of latencies.  With 64 heads a CTA, shared memory bounds a tile: the
 // operands of its products (18 x 8 KB and 32 x 6 KB), the copies in (72 KB) and
@@ -67,9 +67,9 @@
 // prefix, once for every kH rows (sequence, head) of the batch, whatever
 // sequences they are of, and each sequence's own keys.  All pieces leave partial
 // results, and a row's merge takes those of the prefix and its own.  64 x (16384 +
-// 1..2048) keys, 16 heads 61.6 us (without sharing 120: a tile of keys serves 64
+// 1..2048) keys, 16 heads 61.3 us (without sharing 120: a tile of keys serves 64
 // rows, not 16); 32 x (32768 + 1000), 128 heads 254 (1185 TFLOP/s; not shared 274:
-// rows were full, only HBM is spared); 4 x (2048 + 64), 16 heads 18.4, latencies of
+// rows were full, only HBM is spared); 4 x (2048 + 64), 16 heads 17.4, latencies of
 // start, one tile and merge (not shared 16.6).
 #include <cuda.h>
 #include <cuda_runtime.h>
