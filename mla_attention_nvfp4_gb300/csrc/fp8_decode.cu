@@ -132,7 +132,7 @@ struct Misc {
   uint32_t hits[2], moves[2];  // heads (of either half) that may have to be raised; that are
   float scale[C::info][2];  // of a tile's two blocks; 0: the block is no part of the sequence
   int64_t t0, t1, off0;
-  int b0;
+  int b0, longest;  // shared: of the first list's sequences
   uint32_t tmem;
   int chunks, ropes;  // copies issued
   volatile int abort;
@@ -294,7 +294,7 @@ struct Pieces<kH, true> {
   template <class M>
   __device__ __forceinline__ Pieces(const Params& p, const M& ms, int)
       : next_(ms.b0), t_(ms.t0), t1_(ms.t1), off_(ms.off0), lane_(threadIdx.x & 31) {
-    longest_ = load(p);
+    longest_ = ms.longest;  // (the plan has it)
   }
   // (called by whole warps)
   __device__ __forceinline__ bool next(const Params& p) {
@@ -381,13 +381,14 @@ __device__ __forceinline__ bool half_any(int wg, bool v) {
 template <int kH, bool kShared, class M>
 __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan, int range, bool publish) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = kShared ? p.sh.lists : p.a.batch;
+  int longest = 0;  // shared: of the list's sequences
   auto cost_of = [&](int b) {
     if constexpr (kShared) {
       const KeyList k = key_list<kH>(p, b);
-      int most = 0;
+      longest = 0;
 #pragma unroll 1
-      for (int i = k.first; i <= k.last; ++i) most = max(most, clipped_len(p.a, i));
-      return list_cost<kH>(tiles_of(list_keys(p, b, most)));
+      for (int i = k.first; i <= k.last; ++i) longest = max(longest, clipped_len(p.a, i));
+      return list_cost<kH>(tiles_of(list_keys(p, b, longest)));
     } else {
       return tiles_of(clipped_len(p.a, b));
     }
@@ -458,6 +459,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
       if (uncut ? b == range : t0 >= off && t0 < off + n) {
         ms.b0 = b;
         ms.off0 = off;
+        ms.longest = longest;
         if (uncut) {
           ms.t0 = off;
           ms.t1 = off + n;
