@@ -132,7 +132,7 @@ struct Misc {
   uint32_t hits[2], moves[2];  // heads (of either half) that may have to be raised; that are
   float scale[C::info][2];  // of a tile's two blocks; 0: the block is no part of the sequence
   int64_t t0, t1, off0;
-  int b0, longest;  // shared: of the first list's sequences
+  int b0, longest;  // first sequence's keys (shared: of the first list's sequences)
   uint32_t tmem;
   int chunks, ropes;  // copies issued
   volatile int abort;
@@ -206,7 +206,7 @@ struct Pieces {
   __device__ __forceinline__ Pieces(const Params& p, const M& ms, int range)
       : rows(min(kH, p.a.num_heads - static_cast<int>(blockIdx.x % p.groups) * kH)), h0_(blockIdx.x % p.groups * kH), split_(p.split), step_(p.split ? 1 : p.ranges), next_(p.split ? ms.b0 : range), t_(p.split ? ms.t0 : 0),
         t0_(t_), t1_(p.split ? ms.t1 : 0), off_(p.split ? ms.off0 : 0) {
-    next_len_ = load(p);
+    next_len_ = p.split ? ms.longest : load(p);
   }
   __device__ __forceinline__ bool next(const Params& p) {
     do {
@@ -381,7 +381,7 @@ __device__ __forceinline__ bool half_any(int wg, bool v) {
 template <int kH, bool kShared, class M>
 __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan, int range, bool publish) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = kShared ? p.sh.lists : p.a.batch;
-  int longest = 0;  // shared: of the list's sequences
+  int longest = 0;  // of the sequence, or the list's sequences
   auto cost_of = [&](int b) {
     if constexpr (kShared) {
       const KeyList k = key_list<kH>(p, b);
@@ -390,7 +390,8 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
       for (int i = k.first; i <= k.last; ++i) longest = max(longest, clipped_len(p.a, i));
       return list_cost<kH>(tiles_of(list_keys(p, b, longest)));
     } else {
-      return tiles_of(clipped_len(p.a, b));
+      longest = clipped_len(p.a, b);
+      return tiles_of(longest);
     }
   };
   const int per_thread = (B + kThreads - 1) / kThreads;
@@ -471,8 +472,12 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
   }
   if (tid == 0) {
     ms.t0 = t0;
-    ms.t1 = uncut ? (range < B ? tiles_of(clipped_len(p.a, range)) : 0) : t0 + per < total ? t0 + per : total;
-    if (uncut) ms.b0 = range;
+    ms.t1 = t0 + per < total ? t0 + per : total;
+    if (uncut) {
+      ms.b0 = range;
+      ms.longest = range < B ? clipped_len(p.a, range) : 0;
+      ms.t1 = tiles_of(ms.longest);
+    }
   }
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
@@ -484,6 +489,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int64_t* scan,
     if (!uncut && t0 >= off && t0 < off + n) {
       ms.b0 = b;
       ms.off0 = off;
+      ms.longest = longest;
     }
     off += n;
   }

@@ -66,7 +66,7 @@ struct Misc {
   uint64_t peer_full[kGroups<kH>], peer_free[kGroups<kH>];
   float peer[kGroups<kH>][kTile];
   int64_t scan[kThreads<kH> / 32], t0, t1, off0;
-  int b0;
+  int b0, len0;  // the part's first sequence, its keys
   uint32_t tmem;
   int copies;
   volatile int abort;
@@ -103,9 +103,8 @@ struct Pieces {
   int b = 0, len = 0, s = 0, e = 0;
 
   template <class M>
-  __device__ __forceinline__ Pieces(const Params& p, const M& ms) : next_(ms.b0), t_(ms.t0), t1_(ms.t1), off_(ms.off0) {
-    next_len_ = load(p);
-  }
+  __device__ __forceinline__ Pieces(const Params& p, const M& ms)
+      : next_(ms.b0), t_(ms.t0), t1_(ms.t1), off_(ms.off0), next_len_(ms.len0) {}
   __device__ __forceinline__ bool next(const Params& p) {
     while (t_ < t1_ && next_ < p.a.batch) {
       b = next_;
@@ -126,10 +125,11 @@ struct Pieces {
 
  private:
   __device__ __forceinline__ int load(const Params& p) const { return next_ < p.a.batch ? length_of(p, next_) : 0; }
-  int next_, next_len_;
+  int next_;
   int64_t t_;
   const int64_t t1_;
   int64_t off_;
+  int next_len_;
 };
 
 // This CTA's part of the sequences' costs, and its first sequence.
@@ -165,9 +165,10 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int 
   }
 #pragma unroll 1
   for (int b = first; b < last; ++b) {
-    const int n = cost_of(length_of(p, b));
+    const int len = length_of(p, b), n = cost_of(len);
     if (t0 >= off && t0 < off + n) {
       ms.b0 = b;
+      ms.len0 = len;
       ms.off0 = off;
     }
     off += n;
