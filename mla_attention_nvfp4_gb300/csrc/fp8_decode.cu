@@ -67,9 +67,9 @@
 // prefix, once for every kH rows (sequence, head) of the batch, whatever
 // sequences they are of, and each sequence's own keys.  All pieces leave partial
 // results, and a row's merge takes those of the prefix and its own.  64 x (16384 +
-// 1..2048) keys, 16 heads 61.3 us (without sharing 120: a tile of keys serves 64
-// rows, not 16); 32 x (32768 + 1000), 128 heads 254 (1185 TFLOP/s; not shared 274:
-// rows were full, only HBM is spared); 4 x (2048 + 64), 16 heads 17.4, latencies of
+// 1..2048) keys, 16 heads 59.0 us (without sharing 120: a tile of keys serves 64
+// rows, not 16); 32 x (32768 + 1000), 128 heads 251 (1199 TFLOP/s; not shared 274:
+// rows were full, only HBM is spared); 4 x (2048 + 64), 16 heads 14.8, latencies of
 // start, one tile and merge (not shared 16.6).
 #include <cuda.h>
 #include <cuda_runtime.h>

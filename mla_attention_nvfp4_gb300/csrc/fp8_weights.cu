@@ -12,7 +12,7 @@
 // first.  (All 128 in one CTA leave room for one tile: 64 x 4096 keys 48.9 us.)
 // More heads take a launch each 128.
 // Times: 32 sequences of 1k to 32k, 16 heads 32.2 us (5.7 TB/s); 64 x 4096, 64 heads
-// 31.9, 128 heads 43.7 (3.7 TB/s: the pair's two tiles in flight wait for both CTAs'
+// 31.9, 128 heads 43.2 (3.8 TB/s: the pair's two tiles in flight wait for both CTAs'
 // products, and its pieces' starts); 1 x 1000, 16 heads 4.7, a chain of latencies.
 //
 // One CTA per SM, persistent over an equal part of the batch's tiles (and of
