@@ -7,6 +7,10 @@ are off by at most what oracle.fp8.key_weights derives (fp32 sums of exact
 products, the hardware's exp2), and of what the queries' two 8-bit terms leave:
 exact down to 2^-13 of a head's largest feature, 2^-21 of it below
 (tests/fp8_cases.py states and tests that)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -539,3 +543,38 @@ def test_decode_weigh_evict_append_decode():
             w[:, :keep] = rw
             assert np.array_equal(dw.cpu().numpy(), w)
     assert evictions == 1
+
+
+_FIRST_CALLS = """
+import torch
+import mla_attention_nvfp4_gb300 as mla
+D = "cuda"
+cache = torch.zeros((640, 576), dtype=torch.uint8, device=D).view(torch.float8_e4m3fn)
+scales, gs = torch.ones(10, device=D), torch.ones(1, device=D)
+table = torch.arange(4, dtype=torch.int32, device=D).view(2, 2)
+a = dict(page_table=table, seq_lens=torch.tensor([100, 90], dtype=torch.int32, device=D))
+codes, sf = torch.full((512, 512), 0x21, dtype=torch.uint8, device=D), torch.full((512 * 64,), 0x38, dtype=torch.uint8, device=D)
+calls = []
+for h in (16, 128):
+    q, lse = torch.ones((2, h, 576), device=D).bfloat16(), torch.zeros((2, h), device=D)
+    x = torch.ones((h // 8, 1024), device=D).bfloat16()
+    calls += [lambda q=q: mla.mla_nvfp4_fp8_decode_shared(q, cache, scales, 0.1, shared_len=64, **a),
+              lambda q=q, lse=lse: mla.mla_nvfp4_fp8_key_weights(q, cache, scales, 0.1, lse, **a),
+              lambda x=x: mla.mla_nvfp4_gemv(x, codes, sf, gs)]
+w = torch.rand((2, 128), device=D)
+calls.append(lambda: mla.mla_nvfp4_fp8_cache_evict(cache, scales, w, new_page_table=table[:, :1] + 4, keep=40, **a)[0])
+torch.cuda.synchronize()
+for f in calls:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = f()
+    g.replay()
+    assert torch.equal(r, f())
+print("same")
+"""
+
+
+def test_a_process_may_capture_its_first_calls():
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
