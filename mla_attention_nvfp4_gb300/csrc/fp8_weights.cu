@@ -6,14 +6,12 @@
 // features arrive by TMA as they lie and are the 128-row operand, the queries'
 // two e4m3 terms (fp8_query.cuh) the other, so that a key is a TMEM lane and
 // the sum over the heads stays in its thread.  HBM-bound: all heads meet a tile
-// while it is there, and no result of one tile is needed by another.  Up to 64
-// heads are one CTA's; up to 128 a pair's (a cluster of two), each CTA of which
-// loads one of a tile's two blocks for both, and the second sends its sums to the
-// first.  (All 128 in one CTA leave room for one tile: 64 x 4096 keys 48.9 us.)
-// More heads take a launch each 128.
+// while it is there, and no result of one tile is needed by another.  Up to 128
+// heads are one CTA's, whose queries then leave room for one tile in flight, not
+// two; more heads take a launch each 128.
 // Times: 32 sequences of 1k to 32k, 16 heads 32.2 us (5.7 TB/s); 64 x 4096, 64 heads
-// 31.9, 128 heads 43.2 (3.8 TB/s: the pair's two tiles in flight wait for both CTAs'
-// products, and its pieces' starts); 1 x 1000, 16 heads 4.7, a chain of latencies.
+// 31.9, 128 heads 43.8 (3.7 TB/s: the one tile in flight, chunk by chunk behind its
+// products, and the pieces' starts); 1 x 1000, 16 heads 4.7, a chain of latencies.
 //
 // One CTA per SM, persistent over an equal part of the batch's tiles (and of
 // its pieces' starts, a sequence's queries being converted anew):
@@ -38,9 +36,9 @@ using namespace sm100;
 
 constexpr int kKey = kFp8Key, kBlock = MLA_FP8_BLOCK, kTile = 128;
 // Groups of four warps that take a tile each in turn: two keep up with the
-// tiles; with 64 heads the queries want four.
+// tiles; with 64 heads and more the queries want four.
 template <int kH>
-constexpr int kGroups = kH == 64 ? 4 : 2;
+constexpr int kGroups = kH >= 64 ? 4 : 2;
 template <int kH>
 constexpr int kThreads = 64 + 128 * kGroups<kH>;
 constexpr uint32_t kChunkBytes = kTile * 128, kRopeBytes = kTile * 64, kTileBytes = 4 * kChunkBytes + kRopeBytes;
@@ -49,7 +47,7 @@ constexpr int kInfo = 4;   // tiles whose scales are kept
 
 template <int kH>
 struct Cfg {
-  static constexpr int tiles = 2;  // in shared memory
+  static constexpr int tiles = kH == 128 ? 1 : 2;  // in shared memory
   static constexpr int slots = 5 * tiles;          // chunks of them
   static constexpr uint32_t off_rope = 4 * tiles * kChunkBytes, off_q = tiles * kTileBytes;
   static constexpr uint32_t off_misc = off_q + 2 * kH * kKey;
@@ -62,9 +60,6 @@ struct Misc {
   uint64_t s_full[2], s_free[2], q_ready, q_free, retired;
   alignas(16) float2 head[2][kH];  // of a piece, in turn: factor of its scores, log2(e) lse
   float scale[kInfo][2];           // of a tile's two blocks; 0: none of the sequence's
-  // Pair: the second CTA's sums of a tile, one place a group; theirs to read, to write.
-  uint64_t peer_full[kGroups<kH>], peer_free[kGroups<kH>];
-  float peer[kGroups<kH>][kTile];
   int64_t scan[kThreads<kH> / 32], t0, t1, off0;
   int b0, len0;  // the part's first sequence, its keys
   uint32_t tmem;
@@ -76,7 +71,7 @@ template <int kH>
 constexpr uint32_t smem_bytes() {
   return Cfg<kH>::off_misc + static_cast<uint32_t>(sizeof(Misc<kH>));
 }
-static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
 
 struct Params {
   Fp8WeightsArgs a;
@@ -134,7 +129,7 @@ struct Pieces {
 
 // This CTA's part of the sequences' costs, and its first sequence.
 template <int kThreads, class M>
-__device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int parts) {
+__device__ __forceinline__ void make_plan(const Params& p, M& ms) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.a.batch;
   const int per_thread = (B + kThreads - 1) / kThreads;
   const int first = min(tid * per_thread, B), last = min(first + per_thread, B);
@@ -158,7 +153,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int 
     if (i < warp) off += ms.scan[i];
     total += ms.scan[i];
   }
-  const int64_t per = (total + parts - 1) / parts, t0 = part * per;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * per;
   if (tid == 0) {
     ms.t0 = t0;
     ms.t1 = t0 + per < total ? t0 + per : total;
@@ -175,22 +170,7 @@ __device__ __forceinline__ void make_plan(const Params& p, M& ms, int part, int 
   }
 }
 
-// A copy into, and an arrival on a barrier of, both CTAs of a pair.
-__device__ __forceinline__ void tma_load_bytes_pair(uint32_t dst, const void* tmap, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-      "[%4], %5;" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-
-template <int kH, bool kPair>
+template <int kH>
 __global__ void __launch_bounds__(kThreads<kH>, 1)
     fp8_key_weights_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                            const __grid_constant__ Params p) {
@@ -200,8 +180,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
   Misc<kH>& ms = *reinterpret_cast<Misc<kH>*>(smem + C::off_misc);
   const uint32_t s0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? blockIdx.x & 1 : 0, part = kPair ? blockIdx.x >> 1 : blockIdx.x;
-  const int h0 = p.h0 + rank * kH, heads = min(kH, p.a.num_heads - h0);
+  const int heads = min(kH, p.a.num_heads - p.h0);
   uint32_t* err = p.a.error_word;
 
   if (threadIdx.x == 0) {
@@ -210,7 +189,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     ms.off0 = 0;
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(&ms.full[i], 1);
-      mbar_init(&ms.empty[i], kPair ? 2 : 1);
+      mbar_init(&ms.empty[i], 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(&ms.info_full[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -220,10 +199,6 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     mbar_init(&ms.q_ready, kQueryWarps);
     mbar_init(&ms.q_free, 1);
     mbar_init(&ms.retired, 1);
-    for (int i = 0; i < kGroups<kH>; ++i) {
-      mbar_init(&ms.peer_full[i], 4);
-      mbar_init(&ms.peer_free[i], 4);
-    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -235,10 +210,9 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();  // (b0 is set before the plan)
-  make_plan<kThreads<kH>>(p, ms, part, kPair ? gridDim.x >> 1 : gridDim.x);
+  make_plan<kThreads<kH>>(p, ms);
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // (the barriers of both are set)
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
   // chunk c of tile n (4: the RoPE)
@@ -283,12 +257,8 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
             const uint32_t bytes = c < 4 ? kChunkBytes : kRopeBytes, dst = slot_addr(n, c);
             const CUtensorMap* map = c < 4 ? &tm_lat : &tm_rope;
             mbar_expect_tx(&ms.full[i], bytes);
-            if constexpr (kPair) {  // (the place is free in both)
-              tma_load_bytes_pair(dst + rank * (bytes / 2), map, 128 * c, rank == 0 ? y0 : y1, &ms.full[i]);
-            } else {
-              tma_load_bytes(dst, map, 128 * c, y0, &ms.full[i]);
-              tma_load_bytes(dst + bytes / 2, map, 128 * c, y1, &ms.full[i]);
-            }
+            tma_load_bytes(dst, map, 128 * c, y0, &ms.full[i]);
+            tma_load_bytes(dst + bytes / 2, map, 128 * c, y1, &ms.full[i]);
             ++copies;
           }
         }
@@ -326,27 +296,25 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int t = it.s; ok && t < it.e; ++t, ++n) {
-        const int half = uniform(n & 1);
-        static_assert(C::tiles == 2, "tile n in place n & 1");
+        const int half = uniform(n & 1), place = C::tiles == 2 ? half : 0;  // of its scores, its chunks
         const uint32_t d = tmem + half * 2 * kH;
         ok = ready(&ms.s_free[half], ((n >> 1) & 1) ^ 1);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 5; ++c) {
-          uint64_t* empty = &ms.empty[5 * half + c];
-          ok &= ready(&ms.full[5 * half + c], (n >> 1) & 1);
+          ok &= ready(&ms.full[5 * place + c], (n / C::tiles) & 1);
           __syncwarp();
           if (elect_one()) {
             if (c < 4) {
-              const uint64_t da = dk + (4 * half + c) * (kChunkBytes >> 4), db = dq + c * (2 * kH * 128 >> 4);
+              const uint64_t da = dk + (4 * place + c) * (kChunkBytes >> 4), db = dq + c * (2 * kH * 128 >> 4);
 #pragma unroll
               for (int j = 0; j < 4; ++j) mma_e4m3(d, da + 2 * j, db + 2 * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
             } else {
-              const uint64_t da = dk_rope + half * (kRopeBytes >> 4);
+              const uint64_t da = dk_rope + place * (kRopeBytes >> 4);
 #pragma unroll
               for (int j = 0; j < 2; ++j) mma_e4m3(d, da + 2 * j, dq_rope + 2 * j, idesc, 1u);
             }
-            kPair ? mma_commit_pair(empty) : mma_commit(empty);
+            mma_commit(&ms.empty[5 * place + c]);
             if (c == 4) {
               mma_commit(&ms.s_full[half]);
               if (t + 1 == it.e) mma_commit(&ms.q_free);
@@ -366,22 +334,29 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
     int n = 0, piece = 0;
     for (Pieces it(p, ms); it.next(p); ++piece) {
       const int b = it.b, len = it.len;
-      const int64_t row0 = static_cast<int64_t>(b) * p.a.num_heads + h0;
+      const int64_t row0 = static_cast<int64_t>(b) * p.a.num_heads + p.h0;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + row0 * kKey;
       float2* head = ms.head[piece & 1];
       constexpr int kMine = kH / kQueryWarps;
-      QueryHeads<kMine> mine;
+      constexpr int kN = kMine > 4 ? 2 : kMine;  // heads at a time (of 128 two, the next two's loads in flight)
+      QueryHeads<kN> mine;
       mine.load(q, lane, warp - 2, kQueryWarps, heads);
       const float lse = lane < kMine && warp - 2 + lane * kQueryWarps < heads
                             ? p.a.lse[row0 + warp - 2 + lane * kQueryWarps] * kLog2e
                             : INFINITY;  // (no head: its weights are 2^-inf)
       if (piece > 0) mbar_wait(&ms.q_free, (piece - 1) & 1, err, &ms.abort);
-      float c[kMine];
-      query_terms<kH>(mine, lane, warp - 2, kQueryWarps, s0 + C::off_q, p.a.softmax_scale, c);
+#pragma unroll 1
+      for (int j0 = 0; j0 < kMine; j0 += kN) {
+        const int h0 = warp - 2 + j0 * kQueryWarps;
+        const QueryHeads<kN> now = mine;
+        if (kMine > kN) mine.load(q, lane, h0 + kN * kQueryWarps, kQueryWarps, heads);
+        float c[kN];
+        query_terms<kH>(now, lane, h0, kQueryWarps, s0 + C::off_q, p.a.softmax_scale, c);
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        const int h = warp - 2 + j * kQueryWarps;
-        if (lane == j) head[h] = make_float2(h < heads ? c[j] : 0.f, lse);
+        for (int j = 0; j < kN; ++j) {
+          const int h = h0 + j * kQueryWarps;
+          if (lane == j0 + j) head[h] = make_float2(h < heads ? c[j] : 0.f, lse);
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -393,7 +368,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
         if (n % kGroups<kH> != group) continue;
         const int at = t * kTile + key;
         float before = 0.f;
-        if (rank == 0 && p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
+        if (p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
         mbar_wait(&ms.info_full[n % kInfo], (n / kInfo) & 1, err, &ms.abort);
         const float scale = ms.scale[n % kInfo][quad >> 1];
         mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
@@ -420,21 +395,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
             sum[(i + 1) & 3] += ex2_approx(fmaf(x1, f.z, -f.w));
           }
         }
-        float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if constexpr (kPair) {
-          const int turn = n / kGroups<kH> & 1;
-          if (rank == 1) {
-            peer_wait(&ms.peer_free[group], turn ^ 1, err, &ms.abort);
-            peer_store(cluster_addr(smem_u32(&ms.peer[group][key]), 0), all);
-            __syncwarp();
-            if (lane == 0) peer_arrive(cluster_addr(smem_u32(&ms.peer_full[group]), 0));
-            continue;
-          }
-          peer_wait(&ms.peer_full[group], turn, err, &ms.abort);
-          all += ms.peer[group][key];
-          __syncwarp();
-          if (lane == 0) peer_arrive(cluster_addr(smem_u32(&ms.peer_free[group]), 1));
-        }
+        const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         if (at < len) p.a.out[b * p.a.out_stride + at] = before + (scale > 0.f ? all : 0.f);
       }
     }
@@ -444,30 +405,23 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::columns);
   if (warp == 0 && lane == 0 && ms.abort) drain_copies(ms.full, C::slots, ms.copies);
-  if constexpr (kPair) {  // (the other CTA writes here until its end)
-    __syncthreads();
-    cluster_sync();
-  }
 }
 
-template <int kH, bool kPair>
+template <int kH>
 int launch(const Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int slot, int ctas, cudaStream_t stream) {
   constexpr int bytes = static_cast<int>(smem_bytes<kH>());
-  const auto kern = fp8_key_weights_kernel<kH, kPair>;
+  const auto kern = fp8_key_weights_kernel<kH>;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(kern), bytes, slot)) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? ctas / 2 * 2 : ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads<kH>);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
+  cfg.numAttrs = 1;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, lat, rope, p));
 }
 
@@ -484,10 +438,10 @@ int launch_fp8_key_weights(const Fp8WeightsArgs& a, cudaStream_t stream, int num
   }
   for (; p.h0 < a.num_heads; p.h0 += 128) {
     const int heads = a.num_heads - p.h0;
-    const int st = heads <= 16   ? launch<16, false>(p, lat, rope, 32, num_sms, stream)
-                   : heads <= 32 ? launch<32, false>(p, lat, rope, 33, num_sms, stream)
-                   : heads <= 64 ? launch<64, false>(p, lat, rope, 34, num_sms, stream)
-                                 : launch<64, true>(p, lat, rope, 35, num_sms, stream);
+    const int st = heads <= 16   ? launch<16>(p, lat, rope, 32, num_sms, stream)
+                   : heads <= 32 ? launch<32>(p, lat, rope, 33, num_sms, stream)
+                   : heads <= 64 ? launch<64>(p, lat, rope, 34, num_sms, stream)
+                                 : launch<128>(p, lat, rope, 35, num_sms, stream);
     if (st != MLA_OK) return st;
     // the next heads are added to these
     p.a.weights = a.out;

@@ -143,25 +143,6 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, int rank) {
   return v;
 }
 
-// To a cluster_addr; an arrival there, with what this thread (and, behind a
-// __syncwarp, its warp) wrote before.
-__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void peer_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// mbar_wait for arrivals of other CTAs, whose writes before them are seen (by a
-// second look, of the cluster's scope).
-__device__ __forceinline__ bool peer_wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, err, abort);
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(parity)
-      : "memory");
-  return ok;
-}
-
 // generic-proxy shared-memory writes -> visible to the async proxy (MMA, TMA)
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -578,3 +578,20 @@ def test_a_process_may_capture_its_first_calls():
     r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("heads", [64, 72, 96, 128, 200])
+def test_key_weights_repeat_themselves(heads):
+    """Sequences of many tiles and of one, more of both than there are SMs: every call gives the same bits."""
+    rng = np.random.default_rng(heads)
+    lens = (2500, 1, 129, 0, 128, 1023) + (130, 64) * 80
+    q, cache, scales, table, lse = step(rng, heads, lens, 64)
+    w = rng.random((len(lens), 2500)).astype(np.float32)
+    got, flags = weigh(q, cache, scales, table, lens, 64, lse, w)
+    assert flags == 0
+    check_weights(got, q, cache, scales, table, lens, 64, lse, w, f"{heads} heads, many sequences")
+    args = (q.to(DEV), t(cache).view(F8), t(scales), SCALE, t(lse))
+    kw = dict(page_table=t(table), seq_lens=i32(lens), weights=t(w))
+    again = [mla.mla_nvfp4_fp8_key_weights(*args, **kw, out=t(w)) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(np.array_equal(x.cpu().numpy(), got) for x in again)
