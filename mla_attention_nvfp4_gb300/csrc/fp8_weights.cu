@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
       prefetch_tmap(&tm_lat);
       prefetch_tmap(&tm_rope);
     }
-    int n = 0, copies = 0;
+    int n = 0, copies = 0;  // tiles; of them with this lane's chunk asked for
     bool ok = true;
     const int per_page = p.a.page_size / kBlock;
     for (Pieces it(p, ms); ok && it.next(p);) {
@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
       }
     }
-    if (lane == 0) ms.copies = copies;
+    // (chunk c of tile n is copy 5 n + c; of the last tile some lanes may have given up)
+    copies = __reduce_max_sync(0xffffffffu, copies);
+    if (lane == 0) ms.copies = 5 * copies;
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
     // The loop is short: all chunks in one copy, descriptors by additions, and

@@ -5,6 +5,8 @@ import glob
 import os
 import re
 
+import pytest
+
 import mla_attention_nvfp4_gb300 as mla
 
 CSRC = os.path.join(os.path.dirname(mla.__file__), "csrc")
@@ -21,3 +23,22 @@ def test_no_copy_or_commit_reaches_another_ctas_shared_memory():
     assert "fp8_weights.cu" in names
     for name in names:
         assert "multi" + "cast" not in code_of(name), name
+
+
+@pytest.mark.parametrize("tiles", [1, 2])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 7, 100])
+def test_key_weights_wait_for_all_copies_in_flight(tiles, n):
+    """drain_copies looks at the last `stages` copies before `issued`: copy i in slot i % stages, of phase i / stages.
+    Chunk c of tile n is in slot 5 (n % tiles) + c, of phase n / tiles, and those of the last `tiles` tiles may be in
+    flight; of the last tile any lane may be missing."""
+    code = code_of("fp8_weights.cu")
+    assert re.search(r"drain_copies\(ms\.full, C::slots, ms\.copies\)", code)
+    assert re.search(r"i = n % C::tiles \* 5 \+ c;\s*ok = mbar_wait\(&ms\.empty\[i\]", code)
+    counted = re.search(r"(copies = __reduce_max_sync\(0xffffffffu, copies\);\s*)?if \(lane == 0\) ms\.copies = ([^;]+);", code)
+    for missing in (set(), {0}, {1, 4}, {0, 1, 2, 3}):
+        issued = [n - (lane in missing) for lane in range(5)]  # chunks a lane
+        count = eval(counted.group(2), {}, {"copies": max(issued) if counted.group(1) else issued[0]})
+        stages = 5 * tiles
+        waited = {(i % stages, i // stages % 2) for i in range(max(0, count - stages), count)}
+        flying = {(5 * (t % tiles) + c, t // tiles % 2) for c in range(5) for t in range(max(0, n - tiles), issued[c])}
+        assert flying <= waited, (missing, flying - waited)
