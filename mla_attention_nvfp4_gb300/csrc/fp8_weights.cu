@@ -57,7 +57,10 @@ struct Cfg {
 template <int kH>
 struct Misc {
   uint64_t full[Cfg<kH>::slots], empty[Cfg<kH>::slots], info_full[kInfo];
-  uint64_t s_full[2], s_free[2], q_ready, q_free, retired;
+  // A tile's scores are there: a barrier a group of sum warps, of whose tiles it waits
+  // for every one (of two by the scores' place, four groups would each miss every
+  // other phase, and could take a tile's for that four tiles before).
+  uint64_t s_full[kGroups<kH>], s_free[2], q_ready, q_free, retired;
   alignas(16) float2 head[2][kH];  // of a piece, in turn: factor of its scores, log2(e) lse
   float scale[kInfo][2];           // of a tile's two blocks; 0: none of the sequence's
   int64_t scan[kThreads<kH> / 32], t0, t1, off0;
@@ -192,10 +195,8 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
       mbar_init(&ms.empty[i], 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(&ms.info_full[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.s_free[i], 4);
-    }
+    for (int i = 0; i < kGroups<kH>; ++i) mbar_init(&ms.s_full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ms.s_free[i], 4);
     mbar_init(&ms.q_ready, kQueryWarps);
     mbar_init(&ms.q_free, 1);
     mbar_init(&ms.retired, 1);
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
             }
             mma_commit(&ms.empty[5 * place + c]);
             if (c == 4) {
-              mma_commit(&ms.s_full[half]);
+              mma_commit(&ms.s_full[n % kGroups<kH>]);
               if (t + 1 == it.e) mma_commit(&ms.q_free);
             }
           }
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kThreads<kH>, 1)
         if (p.a.weights != nullptr && at < len) before = p.a.weights[b * p.a.weights_stride + at];
         mbar_wait(&ms.info_full[n % kInfo], (n / kInfo) & 1, err, &ms.abort);
         const float scale = ms.scale[n % kInfo][quad >> 1];
-        mbar_wait(&ms.s_full[n & 1], (n >> 1) & 1, err, &ms.abort);
+        mbar_wait(&ms.s_full[group], (n / kGroups<kH>) & 1, err, &ms.abort);
         tc_fence_after();
         const uint32_t src = lanes + (n & 1) * 2 * kH;
         float sum[4] = {};
