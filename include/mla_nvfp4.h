@@ -698,8 +698,10 @@ int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uin
  *   weights         : fp32 [batch, row_len], row stride in elements.  Of equal
  *                     weights the earlier token stays; -0 equals 0, a NaN is
  *                     below all others.
- *   page_table, seq_lens : of the sequences as they are.
- *   new_page_table  : int32 [batch, new_max_pages], row stride in elements.
+ *   page_table, seq_lens : of the sequences as they are; a row of the table for
+ *                     each (stride 0, one row for all, is refused here).
+ *   new_page_table  : int32 [batch, new_max_pages], row stride in elements,
+ *                     likewise.
  *   keep, recent    : 1 <= keep, 0 <= recent <= keep.  A sequence of at most
  *                     keep tokens is moved whole.
  *   kept            : int32 [batch, keep] out: the tokens that stay, ascending,

@@ -785,7 +785,8 @@ def mla_nvfp4_fp8_cache_evict(cache, scales, weights, *, page_table, seq_lens, n
                               kept=None, new_lens=None, new_weights=None, error_word=None):
     """Of every sequence the `recent` last tokens and those of greatest weight
     (fp32 [B, n]; the earlier of equal ones), `keep` in all, moved in order to
-    the pages of new_page_table, which must be none of the old ones.  Returns
+    the pages of new_page_table, which must be none of the old ones; both
+    tables have a row of their own for each sequence (no expanded one).  Returns
     (kept int32 [B, keep]: their tokens, then -1; new_lens int32 [B];
     new_weights fp32 [B, keep] or the wider tensor given: their weights, then
     zeros).  Append to what is left with positions=the tokens there were."""

@@ -392,6 +392,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need(lens.dim() == 1 && lens.is_contiguous(), "seq_lens must be contiguous [B]");
   const int64_t B = lens.size(0);
   const int64_t pt_stride = check_pages(pt, B, page_size), npt_stride = check_pages(npt, B, page_size);
+  need(pt_stride >= pt.size(1) && npt_stride >= npt.size(1), "page_table and new_page_table must have a row for each sequence");
   const int64_t w_stride = check_rows(w, B, "weights must be [B, n] with a contiguous last dimension");
   need(keep >= 1 && keep <= 1 << 30, "keep must be 1 or more");
   need(recent >= 0 && recent <= keep, "recent must lie between 0 and keep");

@@ -595,3 +595,17 @@ def test_key_weights_repeat_themselves(heads):
     again = [mla.mla_nvfp4_fp8_key_weights(*args, **kw, out=t(w)) for _ in range(20)]
     torch.cuda.synchronize()
     assert all(np.array_equal(x.cpu().numpy(), got) for x in again)
+
+
+def test_evict_wants_a_page_table_row_for_each_sequence():
+    # (the decodes and the key weights take one row for all)
+    c = make_evict(np.random.default_rng(40), (64, 64), 32, 64)
+    for name in ("page_table", "new_page_table"):
+        e, kw = errw(), dict(page_table=t(c["table"]), new_page_table=t(c["new"]))
+        kw[name] = kw[name][:1].expand(2, -1)
+        before = t(c["cache"])
+        with pytest.raises(ValueError, match="a row for each sequence"):
+            mla.mla_nvfp4_fp8_cache_evict(before.view(F8), t(c["scales"]), t(c["w"]), seq_lens=i32((64, 64)), keep=32,
+                                          error_word=e, **kw)
+        torch.cuda.synchronize()
+        assert int(e.item()) == 0 and np.array_equal(before.cpu().numpy(), c["cache"])
