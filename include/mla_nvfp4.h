@@ -672,7 +672,8 @@ size_t mla_nvfp4_fp8_decode_shared_workspace_size(int batch, int num_heads);
  *   q, page_table, seq_lens, softmax_scale : as of mla_nvfp4_fp8_decode, and
  *   lse          : fp32 [batch, num_heads], its lse.
  *   weights, out : fp32 [batch, row_len], row strides in elements; weights
- *                  NULL: zeros; out may be weights (with the same stride).
+ *                  NULL: zeros; out may be weights (with the same stride), or
+ *                  lies apart from it (other columns of one matrix do).
  *                  Entries from seq_lens[b] on are left as they are.
  * Sums are fp32, over the heads in order; a query's features are held as
  * mla_nvfp4_fp8_decode holds them.  A head whose lse is NaN makes its
@@ -708,7 +709,8 @@ int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uin
  *                     then -1.
  *   new_lens        : int32 [batch] out: how many.  Not seq_lens itself.
  *   new_weights     : fp32 [batch, new_row_len >= keep] out or NULL, row stride
- *                     in elements: their weights, then zeros; apart from weights.
+ *                     in elements: their weights, then zeros; apart from weights
+ *                     (other columns of one matrix are).
  * A new block's scale is the one that mla_nvfp4_fp8_cache_append would give it
  * for these keys, and their codes are rounded again in it (exact but for
  * results below 2^-6, where e4m3 is subnormal).  Slots of a new page behind the

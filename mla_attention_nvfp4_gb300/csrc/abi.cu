@@ -45,11 +45,16 @@ bool table_ok(int64_t max_pages, int64_t stride) {
 
 constexpr int kSharedRows = 1 << 30;  // sequences times heads of a batch with a shared prefix
 
-// Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.
+// Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.  Of
+// equal strides they may be columns of one wider matrix.
 bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
                   int64_t rows) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return p < q + ((rows - 1) * b_stride + b_len) * sizeof(float) && q < p + ((rows - 1) * a_stride + a_len) * sizeof(float);
+  if (p >= q + ((rows - 1) * b_stride + b_len) * sizeof(float) || q >= p + ((rows - 1) * a_stride + a_len) * sizeof(float))
+    return false;
+  if (a_stride != b_stride || rows == 1 || (q - p) % sizeof(float) != 0) return true;
+  const int64_t d = (static_cast<int64_t>(q - p) / static_cast<int64_t>(sizeof(float))) % a_stride, column = d < 0 ? d + a_stride : d;
+  return column < a_len || column + b_len > a_stride;
 }
 
 thread_local const char* t_last_error = "";

@@ -609,3 +609,28 @@ def test_evict_wants_a_page_table_row_for_each_sequence():
                                           error_word=e, **kw)
         torch.cuda.synchronize()
         assert int(e.item()) == 0 and np.array_equal(before.cpu().numpy(), c["cache"])
+
+
+def test_weights_beside_their_results_in_one_matrix():
+    rng = np.random.default_rng(41)
+    lens = (300, 0, 129)
+    q, cache, scales, table, lse = step(rng, 16, lens, 64)
+    w = rng.random((3, 320)).astype(np.float32)
+    ref, _ = weigh(q, cache, scales, table, lens, 64, lse, w)
+    both = torch.full((3, 700), 7.0, device=DEV)
+    both[:, :320] = t(w)
+    mla.mla_nvfp4_fp8_key_weights(q.to(DEV), t(cache).view(F8), t(scales), SCALE, t(lse), page_table=t(table),
+                                  seq_lens=i32(lens), weights=both[:, :320], out=both[:, 320:640])
+    got = both.cpu().numpy()
+    assert np.array_equal(got[:, :320], w) and np.all(got[:, 640:] == 7)
+    for b, n in enumerate(lens):
+        assert np.array_equal(got[b, 320:320 + n], ref[b, :n]) and np.all(got[b, 320 + n:] == 7)
+    c = make_evict(rng, lens, 100, 64)
+    ref = evict(c, 100, 10)
+    n = c["w"].shape[1]
+    both = torch.full((3, n + 150), 7.0, device=DEV)
+    both[:, :n] = t(c["w"])
+    got = evict(c, 100, 10, w=both[:, :n], new_weights=both[:, n:n + 120])
+    assert all(np.array_equal(a, b) for i, (a, b) in enumerate(zip(got, ref)) if i != 2)
+    assert np.array_equal(got[2][:, :100], ref[2]) and not got[2][:, 100:].any()
+    assert np.array_equal(both[:, :n].cpu().numpy(), c["w"]) and bool((both[:, n + 120:] == 7).all())

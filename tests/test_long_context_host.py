@@ -143,3 +143,18 @@ def test_python_calls_want_cuda_tensors():
 def test_launch_accounting_names_them():
     for name in ("fp8_decode_shared", "fp8_key_weights", "fp8_cache_evict", "gemv"):
         assert mla.LAUNCHES_PER_CALL[name] >= 1 and mla.kernel_kind(name) in ("hbm", "tensor", "alu")
+
+
+@pytest.mark.parametrize("column", [128, 200, 384, -128, -256, -384])
+def test_rows_of_one_wider_matrix_are_apart(column):
+    # 128 columns of weights, others of out (new_weights) in rows of 512: no refusal (3: the cache's alignment, looked at next)
+    at = ctypes.c_void_p((1 << 20) + 4 * column)
+    assert _weights(w_st=512, out=at, out_st=512, cache=ODD) == 3
+    assert _evict(w_st=512, nw=at, nw_st=512, nrow=128, cache=ODD) == 3
+
+
+@pytest.mark.parametrize("column", [127, 385, -127, -385, 512, -512, 0.5, 128.5])
+def test_rows_of_one_wider_matrix_that_overlap(column):
+    at = ctypes.c_void_p((1 << 20) + int(4 * column))
+    assert _weights(w_st=512, out=at, out_st=512, cache=ODD) == 1
+    assert _evict(w_st=512, nw=at, nw_st=512, nrow=128, cache=ODD) == 1
