@@ -707,10 +707,12 @@ int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uin
  *                     keep tokens is moved whole.
  *   kept            : int32 [batch, keep] out: the tokens that stay, ascending,
  *                     then -1.
- *   new_lens        : int32 [batch] out: how many.  Not seq_lens itself.
+ *   new_lens        : int32 [batch] out: how many.
  *   new_weights     : fp32 [batch, new_row_len >= keep] out or NULL, row stride
  *                     in elements: their weights, then zeros; apart from weights
  *                     (other columns of one matrix are).
+ *   kept, new_lens and new_weights share memory neither with each other nor with
+ *   the page tables and seq_lens; kept and new_lens not with weights either.
  * A new block's scale is the one that mla_nvfp4_fp8_cache_append would give it
  * for these keys, and their codes are rounded again in it (exact but for
  * results below 2^-6, where e4m3 is subnormal).  Slots of a new page behind the

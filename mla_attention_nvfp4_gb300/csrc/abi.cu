@@ -45,6 +45,16 @@ bool table_ok(int64_t max_pages, int64_t stride) {
 
 constexpr int kSharedRows = 1 << 30;  // sequences times heads of a batch with a shared prefix
 
+// Whether two arrays share memory.
+struct Bytes {
+  const void* p;
+  uint64_t bytes;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  return a.bytes != 0 && b.bytes != 0 && p < q + b.bytes && q < p + a.bytes;
+}
+
 // Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.  Of
 // equal strides they may be columns of one wider matrix.
 bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
@@ -698,7 +708,17 @@ int mla_nvfp4_fp8_cache_evict(uint8_t* cache, int64_t num_slots, float* scales, 
       new_page_table == nullptr || seq_lens == nullptr || kept == nullptr || new_lens == nullptr || num_slots == 0 ||
       weights_stride < row_len)
     return MLA_ERR_INVALID_ARG;
-  if (new_lens == seq_lens || new_lens == kept) return MLA_ERR_INVALID_ARG;
+  // one CTA's results are no other's arguments, and no results of another kind
+  const uint64_t word = sizeof(int32_t), B = batch;
+  const Bytes in[] = {{seq_lens, B * word},
+                      {weights, row_len > 0 ? ((B - 1) * weights_stride + row_len) * word : 0},
+                      {page_table, ((B - 1) * page_table_stride + max_pages) * word},
+                      {new_page_table, ((B - 1) * new_page_table_stride + new_max_pages) * word}};
+  const Bytes rows{kept, B * keep * word}, lens{new_lens, B * word};
+  const Bytes more{new_weights, new_weights != nullptr ? ((B - 1) * new_weights_stride + new_row_len) * word : 0};
+  for (const Bytes& a : in)
+    if (overlap(a, rows) || overlap(a, lens) || (a.p != weights && overlap(a, more))) return MLA_ERR_INVALID_ARG;
+  if (overlap(rows, lens) || overlap(rows, more) || overlap(lens, more)) return MLA_ERR_INVALID_ARG;
   if (new_weights != nullptr &&
       (new_row_len < keep || new_weights_stride < new_row_len ||
        rows_overlap(weights, weights_stride, row_len, new_weights, new_weights_stride, new_row_len, batch)))

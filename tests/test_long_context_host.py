@@ -158,3 +158,16 @@ def test_rows_of_one_wider_matrix_that_overlap(column):
     at = ctypes.c_void_p((1 << 20) + int(4 * column))
     assert _weights(w_st=512, out=at, out_st=512, cache=ODD) == 1
     assert _evict(w_st=512, nw=at, nw_st=512, nrow=128, cache=ODD) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    # seq_lens 4096.., weights 2^20.., page_table 8192.., new_page_table 8256.., kept 16384.., new_lens 32768.., new_weights 2^21..
+    dict(nlens=4100), dict(nlens=4092), dict(nlens=8192 + 12), dict(nlens=8256 + 4), dict(nlens=(1 << 20) + 4 * 255),
+    dict(nlens=16384 + 4 * 79), dict(nlens=(1 << 21) + 4 * 79), dict(kept=4092), dict(kept=4096 - 4 * 79), dict(kept=8192 + 8),
+    dict(kept=8256 - 4 * 79), dict(kept=(1 << 20) - 4), dict(kept=(1 << 21) - 4), dict(nw=4100), dict(nw=8192 + 12),
+    dict(nw=8256 - 4 * 79), dict(nw=16384 - 4 * 79), dict(nw=32768 + 4)])
+def test_evict_refuses_results_in_its_arguments(kw):
+    base = dict(lens=4096, pt=8192, npt=8256, kept=16384, nlens=32768, nw=1 << 21, cache=264)
+    args = lambda d: {k: ctypes.c_void_p(v) for k, v in d.items()}
+    assert _evict(**args(base)) == 3  # (the cache's alignment)
+    assert _evict(**args({**base, **kw})) == 1
