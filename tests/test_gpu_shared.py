@@ -384,3 +384,52 @@ def test_one_decode_step_of_four_bit_projections_around_a_shared_prefix():
     values = gemv(out, w_uv, "values")
     final = gemv(values.reshape(B, H * 128), w_o, "output")
     assert final.shape == (B, 300) and bool(torch.isfinite(final).all()) and float(one) == 1
+
+
+@pytest.mark.parametrize("heads", [16, 40, 128])
+def test_shared_replays_read_lengths_pages_and_keys_anew(heads):
+    """One captured call (its plan, cuts and first lists are made on the device) over batches of other lengths, among them one
+    that falls below the prefix, empty ones, and one that shares with nobody; and the first batch again."""
+    rng = np.random.default_rng(50 + heads)
+    shared = 1024
+    batches = [(1024 + 700, 1024, 1024 + 9, 17, 1024 + 64), (1024 + 650, 100, 1024, 0, 1024 + 1), (0, 0, 1024 + 300, 1023, 0),
+               (64, 1, 0, 1000, 960), (0,) * 5, (1024 + 3000, 1024 + 3000, 5, 1024 + 1, 1024)]
+    made = [make(rng, shared, lens, 64) for lens in batches]
+    slots, width = max(c[0].shape[0] for c in made), max(c[2].shape[1] for c in made)
+    cache = torch.zeros((slots, 576), dtype=torch.uint8, device=DEV)
+    sc = torch.ones(slots // 64, device=DEV)
+    table = torch.full((5, width), FAR, dtype=torch.int32, device=DEV)
+    ln = torch.zeros(5, dtype=torch.int32, device=DEV)
+    qs = [queries(rng, 5, heads) for _ in batches]
+    q, e = torch.empty((5, heads, 576), dtype=torch.bfloat16, device=DEV), errw()
+
+    def put(i):
+        c = made[i]
+        cache[:c[0].shape[0]].copy_(t(c[0]))
+        sc[:c[1].shape[0]].copy_(t(c[1]))
+        table.fill_(FAR)
+        table[:, :c[2].shape[1]].copy_(t(c[2]))
+        ln.copy_(torch.tensor(batches[i], dtype=torch.int32))
+        q.copy_(qs[i])
+
+    def call():
+        return mla.mla_nvfp4_fp8_decode_shared(q, cache.view(F8), sc, SCALE, page_table=table, seq_lens=ln, shared_len=shared,
+                                               return_lse=True, error_word=e)
+
+    put(0)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = call()
+    for i in list(range(len(batches))) + [0]:
+        put(i)
+        for x in held:
+            x.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        eager = call()
+        torch.cuda.synchronize()
+        assert int(e.item()) == 0, batches[i]
+        assert torch.equal(held[0], eager[0]) and torch.equal(held[1], eager[1]), batches[i]
+        check_decode((f32(held[0]), f32(held[1])), qs[i], *made[i][:2], made[i][3], batches[i], 64, what=f"replay of {batches[i]}")
