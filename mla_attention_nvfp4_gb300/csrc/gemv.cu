@@ -391,29 +391,56 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (splits > 1) cluster_sync();  // (the others' shared memory is read until here)
 }
 
-// Clusters of each size that the current device holds at once, asked for once.
+// A CTA's shared memory with 2^row_log warps that have rows of their own: two chunks
+// of x, and as many stages of weights as its share of an SM holds (or three, where
+// that is more than its share: one CTA an SM).
+struct Form {
+  int stages;
+  uint32_t bytes;
+};
 template <int kPad, int kGroups>
-int resident_clusters(int splits, int dev, int num_sms) {
-  static std::atomic<int> known[64][kMaxSplits + 1];
-  if (splits == 1 || dev >= 64) return splits > 8 ? -1 : num_sms * kCtas / splits;
-  int n = known[dev][splits].load(std::memory_order_relaxed);
+constexpr Form form_of(int row_log) {
+  using C = Cfg<kGroups>;
+  const int subs = kWarps >> row_log;
+  const uint32_t x = 2u * C::chunk(kPad, subs) * subs * kPad * C::step * 2, stage = C::stage(row_log);
+  int stages = x + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x) / stage);
+  if (stages > kMaxStages) stages = kMaxStages;
+  return Form{stages, x + stages * stage};
+}
+
+// Clusters of a size and a form that the current device holds at once, asked for once.
+template <int kPad, int kGroups>
+int resident_clusters(int splits, int row_log, int dev, int num_sms) {
+  static std::atomic<int> known[64][4][kMaxSplits + 1];
+  const uint32_t bytes = form_of<kPad, kGroups>(row_log).bytes;
+  const int most = num_sms * (bytes <= kShare ? kCtas : 1) / splits;
+  if (dev >= 64) return splits > 8 ? -1 : most;
+  int n = known[dev][row_log][splits].load(std::memory_order_relaxed);
   if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(splits * num_sms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kShare;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((splits > 8 && cudaFuncSetAttribute(nvfp4_gemv_kernel<kPad, kGroups, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
-        cudaOccupancyMaxActiveClusters(&n, nvfp4_gemv_kernel<kPad, kGroups, true>, &cfg) != cudaSuccess || n < 1) {
-      (void)cudaGetLastError();
-      n = splits > 8 ? -1 : num_sms * kCtas / splits;  // -1: none
+    cudaError_t st;
+    if (splits == 1) {
+      st = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, nvfp4_gemv_kernel<kPad, kGroups, false>, kThreads, bytes);
+      n *= num_sms;
+    } else {
+      const auto kern = nvfp4_gemv_kernel<kPad, kGroups, true>;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = splits;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(static_cast<unsigned>(splits * num_sms));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = bytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      st = splits > 8 ? cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+      if (st == cudaSuccess) st = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
     }
-    known[dev][splits].store(n, std::memory_order_relaxed);
+    if (st != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = splits > 8 ? -1 : most;  // -1: none
+    }
+    known[dev][row_log][splits].store(n, std::memory_order_relaxed);
   }
   return n;
 }
@@ -425,7 +452,6 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   const auto split_kern = nvfp4_gemv_kernel<kPad, kGroups, true>, whole_kern = nvfp4_gemv_kernel<kPad, kGroups, false>;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(split_kern), static_cast<int>(kLimit), slot)) return st;
   if (const int st = smem_limit_once(reinterpret_cast<const void*>(whole_kern), static_cast<int>(kLimit), slot + 9)) return st;
-  const auto x_bytes = [](int subs) { return 2u * C::chunk(kPad, subs) * subs * kPad * C::step * 2; };
 
   p.tiles = static_cast<int>((p.a.N + C::rows - 1) / C::rows);
 
@@ -438,10 +464,10 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   int64_t best_time = INT64_MAX, ctas = 0;
   for (int log = 3; log >= 0; --log) {
     const int subs = kWarps >> log;
-    if (x_bytes(subs) + kMinStages * C::stage(log) > kLimit) break;
+    if (form_of<kPad, kGroups>(log).bytes > kLimit) break;
     const int64_t stages = (steps + subs - 1) / subs;
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
-      const int64_t held = resident_clusters<kPad, kGroups>(s, dev, num_sms), clusters = units * subs * m_tiles;
+      const int64_t held = resident_clusters<kPad, kGroups>(s, log, dev, num_sms), clusters = units * subs * m_tiles;
       if (held < 1) continue;
       const int64_t time = (clusters + held - 1) / held * ((stages + s - 1) / s + 4);
       if (time < best_time) best_time = time, ctas = units * subs * s, p.row_log = log, p.splits = s;
@@ -449,10 +475,9 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   }
   if (ctas > (int64_t(1) << 31) - 1 || m_tiles > 65535) return MLA_ERR_INVALID_ARG;
   const int subs = kWarps >> p.row_log;
-  const uint32_t stage = C::stage(p.row_log), x = x_bytes(subs);
+  const Form form = form_of<kPad, kGroups>(p.row_log);
   p.row_stages = static_cast<int>((steps + subs - 1) / subs);
-  p.stages = x + kMinStages * stage >= kShare ? kMinStages : static_cast<int>((kShare - x) / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages = form.stages;
 
   CUtensorMap map;
   if (!encode_byte_map(&map, p.a.w_codes, p.a.K / 2, p.a.groups * p.a.N, p.a.K / 2, C::line, 1 << (C::log + p.row_log), kGroups == 2)) {
@@ -462,7 +487,7 @@ int launch(Params p, int slot, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(m_tiles));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = x + p.stages * stage;
+  cfg.dynamicSmemBytes = form.bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (griddepcontrol)

@@ -250,3 +250,33 @@ def test_gemv_calls_in_a_row_read_what_the_work_ahead_wrote():
         again = mla.mla_nvfp4_gemv(x, *square, one)
         torch.cuda.synchronize()
         assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,few,more,K", [(16, 1024, 1536, 7168), (16, 576, 1536, 7168), (8, 256, 1024, 16384)])
+def test_gemv_of_fewer_weights_takes_no_longer(M, few, more, K):
+    """The split of K goes by the CTAs that the device holds of the form at hand.  By a count for smaller ones a matrix of
+    1024 rows was cut for twice the CTAs that fit, and took twice the time of one of 1536.  (1.4: noise; least of nine.)"""
+    rng = np.random.default_rng(60)
+
+    def least(N):
+        x = torch.randn(M, K, device=DEV).bfloat16()
+        w = [to(a[0]) for a in weights(rng, 1, N, K)]
+        gs = torch.ones(1, device=DEV)
+        mla.mla_nvfp4_gemv(x, *w, gs)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                mla.mla_nvfp4_gemv(x, *w, gs)
+        times = []
+        for _ in range(9):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    a, b = least(few), least(more)
+    assert a <= 1.4 * b, f"{few} rows {a * 50:.1f} us, {more} rows {b * 50:.1f} us"
