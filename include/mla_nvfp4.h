@@ -675,7 +675,7 @@ size_t mla_nvfp4_fp8_decode_shared_workspace_size(int batch, int num_heads);
  *                  NULL: zeros; out may be weights (with the same stride), or
  *                  lies apart from it (other columns of one matrix do).
  *                  Entries from seq_lens[b] on are left as they are.
- * Sums are fp32, over the heads in order; a query's features are held as
+ * Sums are fp32, over the heads in a fixed order; a query's features are held as
  * mla_nvfp4_fp8_decode holds them.  A head whose lse is NaN makes its
  * sequence's weights NaN, a NaN code in a key that key's.
  *   Errors       : MLA_DEVERR_BOUNDS for a length past row_len or the page

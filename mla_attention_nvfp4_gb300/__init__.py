@@ -762,9 +762,10 @@ def mla_nvfp4_fp8_decode_shared(q, cache, scales, softmax_scale, *, page_table, 
     row 0 of the page table; seq_lens counts them too, and a sequence shorter
     than shared_len is attended to by itself.  It pays where a sequence has
     few heads (64 sequences, 16384 shared keys and up to 2048 of their own, 16
-    heads: 59 us, not 120), less where its heads fill a CTA's 64 rows (32 x
-    (32768 + 1000), 128 heads: 251 us, not 274) or the prefix is short (4 x (2048
-    + 64), 16 heads: 14.8 us, not 16.6).  A workspace is allocated unless given."""
+    heads: 59 us, mla_nvfp4_fp8_decode over the same pages 110), hardly where
+    its heads fill a CTA's 64 rows (32 x (32768 + 1000), 128 heads: 251 us, not
+    253; 273 if every sequence has pages of its own) or the prefix is short (4 x
+    (2048 + 64), 16 heads: 14.8 us, not 15.9).  A workspace is allocated unless given."""
     return _result("mla_nvfp4_fp8_decode_shared", _fp8().decode_shared(
         q, cache, scales, softmax_scale, page_table, seq_lens, shared_len, page_size, out, lse, workspace, error_word,
         return_lse))

@@ -67,10 +67,12 @@
 // prefix, once for every kH rows (sequence, head) of the batch, whatever
 // sequences they are of, and each sequence's own keys.  All pieces leave partial
 // results, and a row's merge takes those of the prefix and its own.  64 x (16384 +
-// 1..2048) keys, 16 heads 59.0 us (without sharing 120: a tile of keys serves 64
-// rows, not 16); 32 x (32768 + 1000), 128 heads 251 (1199 TFLOP/s; not shared 274:
-// rows were full, only HBM is spared); 4 x (2048 + 64), 16 heads 14.8, latencies of
-// start, one tile and merge (not shared 16.6).
+// 1..2048) keys, 16 heads 59.0 us (the decode 119, 110 where its tables name the same
+// pages: a tile of keys serves 64 rows, not 16); 32 x (32768 + 1000), 128 heads 251
+// (1199 TFLOP/s; the decode 273, and 253 of the same pages: its rows were full, only
+// HBM is spared); 4 x (2048 + 64), 16 heads 14.8, latencies of start, one tile and
+// merge (the decode 15.9); 16 x (12800 + 100), 16 heads 28.4 (37.2), 128 x (4096 + 64),
+// one head 25.0 (65.1), where the starts are most of it.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1320,7 +1322,10 @@ int launch_fp8_shared(const Fp8DecodeArgs& a, int64_t shared_len, cudaStream_t s
   // 64 rows a CTA, where the keys are read half as often and a tile of 64 rows
   // takes little longer than one of 32; 32 where no CTA would have two tiles of
   // the prefix, and its start counts (but not for heads that fill 64 rows: their
-  // own keys may be many).
+  // own keys may be many).  4 x (2048 + 64) keys of 16 heads 14.8 us with 32 rows, 17.9
+  // with 64; 64 x (4096 + 64) 31.8 and 34.9, x (8192 + 64) 42.8 and 41.8, x (32768 + 64)
+  // 113 and 85.  (Long prefixes of few rows would do better with 32 up to about 100
+  // tiles a list: 4 x (32768 + 64) 23.1 and 27.9.)
   const int64_t rows = static_cast<int64_t>(a.batch) * a.num_heads;
   const bool few = a.num_heads <= 32 && (rows + 31) / 32 * ((shared_len + kTile - 1) / kTile) <= num_sms;
   const SharedLayout l = shared_layout(few ? 32 : 64, a.batch, a.num_heads, num_sms, shared_len);

@@ -10,7 +10,7 @@
 // heads are one CTA's, whose queries then leave room for one tile in flight, not
 // two; more heads take a launch each 128.
 // Times: 32 sequences of 1k to 32k, 16 heads 32.2 us (5.7 TB/s); 64 x 4096, 64 heads
-// 31.9, 128 heads 43.8 (3.7 TB/s: the one tile in flight, chunk by chunk behind its
+// 29.8, 128 heads 43.7 (3.7 TB/s: the one tile in flight, chunk by chunk behind its
 // products, and the pieces' starts); 1 x 1000, 16 heads 4.7, a chain of latencies.
 //
 // One CTA per SM, persistent over an equal part of the batch's tiles (and of

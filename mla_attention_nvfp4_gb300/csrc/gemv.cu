@@ -2,9 +2,11 @@
 //   out[m, g, n] = gs sum_k x[m, g, k] code[g, n, k] scale[g, n, k / 16].
 //
 // Every weight is 9/16 of a byte, read once for up to 16 rows: HBM would bound it
-// (9.9 us for 7168 x 16384).  What does is the conversion of the weights: of some
-// 290 instructions a warp for 16 rows x 256 features 160 are the codes' conversion
-// and the scales' products.  The sums run on mma.sync m16n8k16 (f16 operands, fp32
+// (9.9 us for 7168 x 16384).  What does is the latency of the weights' conversion: of
+// some 290 instructions a warp for 16 rows x 256 features 160 are the codes' conversion
+// and the scales' products, in chains that four warps a scheduler do not hide (one row
+// of x issues in 42 % of the cycles, 16 rows in 38 %; at full issue one row's would
+// take 7 us), beside a start of 2.7 us and the clusters' sum of 2.4.  The sums run on mma.sync m16n8k16 (f16 operands, fp32
 // sums): weights are its 16 rows, x its 8 columns.  (tcgen05 wants its operands in
 // shared memory: f16 weights would be written there and read again.)
 //   weights  code * scale has 6 significant bits between 2^-10 and 2688: exact in
@@ -21,8 +23,9 @@
 // Weights come by TMA into a ring (a box of lines of 128 or 64 bytes, and the
 // scales as they lie), x is read ahead of them (asked for behind 25 MB of weights
 // it came 5 us later).
-// Times: 1 x 7168 x 16384 17.9 us (3.7 TB/s), 16 rows 27.6, 1 x 576 x 7168 4.0,
-// 4 rows of 128 matrices of 512 x 128 3.5.  What was tried beside that: weights
+// Times, calls overlapping in a graph: 1 x 7168 x 16384 17.9 us (3.7 TB/s), 16 rows
+// 27.6, 1 x 576 x 7168 4.2, 4 rows of 128 matrices of 512 x 128 3.5, of 128 x 512 5.5,
+// 16 x 1024 x 7168 8.6.  What was tried beside that: weights
 // from global memory to registers (23.3 us), three CTAs an SM (clusters of 8 then
 // fill the SMs one and a half times: 31 us), 16 warps a CTA (16 rows: 31.8 us).
 #include <cuda.h>
@@ -510,8 +513,11 @@ int launch_gemv(const GemvArgs& a, cudaStream_t stream, int num_sms) {
   p.scale_bytes = p.sf_tiles * p.k_tiles * 512;
   // Two groups of 16 rows a warp, in steps of half the features, where x is much
   // (more than 8 rows: 16 x 7168 x 16384 27.6 us, with one 28.5) or a row of weights
-  // short (4 x 128 heads x 512 x 128 3.5 us, with one 6.4).  One otherwise: 1 x 7168 x
-  // 16384 17.9 us, with two 20.4; 1 x 576 x 7168 4.0, with two 4.4.
+  // short (4 x 128 heads x 512 x 128 3.5 us, with one 5.9; x 512 6.8, with one 7.9).
+  // One otherwise: 1 x 7168 x 16384 17.9 us, with two 20.4; 1 x 576 x 7168 4.0, with two
+  // 4.4.  (Near the border the matrices' number counts too: 4 x 128 heads x 512 x 1024
+  // 12.5 us, with two 11.7; 4 x 16 heads x 512 x 512 4.2, with one 3.8; x 256 3.8, with
+  // one 2.7.)
   const bool two = a.K <= 512;
   constexpr int kSlot = 37;  // 9 and 9 more
   if (a.M <= 1) return two ? launch<1, 2>(p, kSlot, num_sms, stream) : launch<1, 1>(p, kSlot + 1, num_sms, stream);
