@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <utility>
 
 #include "launch.h"
 
@@ -45,26 +46,32 @@ bool table_ok(int64_t max_pages, int64_t stride) {
 
 constexpr int kSharedRows = 1 << 30;  // sequences times heads of a batch with a shared prefix
 
-// Whether two arrays share memory.
-struct Bytes {
+// A row of 4-byte words for each sequence: `len` of them, `stride` apart.
+struct Rows {
   const void* p;
-  uint64_t bytes;
+  int64_t stride, len;
 };
-bool overlap(const Bytes& a, const Bytes& b) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-  return a.bytes != 0 && b.bytes != 0 && p < q + b.bytes && q < p + a.bytes;
-}
-
-// Whether two matrices of fp32 rows (of `len`, `stride` apart) share memory.  Of
-// equal strides they may be columns of one wider matrix.
-bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
-                  int64_t rows) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  if (p >= q + ((rows - 1) * b_stride + b_len) * sizeof(float) || q >= p + ((rows - 1) * a_stride + a_len) * sizeof(float))
-    return false;
-  if (a_stride != b_stride || rows == 1 || (q - p) % sizeof(float) != 0) return true;
-  const int64_t d = (static_cast<int64_t>(q - p) / static_cast<int64_t>(sizeof(float))) % a_stride, column = d < 0 ? d + a_stride : d;
-  return column < a_len || column + b_len > a_stride;
+// Whether those of two arrays share memory.  Decided exactly where both have the same
+// stride (they may be columns of one wider matrix) or one has no gaps; else by the
+// memory that they lie in.
+bool overlap(Rows a, Rows b, int64_t rows) {
+  if (a.p == nullptr || b.p == nullptr || a.len == 0 || b.len == 0) return false;
+  const auto at = [](const Rows& r) { return static_cast<uint64_t>(reinterpret_cast<uintptr_t>(r.p)); };
+  const auto bytes = [](int64_t words) { return static_cast<uint64_t>(words) * 4; };
+  const auto end = [&](const Rows& r) { return at(r) + (rows - 1) * bytes(r.stride) + bytes(r.len); };
+  if (at(a) >= end(b) || at(b) >= end(a)) return false;
+  if (rows == 1 || (at(b) - at(a)) % 4 != 0) return true;
+  if (at(b) < at(a)) std::swap(a, b);  // a begins first
+  const uint64_t step = bytes(a.stride), before = at(b) - at(a);
+  if (a.stride == b.stride) {
+    const uint64_t column = before % step;
+    return column < bytes(a.len) || column + bytes(b.len) > step;
+  }
+  if (b.stride == b.len) {  // in a gap of a's, or behind its last row
+    const uint64_t column = before % step;
+    return column < bytes(a.len) || end(b) - at(b) > step - column;
+  }
+  return true;
 }
 
 thread_local const char* t_last_error = "";
@@ -679,7 +686,7 @@ int mla_nvfp4_fp8_key_weights(const void* q, int batch, int num_heads, const uin
       (weights != nullptr && weights_stride < row_len))
     return MLA_ERR_INVALID_ARG;
   if (weights != nullptr && (weights != out || weights_stride != out_stride) &&
-      rows_overlap(weights, weights_stride, row_len, out, out_stride, row_len, batch))
+      overlap({weights, weights_stride, row_len}, {out, out_stride, row_len}, batch))
     return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || !(softmax_scale < 3.0e38f)) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache)) return MLA_ERR_ALIGNMENT;
@@ -708,21 +715,18 @@ int mla_nvfp4_fp8_cache_evict(uint8_t* cache, int64_t num_slots, float* scales, 
       new_page_table == nullptr || seq_lens == nullptr || kept == nullptr || new_lens == nullptr || num_slots == 0 ||
       weights_stride < row_len)
     return MLA_ERR_INVALID_ARG;
+  if (new_weights != nullptr && (new_row_len < keep || new_weights_stride < new_row_len)) return MLA_ERR_INVALID_ARG;
   // one CTA's results are no other's arguments, and no results of another kind
-  const uint64_t word = sizeof(int32_t), B = batch;
-  const Bytes in[] = {{seq_lens, B * word},
-                      {weights, row_len > 0 ? ((B - 1) * weights_stride + row_len) * word : 0},
-                      {page_table, ((B - 1) * page_table_stride + max_pages) * word},
-                      {new_page_table, ((B - 1) * new_page_table_stride + new_max_pages) * word}};
-  const Bytes rows{kept, B * keep * word}, lens{new_lens, B * word};
-  const Bytes more{new_weights, new_weights != nullptr ? ((B - 1) * new_weights_stride + new_row_len) * word : 0};
-  for (const Bytes& a : in)
-    if (overlap(a, rows) || overlap(a, lens) || (a.p != weights && overlap(a, more))) return MLA_ERR_INVALID_ARG;
-  if (overlap(rows, lens) || overlap(rows, more) || overlap(lens, more)) return MLA_ERR_INVALID_ARG;
-  if (new_weights != nullptr &&
-      (new_row_len < keep || new_weights_stride < new_row_len ||
-       rows_overlap(weights, weights_stride, row_len, new_weights, new_weights_stride, new_row_len, batch)))
-    return MLA_ERR_INVALID_ARG;
+  const Rows in[] = {{seq_lens, 1, 1},
+                     {weights, weights_stride, row_len},
+                     {page_table, page_table_stride, max_pages},
+                     {new_page_table, new_page_table_stride, new_max_pages}};
+  const Rows res[] = {{kept, keep, keep}, {new_lens, 1, 1}, {new_weights, new_weights_stride, new_row_len}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& a : in)
+      if (overlap(a, res[i], batch)) return MLA_ERR_INVALID_ARG;
+    if (overlap(res[i], res[(i + 1) % 3], batch)) return MLA_ERR_INVALID_ARG;
+  }
   if (!aligned16(cache)) return MLA_ERR_ALIGNMENT;
   const int sms = device_sms();
   if (sms < 0) return -sms;

@@ -171,3 +171,18 @@ def test_evict_refuses_results_in_its_arguments(kw):
     args = lambda d: {k: ctypes.c_void_p(v) for k, v in d.items()}
     assert _evict(**args(base)) == 3  # (the cache's alignment)
     assert _evict(**args({**base, **kw})) == 1
+
+
+def test_evict_takes_a_record_for_each_sequence():
+    # a sequence's table, new table, weights and their result in one record of 512 words; what is contiguous lies elsewhere, or
+    # (seq_lens) in a gap
+    at = lambda words: ctypes.c_void_p((1 << 20) + 4 * words)
+    rec = dict(pt=at(0), pt_st=512, npt=at(2), npt_st=512, w=at(8), w_st=512, nw=at(200), nw_st=512, lens=at(504), cache=ODD,
+               kept=ctypes.c_void_p(1 << 24), nlens=ctypes.c_void_p(1 << 25))
+    assert _evict(**rec) == 3  # (the cache's alignment)
+    assert _evict(**rec | dict(nlens=at(506))) == 3  # in the same gap
+    assert _evict(**rec | dict(nlens=at(508), B=4)) == 3
+    assert _evict(**rec | dict(kept=at(380))) == 3  # words 380 .. 460
+    for kw in (dict(nlens=at(505)), dict(nlens=at(511)), dict(nlens=at(135)), dict(nlens=at(508), B=5), dict(kept=at(430)),
+               dict(nw=at(135)), dict(nw=at(475)), dict(nw=at(1), nrow=40), dict(npt=at(210))):
+        assert _evict(**rec | kw) == 1, kw
