@@ -6,9 +6,10 @@
 // some 290 instructions a warp for 16 rows x 256 features 160 are the codes' conversion
 // and the scales' products, in chains that four warps a scheduler do not hide (one row
 // of x issues in 42 % of the cycles, 16 rows in 38 %; at full issue one row's would
-// take 7 us), beside a start of 2.7 us and the clusters' sum of 2.4.  The sums run on mma.sync m16n8k16 (f16 operands, fp32
-// sums): weights are its 16 rows, x its 8 columns.  (tcgen05 wants its operands in
-// shared memory: f16 weights would be written there and read again.)
+// take 7 us), beside a start of 2.7 us and the clusters' sum of 2.4.  The sums run on
+// mma.sync m16n8k16 (f16 operands, fp32 sums): weights are its 16 rows, x its 8 columns.
+// (tcgen05 wants its operands in shared memory: f16 weights would be written there and
+// read again.)
 //   weights  code * scale has 6 significant bits between 2^-10 and 2688: exact in
 //            f16.  A thread of a quad holds a quarter of a step's features of a row,
 //            whole blocks of 16.  Which feature of an instruction they are is free,
